@@ -270,6 +270,156 @@ LMOE_API size_t lmoe_block_workspace_bytes(const lmoe_dims* dims);
 LMOE_API int lmoe_block_forward(const lmoe_dims* dims, const lmoe_weights* weights, const lmoe_block_norms* norms,
                                 const uint16_t* x, uint16_t* y, void* ws, size_t ws_bytes, lmoe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Speculative decoding over a paged key/value cache.
+ *
+ * The attention half of a verify step, next to the layer's own verify sizes
+ * ("Soporte de dia 0 para Muse Spark Open en vLLM", section "DSpark": seven
+ * drafted tokens are verified at once; the pages give no attention kernel, no
+ * cache layout and no tree form, so those are this library's own).  One step:
+ *   lmoe_tree_masks      parents of the drafted tokens -> masks, positions
+ *   lmoe_tree_attention  drafted tokens over the cached prefix and the drafts
+ *   (the caller accepts a path of each tree)
+ *   lmoe_kv_plan         request lengths -> block tables and slots
+ *   lmoe_kv_write        accepted rows -> their slots in the cache
+ * The drafts' keys and values stay in the caller's rows until they are
+ * accepted, so a rejected draft never touches the cache.  A prompt enters the
+ * cache the same way, by lmoe_kv_plan and lmoe_kv_write.
+ *
+ * Rows are ragged: request b has the rows token_offsets[b] ..
+ * token_offsets[b + 1] - 1 (int32 [B + 1], ascending, in the caller's hands).
+ * Position p of request b is block block_table[b][p / block_size], slot
+ * p % block_size; the slot number of lmoe_kv_plan and lmoe_kv_write is
+ * block * block_size + p % block_size.
+ * ------------------------------------------------------------------------- */
+
+/* The cache of one layer, keys and values alike: bf16, the element (block,
+ * head, slot, d) at block * block_stride + head * head_stride +
+ * slot * slot_stride + d.  Strides are in elements, multiples of 8, so both
+ * the [block][head][slot][d] and the [block][slot][head][d] order fit; k and v
+ * are 16-byte aligned.  block_size is 16, 32, 64, 128 or 256; head_dim 64 or
+ * 128 (else LMOE_EUNSUPPORTED); kv_heads 1 .. 256. */
+typedef struct {
+  uint16_t* k;
+  uint16_t* v;
+  int32_t n_blocks;
+  int32_t block_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int64_t block_stride;
+  int64_t head_stride;
+  int64_t slot_stride;
+} lmoe_kv_cache;
+
+typedef struct {
+  int32_t n_requests;         /* B, 1 .. 8192 */
+  int32_t n_tokens;           /* rows of q, k_new, v_new and out, 1 .. 1048576 */
+  int32_t max_request_tokens; /* no request has more drafted rows than this, 1 .. 256 */
+  int32_t q_heads;            /* a multiple of the cache's kv_heads, at most 128 per kv head */
+  int32_t max_blocks;         /* row length of block_table */
+  int32_t mask_words;         /* 64-bit words per row of the mask, 1 .. 4 */
+  int32_t window;             /* tokens in sight, the row's own included; 0 = all */
+  float scale;                /* of the scores, > 0, e.g. 1/sqrt(head_dim) */
+} lmoe_attn_dims;
+
+/* Tree masks: for row i of a request, mask bit j (word j / 64, bit j % 64) is
+ * set iff row j of the same request is i itself or an ancestor of i, and
+ * pos[i] = lens[b] + the number of i's ancestors among the drafts.
+ *   parents  int32 [T], the parent's row inside the request, below the row's
+ *            own, or -1 for a child of the cached prefix
+ *   lens     int32 [B], cached tokens, or NULL for none
+ *   mask     out uint64 [T][mask_words];  pos out int32 [T]
+ *   ws       optional, as for lmoe_pool: with a workspace (256-byte aligned,
+ *            at least 8 bytes) its status word is zeroed and a parent at or
+ *            above its row, offsets that descend or pass n_tokens, or a
+ *            request of more than 64 * mask_words rows is reported there
+ *            (LMOE_EDEVICE_CHECK).  Such a parent counts as -1; such a
+ *            request's rows are left as they are, those within n_tokens and
+ *            past the mask's width with an empty mask. */
+LMOE_API int lmoe_tree_masks(int32_t n_requests, int32_t n_tokens, int32_t mask_words,
+                             const int32_t* token_offsets, const int32_t* parents, const int32_t* lens,
+                             uint64_t* mask, int32_t* pos, void* ws, size_t ws_bytes, lmoe_stream_t stream);
+
+/* Workspace size of lmoe_tree_attention (0 if dims or cache are invalid; of
+ * the cache only kv_heads and head_dim count).  256-byte aligned device
+ * memory, no initialisation needed. */
+LMOE_API size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* dims, const lmoe_kv_cache* cache);
+
+/* Attention of each request's drafted rows over its cached prefix and its
+ * drafts.  Query head h reads kv head h / (q_heads / kv_heads).  Row i sees
+ *   the cached positions t < lens[b] with pos[i] - t < window, and
+ *   the drafted rows j of its request with mask bit j set and
+ *   pos[i] - pos[j] < window        (no window test when window is 0);
+ *   out[i][h] = sum_j p_j v_j,  p = softmax over what the row sees of
+ *   scale * (q . k_j);  lse[i][h] = ln sum_j exp(scale * (q . k_j)).
+ * A row that sees nothing gets out = 0 and lse = -infinity.  Keys and values
+ * that a row does not see have no effect on it, whatever bits they hold.
+ *   q        bf16 [T][q_heads][head_dim], q_stride elements from token to token
+ *   k_new, v_new  bf16 [T][kv_heads][head_dim], strides k_stride, v_stride
+ *            (strides are multiples of 8: slices of a fused projection fit)
+ *   lens     int32 [B], cached tokens, at most max_blocks * block_size
+ *   block_table  int32 [B][max_blocks]
+ *   mask     uint64 [T][mask_words], or NULL: every row sees the rows of its
+ *            request up to its own (a chain, or plain decoding)
+ *   pos      int32 [T], or NULL for lens[b] + the row's index; only a window
+ *            reads it; a position below lens[b] counts as lens[b]
+ *   out      out bf16 [T][q_heads][head_dim], contiguous
+ *   lse      out fp32 [T][q_heads], or NULL
+ * Scores, the running maximum and sum, and the accumulators are fp32; the
+ * probabilities are rounded to bf16 for the product with the values.
+ * Reported on the device (LMOE_EDEVICE_CHECK through lmoe_status_check):
+ * offsets that descend, pass n_tokens or give a request more than
+ * max_request_tokens rows, and a length below 0 or past its table: the rows
+ * of such a request are not written; a block number outside the cache: the
+ * request's rows hold no meaning.  Nothing is read out of bounds. */
+LMOE_API int lmoe_tree_attention(const lmoe_attn_dims* dims, const lmoe_kv_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k_new, int64_t k_stride, const uint16_t* v_new,
+                                 int64_t v_stride, const int32_t* token_offsets, const int32_t* lens,
+                                 const int32_t* block_table, const uint64_t* mask, const int32_t* pos, uint16_t* out,
+                                 float* lse, void* ws, size_t ws_bytes, lmoe_stream_t stream);
+
+/* Block tables and slots from request lengths.  Free blocks stand in a ring:
+ * ring_state = {head, count}, the free block i at ring[(head + i) % ring_size].
+ * Request b holds lens[b] tokens in owned[b] blocks and gets new_tokens[b]
+ * more (below 0: the request ends).  In request order:
+ *   need = max(0, ceil((lens + new) / block_size) - owned);
+ *   b is served iff its blocks fit its table row, its tokens fit slots[] and
+ *   the needs of the requests up to it (those that fit) fit the free count;
+ *   a served request's new blocks come from the ring's head, an ended
+ *   request's blocks go to its tail (they are free for the next call).
+ *   block_table  int32 [B][max_blocks], in place: entries owned .. owned +
+ *            need - 1 of served requests are written
+ *   ring     int32 [ring_size], in place
+ *   lens_out, owned_out  out int32 [B]: lens + new and owned + need for a
+ *            served request, unchanged for one that is not (how the caller
+ *            learns of it), 0 for an ended one
+ *   ring_state_out  out int32 [2]
+ *   token_offsets   out int32 [B + 1], sums of new_tokens
+ *   slots    out int32 [n_slots]: the slot of each new token in ragged order,
+ *            -1 for tokens of requests not served and past the last token
+ * Outputs other than block_table and ring must not overlap the inputs
+ * (LMOE_EINVAL where two are the same pointer).  Called again on the same
+ * inputs it writes the same values. */
+LMOE_API int lmoe_kv_plan(int32_t n_requests, int32_t block_size, int32_t max_blocks, int32_t n_slots,
+                          const int32_t* lens, const int32_t* new_tokens, const int32_t* owned, int32_t* block_table,
+                          int32_t* ring, int32_t ring_size, const int32_t* ring_state, int32_t* lens_out,
+                          int32_t* owned_out, int32_t* ring_state_out, int32_t* token_offsets, int32_t* slots,
+                          lmoe_stream_t stream);
+
+/* Writes rows into the cache: for t < n_tokens, slot slots[t] of K and V gets
+ * row src[t] of k_new and v_new.
+ *   k_new, v_new  bf16 [n_rows][kv_heads][head_dim], strides as for
+ *            lmoe_tree_attention
+ *   src      int32 [n_tokens], or NULL for t itself (n_tokens <= n_rows)
+ *   slots    int32 [n_tokens]; a negative slot is passed over
+ *   ws       optional, as for lmoe_tree_masks: a slot past the cache or a row
+ *            outside [0, n_rows) is reported there; it is passed over in any
+ *            case
+ * Slots must differ from one another. */
+LMOE_API int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, int64_t k_stride, const uint16_t* v_new,
+                           int64_t v_stride, int32_t n_rows, const int32_t* src, const int32_t* slots,
+                           int32_t n_tokens, void* ws, size_t ws_bytes, lmoe_stream_t stream);
+
 /* Synchronises `stream`, reads the device status word of `ws` and returns it
  * (LMOE_OK, LMOE_ETIMEOUT or LMOE_EDEVICE_CHECK), or LMOE_ECUDA if the
  * stream itself reports an error.  `ws` is a device pointer. */

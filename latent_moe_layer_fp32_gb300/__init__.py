@@ -24,7 +24,8 @@ __all__ = [
     "lmoe_block_forward", "norms_of", "lmoe_experts_nvfp4", "lmoe_forward_nvfp4", "nvfp4_of",
     "lmoe_status_check", "lmoe_error_string",
     "lmoe_last_launch_count", "lmoe_selftest_e2m1", "lmoe_selftest_timeout", "lmoe_profile_events", "dims_of",
-    "weights_of",
+    "weights_of", "LmoeKvCache", "LmoeAttnDims", "kv_cache_of", "attn_dims_of", "lmoe_tree_masks",
+    "lmoe_tree_attention", "lmoe_tree_attention_workspace_bytes", "lmoe_kv_plan", "lmoe_kv_write",
 ]
 
 LMOE_OK, LMOE_EINVAL, LMOE_EUNSUPPORTED, LMOE_ECUDA, LMOE_ETIMEOUT, LMOE_EDEVICE_CHECK, LMOE_EWORKSPACE = \
@@ -54,6 +55,17 @@ class LmoeNvfp4Scales(ctypes.Structure):
 class LmoeWsLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("status", "topk_idx", "topk_w", "expert_offsets", "sorted_rows",
                                                "row_pos", "x_lat", "y", "z", "total")]
+
+
+class LmoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+
+
+class LmoeAttnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_requests", "n_tokens", "max_request_tokens", "q_heads", "max_blocks",
+                                              "mask_words", "window")] + [("scale", ctypes.c_float)]
 
 
 class LmoeError(RuntimeError):
@@ -108,7 +120,15 @@ def load(path: str | None = None):
     lib.lmoe_set_option.argtypes = [i32, i32]
     lib.lmoe_last_launch_name.argtypes = [i32]
     lib.lmoe_last_launch_name.restype = ctypes.c_char_p
-    for f in ("lmoe_workspace_layout", "lmoe_route", "lmoe_pool", "lmoe_experts_mxfp4", "lmoe_norm_combine_unpool",
+    i64, cp, ap = ctypes.c_int64, ctypes.POINTER(LmoeKvCache), ctypes.POINTER(LmoeAttnDims)
+    lib.lmoe_tree_masks.argtypes = [i32, i32, i32] + [vp] * 6 + [sz, vp]
+    lib.lmoe_tree_attention_workspace_bytes.argtypes = [ap, cp]
+    lib.lmoe_tree_attention_workspace_bytes.restype = sz
+    lib.lmoe_tree_attention.argtypes = [ap, cp, vp, i64, vp, i64, vp, i64] + [vp] * 8 + [sz, vp]
+    lib.lmoe_kv_plan.argtypes = [i32] * 4 + [vp] * 5 + [i32] + [vp] * 7
+    lib.lmoe_kv_write.argtypes = [cp, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz, vp]
+    for f in ("lmoe_tree_masks", "lmoe_tree_attention", "lmoe_kv_plan", "lmoe_kv_write",
+              "lmoe_workspace_layout", "lmoe_route", "lmoe_pool", "lmoe_experts_mxfp4", "lmoe_norm_combine_unpool",
               "lmoe_forward", "lmoe_forward_routed", "lmoe_block_forward", "lmoe_forward_nvfp4", "lmoe_experts_nvfp4",
               "lmoe_status_check", "lmoe_last_launch_count", "lmoe_selftest_e2m1",
               "lmoe_profile_events", "lmoe_route_noalloc", "lmoe_set_option", "lmoe_selftest_dequant_bf16",
@@ -289,6 +309,121 @@ def lmoe_block_forward(dims, weights: LmoeWeights, norms: LmoeBlockNorms, x, y, 
     _check(load().lmoe_block_forward(ctypes.byref(dims), ctypes.byref(weights), ctypes.byref(norms),
                                      _ptr(x, _BF16), _ptr(y, _BF16), _ptr(ws), ws.numel() * ws.element_size(),
                                      _stream(stream)), "lmoe_block_forward")
+
+
+# ---------------------------------------------------------------------------------------------
+# speculative decoding over a paged key/value cache
+# ---------------------------------------------------------------------------------------------
+
+_I64 = (torch.int64, torch.uint64)
+_BF16_ONLY = (torch.bfloat16,)
+
+
+def kv_cache_of(k, v) -> LmoeKvCache:
+    """LmoeKvCache of two bf16 tensors [n_blocks, kv_heads, block_size, head_dim] of equal
+    strides; any order in memory with head_dim contiguous (a [block][slot][head][d] cache
+    is passed as its transpose(1, 2)).  The caller keeps the tensors alive."""
+    for t in (k, v):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("expected CUDA tensors (the library takes device pointers)")
+        if t.dtype not in _BF16_ONLY:
+            raise TypeError(f"unexpected dtype {t.dtype}, want torch.bfloat16")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError("expected [n_blocks, kv_heads, block_size, head_dim] with head_dim contiguous")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    n, h, b, d = k.shape
+    return LmoeKvCache(k.data_ptr(), v.data_ptr(), n, b, h, d, k.stride(0), k.stride(1), k.stride(2))
+
+
+def attn_dims_of(n_requests, n_tokens, max_request_tokens, q_heads, max_blocks, mask_words, scale,
+                 window=0) -> LmoeAttnDims:
+    return LmoeAttnDims(n_requests, n_tokens, max_request_tokens, q_heads, max_blocks, mask_words, window, scale)
+
+
+def _rows(t, heads, width):
+    """Address and row stride of a bf16 [rows, heads, width] tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch tensor")
+    if t.dtype not in _BF16_ONLY:
+        raise TypeError(f"unexpected dtype {t.dtype}, want torch.bfloat16")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor (the library takes device pointers)")
+    st = t.stride()
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width or st[2] != 1 or (heads > 1 and st[1] != width):
+        raise ValueError(f"expected [rows, {heads}, {width}] with contiguous rows, got {tuple(t.shape)} with strides "
+                         f"{tuple(st)}")
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * width
+
+
+def _sized(t, n, dtype, what):
+    p = _ptr(t, dtype)
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{what}: expected at least {n} elements, got {t.numel()}")
+    return p
+
+
+def _ws(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+def lmoe_tree_masks(token_offsets, parents, lens, mask, pos, ws=None, stream=None):
+    """Ancestor masks (int64 or uint64 [T, mask_words]) and positions (int32 [T]) of drafted
+    tokens from their parents (int32 [T], -1: the cached prefix); lens int32 [B] or None."""
+    b, t = token_offsets.numel() - 1, parents.numel()
+    if mask.dim() != 2 or mask.shape[0] != t:
+        raise ValueError(f"mask: expected [{t}, mask_words], got {tuple(mask.shape)}")
+    w, nb = _ws(ws)
+    _check(load().lmoe_tree_masks(b, t, mask.shape[1], _ptr(token_offsets, _I32), _ptr(parents, _I32),
+                                  _sized(lens, b, _I32, "lens"), _ptr(mask, _I64), _sized(pos, t, _I32, "pos"), w, nb,
+                                  _stream(stream)), "lmoe_tree_masks")
+
+
+def lmoe_tree_attention_workspace_bytes(dims: LmoeAttnDims, cache: LmoeKvCache) -> int:
+    return int(load().lmoe_tree_attention_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache)))
+
+
+def lmoe_tree_attention(dims, cache, q, k_new, v_new, token_offsets, lens, block_table, mask, pos, out, lse, ws,
+                        stream=None):
+    """Drafted rows over the cached prefix and the tree of drafts.  q [T, q_heads, d], k_new and
+    v_new [T, kv_heads, d] may be slices of one projection; mask, pos and lse may be None."""
+    n, d = dims.n_tokens, cache.head_dim
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(q, dims.q_heads, d), _rows(k_new, cache.kv_heads, d),
+                                    _rows(v_new, cache.kv_heads, d))
+    if min(q.shape[0], k_new.shape[0], v_new.shape[0]) < n:
+        raise ValueError(f"expected {n} rows in q, k_new and v_new")
+    _check(load().lmoe_tree_attention(
+        ctypes.byref(dims), ctypes.byref(cache), qp, qs, kp, ks, vp, vs,
+        _sized(token_offsets, dims.n_requests + 1, _I32, "token_offsets"), _sized(lens, dims.n_requests, _I32, "lens"),
+        _sized(block_table, dims.n_requests * dims.max_blocks, _I32, "block_table"),
+        _sized(mask, n * dims.mask_words, _I64, "mask"), _sized(pos, n, _I32, "pos"),
+        _sized(out, n * dims.q_heads * d, _BF16, "out"), _sized(lse, n * dims.q_heads, _F32, "lse"), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)), "lmoe_tree_attention")
+
+
+def lmoe_kv_plan(block_size, lens, new_tokens, owned, block_table, ring, ring_state, lens_out, owned_out,
+                 ring_state_out, token_offsets, slots, stream=None):
+    """Block tables (in place), slots and the free ring's next state from request lengths."""
+    b = lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != b:
+        raise ValueError(f"block_table: expected [{b}, max_blocks], got {tuple(block_table.shape)}")
+    _check(load().lmoe_kv_plan(
+        b, int(block_size), block_table.shape[1], slots.numel(), _ptr(lens, _I32),
+        _sized(new_tokens, b, _I32, "new_tokens"), _sized(owned, b, _I32, "owned"), _ptr(block_table, _I32),
+        _ptr(ring, _I32), ring.numel(), _sized(ring_state, 2, _I32, "ring_state"),
+        _sized(lens_out, b, _I32, "lens_out"), _sized(owned_out, b, _I32, "owned_out"),
+        _sized(ring_state_out, 2, _I32, "ring_state_out"), _sized(token_offsets, b + 1, _I32, "token_offsets"),
+        _ptr(slots, _I32), _stream(stream)), "lmoe_kv_plan")
+
+
+def lmoe_kv_write(cache, k_new, v_new, src, slots, ws=None, stream=None):
+    """Rows src[t] (or t, src None) of k_new and v_new [rows, kv_heads, d] into the cache's slots[t]."""
+    (kp, ks), (vp, vs) = (_rows(k_new, cache.kv_heads, cache.head_dim), _rows(v_new, cache.kv_heads, cache.head_dim))
+    n = slots.numel()
+    w, nb = _ws(ws)
+    _check(load().lmoe_kv_write(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
+                                _sized(src, n, _I32, "src"), _ptr(slots, _I32), n, w, nb, _stream(stream)),
+           "lmoe_kv_write")
 
 
 def lmoe_status_check(ws, stream=None) -> int:

@@ -48,6 +48,22 @@ int check_dims(const lmoe_dims* d) {
   return LMOE_OK;
 }
 
+int dev_info(DevInfo* out) {
+  static DevInfo cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LMOE_ECUDA;
+  DevInfo& c = cache[dev & 63];
+  if (c.sms == 0) {
+    if (cudaDeviceGetAttribute(&c.major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&c.minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return LMOE_ECUDA;
+  }
+  *out = c;
+  if (c.major != 10 || c.minor != 3) return LMOE_EUNSUPPORTED;
+  return LMOE_OK;
+}
+
 int fast_route_ks(int H) {
   const int ks = H % 1024 == 0 ? 1024 : (H % 512 == 0 ? 512 : (H % 256 == 0 ? 256 : 0));
   return (ks > 0 && H / ks <= 16) ? ks : 0;
@@ -109,27 +125,6 @@ bool down_forms_z(const lmoe_dims* d) { return d->T <= t_downz_max_t && d->T * d
 // rows per group of the routing table: what the expert kernels of this regime consume
 int group_rows(int T) { return experts_tc(T) ? kTcExpertGroup : expert_max_group(T); }
 
-
-struct DevInfo {
-  int sms = 0;
-  int major = 0, minor = 0;
-};
-
-int dev_info(DevInfo* out) {
-  static DevInfo cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return LMOE_ECUDA;
-  DevInfo& c = cache[dev & 63];
-  if (c.sms == 0) {
-    if (cudaDeviceGetAttribute(&c.major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&c.minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return LMOE_ECUDA;
-  }
-  *out = c;
-  if (c.major != 10 || c.minor != 3) return LMOE_EUNSUPPORTED;
-  return LMOE_OK;
-}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -9,6 +9,12 @@ namespace lmoe {
 // ---- api.cu: argument checks and launch bookkeeping shared by the entry points ----
 // LMOE_OK, LMOE_EINVAL or LMOE_EUNSUPPORTED for the layer dimensions
 int check_dims(const lmoe_dims* d);
+// SM count and compute capability of the current device; LMOE_EUNSUPPORTED unless it is 10.3
+struct DevInfo {
+  int sms = 0;
+  int major = 0, minor = 0;
+};
+int dev_info(DevInfo* out);
 // split-K factor of the CUDA-core router: enough CTAs for the GPU, at most max_split
 int router_splits(int T, int E, int H, int sms, int max_split);
 // K range per warp of route_fast_kernel (at most 16 ranges), or 0 when H does not allow it
@@ -186,6 +192,7 @@ __global__ void groups_from_offsets_kernel(const int32_t* offsets, const int32_t
                                            int4* groups, int32_t* n_groups, Status* st);
 __global__ void ssq_kernel(const float* y, int R, int L, float* ssq);
 __global__ void ws_zero_kernel(uint4* p, int n16);
+__global__ void status_zero_kernel(Status* st);
 __global__ void io_in_kernel(const uint4* x_host, uint4* x_dev, size_t n16, uint4* zero, int nzero16);
 __global__ void io_out_kernel(const uint4* out_dev, uint4* out_host, size_t n16);
 __global__ void timeout_selftest_kernel(Status* st, unsigned long long limit_ns);

@@ -1,0 +1,390 @@
+// The paged key/value cache's bookkeeping: tree masks of drafted tokens, block
+// tables and slots from request lengths, and the write of rows into slots.
+// See include/lmoe.h for the contract of every call.
+//
+// All three move few bytes, so what bounds them is the launch and the chain of
+// dependent loads, except the write of a prompt, which is a copy.
+#include <atomic>
+
+#include "common.cuh"
+#include "launch.cuh"
+
+namespace lmoe {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// tree masks
+// ---------------------------------------------------------------------------
+// One CTA per request, one thread per drafted row.  Ancestor sets by pointer
+// doubling: after round r a row's mask holds its nearest 2^r ancestors-or-self
+// and up points past them, so ceil(log2 n) rounds close any tree and the loop
+// ends as soon as every pointer has left the tree.
+template <int W>
+__global__ void __launch_bounds__(64 * W)
+    tree_masks_kernel(int n_tokens, const int32_t* __restrict__ offsets, const int32_t* __restrict__ parents,
+                      const int32_t* __restrict__ lens, uint64_t* __restrict__ mask, int32_t* __restrict__ pos,
+                      Status* st) {
+  constexpr int N = 64 * W;
+  __shared__ uint64_t s_mask[2][W][N];
+  __shared__ int s_up[2][N];
+  __shared__ int s_depth[2][N];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x, i = threadIdx.x;
+  const int t0 = offsets[b], t1 = offsets[b + 1];
+  const int len = lens ? lens[b] : 0;
+  if (t0 < 0 || t1 < t0 || t1 > n_tokens) {
+    if (i == 0) set_error(st, LMOE_EDEVICE_CHECK, 201);
+    return;
+  }
+  const int n = t1 - t0;
+  if (n > N) {
+    if (i == 0) set_error(st, LMOE_EDEVICE_CHECK, 202);
+    for (int r = i; r < n; r += N) {
+      for (int w = 0; w < W; ++w) mask[(size_t)(t0 + r) * W + w] = 0;
+      pos[t0 + r] = len;
+    }
+    return;
+  }
+  int up = -1;
+  if (i < n) {
+    up = parents[t0 + i];
+    if (up >= i || up < -1) {
+      set_error(st, LMOE_EDEVICE_CHECK, 203);
+      up = -1;
+    }
+  }
+  uint64_t m[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) m[w] = (i >> 6) == w ? 1ull << (i & 63) : 0ull;
+  int depth = 0;  // ancestors counted so far
+  int span = up >= 0 ? 1 : 0;
+  int cur = 0;
+  while (__syncthreads_or(up >= 0)) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) s_mask[cur][w][i] = m[w];
+    s_up[cur][i] = up;
+    s_depth[cur][i] = span;
+    __syncthreads();
+    if (up >= 0) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) m[w] |= s_mask[cur][w][up];
+      span += s_depth[cur][up];
+      up = s_up[cur][up];
+    }
+    cur ^= 1;
+  }
+  depth = span;
+  if (i < n) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) mask[(size_t)(t0 + i) * W + w] = m[w];
+    pos[t0 + i] = len + depth;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// block plan
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxRequests = 8192;
+
+struct PlanArgs {
+  int B, bs, max_blocks, n_slots, ring_size;
+  const int32_t *lens, *add, *owned, *ring_state;
+  int32_t *table, *ring, *lens_out, *owned_out, *ring_state_out, *offsets, *slots;
+};
+
+struct PlanReq {
+  int len, add, owned, after;  // tokens held, tokens to append (0 for an ended request), blocks held / needed in all
+  bool ends;
+};
+
+__device__ __forceinline__ PlanReq plan_req(const PlanArgs& a, int b) {
+  PlanReq r;
+  const int add = a.add[b];
+  r.ends = add < 0;
+  r.add = max(add, 0);
+  r.len = max(a.lens[b], 0);
+  r.owned = min(max(a.owned[b], 0), a.max_blocks);
+  const long long after = ((long long)r.len + r.add + a.bs - 1) / a.bs;
+  r.after = (int)min(after, (long long)a.max_blocks + 1);
+  return r;
+}
+
+// Sum of v over the threads before this one, and over all in *total.
+__device__ __forceinline__ unsigned long long scan_excl(unsigned long long v, unsigned long long* s_warp,
+                                                        unsigned long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  unsigned long long w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const unsigned long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  __syncthreads();
+  return x - v + (warp ? before : 0ull);
+}
+
+__device__ __forceinline__ int ring_at(int head, long long i, int size) {
+  return (int)(((long long)head + i) % size);
+}
+
+// Every CTA scans all requests (at most 8192: 8 passes of 1024 threads over
+// L2-resident lengths) and keeps three prefix sums in shared memory, then
+// takes its share of the requests (a warp each) and of the tokens (a thread
+// each, its request found by bisection).  Nothing is passed between CTAs, so
+// one launch does it.
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a) {
+  extern __shared__ int s_plan[];
+  int* s_tok = s_plan;             // [B + 1] first token of each request, saturated at n_slots + 1
+  int* s_pop = s_plan + a.B + 1;   // [B] blocks popped by the requests before it; -1: not served
+  int* s_push = s_pop + a.B;       // [B] blocks pushed by the requests before it
+  __shared__ unsigned long long s_warp[32];
+  __shared__ int s_taken;
+  pdl_wait();
+  pdl_trigger();
+  const int head = a.ring_state[0], count = min(max(a.ring_state[1], 0), a.ring_size);
+  const int hd = head < 0 || head >= a.ring_size ? 0 : head;
+  if (threadIdx.x == 0) s_taken = 0;
+  unsigned long long tok = 0, pops = 0, pushes = 0;
+  for (int c = 0; c < a.B; c += kPlanThreads) {
+    const int b = c + threadIdx.x;
+    PlanReq r = {0, 0, 0, 0, false};
+    if (b < a.B) r = plan_req(a, b);
+    unsigned long long sum;
+    const unsigned long long t0 = tok + scan_excl((unsigned)r.add, s_warp, &sum);
+    tok += sum;
+    const bool fits = b < a.B && !r.ends && r.after <= a.max_blocks && t0 + r.add <= (unsigned long long)a.n_slots;
+    const int need = fits ? max(r.after - r.owned, 0) : 0;
+    const unsigned long long both = (unsigned long long)need << 32 | (unsigned)(r.ends ? r.owned : 0);
+    const unsigned long long at = scan_excl(both, s_warp, &sum);
+    const unsigned long long pop0 = pops + (at >> 32);
+    if (b < a.B) {
+      const bool served = fits && (need == 0 || pop0 + need <= (unsigned long long)count);
+      s_tok[b] = (int)min(t0, (unsigned long long)a.n_slots + 1);
+      s_pop[b] = served ? (int)min(pop0, (unsigned long long)0x7fffffff) : -1;
+      s_push[b] = (int)(pushes + (at & 0xffffffffu));
+      if (served && need > 0) atomicMax(&s_taken, (int)(pop0 + need));
+      if (blockIdx.x == 0) a.offsets[b] = (int)min(t0, 0x7fffffffull);
+    }
+    pops += sum >> 32;
+    pushes += sum & 0xffffffffu;
+  }
+  if (threadIdx.x == 0) {
+    s_tok[a.B] = (int)min(tok, (unsigned long long)a.n_slots + 1);
+    if (blockIdx.x == 0) a.offsets[a.B] = (int)min(tok, 0x7fffffffull);
+  }
+  __syncthreads();
+  const int room = a.ring_size - count;  // ring entries that hold no free block
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    const int back = (int)min(pushes, (unsigned long long)room);
+    a.ring_state_out[0] = ring_at(hd, s_taken, a.ring_size);
+    a.ring_state_out[1] = count - s_taken + back;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5); b < a.B; b += gridDim.x * (kPlanThreads / 32)) {
+    const PlanReq r = plan_req(a, b);
+    int32_t* row = a.table + (size_t)b * a.max_blocks;
+    if (r.ends) {
+      for (int j = lane; j < r.owned && s_push[b] + j < room; j += 32)
+        a.ring[ring_at(hd, (long long)count + s_push[b] + j, a.ring_size)] = row[j];
+      if (lane == 0) a.lens_out[b] = a.owned_out[b] = 0;
+      continue;
+    }
+    const bool served = s_pop[b] >= 0;
+    const int need = served ? max(r.after - r.owned, 0) : 0;
+    for (int j = lane; j < need; j += 32) row[r.owned + j] = a.ring[ring_at(hd, s_pop[b] + j, a.ring_size)];
+    if (lane == 0) {
+      a.lens_out[b] = served ? r.len + r.add : a.lens[b];
+      a.owned_out[b] = served ? r.owned + need : a.owned[b];
+    }
+  }
+  // a token's slot: from the table for a block held before the call, else straight from the ring
+  const int n_tok = min(s_tok[a.B], a.n_slots);
+  for (int t = blockIdx.x * kPlanThreads + threadIdx.x; t < a.n_slots; t += gridDim.x * kPlanThreads) {
+    int slot = -1;
+    if (t < n_tok) {
+      int lo = 0, hi = a.B - 1;  // the last request whose first token is at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_tok[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      if (s_pop[lo] >= 0) {
+        const PlanReq r = plan_req(a, lo);
+        const int p = r.len + t - s_tok[lo], blk = p / a.bs;
+        const int id = blk < r.owned ? a.table[(size_t)lo * a.max_blocks + blk]
+                                     : a.ring[ring_at(hd, (long long)s_pop[lo] + blk - r.owned, a.ring_size)];
+        slot = id * a.bs + p % a.bs;
+      }
+    }
+    a.slots[t] = slot;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// slot writes
+// ---------------------------------------------------------------------------
+// A thread moves one 16-byte piece of a row's K and the same of its V.
+__global__ void __launch_bounds__(256)
+    kv_write_kernel(const lmoe_kv_cache c, const uint16_t* __restrict__ k_new, long long ks,
+                    const uint16_t* __restrict__ v_new, long long vs, int n_rows, const int32_t* __restrict__ src,
+                    const int32_t* __restrict__ slots, int n_tokens, int pieces, int bs_shift, int d_shift,
+                    Status* st) {
+  pdl_wait();
+  pdl_trigger();
+  const unsigned total = (unsigned)n_tokens * (unsigned)pieces;
+  for (unsigned x = blockIdx.x * 256u + threadIdx.x; x < total; x += gridDim.x * 256u) {
+    const unsigned t = x / (unsigned)pieces, p = x - t * (unsigned)pieces;
+    const int slot = slots[t];
+    if (slot < 0) continue;
+    const int row = src ? src[t] : (int)t;
+    const int block = slot >> bs_shift;
+    if (block >= c.n_blocks || row < 0 || row >= n_rows) {
+      set_error(st, LMOE_EDEVICE_CHECK, 221);
+      continue;
+    }
+    const unsigned h = p >> d_shift, d = (p & ((1u << d_shift) - 1)) * 8;
+    const size_t to = (size_t)block * c.block_stride + (size_t)h * c.head_stride +
+                      (size_t)(slot & ((1 << bs_shift) - 1)) * c.slot_stride + d;
+    const uint4 kv = __ldcs(reinterpret_cast<const uint4*>(k_new + (size_t)row * ks + (size_t)p * 8));
+    const uint4 vv = __ldcs(reinterpret_cast<const uint4*>(v_new + (size_t)row * vs + (size_t)p * 8));
+    *reinterpret_cast<uint4*>(c.k + to) = kv;
+    *reinterpret_cast<uint4*>(c.v + to) = vv;
+  }
+}
+
+bool al16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al8(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool al4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+}  // namespace
+
+int optional_status(void* ws, size_t ws_bytes, cudaStream_t s, Status** st) {
+  *st = nullptr;
+  if (!ws) return LMOE_OK;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return LMOE_EINVAL;
+  if (ws_bytes < sizeof(Status)) return LMOE_EWORKSPACE;
+  *st = static_cast<Status*>(ws);
+  return launch_pdl("status_zero_kernel", dim3(1), dim3(32), 0, s, status_zero_kernel, *st);
+}
+
+int check_cache(const lmoe_kv_cache* c, bool memory) {
+  if (!c || c->kv_heads < 1 || c->kv_heads > 256 || c->head_dim < 1) return LMOE_EINVAL;
+  if (c->head_dim != 64 && c->head_dim != 128) return LMOE_EUNSUPPORTED;
+  if (!memory) return LMOE_OK;
+  if (!al16(c->k) || !al16(c->v) || c->n_blocks < 1 || c->block_size < 1) return LMOE_EINVAL;
+  const int bs = c->block_size;
+  if (bs < 16 || bs > 256 || (bs & (bs - 1))) return LMOE_EUNSUPPORTED;
+  // slot numbers are 32-bit
+  if ((long long)c->n_blocks * bs > 0x7fffffffll) return LMOE_EUNSUPPORTED;
+  const int64_t st[3] = {c->block_stride, c->head_stride, c->slot_stride};
+  for (int64_t x : st)
+    if (x < 0 || x % 8) return LMOE_EINVAL;
+  // rows of one block do not overlap
+  if (c->slot_stride < c->head_dim || (c->kv_heads > 1 && c->head_stride < c->head_dim) ||
+      (c->n_blocks > 1 && c->block_stride < c->head_dim))
+    return LMOE_EINVAL;
+  return LMOE_OK;
+}
+
+}  // namespace lmoe
+
+using namespace lmoe;
+
+extern "C" {
+
+int lmoe_tree_masks(int32_t n_requests, int32_t n_tokens, int32_t mask_words, const int32_t* token_offsets,
+                    const int32_t* parents, const int32_t* lens, uint64_t* mask, int32_t* pos, void* ws,
+                    size_t ws_bytes, lmoe_stream_t stream) {
+  calls_begin();
+  if (n_requests < 1 || n_requests > kPlanMaxRequests || n_tokens < 1 || n_tokens > (1 << 20) || mask_words < 1 ||
+      mask_words > 4 || !al4(token_offsets) || !al4(parents) || (lens && !al4(lens)) || !al8(mask) || !al4(pos))
+    return LMOE_EINVAL;
+  DevInfo di;
+  int rc = dev_info(&di);
+  if (rc) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  Status* st;
+  if ((rc = optional_status(ws, ws_bytes, s, &st))) return rc;
+  void (*const kern[4])(int, const int32_t*, const int32_t*, const int32_t*, uint64_t*, int32_t*, Status*) = {
+      tree_masks_kernel<1>, tree_masks_kernel<2>, tree_masks_kernel<3>, tree_masks_kernel<4>};
+  return launch_pdl("tree_masks_kernel", dim3(n_requests), dim3(64 * mask_words), 0, s, kern[mask_words - 1], n_tokens,
+                    token_offsets, parents, lens, mask, pos, st);
+}
+
+int lmoe_kv_plan(int32_t n_requests, int32_t block_size, int32_t max_blocks, int32_t n_slots, const int32_t* lens,
+                 const int32_t* new_tokens, const int32_t* owned, int32_t* block_table, int32_t* ring,
+                 int32_t ring_size, const int32_t* ring_state, int32_t* lens_out, int32_t* owned_out,
+                 int32_t* ring_state_out, int32_t* token_offsets, int32_t* slots, lmoe_stream_t stream) {
+  calls_begin();
+  if (n_requests < 1 || n_requests > kPlanMaxRequests || block_size < 1 || max_blocks < 1 || max_blocks > (1 << 24) || n_slots < 1 ||
+      ring_size < 1)
+    return LMOE_EINVAL;
+  const void* in[] = {lens, new_tokens, owned, block_table, ring, ring_state};
+  const void* out[] = {lens_out, owned_out, ring_state_out, token_offsets, slots};
+  for (const void* p : in)
+    if (!al4(p)) return LMOE_EINVAL;
+  for (int i = 0; i < 5; ++i) {
+    if (!al4(out[i])) return LMOE_EINVAL;
+    for (const void* p : in)
+      if (out[i] == p) return LMOE_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return LMOE_EINVAL;
+  }
+  if (block_table == ring) return LMOE_EINVAL;
+  DevInfo di;
+  int rc = dev_info(&di);
+  if (rc) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  static std::atomic<unsigned long long> done{0};
+  if ((rc = allow_smem(done, kv_plan_kernel, (3 * kPlanMaxRequests + 1) * 4))) return rc;
+  const PlanArgs a = {n_requests, block_size,  max_blocks, n_slots,  ring_size, lens,           new_tokens, owned,
+                      ring_state, block_table, ring,       lens_out, owned_out, ring_state_out, token_offsets, slots};
+  // one CTA per 64 requests (two rounds of its warps) or 2048 tokens, whichever asks for more
+  const int want = max((n_requests + 63) / 64, (int)((n_slots + 2047ll) / 2048));
+  return launch_pdl("kv_plan_kernel", dim3(min(want, di.sms)), dim3(kPlanThreads), (3 * (size_t)n_requests + 1) * 4, s,
+                    kv_plan_kernel, a);
+}
+
+int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, int64_t k_stride, const uint16_t* v_new,
+                  int64_t v_stride, int32_t n_rows, const int32_t* src, const int32_t* slots, int32_t n_tokens,
+                  void* ws, size_t ws_bytes, lmoe_stream_t stream) {
+  calls_begin();
+  int rc = check_cache(cache, true);
+  if (rc) return rc;
+  const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
+  if (!al16(k_new) || !al16(v_new) || k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || n_rows < 1 ||
+      n_tokens < 1 || n_tokens > (1 << 20) || (!src && n_tokens > n_rows) || (src && !al4(src)) || !al4(slots))
+    return LMOE_EINVAL;
+  DevInfo di;
+  if ((rc = dev_info(&di))) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  Status* st;
+  if ((rc = optional_status(ws, ws_bytes, s, &st))) return rc;
+  const int pieces = (int)(row / 8);
+  const long long total = (long long)n_tokens * pieces;
+  if (total > 0x7fffffffll) return LMOE_EUNSUPPORTED;
+  const int grid = (int)min((total + 255) / 256, (long long)di.sms * 16);
+  return launch_pdl("kv_write_kernel", dim3(grid), dim3(256), 0, s, kv_write_kernel, *cache, k_new,
+                    (long long)k_stride, v_new, (long long)v_stride, n_rows, src, slots, n_tokens, pieces,
+                    log2_of(cache->block_size), log2_of(cache->head_dim / 8), st);
+}
+
+}  // extern "C"

@@ -170,6 +170,14 @@ __global__ void __launch_bounds__(64) ws_zero_kernel(uint4* __restrict__ p, int 
   for (int i = threadIdx.x; i < n16; i += blockDim.x) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// The status word alone, for the calls whose workspace is optional and holds
+// nothing else.
+__global__ void __launch_bounds__(32) status_zero_kernel(Status* st) {
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) *st = Status{0, 0};
+}
+
 // Host I/O for lmoe_forward_host.  io_in_kernel zeroes the workspace's zeroed
 // region (in place of ws_zero_kernel) and copies the tokens from pinned host
 // memory into the device staging buffer; io_out_kernel, after the unpooler,

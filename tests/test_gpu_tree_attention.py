@@ -1,0 +1,348 @@
+"""Tree attention over the paged cache against plain 64-bit loops.
+
+Bounds, from the arithmetic that include/lmoe.h states (u = 2^-9, bf16's unit
+roundoff; A = sum_j p_j |v_j|; S = max_j scale sum_d |q_d k_jd|):
+  scores   products are exact in fp32, head_dim additions of at most 2^-23
+           relative each (truncating accumulators), the scale and the change
+           of base: |ds| <= (head_dim + 8) 2^-23 S + 2^-22 |s|; exponentials
+           2^-21; so p is off by at most e = (head_dim + 16) 2^-23 S + 2^-20
+           relative, before and after the division
+  out      p rounded to bf16: u A; the result rounded to bf16: u |out| <= u A;
+           fp32 sums over the keys: 2^-14 A;  in all (2 u + 2^-12 + 4 e) A,
+           with a subnormal's worth of absolute slack
+  lse      e + 2^-19 (1 + |lse|)
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import kv_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lm():
+    import latent_moe_layer_fp32_gb300 as lm
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    lm.load()
+    return lm
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Case:
+    """Inputs of one call: a paged cache with shuffled blocks, drafts as slices of one projection."""
+
+    def __init__(self, lens, ns, hq=8, hk=2, d=64, bs=16, window=0, mask="tree", pos=True, order="head", seed=0,
+                 qscale=1.0, spare=3, scale=None):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lens, self.ns = np.array(lens, np.int32), np.array(ns, np.int32)
+        self.hq, self.hk, self.d, self.bs, self.window = hq, hk, d, bs, window
+        self.off = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+        T = max(1, int(self.off[-1]))
+        held = -(-self.lens // bs)
+        self.blocks = int(held.sum()) + spare
+        ids = rng.permutation(self.blocks).astype(np.int32)
+        self.table = np.full((len(lens), max(1, int(held.max()))), self.blocks - 1, np.int32)
+        at = 0
+        for b, h in enumerate(held):
+            self.table[b, :h] = ids[at:at + h]
+            at += h
+        shape = (self.blocks, hk, bs, d) if order == "head" else (self.blocks, bs, hk, d)
+        self.k, self.v = (torch.randn(shape, device="cuda", generator=g).bfloat16() for _ in range(2))
+        if order != "head":
+            self.k, self.v = self.k.transpose(1, 2), self.v.transpose(1, 2)
+        w = torch.randn(T, (hq + 2 * hk) * d + 16, device="cuda", generator=g)
+        w[:, :hq * d] *= qscale
+        w = w.bfloat16()
+        self.q = w[:, :hq * d].unflatten(1, (hq, d))
+        self.kn = w[:, hq * d:(hq + hk) * d].unflatten(1, (hk, d))
+        self.vn = w[:, (hq + hk) * d:(hq + 2 * hk) * d].unflatten(1, (hk, d))
+        self.words = max(1, (int(self.ns.max()) + 63) // 64)
+        self.mask = self.pos = None
+        par = np.concatenate([[int(rng.integers(-1, i)) if i else -1 for i in range(n)] for n in ns] or [[]])
+        m, p = kv_ref.tree_masks(self.off, par.astype(int), self.lens, self.words)
+        if mask == "tree":
+            self.mask = m
+        elif mask == "any":  # arbitrary bits, rows without their own among them
+            self.mask = rng.integers(0, 1 << 63, (T, self.words)).astype(np.uint64) * 2 + 1
+            self.mask &= rng.integers(0, 1 << 63, (T, self.words)).astype(np.uint64)
+        elif mask == "none":
+            self.mask = np.zeros((T, self.words), np.uint64)
+        if pos:
+            self.pos = p
+        if not len(par):  # no drafts at all: one row that belongs to no request
+            self.mask, self.pos = np.zeros((1, 1), np.uint64), np.zeros(1, np.int32)
+        self.scale = float(scale if scale is not None else d ** -0.5)
+
+    def dims(self, lm, **kw):
+        a = dict(n_requests=len(self.lens), n_tokens=self.q.shape[0], max_request_tokens=max(1, int(self.ns.max())),
+                 q_heads=self.hq, max_blocks=self.table.shape[1], mask_words=self.words, window=self.window,
+                 scale=self.scale)
+        return lm.attn_dims_of(**(a | kw))
+
+    def run(self, lm, want=0, ws=None, stream=None, lse=True, **kw):
+        cache, dims = lm.kv_cache_of(self.k, self.v), self.dims(lm, **kw)
+        out = torch.full(self.q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+        ls = torch.full(self.q.shape[:2], 9.0, device="cuda") if lse else None
+        if ws is None:
+            ws = torch.full((lm.lmoe_tree_attention_workspace_bytes(dims, cache),), 255, dtype=torch.uint8,
+                            device="cuda")
+        # the caller's arrays on the device, kept until the status has been read
+        self.kept = (dev(self.off), dev(self.lens), dev(self.table),
+                     None if self.mask is None else dev(self.mask.view(np.int64)),
+                     None if self.pos is None else dev(self.pos))
+        off, lens, table, mask, pos = self.kept
+        lm.lmoe_tree_attention(dims, cache, self.q, self.kn, self.vn, off, lens, table, mask, pos, out, ls, ws,
+                               stream=stream)
+        assert lm.lmoe_status_check(ws, stream) == want
+        return out, ls
+
+    def ref(self):
+        f = [x.float().cpu().numpy().astype(np.float64) for x in (self.q, self.kn, self.vn, self.k, self.v)]
+        return kv_ref.attention(*f, self.off, self.lens, self.table, self.mask, self.pos, self.window, self.scale)
+
+    def check(self, lm, **kw):
+        out, ls = self.run(lm, **kw)
+        with np.errstate(invalid="ignore"):
+            ref, lse, mass, dot = self.ref()
+        n = int(self.off[-1])
+        got = out.float().cpu().numpy().astype(np.float64)[:n]
+        ref, lse, mass, dot = ref[:n], lse[:n], mass[:n], dot[:n]
+        e = (self.d + 16) * 2.0**-23 * dot + 2.0**-20
+        tol = (2.0**-8 + 2.0**-12 + 4 * e[..., None]) * mass + 2.0**-133
+        bad = ~(np.abs(got - ref) <= tol)
+        assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], ref[bad][:5], tol[bad][:5])
+        empty = np.isneginf(lse)
+        assert (got[empty] == 0).all()
+        if ls is not None:
+            gl = ls.cpu().numpy().astype(np.float64)[:n]
+            assert np.array_equal(np.isneginf(gl), empty)
+            with np.errstate(invalid="ignore"):
+                bad = ~(np.abs(gl - lse) <= e + 2.0**-19 * (1 + np.abs(lse))) & ~empty
+            assert not bad.any(), (np.argwhere(bad)[:5], gl[bad][:5], lse[bad][:5])
+        return out
+
+
+LENGTHS = [[0], [1], [15], [16], [17], [127], [128], [129], [255], [256], [257], [1000], [3001], [0, 1, 130, 513]]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", LENGTHS, ids=["-".join(map(str, x)) for x in LENGTHS])
+def test_prefix_lengths(lm, lens, d):
+    Case(lens, [3] * len(lens), d=d, seed=len(lens) + lens[0]).check(lm)
+    Case(lens, [1] * len(lens), d=d, seed=1, mask=None, pos=False).check(lm)
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (2, 2), (3, 1), (8, 8), (24, 8), (40, 8), (7, 1), (64, 8), (128, 1)])
+@pytest.mark.parametrize("n", [1, 5])
+def test_head_layouts(lm, hq, hk, n):
+    Case([77, 300], [n, n], hq=hq, hk=hk, d=128, seed=hq).check(lm)
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 192, 200, 255, 256])
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 1, 128)])
+def test_tree_sizes(lm, n, hq, hk, d):
+    Case([150, 0], [n, max(0, n - 3)], hq=hq, hk=hk, d=d, seed=n).check(lm)
+
+
+@pytest.mark.parametrize("order", ["head", "slot"])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
+def test_block_sizes_and_orders(lm, bs, order, d):
+    Case([bs - 1, 2 * bs, 5 * bs + 3, 700], [4, 1, 3, 8], d=d, bs=bs, order=order, seed=bs).check(lm)
+
+
+@pytest.mark.parametrize("window", [1, 2, 5, 16, 100, 128, 129, 333, 5000])
+@pytest.mark.parametrize("pos,mask", [(True, "tree"), (False, None), (False, "any")])
+def test_windows(lm, window, pos, mask):
+    Case([0, 3, 127, 128, 400, 1111], [5, 9, 3, 8, 20, 33], window=window, pos=pos, mask=mask, seed=window).check(lm)
+
+
+def test_positions_below_the_prefix_count_as_its_end(lm):
+    c = Case([200, 40], [6, 6], window=30, seed=2)
+    c.pos = c.pos - np.int32(100)
+    c.check(lm)
+
+
+@pytest.mark.parametrize("mask", ["any", "none"])
+def test_masks_that_leave_rows_empty(lm, mask):
+    # no prefix and no visible draft: zeros and an lse of -infinity, next to rows that do see something
+    Case([0, 0, 5, 0], [7, 1, 3, 130], mask=mask, seed=3).check(lm)
+    Case([0, 40], [9, 9], mask=mask, window=4, seed=4).check(lm)
+
+
+def test_requests_without_drafts(lm):
+    Case([10, 500, 0, 70], [0, 3, 0, 0], seed=5).check(lm)
+    Case([10, 20], [0, 0], seed=5).check(lm)
+
+
+@pytest.mark.parametrize("qscale", [0.0, 1e-30, 40.0, 1e4, 1e30])
+def test_score_ranges(lm, qscale):
+    # from all-equal scores to a softmax that is one key, in tiles far apart
+    Case([900, 130], [5, 2], qscale=qscale, d=128, seed=7).check(lm)
+
+
+def test_rising_and_falling_maxima(lm):
+    # the running maximum moves in every tile (rising), or only in the first (falling)
+    for sign in (1.0, -1.0):
+        c = Case([1500], [4], d=64, hk=1, hq=4, seed=8)
+        ramp = torch.linspace(-30 * sign, 30 * sign, 1500, device="cuda")
+        at = torch.arange(1500, device="cuda")
+        blk = dev(c.table[0]).long()[at // 16]
+        c.q.copy_(torch.full_like(c.q, 1.0))
+        c.k[blk, 0, at % 16] = (ramp[:, None] / 8).expand(1500, 64).bfloat16()
+        c.check(lm)
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("d", [64, 128])
+def test_poison_in_unseen_places(lm, poison, window, d):
+    """Stale slots, foreign blocks, cached keys behind the window, other requests' drafts and
+    unseen drafts of the own request hold NaN or infinities; the reference skips them."""
+    lens, ns = [37, 300, 0, 128], [6, 3, 5, 9]
+    c = Case(lens, ns, window=window, seed=11, d=d)
+    used = torch.zeros(c.blocks, c.bs, dtype=torch.bool)
+    for b, ln in enumerate(lens):
+        lo = max(0, ln - window + 1) if window else 0
+        for p in range(lo, ln):
+            used[c.table[b, p // c.bs], p % c.bs] = True
+    hide = (~used).cuda()[:, None, :, None]
+    c.k.masked_fill_(hide, poison)
+    c.v.masked_fill_(hide, poison)
+    # one branch of each tree is poisoned: its rows see it, the others must not
+    for b, n in enumerate(ns):
+        c.kn[int(c.off[b]) + n - 1] = poison
+        c.vn[int(c.off[b]) + n - 1, :, 3] = poison
+    out, ls = c.run(lm)
+    with np.errstate(invalid="ignore"):
+        ref, lse, mass, dot = c.ref()
+    sick = np.zeros(len(ref), bool)
+    for b, n in enumerate(ns):
+        for i in range(n):
+            bits = int(c.mask[c.off[b] + i, 0])
+            sick[c.off[b] + i] = bits >> (n - 1) & 1
+    assert sick.sum() >= len(ns) and not sick.all()
+    got = out.float().cpu().numpy().astype(np.float64)
+    e = (c.d + 16) * 2.0**-23 * dot + 2.0**-20
+    tol = (2.0**-8 + 2.0**-12 + 4 * e[..., None]) * mass + 2.0**-133
+    assert (np.abs(got - ref) <= tol)[~sick].all()
+    assert np.isfinite(ls.cpu().numpy()[~sick]).all()
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ["draft", "window"])
+def test_poisoned_values_reach_only_the_rows_that_see_them(lm, poison, where):
+    """A value of a draft (or of a cached position inside some rows' window) that is not finite
+    makes that element of the rows that see it not finite, and of no other row."""
+    c = Case([300], [8], hq=16, hk=2, d=128, window=40 if where == "window" else 0, seed=13)
+    c.mask = np.array([[(1 << i) | 1] for i in range(8)], np.uint64)  # eight leaves of one root
+    c.pos = np.array([300, 301, 302, 303, 304, 305, 306, 307], np.int32)
+    if where == "draft":
+        c.vn[5, 1, 77] = poison
+        sees = np.arange(8) == 5
+    else:
+        p = 300 - 40 + 4  # in sight of positions up to 303
+        c.v[int(c.table[0, p // 16]), 1, p % 16, 77] = poison
+        sees = np.arange(8) <= 3
+    out, ls = c.run(lm)
+    got = out.float().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        ref, lse, mass, dot = c.ref()
+    hit = np.zeros(got.shape, bool)
+    hit[sees, 8:, 77] = True
+    assert not np.isfinite(got[hit]).any()
+    assert np.array_equal(np.isnan(got[hit]), np.isnan(ref[hit]))
+    e = (c.d + 16) * 2.0**-23 * dot + 2.0**-20
+    with np.errstate(invalid="ignore"):
+        ok = np.abs(got - ref) <= (2.0**-8 + 2.0**-12 + 4 * e[..., None]) * mass + 2.0**-133
+    assert ok[~hit].all()
+    assert np.isfinite(ls.cpu().numpy()).all()
+
+
+def test_many_requests_and_repeatability(lm):
+    rng = np.random.default_rng(17)
+    c = Case(rng.integers(0, 700, 60), rng.integers(0, 12, 60), hq=16, hk=4, seed=17)
+    a = c.check(lm)
+    b, _ = c.run(lm)
+    assert torch.equal(a, b)
+    # the order of the requests does not matter to the bits of a one-request call... only to its split:
+    # a second call without an lse gives the same output
+    d, _ = c.run(lm, lse=False)
+    assert torch.equal(a, d)
+
+
+def test_offsets_past_32_bits(lm):
+    c = Case([200], [4], hq=16, hk=8, d=128, bs=64, seed=19)
+    blocks = 36000  # more than 2^31 elements and 2^32 bytes per tensor
+    big = [torch.empty(blocks, 8, 64, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    new = np.array([[blocks - 1, blocks - 7, 3, blocks - 2]], np.int32)
+    for x, y in zip(big, (c.k, c.v)):
+        for o, n in zip(c.table[0], new[0]):
+            x[int(n)] = y[int(o)]
+    ref = c.check(lm)
+    c.k, c.v, c.table = big[0], big[1], new
+    out, _ = c.run(lm)
+    assert torch.equal(out, ref)
+
+
+def test_another_stream_and_a_graph(lm):
+    c = Case([500, 90], [8, 3], hq=16, hk=2, d=128, seed=23)
+    ref = c.check(lm)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out, _ = c.run(lm, stream=s)
+    assert torch.equal(out, ref)
+    cache, dims = lm.kv_cache_of(c.k, c.v), c.dims(lm)
+    ws = torch.empty(lm.lmoe_tree_attention_workspace_bytes(dims, cache), dtype=torch.uint8, device="cuda")
+    args = [dev(x) for x in (c.off, c.lens, c.table, c.mask.view(np.int64), c.pos)]
+    out = torch.zeros_like(ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lm.lmoe_tree_attention(dims, cache, c.q, c.kn, c.vn, *args, out, None, ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    # the graph reads lengths and tables on the device: a replay with other lengths is another step
+    args[1].copy_(torch.tensor([333, 17], dtype=torch.int32))
+    c.lens = np.array([333, 17], np.int32)
+    args[4].sub_(dev(np.repeat(np.array([500 - 333, 90 - 17], np.int32), [8, 3])))
+    g.replay()
+    c.pos = c.pos - np.repeat(np.array([500 - 333, 90 - 17], np.int32), [8, 3])
+    assert torch.equal(c.check(lm), out)
+
+
+def test_device_checks(lm):
+    # a bad request is reported and skipped, the others are computed
+    c = Case([40, 50, 60], [3, 3, 3], seed=29)
+    ref, _ = c.run(lm)
+    for field, value in (("lens", -1), ("lens", c.table.shape[1] * c.bs + 1), ("lens", 2**31 - 1)):
+        good = getattr(c, field).copy()
+        getattr(c, field)[1] = value
+        out, _ = c.run(lm, want=-5)
+        assert torch.equal(out[:3], ref[:3]) and torch.equal(out[6:], ref[6:]) and (out[3:6] == 9.0).all()
+        setattr(c, field, good)
+    for off in ([0, 3, 2, 9], [0, 3, 20, 9], [-1, 3, 6, 9], [0, 3, 6, 10]):
+        good, c.off = c.off, np.array(off, np.int32)
+        c.run(lm, want=-5)
+        c.off = good
+    out, _ = c.run(lm, want=-5, max_request_tokens=2)
+    assert (out == 9.0).all()
+    for bad in (-1, c.blocks, 2**31 - 1, -2**31):
+        good = c.table.copy()
+        c.table[1, 0] = bad
+        out, _ = c.run(lm, want=-5)
+        assert torch.equal(out[:3], ref[:3]) and torch.equal(out[6:], ref[6:])
+        c.table = good
+    assert torch.equal(c.run(lm)[0], ref)
