@@ -35,6 +35,15 @@ __host__ __device__ constexpr uint64_t smem_desc_sw128(uint32_t saddr) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The same for an MN-major operand (64 consecutive M/N elements per 128-byte
+// row, one row per k): SBO is the 1024-byte stride from one group of 8 k to
+// the next, LBO the stride from one block of 64 M/N elements to the next.
+__host__ __device__ constexpr uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;  // B is MN-major
+
 // Instruction descriptor, kind::f16: D format bits 4-5 (1 = f32), A format
 // bits 7-9 and B format bits 10-12 (1 = bf16), A/B major bits 15/16 (0 =
 // K-major), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -98,6 +107,17 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same for accumulation into some of D's lanes only: bit i of off[w] keeps
+// lane 32 w + i as it is.
+__device__ __forceinline__ void tc_mma_bf16_ts_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                     const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
       : "memory");
 }
 

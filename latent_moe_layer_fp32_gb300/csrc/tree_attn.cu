@@ -1,83 +1,849 @@
 // Attention of drafted tokens over a paged cache and the tree of drafts.
 // See include/lmoe.h for the contract.
+//
+// Work.  The rows that share a key head's keys are one request's drafted
+// tokens times the q_heads / kv_heads query heads of the group; 128 (or 256)
+// of them form a row group, 128 keys a tile: the cached prefix in tiles of
+// consecutive positions, then the drafts.  A segment is one (request, kv head,
+// row group); its tiles are laid end to end with those of all other segments
+// and the whole line is cut into equal ranges, one per CTA, so ragged lengths
+// and single long requests both fill the GPU.  A segment inside one CTA's
+// range is finished there; one that is cut leaves fp32 partial sums (running
+// maximum, sum, unnormalised output), which tree_attn_merge_kernel joins in
+// the order of the ranges, so results do not depend on timing.
+//
+// CTA.  One producer warp copies K and V tiles page by page with TMA (128-byte
+// swizzle) into a ring; one thread issues tcgen05.mma: S = Q K^T (both K-major
+// from shared memory) into tensor memory, and O += P V with P read from tensor
+// memory and V as an MN-major operand straight from its pages' layout.  Warps
+// of the softmax group own 32 rows each, one row per thread: they read S, keep
+// the row's running maximum and sum in registers, write P (bf16, with a second
+// bf16 part where one key dominates a row, in place of S) and rescale O only when the maximum has grown by more than 2^8 (P is then at
+// most 2^8, which bf16 and the fp32 sums hold without loss).
+// With up to 128 rows the next tile's S is computed during the softmax of this
+// one (two S buffers); with more, two row tiles take turns.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
 #include "launch.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
 
 namespace lmoe {
 
 namespace {
 
+constexpr int kTile = 128;  // keys per tile, rows per row tile
+
 struct AttnArgs {
-  lmoe_kv_cache c;
-  const uint16_t *q, *k_new, *v_new;
-  long long qs, ks, vs;
+  const uint16_t* q;
+  const uint16_t* v_cache;  // also read directly where a value is not finite
+  const uint16_t* v_new;
+  long long qs, vs, block_stride, head_stride, slot_stride;
   const int32_t *offsets, *lens, *table, *pos;
   const uint64_t* mask;
   uint16_t* out;
   float* lse;
-  Status* st;
-  int B, T, max_n, hq, max_blocks, words, window;
-  float scale;
+  Status* status;  // the workspace's status word
+  Status* err;     // [CTAs], joined into *status by the merge kernel
+  int4* cut;       // [CTAs][2], the segment that starts in a CTA's range and ends past it
+  float2* part_ml; // [2 CTAs][rows] running maximum (base 2) and sum
+  float* part_o;   // [2 CTAs][rows][D]
+  int B, T, max_n, hk, G, max_blocks, n_blocks, bs_shift, words, window, ctas;
+  float scale_log2;
 };
 
-// One warp per (row, query head): a pass over what the row sees with a running
-// maximum and sum; a lane holds head_dim / 32 elements.
-template <int D>
-__global__ void __launch_bounds__(128) tree_attn_rows_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= a.hq) return;
-  const int kvh = h / (a.hq / a.c.kv_heads);
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int t0 = a.offsets[b], t1 = a.offsets[b + 1], len = a.lens[b];
-    if (t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 > a.max_n || len < 0 ||
-        len > (long long)a.max_blocks * a.c.block_size) {
-      if (lane == 0) set_error(a.st, LMOE_EDEVICE_CHECK, 211);
-      continue;
+// One request's share of the line of tiles.
+struct Req {
+  int t0, n, len, tile0, np, nt, groups;
+  bool bad;
+  long long units;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Req load_req(const AttnArgs& a, int b) {
+  Req r;
+  const int t0 = __ldg(a.offsets + b), t1 = __ldg(a.offsets + b + 1), len = __ldg(a.lens + b);
+  r.bad = t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 > a.max_n || len < 0 ||
+          len > ((long long)a.max_blocks << a.bs_shift);
+  r.t0 = t0;
+  r.n = r.bad ? 0 : t1 - t0;
+  r.len = len;
+  const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;  // the first position that any row sees
+  r.tile0 = lo >> 7;
+  r.np = lo < len ? (len >> 7) + ((len & 127) != 0) - r.tile0 : 0;
+  r.nt = r.np + ((r.n + kTile - 1) >> 7);
+  r.groups = (r.n * a.G + ROWS - 1) / ROWS;
+  r.units = (long long)a.hk * r.groups * r.nt;
+  return r;
+}
+
+// The part of one segment that falls into a CTA's range.
+struct Seg {
+  Req r;
+  int b, h, m;   // request, kv head, row group
+  int i0, i1;    // tiles [i0, i1) of r.nt
+  int rows;      // valid rows of this row group
+};
+
+// Walks the segments of the unit range [u, end): every role of the CTA takes the same walk.
+template <int ROWS>
+struct Walk {
+  const AttnArgs& a;
+  int b;
+  long long off, left;  // units into request b, units left in the range
+  Req r;
+  __device__ Walk(const AttnArgs& args, int b0, long long off0, long long n) : a(args), b(b0), off(off0), left(n) {
+    if (left > 0) r = load_req<ROWS>(a, b);
+  }
+  __device__ bool next(Seg* s) {
+    if (left <= 0) return false;
+    while (off >= r.units) {
+      off -= r.units;
+      ++b;
+      r = load_req<ROWS>(a, b);
     }
-    for (int t = t0; t < t1; ++t) {
-      const int p = a.pos ? max(a.pos[t], len) : len + t - t0;
-      float q[E], o[E], m = -INFINITY, l = 0.f;
-      for (int e = 0; e < E; ++e) {
-        q[e] = bf16_bits_to_f32(a.q[(size_t)t * a.qs + (size_t)h * D + lane * E + e]) * a.scale;
-        o[e] = 0.f;
-      }
-      auto key = [&](const uint16_t* k, const uint16_t* v) {
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += q[e] * bf16_bits_to_f32(k[lane * E + e]);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), f = __expf(m - mn), w = __expf(s - mn);
-        m = mn;
-        l = l * f + w;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * bf16_bits_to_f32(v[lane * E + e]);
-      };
-      for (int x = a.window > 0 ? max(0, p - a.window + 1) : 0; x < len; ++x) {
-        const int id = a.table[(size_t)b * a.max_blocks + x / a.c.block_size];
-        if (id < 0 || id >= a.c.n_blocks) {
-          if (lane == 0) set_error(a.st, LMOE_EDEVICE_CHECK, 212);
-          continue;
-        }
-        const size_t at = (size_t)id * a.c.block_stride + (size_t)kvh * a.c.head_stride +
-                          (size_t)(x % a.c.block_size) * a.c.slot_stride;
-        key(a.c.k + at, a.c.v + at);
-      }
-      for (int j = t0; j < t1; ++j) {
-        const int i = j - t0;
-        const bool see = a.mask ? (i >> 6) < a.words && (a.mask[(size_t)t * a.words + (i >> 6)] >> (i & 63) & 1) : j <= t;
-        if (!see) continue;
-        if (a.window > 0 && p - (a.pos ? max(a.pos[j], len) : len + i) >= a.window) continue;
-        key(a.k_new + (size_t)j * a.ks + (size_t)kvh * D, a.v_new + (size_t)j * a.vs + (size_t)kvh * D);
-      }
-      for (int e = 0; e < E; ++e)
-        a.out[((size_t)t * a.hq + h) * D + lane * E + e] = f32_to_bf16_bits(l > 0.f ? o[e] / l : 0.f);
-      if (a.lse && lane == 0) a.lse[(size_t)t * a.hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    const long long k = off / r.nt;
+    s->r = r;
+    s->b = b;
+    s->h = (int)(k / r.groups);
+    s->m = (int)(k - (long long)s->h * r.groups);
+    s->i0 = (int)(off - k * r.nt);
+    s->i1 = (int)min((long long)r.nt, s->i0 + left);
+    s->rows = min(ROWS, r.n * a.G - s->m * ROWS);
+    off += s->i1 - s->i0;
+    left -= s->i1 - s->i0;
+    return true;
+  }
+};
+
+// What one row sees of a tile, as 128 bits.
+struct RowView {
+  bool valid;
+  int i, p;  // draft index, position
+};
+
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {  // bits [lo, hi) of word w
+  const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+  const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
+__device__ __forceinline__ void tile_bits(const AttnArgs& a, const Seg& s, int i, const RowView& v,
+                                          const int* s_dpos, uint32_t (&bits)[4]) {
+  if (!v.valid) {
+    bits[0] = bits[1] = bits[2] = bits[3] = 0u;
+    return;
+  }
+  if (i < s.r.np) {
+    const int base = (s.r.tile0 + i) << 7;
+    const int hi = min(kTile, s.r.len - base);
+    const int lo = a.window > 0 ? min(max(v.p - a.window + 1 - base, 0), kTile) : 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) bits[w] = range_bits(lo, hi, w);
+    return;
+  }
+  const int d0 = (i - s.r.np) << 7, n = s.r.n - d0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t x;
+    if (a.mask) {
+      const int word = (d0 >> 6) + (w >> 1);
+      const uint64_t m = word < a.words ? __ldg(a.mask + (size_t)(s.r.t0 + v.i) * a.words + word) : 0ull;
+      x = (uint32_t)(m >> (32 * (w & 1))) & range_bits(0, n, w);
+    } else {
+      x = range_bits(0, min(n, v.i - d0 + 1), w);
+    }
+    if (a.window > 0)
+      for (int j = 0; j < 32; ++j)
+        if ((x >> j & 1u) && v.p - s_dpos[d0 + 32 * w + j] >= a.window) x &= ~(1u << j);
+    bits[w] = x;
+  }
+}
+
+// Adds the values that are not finite, of the keys that a row sees, to 32
+// elements of its output: sanitize() took them out of the tile so that they
+// reach no other row.  Runs only where there was such a value.
+__device__ __noinline__ void add_not_finite(const AttnArgs& a, const Seg& s, int i, const uint32_t* bits, int d0,
+                                            int width, uint32_t* o) {
+  for (int j = 0; j < kTile; ++j) {
+    if (!(bits[j >> 5] >> (j & 31) & 1u)) continue;
+    const uint16_t* v;
+    if (i < s.r.np) {
+      const int p = ((s.r.tile0 + i) << 7) + j;
+      const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (p >> a.bs_shift));
+      if (id < 0 || id >= a.n_blocks) continue;
+      v = a.v_cache + (size_t)id * a.block_stride + (size_t)s.h * a.head_stride +
+          (size_t)(p & ((1 << a.bs_shift) - 1)) * a.slot_stride;
+    } else {
+      v = a.v_new + (size_t)(s.r.t0 + ((i - s.r.np) << 7) + j) * a.vs + s.h * width;
+    }
+#pragma unroll
+    for (int d = 0; d < 32; ++d) {
+      const uint32_t x = v[d0 + d];
+      if ((x & 0x7f80u) == 0x7f80u) o[d] = __float_as_uint(__uint_as_float(o[d]) + bf16_bits_to_f32(x));
     }
   }
+}
+
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kRows = NT * kTile;
+  static constexpr int kStageBytes = kTile * D * 2;   // one K or V tile
+  static constexpr int kQBytes = NT * kTile * D * 2;
+  static constexpr int kStages = (D == 128 ? (NT == 1 ? 6 : 5) : 12);  // 160 to 192 KB of keys and values in flight
+  static constexpr int kThreads = NT == 1 ? 192 : 384;  // softmax warps, producer, MMA (two: and two idle)
+  static constexpr int kMisc = 2048;
+  static constexpr int kSmem = kQBytes + kStages * kStageBytes + kMisc + 1024;
+  static constexpr uint32_t kO = 2 * kTile;           // first O column; S buffers at 0 and 128
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// First ring position of K and V of tile i of n in a segment's order of use.
+// One row tile: K0 K1 V0 K2 V1 ... (S runs one tile ahead); two: K0 V0 K1 V1 ...
+template <int NT>
+__device__ __forceinline__ uint32_t k_seq(int i) {
+  return NT == 2 ? 2 * i : (i == 0 ? 0 : 2 * i - 1);
+}
+template <int NT>
+__device__ __forceinline__ uint32_t v_seq(int i, int n) {
+  return NT == 2 ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    tree_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
+                     const __grid_constant__ CUtensorMap tm_vn) {
+  using C = Cfg<D, NT>;
+  constexpr int ST = C::kStages, ROWS = C::kRows, HALVES = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem;
+  uint8_t* s_ring = smem + C::kQBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ring + ST * C::kStageBytes);
+  uint64_t* empty = full + ST;
+  uint64_t* s_full = empty + ST;  // a tile's scores are in tensor memory: [S buffer] or [row tile]
+  uint64_t* p_full = s_full + 2;  // its probabilities are
+  uint64_t* pv_done = p_full + 2; // its product with V has been added to O (with one row tile, P can be
+                                  // a tile ahead of O: a barrier each for even and odd tiles)
+  uint64_t* q_full = pv_done + 2; // the segment's queries are in shared memory
+  uint64_t* done = q_full + 1;
+  long long* s_start = reinterpret_cast<long long*>(done + 1);  // request, units into it, units in the range
+  unsigned long long* s_warp = reinterpret_cast<unsigned long long*>(s_start + 3);  // [threads / 32]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_warp + 12);
+  volatile uint32_t* s_lo = tmem_slot + 1;  // [2][4] by S buffer or row tile, and warp: P has a second part
+  int* s_maxpos = reinterpret_cast<int*>(tmem_slot + 9);
+  int* s_dpos = s_maxpos + 1;     // [256] positions of the drafts (only with a window)
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kProducer = NT * 4, kMma = NT * 4 + 1;
+  Status* st = a.err + blockIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, NT * 4);
+    mbar_init(done, 1);
+    fence_barrier_init();
+    s_start[2] = 0;
+  }
+  if (warp == kMma) tmem_alloc(tmem_slot, 512);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's range of the line of tiles ----
+  if (tid == 0) *st = Status{0, 0};
+  {
+    const int per = (a.B + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    unsigned long long mine = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+      const Req r = load_req<ROWS>(a, b);
+      mine += r.units;
+      bad |= r.bad;
+    }
+    unsigned long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    unsigned long long before = x - mine, total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+    if (bad) set_error(st, LMOE_EDEVICE_CHECK, 211);
+    const unsigned long long n = min((unsigned long long)a.ctas, total);  // ranges, none of them empty
+    const unsigned long long c = blockIdx.x;
+    if (c < n) {
+      // the threads whose requests hold the range's first and last unit
+      const unsigned long long u0 = total * c / n, u1 = total * (c + 1) / n;
+      auto find = [&](unsigned long long u, unsigned long long* at, Req* r) {
+        *at = before;
+        int b = b0;
+        for (;; ++b) {
+          *r = load_req<ROWS>(a, b);
+          if (u < *at + r->units) return b;
+          *at += r->units;
+        }
+      };
+      unsigned long long at;
+      Req r;
+      if (u0 >= before && u0 < before + mine) {
+        s_start[0] = find(u0, &at, &r);
+        s_start[1] = (long long)(u0 - at);
+        s_start[2] = (long long)(u1 - u0);
+      }
+      if (u1 - 1 >= before && u1 - 1 < before + mine) {
+        // does the range's last segment start in it and end past it?  Then its last CTA is the
+        // first one whose range ends at or after the segment's end
+        find(u1 - 1, &at, &r);
+        const unsigned long long k = (u1 - 1 - at) / r.nt, start = at + k * r.nt, e = start + r.nt;
+        int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
+        if (start >= u0 && e > u1) {
+          const int h = (int)(k / r.groups), m = (int)(k % r.groups);
+          const int last = (int)((e * n + total - 1) / total) - 1;
+          c0 = make_int4(last - (int)c + 1, r.t0, min(ROWS, r.n * a.G - m * ROWS), h);
+          c1 = make_int4(m, 0, 0, 0);
+        }
+        a.cut[2 * c] = c0;
+        a.cut[2 * c + 1] = c1;
+      }
+    } else if (tid == 0) {
+      a.cut[2 * c] = make_int4(0, 0, 0, 0);
+    }
+    __syncthreads();
+  }
+  const uint32_t tmem = *tmem_slot;
+  // two row tiles: 384 threads start with 168 registers each; the service warps hand most of
+  // theirs to the softmax warps (56 + 2 x 224 = 3 x 168)
+  auto fewer = [] {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  };
+  Walk<ROWS> walk(a, (int)s_start[0], s_start[1], s_start[2]);
+  Seg s{};
+
+  if (warp == kProducer) {
+    // ---------------- TMA producer: one lane per page (or 8 drafts) ----------------
+    fewer();
+    const uint64_t pol = policy_evict_first();
+    const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a cached tile
+    const int ppt = kTile / box;                  // pages per tile
+    uint32_t x = 0, issued = 0;                   // ring position of the segment, copies issued
+    bool ok = true;
+    // copies of lane `lane` of tile i into ring position x; `id` is the lane's page
+    auto copy = [&](const CUtensorMap* tc, const CUtensorMap* td, int i, int id, uint32_t at) {
+      const uint32_t stage = at % ST;
+      if (!mbar_wait(&empty[stage], ((at / ST) & 1) ^ 1, st, 221)) return false;
+      uint8_t* dst = s_ring + stage * C::kStageBytes;
+      int copies, bytes;
+      if (i < s.r.np) {
+        const int keys = min(kTile, s.r.len - ((s.r.tile0 + i) << 7));
+        copies = (keys + box - 1) / box;
+        bytes = box * 128;
+      } else {
+        copies = (min(kTile, s.r.n - ((i - s.r.np) << 7)) + 7) >> 3;
+        bytes = 8 * 128;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], copies * bytes * HALVES);
+      __syncwarp();
+      if (lane < copies) {
+        if (i < s.r.np) {
+          const int slot = ((s.r.tile0 + i) << 7) & ((1 << a.bs_shift) - 1);
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_4d(dst + hf * (kTile * 128) + lane * bytes, tc, hf * 64, ppt == 1 ? slot : 0, s.h, id,
+                        &full[stage], pol);
+        } else {
+          const int row = s.r.t0 + ((i - s.r.np) << 7) + lane * 8;
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_3d(dst + hf * (kTile * 128) + lane * bytes, td, hf * 64, s.h, row, &full[stage], pol);
+        }
+      }
+      __syncwarp();
+      issued = at + 1;
+      return true;
+    };
+    auto page = [&](int i) {  // this lane's page of tile i
+      if (i >= s.r.np || lane >= ppt) return 0;
+      const int blk = (((s.r.tile0 + i) << 7) >> a.bs_shift) + lane;
+      if (ppt > 1 && ((long long)blk << a.bs_shift) >= s.r.len) return 0;
+      return __ldg(a.table + (size_t)s.b * a.max_blocks + blk);
+    };
+    while (ok && walk.next(&s)) {
+      const int n = s.i1 - s.i0;
+      int id = page(s.i0), id_prev = 0;
+      for (int k = 0; k < n && ok; ++k) {
+        const int i = s.i0 + k;
+        const int id_next = k + 1 < n ? page(i + 1) : 0;
+        if (i < s.r.np && (id < 0 || id >= a.n_blocks)) {  // out of the cache: the copy reads zeros
+          set_error(st, LMOE_EDEVICE_CHECK, 212);
+          id = a.n_blocks;
+        }
+        ok = copy(&tm_k, &tm_kn, i, id, x + k_seq<NT>(k));
+        if (NT == 2)
+          ok = ok && copy(&tm_v, &tm_vn, i, id, x + v_seq<NT>(k, n));
+        else if (k > 0)
+          ok = ok && copy(&tm_v, &tm_vn, i - 1, id_prev, x + v_seq<NT>(k - 1, n));
+        id_prev = id;
+        id = id_next;
+      }
+      if (NT == 1) ok = ok && copy(&tm_v, &tm_vn, s.i1 - 1, id_prev, x + v_seq<NT>(n - 1, n));
+      x += 2 * n;
+    }
+    // the last copies land before the CTA can finish (also after a wait that ran out)
+    if (lane == 0)
+      for (uint32_t k = issued < ST ? 0 : issued - ST; k < issued; ++k) mbar_wait(&full[k % ST], (k / ST) & 1, st, 222);
+  } else if (warp == kMma) {
+    // ---------------- MMA issuer ----------------
+    fewer();
+    if (lane == 0) {
+      constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
+      constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
+      uint32_t x = 0, seg = 0, g0 = 0, g1 = 0;  // ring position, segments, tiles of row tile 0 / 1 so far
+      bool ok = true;
+      const uint32_t q0 = smem_u32(s_q), r0 = smem_u32(s_ring);
+      auto qk = [&](int rt, uint32_t buf, uint32_t stage) {
+        const uint32_t kb = r0 + stage * C::kStageBytes, qb = q0 + rt * (kTile * D * 2);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+          tc_mma_bf16(tmem + buf * kTile, smem_desc_sw128(qb + o), smem_desc_sw128(kb + o), kQk, kk != 0);
+        }
+        tc_commit(&s_full[buf]);
+      };
+      auto pv = [&](int rt, uint32_t buf, uint32_t stage, bool first) {
+        const uint32_t vb = r0 + stage * C::kStageBytes;
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          tc_mma_bf16_ts(tmem + C::kO + rt * D, tmem + buf * kTile + kk * 8,
+                         smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128), kPv, !(first && kk == 0));
+        uint32_t off[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) off[w] = s_lo[buf * 4 + w] ? 0u : 0xffffffffu;
+        if ((off[0] & off[1] & off[2] & off[3]) == 0u) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_bf16_ts_lanes(tmem + C::kO + rt * D, tmem + buf * kTile + kTile / 2 + kk * 8,
+                                 smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128), kPv, off);
+        }
+        tc_commit(&pv_done[buf]);
+      };
+      auto tile = [&](uint32_t at) {  // the tile at ring position `at` has landed
+        if (!mbar_wait(&full[at % ST], (at / ST) & 1, st, 231)) return false;
+        tc_fence_after();
+        return true;
+      };
+      while (ok && walk.next(&s)) {
+        const int n = s.i1 - s.i0;
+        const bool two = NT == 2 && s.rows > kTile;
+        if (!(ok = mbar_wait(q_full, seg & 1, st, 232))) break;
+        tc_fence_after();
+        if (!(ok = tile(x))) break;
+        if constexpr (NT == 1) {
+          qk(0, g0 & 1, x % ST);
+          tc_commit(&empty[x % ST]);
+          for (int k = 0; k < n; ++k) {
+            if (k + 1 < n) {
+              const uint32_t at = x + k_seq<1>(k + 1);
+              if (!(ok = tile(at))) break;
+              qk(0, (g0 + k + 1) & 1, at % ST);
+              tc_commit(&empty[at % ST]);
+            }
+            const uint32_t g = g0 + k, at = x + v_seq<1>(k, n);
+            if (!(ok = tile(at))) break;
+            if (!(ok = mbar_wait(&p_full[g & 1], (g >> 1) & 1, st, 233))) break;
+            tc_fence_after();
+            pv(0, g & 1, at % ST, k == 0);
+            tc_commit(&empty[at % ST]);
+          }
+        } else {
+          qk(0, 0, x % ST);
+          if (two) qk(1, 1, x % ST);
+          tc_commit(&empty[x % ST]);
+          for (int k = 0; k < n; ++k) {
+            const uint32_t va = x + v_seq<2>(k, n), ka = x + k_seq<2>(k + 1);
+            if (!(ok = tile(va))) break;
+            if (!(ok = mbar_wait(&p_full[0], (g0 + k) & 1, st, 233))) break;
+            tc_fence_after();
+            pv(0, 0, va % ST, k == 0);
+            if (k + 1 < n) {
+              if (!(ok = tile(ka))) break;
+              qk(0, 0, ka % ST);
+            }
+            if (two) {
+              if (!(ok = mbar_wait(&p_full[1], (g1 + k) & 1, st, 234))) break;
+              tc_fence_after();
+              pv(1, 1, va % ST, k == 0);
+            }
+            tc_commit(&empty[va % ST]);
+            if (k + 1 < n) {
+              if (two) qk(1, 1, ka % ST);
+              tc_commit(&empty[ka % ST]);
+            }
+          }
+        }
+        if (!ok) break;
+        x += 2 * n;
+        g0 += n;
+        if (two) g1 += n;
+        ++seg;
+      }
+      tc_commit(done);  // every MMA issued has completed before TMEM is released
+      mbar_wait(done, 0, st, 235);
+    }
+  } else if (warp < kProducer) {
+    // ---------------- softmax: one row per thread ----------------
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int rt = warp >> 2, row = tid & 127;  // row tile, row in it
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t x = 0, seg = 0, g = 0;
+    // After a wait that ran out the warp goes on without waiting: what it writes is void, but
+    // the barriers between the warps stay complete and the CTA ends.
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+      if (ok) ok = mbar_wait(bar, parity, st, where);
+      tc_fence_after();
+    };
+    while (walk.next(&s)) {
+      const int n = s.i1 - s.i0;
+      const bool two = NT == 2 && s.rows > kTile;
+      const int group = two || NT == 1 ? NT * 128 : 128;  // threads that take part in this segment's barriers
+      const int local = rt * kTile + row;                 // row of the row group
+      RowView v;
+      v.valid = local < s.rows;
+      const int rr = s.m * ROWS + local;
+      v.i = v.valid ? rr / a.G : 0;
+      const int qh = s.h * a.G + (rr - v.i * a.G), tok = s.r.t0 + v.i;
+      v.p = s.r.len + v.i;
+      const bool warp_live = __any_sync(0xffffffffu, v.valid);
+      if (a.window > 0) {
+        if (v.valid && a.pos) v.p = max(__ldg(a.pos + tok), s.r.len);
+        named_bar(3, NT * 128);
+        for (int j = tid; j < s.r.n; j += NT * 128)
+          s_dpos[j] = a.pos ? max(__ldg(a.pos + s.r.t0 + j), s.r.len) : s.r.len + j;
+        if (tid == 0) *s_maxpos = 0;
+        named_bar(3, NT * 128);
+        const int top = __reduce_max_sync(0xffffffffu, v.valid ? v.p : 0);
+        if (lane == 0) atomicMax(s_maxpos, top);
+        named_bar(3, NT * 128);
+      }
+      // queries: the thread's row, 16 bytes at a time, in the swizzled K-major layout
+      if (warp_live) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)tok * a.qs + (size_t)qh * D);
+        uint8_t* dst = s_q + rt * (kTile * D * 2) + row * 128;
+        uint4 w[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) w[c] = v.valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4)) = w[c];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      if (NT == 2 && rt == 1 && !two) {
+        // no rows here: only keep in step with the segments
+        wait(q_full, seg & 1, 241);
+        ++seg;
+        x += 2 * n;
+        continue;
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      bool dirty = false;
+      for (int k = 0; k < n; ++k) {
+        const int i = s.i0 + k;
+        const uint32_t gi = g + k;
+        const uint32_t buf = NT == 1 ? (gi & 1) : rt;
+        const uint32_t sp = NT == 1 ? ((gi >> 1) & 1) : (gi & 1);
+        wait(&s_full[buf], sp, 242);
+        // tiles at an edge: the prefix's end, the drafts, and where a window cuts
+        const int base = (s.r.tile0 + i) << 7;
+        const bool draft = i >= s.r.np;
+        const bool edge = draft || s.r.len - base < kTile || (a.window > 0 && base < *s_maxpos - a.window + 1);
+        const uint32_t s_addr = tmem + lane_base + buf * kTile;
+        if (warp_live) {
+          uint32_t sv[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+          tmem_ld_wait();
+          if (edge) {
+            uint32_t bits[4];
+            tile_bits(a, s, i, v, s_dpos, bits);
+#pragma unroll
+            for (int j = 0; j < kTile; ++j)
+              if (!(bits[j >> 5] >> (j & 31) & 1u)) sv[j] = 0xff800000u;  // -infinity
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
+          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          const bool grow = m_new > m_ref + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m_ref - m_new) : 1.f;
+            if (k > 0) {
+              wait(&pv_done[NT == 1 ? (gi - 1) & 1 : rt], NT == 1 ? ((gi - 1) >> 1) & 1 : (gi - 1) & 1, 243);
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_base + C::kO + rt * D + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st32(tmem + lane_base + C::kO + rt * D + c * 32, o);
+              }
+              l *= f;
+            }
+            if (grow) m_ref = m_new;
+          }
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
+          // holds over 1/16 of the row's sum so far that would show in the output next to its own
+          // rounding, so the remainder goes along as a second part; with more keys in play it
+          // averages out.  After a prefix's first tiles this is rare.
+          const bool lo = __any_sync(0xffffffffu, v.valid && ex2(m_new - mu) > l * 0.0625f);
+          if (lane == 0) s_lo[buf * 4 + (warp & 3)] = lo;
+          // p = 2^(scale s - mu) in one fused step, whose error against the rounded mu is common to
+          // the row.  Past 2^24 that error alone could overflow: there scale s is rounded first too.
+          float sc = a.scale_log2;
+          if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.f)) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) sv[j] = __float_as_uint(__uint_as_float(sv[j]) * sc);
+            sc = 1.f;
+          }
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float e0 = ex2(fmaf(__uint_as_float(sv[c * 64 + 2 * j]), sc, -mu));
+              const float e1 = ex2(fmaf(__uint_as_float(sv[c * 64 + 2 * j + 1]), sc, -mu));
+              sum[(2 * j) & 3] += e0;
+              sum[(2 * j + 1) & 3] += e1;
+              p[j] = pack_bf16(e0, e1);
+              sv[c * 64 + 2 * j] = __float_as_uint(e0);
+              sv[c * 64 + 2 * j + 1] = __float_as_uint(e1);
+            }
+            tmem_st32(s_addr + c * 32, p);
+            if (lo) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                p[j] = pack_bf16(__uint_as_float(sv[c * 64 + 2 * j]) - __uint_as_float(p[j] << 16),
+                                 __uint_as_float(sv[c * 64 + 2 * j + 1]) - __uint_as_float(p[j] & 0xffff0000u));
+              tmem_st32(s_addr + kTile / 2 + c * 32, p);
+            }
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        } else if (lane == 0) {
+          s_lo[buf * 4 + (warp & 3)] = 0;
+        }
+        if (edge) {
+          // values that no row sees become zero, and those that are not finite too (0 * NaN would
+          // reach every row): they are added back to the rows that see them at the end
+          const uint32_t at = x + v_seq<NT>(k, n);
+          wait(&full[at % ST], (at / ST) & 1, 244);
+          uint8_t* vt = s_ring + (at % ST) * C::kStageBytes;
+          const int hi = draft ? s.r.n - ((i - s.r.np) << 7) : s.r.len - base;
+          const int lo = draft || a.window == 0 ? 0 : s.r.len - a.window + 1 - base;
+          bool found = false;
+          for (int c = tid; c < kTile * HALVES * 8; c += group) {
+            const int key = (c >> 3) & (kTile - 1);
+            uint4* w = reinterpret_cast<uint4*>(vt + (c << 4));
+            if (key >= hi || key < lo) {
+              *w = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint4 y = *w;
+            uint32_t* e = &y.x;
+            bool change = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u, change = true;
+              if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0xffffu, change = true;
+            }
+            if (change) {
+              *w = y;
+              found = true;
+            }
+          }
+          fence_proxy_async_smem();
+          dirty |= named_bar_or(group == 256 ? 1 : 2, group, found);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      // ---- the segment's end: finished rows to out, cut ones to the partial sums ----
+      const uint32_t ge = g + n - 1;  // the segment's last tile
+      wait(&pv_done[NT == 1 ? ge & 1 : rt], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
+      if (warp_live) {
+        const bool whole = s.i0 == 0 && s.i1 == s.r.nt;
+        const size_t prow = (size_t)(2 * blockIdx.x + (s.i0 == 0)) * ROWS + local;
+        const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_base + C::kO + rt * D + c * 32, o);
+          tmem_ld_wait();
+          if (dirty && v.valid) {
+            uint32_t y[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = o[j];
+            for (int k = 0; k < n; ++k) {
+              const int i = s.i0 + k, base = (s.r.tile0 + i) << 7;
+              if (!(i >= s.r.np || s.r.len - base < kTile || (a.window > 0 && base < *s_maxpos - a.window + 1)))
+                continue;
+              uint32_t bits[4];
+              tile_bits(a, s, i, v, s_dpos, bits);
+              add_not_finite(a, s, i, bits, c * 32, D, y);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = y[j];
+          }
+          if (!v.valid) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + c * 32);
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        if (v.valid) {
+          if (!whole)
+            a.part_ml[prow] = make_float2(m_ref, l);
+          else if (a.lse)
+            a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+        }
+      }
+      x += 2 * n;
+      g += n;
+      ++seg;
+    }
+  } else {
+    fewer();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of each cut segment, one warp per row: block x is the CTA in
+// whose range a segment starts, its pieces lie in that CTA's tail slot and the
+// head slots of the CTAs after it.
+//   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum O_i 2^(m_i - M) / L
+template <int D>
+__global__ void __launch_bounds__(256) tree_attn_merge_kernel(const AttnArgs a, int rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {  // the call's status: the first CTA's error
+    Status e{0, 0};
+    for (int c = lane; c < a.ctas; c += 32) {
+      const Status x = a.err[c];
+      if (e.code == 0) e = x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, e.code != 0);
+    const int from = hit ? __ffs(hit) - 1 : 0;
+    e.code = __shfl_sync(0xffffffffu, e.code, from);
+    e.where = __shfl_sync(0xffffffffu, e.where, from);
+    if (lane == 0) *a.status = e;
+  }
+  const int4 c0 = a.cut[2 * blockIdx.x];
+  const int pieces = c0.x, local = blockIdx.y * 8 + warp;
+  if (pieces < 2 || local >= c0.z) return;
+  const int rr = a.cut[2 * blockIdx.x + 1].x * rows + local;
+  const int i = rr / a.G, tok = c0.y + i, qh = c0.w * a.G + rr - i * a.G;
+  auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)) * rows + local; };
+  float M = -INFINITY;
+  for (int p = lane; p < pieces; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float mu = M == -INFINITY ? 0.f : M;
+  constexpr int E = D / 32;
+  float acc[E] = {}, L = 0.f;
+  for (int p0 = 0; p0 < pieces; p0 += 32) {
+    float w = 0.f, lw = 0.f;
+    if (p0 + lane < pieces) {
+      const float2 ml = a.part_ml[slot(p0 + lane)];
+      w = ex2(ml.x - mu);
+      lw = w * ml.y;
+    }
+    L += warp_sum(lw);
+    const int np = min(32, pieces - p0);
+#pragma unroll 4
+    for (int p = 0; p < np; ++p) {
+      const float wp = __shfl_sync(0xffffffffu, w, p);
+      const float* o = a.part_o + slot(p0 + p) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(o);
+        acc[0] = fmaf(wp, y.x, acc[0]);
+        acc[1] = fmaf(wp, y.y, acc[1]);
+        acc[2] = fmaf(wp, y.z, acc[2]);
+        acc[3] = fmaf(wp, y.w, acc[3]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(o);
+        acc[0] = fmaf(wp, y.x, acc[0]);
+        acc[1] = fmaf(wp, y.y, acc[1]);
+      }
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(size_t)tok * (a.hk * a.G) + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 bool al(const void* p, unsigned n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -94,6 +860,45 @@ int check_attn(const lmoe_attn_dims* d, const lmoe_kv_cache* c, bool memory) {
   return LMOE_OK;
 }
 
+// Two row tiles per CTA where some request can have more than 128 rows per kv head.
+int row_tiles(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
+  return d->max_request_tokens * (d->q_heads / c->kv_heads) > kTile ? 2 : 1;
+}
+
+struct AttnWs {
+  size_t err, cut, ml, o, total;
+};
+
+AttnWs attn_ws(const lmoe_attn_dims* d, const lmoe_kv_cache* c, int ctas) {
+  const size_t rows = (size_t)row_tiles(d, c) * kTile;
+  AttnWs w;
+  size_t at = 256;  // the status word
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at = (at + bytes + 255) & ~size_t(255);
+    return x;
+  };
+  w.err = take(sizeof(Status) * ctas);
+  w.cut = take(2 * sizeof(int4) * ctas);
+  w.ml = take(2 * (size_t)ctas * rows * sizeof(float2));
+  w.o = take(2 * (size_t)ctas * rows * c->head_dim * sizeof(float));
+  w.total = at;
+  return w;
+}
+
+template <int D, int NT>
+int run_attn(const AttnArgs& a, const CUtensorMap (&tm)[4], int max_rows, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  static std::atomic<unsigned long long> done{0};
+  int rc = allow_smem(done, tree_attn_kernel<D, NT>, C::kSmem);
+  if (rc) return rc;
+  rc = launch_pdl("tree_attn_kernel", dim3(a.ctas), dim3(C::kThreads), C::kSmem, s, tree_attn_kernel<D, NT>, a, tm[0],
+                  tm[1], tm[2], tm[3]);
+  if (rc) return rc;
+  return launch_pdl("tree_attn_merge_kernel", dim3(a.ctas, (min(max_rows, C::kRows) + 7) / 8), dim3(256), 0, s,
+                    tree_attn_merge_kernel<D>, a, C::kRows);
+}
+
 }  // namespace
 
 }  // namespace lmoe
@@ -104,7 +909,8 @@ extern "C" {
 
 size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
   if (check_attn(d, c, false) != LMOE_OK) return 0;
-  return 256;
+  DevInfo di;
+  return attn_ws(d, c, dev_info(&di) == LMOE_OK ? di.sms : 152).total;
 }
 
 int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const uint16_t* q, int64_t q_stride,
@@ -115,7 +921,7 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
   calls_begin();
   int rc = check_attn(d, c, true);
   if (rc) return rc;
-  const int64_t qrow = (int64_t)d->q_heads * c->head_dim, krow = (int64_t)c->kv_heads * c->head_dim;
+  const int64_t D = c->head_dim, qrow = d->q_heads * D, krow = c->kv_heads * D;
   if (!al(q, 16) || !al(k_new, 16) || !al(v_new, 16) || !al(out, 16) || !al(token_offsets, 4) || !al(lens, 4) ||
       !al(block_table, 4) || (mask && !al(mask, 8)) || (pos && !al(pos, 4)) || (lse && !al(lse, 4)) ||
       q_stride < qrow || k_stride < krow || v_stride < krow || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
@@ -123,15 +929,71 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
     return LMOE_EINVAL;
   DevInfo di;
   if ((rc = dev_info(&di))) return rc;
-  if (ws_bytes < lmoe_tree_attention_workspace_bytes(d, c)) return LMOE_EWORKSPACE;
+  const AttnWs w = attn_ws(d, c, di.sms);
+  if (ws_bytes < w.total) return LMOE_EWORKSPACE;
+  // tensor maps: the cache as [block][head][slot][d], copied 64 columns by one page (at most a
+  // tile) at a time; the drafts as [token][head][d], 64 columns by 8 tokens
+  CUtensorMap tm[4];
+  const uint16_t* const base[4] = {c->k, c->v, k_new, v_new};
+  const uint64_t step[2] = {(uint64_t)k_stride * 2, (uint64_t)v_stride * 2};
+  // a dimension of extent 1 never steps: any valid stride will do
+  auto stride = [](int64_t elements, int64_t extent) { return (uint64_t)(extent > 1 ? elements : 64) * 2; };
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)c->block_size, (uint64_t)c->kv_heads, (uint64_t)c->n_blocks};
+    const uint64_t strides[3] = {stride(c->slot_stride, c->block_size), stride(c->head_stride, c->kv_heads),
+                                 stride(c->block_stride, c->n_blocks)};
+    const uint32_t box[4] = {64, (uint32_t)min(c->block_size, kTile), 1, 1};
+    if (encode_tmap(&tm[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return LMOE_ECUDA;
+    const uint64_t ndims[3] = {(uint64_t)D, (uint64_t)c->kv_heads, (uint64_t)d->n_tokens};
+    const uint64_t nstrides[2] = {(uint64_t)D * 2, step[i]};
+    const uint32_t nbox[3] = {64, 1, 8};
+    if (encode_tmap(&tm[2 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base[2 + i], ndims, nstrides, nbox,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return LMOE_ECUDA;
+  }
+  int bs_shift = 4;
+  while ((1 << bs_shift) < c->block_size) ++bs_shift;
+  char* base_ws = static_cast<char*>(ws);
+  AttnArgs a;
+  a.q = q;
+  a.v_cache = c->v;
+  a.v_new = v_new;
+  a.qs = q_stride;
+  a.vs = v_stride;
+  a.block_stride = c->block_stride;
+  a.head_stride = c->head_stride;
+  a.slot_stride = c->slot_stride;
+  a.offsets = token_offsets;
+  a.lens = lens;
+  a.table = block_table;
+  a.pos = pos;
+  a.mask = mask;
+  a.out = out;
+  a.lse = lse;
+  a.status = reinterpret_cast<Status*>(base_ws);
+  a.err = reinterpret_cast<Status*>(base_ws + w.err);
+  a.cut = reinterpret_cast<int4*>(base_ws + w.cut);
+  a.part_ml = reinterpret_cast<float2*>(base_ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(base_ws + w.o);
+  a.B = d->n_requests;
+  a.T = d->n_tokens;
+  a.max_n = d->max_request_tokens;
+  a.hk = c->kv_heads;
+  a.G = d->q_heads / c->kv_heads;
+  a.max_blocks = d->max_blocks;
+  a.n_blocks = c->n_blocks;
+  a.bs_shift = bs_shift;
+  a.words = d->mask_words;
+  a.window = d->window;
+  a.ctas = di.sms;
+  a.scale_log2 = d->scale * 1.4426950408889634f;
+  const int max_rows = a.max_n * a.G;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  Status* st;
-  if ((rc = optional_status(ws, ws_bytes, s, &st))) return rc;
-  const AttnArgs a = {*c,  q,   k_new, v_new, q_stride,      k_stride,    v_stride,   token_offsets,         lens,
-                      block_table, pos, mask,  out,   lse, st, d->n_requests, d->n_tokens, d->max_request_tokens,
-                      d->q_heads,  d->max_blocks, d->mask_words, d->window, d->scale};
-  return launch_pdl("tree_attn_rows_kernel", dim3(d->n_requests, (d->q_heads + 3) / 4), dim3(128), 0, s,
-                    c->head_dim == 64 ? tree_attn_rows_kernel<64> : tree_attn_rows_kernel<128>, a);
+  if (row_tiles(d, c) == 1)
+    return D == 64 ? run_attn<64, 1>(a, tm, max_rows, s) : run_attn<128, 1>(a, tm, max_rows, s);
+  return D == 64 ? run_attn<64, 2>(a, tm, max_rows, s) : run_attn<128, 2>(a, tm, max_rows, s);
 }
 
 }  // extern "C"

@@ -280,6 +280,15 @@ def test_many_requests_and_repeatability(lm):
     assert torch.equal(a, d)
 
 
+@pytest.mark.parametrize("n,d", [(8, 128), (8, 64), (30, 128), (30, 64)])
+def test_many_tiles_in_a_row(lm, n, d):
+    # long enough that every part of the split walks many tiles and several heads; the same bits each time
+    c = Case([20000, 311], [n, 3], hq=64, hk=8, d=d, bs=32, seed=31)
+    ref = c.check(lm)
+    for _ in range(10):
+        assert torch.equal(c.run(lm)[0], ref)
+
+
 def test_offsets_past_32_bits(lm):
     c = Case([200], [4], hq=16, hk=8, d=128, bs=64, seed=19)
     blocks = 36000  # more than 2^31 elements and 2^32 bytes per tensor
