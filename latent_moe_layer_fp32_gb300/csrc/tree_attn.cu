@@ -54,11 +54,23 @@ struct AttnArgs {
   float scale_log2;
 };
 
-// One request's share of the line of tiles.
+// One request's share of the line of tiles: np tiles of 128 cached positions
+// from base0 on (a page boundary at or below the first position in sight),
+// then nd tiles of drafts.  Up to 128 drafts move in behind the cached
+// positions of the last, partial tile when they fit there (at column c0, a
+// multiple of 8 rows for the copies), which saves a tile of its own.
 struct Req {
-  int t0, n, len, tile0, np, nt, groups;
+  int t0, n, len, base0, np, nt, c0, groups;
   bool bad;
   long long units;
+  __device__ __forceinline__ int base(int i) const { return base0 + (i << 7); }
+  // cached positions in tile i, the drafts in it: n_draft of them from d0 on, at columns from col on
+  __device__ __forceinline__ int cached(int i) const { return i < np ? min(kTile, len - base(i)) : 0; }
+  __device__ __forceinline__ int d0(int i) const { return c0 ? 0 : (i - np) << 7; }
+  __device__ __forceinline__ int drafts(int i) const {
+    return i < nt - 1 && i < np ? 0 : (i < np ? (c0 ? n : 0) : min(kTile, n - ((i - np) << 7)));
+  }
+  __device__ __forceinline__ int col(int i) const { return i < np ? c0 : 0; }
 };
 
 template <int ROWS>
@@ -71,9 +83,12 @@ __device__ __forceinline__ Req load_req(const AttnArgs& a, int b) {
   r.n = r.bad ? 0 : t1 - t0;
   r.len = len;
   const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;  // the first position that any row sees
-  r.tile0 = lo >> 7;
-  r.np = lo < len ? (len >> 7) + ((len & 127) != 0) - r.tile0 : 0;
-  r.nt = r.np + ((r.n + kTile - 1) >> 7);
+  r.base0 = lo & ~((1 << min(a.bs_shift, 7)) - 1);
+  const int held = lo < len ? len - r.base0 : 0;
+  r.np = (held >> 7) + ((held & 127) != 0);
+  const int tail = ((held & 127) + 7) & ~7;
+  r.c0 = (held & 127) != 0 && tail + r.n <= kTile ? tail : 0;
+  r.nt = r.np + (r.c0 ? 0 : (r.n + kTile - 1) >> 7);
   r.groups = (r.n * a.G + ROWS - 1) / ROWS;
   r.units = (long long)a.hk * r.groups * r.nt;
   return r;
@@ -118,66 +133,64 @@ struct Walk {
   }
 };
 
-// What one row sees of a tile, as 128 bits.
 struct RowView {
   bool valid;
   int i, p;  // draft index, position
 };
 
-__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {  // bits [lo, hi) of word w
-  const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {  // bits [lo, hi) of a 32-bit word
+  const int a = min(max(lo, 0), 32), b = min(max(hi, 0), 32);
   const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
   return below_b & ~below_a;
 }
 
-__device__ __forceinline__ void tile_bits(const AttnArgs& a, const Seg& s, int i, const RowView& v,
-                                          const int* s_dpos, uint32_t (&bits)[4]) {
-  if (!v.valid) {
-    bits[0] = bits[1] = bits[2] = bits[3] = 0u;
-    return;
-  }
-  if (i < s.r.np) {
-    const int base = (s.r.tile0 + i) << 7;
-    const int hi = min(kTile, s.r.len - base);
-    const int lo = a.window > 0 ? min(max(v.p - a.window + 1 - base, 0), kTile) : 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) bits[w] = range_bits(lo, hi, w);
-    return;
-  }
-  const int d0 = (i - s.r.np) << 7, n = s.r.n - d0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t x;
-    if (a.mask) {
-      const int word = (d0 >> 6) + (w >> 1);
-      const uint64_t m = word < a.words ? __ldg(a.mask + (size_t)(s.r.t0 + v.i) * a.words + word) : 0ull;
-      x = (uint32_t)(m >> (32 * (w & 1))) & range_bits(0, n, w);
-    } else {
-      x = range_bits(0, min(n, v.i - d0 + 1), w);
-    }
-    if (a.window > 0)
+// 32 bits of a row's mask from draft j on (j may be negative; bits of drafts below 0 are 0).
+__device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int j) {
+  const int w = j >> 6, o = j & 63;  // floor
+  const uint64_t lo = w >= 0 && w < words ? __ldg(m + w) : 0ull;
+  uint64_t x = lo >> o;
+  if (o > 32 && w + 1 >= 0 && w + 1 < words) x |= __ldg(m + w + 1) << (64 - o);
+  return (uint32_t)x;
+}
+
+// What a row sees of columns 32 w .. 32 w + 31 of tile i, as bits.
+__device__ __noinline__ uint32_t tile_word(const AttnArgs& a, const Seg& s, int i, int w, const RowView& v,
+                                           const int* s_dpos, bool dwindow) {
+  if (!v.valid) return 0u;
+  const int base = s.r.base(i) + 32 * w;
+  uint32_t x = range_bits(a.window > 0 ? v.p - a.window + 1 - base : 0, s.r.cached(i) - 32 * w);
+  const int nd = s.r.drafts(i);
+  if (nd > 0) {
+    const int d0 = s.r.d0(i), c = 32 * w - s.r.col(i);  // the first column's draft is d0 + c
+    uint32_t y = range_bits(-c, nd - c);
+    if (a.mask)
+      y &= mask_bits(a.mask + (size_t)(s.r.t0 + v.i) * a.words, a.words, d0 + c);
+    else
+      y &= range_bits(0, v.i - d0 - c + 1);
+    if (dwindow)
       for (int j = 0; j < 32; ++j)
-        if ((x >> j & 1u) && v.p - s_dpos[d0 + 32 * w + j] >= a.window) x &= ~(1u << j);
-    bits[w] = x;
+        if ((y >> j & 1u) && v.p - s_dpos[d0 + c + j] >= a.window) y &= ~(1u << j);
+    x |= y;
   }
+  return x;
 }
 
 // Adds the values that are not finite, of the keys that a row sees, to 32
 // elements of its output: sanitize() took them out of the tile so that they
 // reach no other row.  Runs only where there was such a value.
-__device__ __noinline__ void add_not_finite(const AttnArgs& a, const Seg& s, int i, const uint32_t* bits, int d0,
+__device__ __noinline__ void add_not_finite(const AttnArgs& a, const Seg& s, int i, int w, uint32_t bits, int d0,
                                             int width, uint32_t* o) {
-  for (int j = 0; j < kTile; ++j) {
-    if (!(bits[j >> 5] >> (j & 31) & 1u)) continue;
+  for (; bits; bits &= bits - 1) {
+    const int j = 32 * w + __ffs(bits) - 1;
     const uint16_t* v;
-    if (i < s.r.np) {
-      const int p = ((s.r.tile0 + i) << 7) + j;
+    if (j < s.r.cached(i)) {
+      const int p = s.r.base(i) + j;
       const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (p >> a.bs_shift));
       if (id < 0 || id >= a.n_blocks) continue;
       v = a.v_cache + (size_t)id * a.block_stride + (size_t)s.h * a.head_stride +
           (size_t)(p & ((1 << a.bs_shift) - 1)) * a.slot_stride;
     } else {
-      v = a.v_new + (size_t)(s.r.t0 + ((i - s.r.np) << 7) + j) * a.vs + s.h * width;
+      v = a.v_new + (size_t)(s.r.t0 + s.r.d0(i) + j - s.r.col(i)) * a.vs + s.h * width;
     }
 #pragma unroll
     for (int d = 0; d < 32; ++d) {
@@ -211,15 +224,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-template <int D, int NT>
+// D: head width.  NT: row tiles of 128 rows per CTA.  KS: with few rows (128 / KS at most) each row
+// stands KS times in the row tile, and the copies take 128 / KS of a tile's keys each, so that all four
+// softmax warps work on 32 rows or less.
+template <int D, int NT, int KS>
 struct Cfg {
-  static constexpr int kRows = NT * kTile;
+  static_assert(NT == 1 || KS == 1, "copies of rows only in a single row tile");
+  static constexpr int kRows = NT * kTile / KS;
+  static constexpr int kCols = kTile / KS;            // keys of a tile per softmax thread
   static constexpr int kStageBytes = kTile * D * 2;   // one K or V tile
-  static constexpr int kQBytes = NT * kTile * D * 2;
-  static constexpr int kStages = (D == 128 ? (NT == 1 ? 6 : 5) : 12);  // 160 to 192 KB of keys and values in flight
+  static constexpr int kQBytes = NT == 1 ? 32768 : NT * kTile * D * 2;  // also 2 x 16 KB for the copies' sums
+  static constexpr int kStages = D == 128 ? (NT == 1 ? 6 : 5) : (NT == 1 ? 12 : 12);
   static constexpr int kThreads = NT == 1 ? 192 : 384;  // softmax warps, producer, MMA (two: and two idle)
-  static constexpr int kMisc = 2048;
-  static constexpr int kSmem = kQBytes + kStages * kStageBytes + kMisc + 1024;
+  static constexpr int kMisc = 2048 + 1024;
+  static constexpr int kSmem = kQBytes + kStages * kStageBytes + kMisc;
   static constexpr uint32_t kO = 2 * kTile;           // first O column; S buffers at 0 and 128
   static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -235,15 +253,15 @@ __device__ __forceinline__ uint32_t v_seq(int i, int n) {
   return NT == 2 ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+template <int D, int NT, int KS>
+__global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     tree_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
-                     const __grid_constant__ CUtensorMap tm_vn) {
-  using C = Cfg<D, NT>;
+                     const __grid_constant__ CUtensorMap tm_vn, const __grid_constant__ CUtensorMap tm_k8,
+                     const __grid_constant__ CUtensorMap tm_v8) {
+  using C = Cfg<D, NT, KS>;
   constexpr int ST = C::kStages, ROWS = C::kRows, HALVES = D / 64;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // no static shared memory: the base is 1024-byte aligned
   uint8_t* s_q = smem;
   uint8_t* s_ring = smem + C::kQBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(s_ring + ST * C::kStageBytes);
@@ -260,6 +278,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   volatile uint32_t* s_lo = tmem_slot + 1;  // [2][4] by S buffer or row tile, and warp: P has a second part
   int* s_maxpos = reinterpret_cast<int*>(tmem_slot + 9);
   int* s_dpos = s_maxpos + 1;     // [256] positions of the drafts (only with a window)
+  float2* s_ml = reinterpret_cast<float2*>(s_q + C::kQBytes + ST * C::kStageBytes + 2048);  // [128] of the copies
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kProducer = NT * 4, kMma = NT * 4 + 1;
@@ -365,49 +384,42 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // ---------------- TMA producer: one lane per page (or 8 drafts) ----------------
     fewer();
     const uint64_t pol = policy_evict_first();
-    const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a cached tile
-    const int ppt = kTile / box;                  // pages per tile
+    const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a whole cached tile
+    const int ppt = kTile / box;                  // pages per such tile
     uint32_t x = 0, issued = 0;                   // ring position of the segment, copies issued
     bool ok = true;
-    // copies of lane `lane` of tile i into ring position x; `id` is the lane's page
-    auto copy = [&](const CUtensorMap* tc, const CUtensorMap* td, int i, int id, uint32_t at) {
+    // the lane's copies of tile i into ring position `at`: a whole tile page by page, a partial one and
+    // the drafts 8 rows at a time; `id` is the block that holds the lane's cached rows
+    auto copy = [&](const CUtensorMap* tp, const CUtensorMap* t8, const CUtensorMap* td, int i, int id, uint32_t at) {
       const uint32_t stage = at % ST;
       if (!mbar_wait(&empty[stage], ((at / ST) & 1) ^ 1, st, 221)) return false;
       uint8_t* dst = s_ring + stage * C::kStageBytes;
-      int copies, bytes;
-      if (i < s.r.np) {
-        const int keys = min(kTile, s.r.len - ((s.r.tile0 + i) << 7));
-        copies = (keys + box - 1) / box;
-        bytes = box * 128;
-      } else {
-        copies = (min(kTile, s.r.n - ((i - s.r.np) << 7)) + 7) >> 3;
-        bytes = 8 * 128;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&full[stage], copies * bytes * HALVES);
+      const int cached = s.r.cached(i);
+      const int rows = cached == kTile ? box : 8;
+      const int nc = cached == kTile ? ppt : (cached + 7) >> 3, nd = (s.r.drafts(i) + 7) >> 3;
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
       __syncwarp();
-      if (lane < copies) {
-        if (i < s.r.np) {
-          const int slot = ((s.r.tile0 + i) << 7) & ((1 << a.bs_shift) - 1);
+      if (lane < nc) {
+        const int slot = (s.r.base(i) + lane * rows) & ((1 << a.bs_shift) - 1);
 #pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_4d(dst + hf * (kTile * 128) + lane * bytes, tc, hf * 64, ppt == 1 ? slot : 0, s.h, id,
-                        &full[stage], pol);
-        } else {
-          const int row = s.r.t0 + ((i - s.r.np) << 7) + lane * 8;
+        for (int hf = 0; hf < HALVES; ++hf)
+          tma_load_4d(dst + hf * (kTile * 128) + lane * rows * 128, rows == 8 ? t8 : tp, hf * 64, slot, s.h, id,
+                      &full[stage], pol);
+      } else if (lane < nc + nd) {
+        const int j = (lane - nc) * 8;
 #pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_3d(dst + hf * (kTile * 128) + lane * bytes, td, hf * 64, s.h, row, &full[stage], pol);
-        }
+        for (int hf = 0; hf < HALVES; ++hf)
+          tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, td, hf * 64, s.h, s.r.t0 + s.r.d0(i) + j,
+                      &full[stage], pol);
       }
       __syncwarp();
       issued = at + 1;
       return true;
     };
-    auto page = [&](int i) {  // this lane's page of tile i
-      if (i >= s.r.np || lane >= ppt) return 0;
-      const int blk = (((s.r.tile0 + i) << 7) >> a.bs_shift) + lane;
-      if (ppt > 1 && ((long long)blk << a.bs_shift) >= s.r.len) return 0;
-      return __ldg(a.table + (size_t)s.b * a.max_blocks + blk);
+    auto page = [&](int i) {  // the block of this lane's cached rows of tile i
+      const int cached = s.r.cached(i), rows = cached == kTile ? box : 8;
+      if (lane * rows >= cached) return 0;
+      return __ldg(a.table + (size_t)s.b * a.max_blocks + ((s.r.base(i) + lane * rows) >> a.bs_shift));
     };
     while (ok && walk.next(&s)) {
       const int n = s.i1 - s.i0;
@@ -415,19 +427,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       for (int k = 0; k < n && ok; ++k) {
         const int i = s.i0 + k;
         const int id_next = k + 1 < n ? page(i + 1) : 0;
-        if (i < s.r.np && (id < 0 || id >= a.n_blocks)) {  // out of the cache: the copy reads zeros
+        if (id < 0 || id >= a.n_blocks) {  // out of the cache: the copy reads zeros
           set_error(st, LMOE_EDEVICE_CHECK, 212);
           id = a.n_blocks;
         }
-        ok = copy(&tm_k, &tm_kn, i, id, x + k_seq<NT>(k));
+        ok = copy(&tm_k, &tm_k8, &tm_kn, i, id, x + k_seq<NT>(k));
         if (NT == 2)
-          ok = ok && copy(&tm_v, &tm_vn, i, id, x + v_seq<NT>(k, n));
+          ok = ok && copy(&tm_v, &tm_v8, &tm_vn, i, id, x + v_seq<NT>(k, n));
         else if (k > 0)
-          ok = ok && copy(&tm_v, &tm_vn, i - 1, id_prev, x + v_seq<NT>(k - 1, n));
+          ok = ok && copy(&tm_v, &tm_v8, &tm_vn, i - 1, id_prev, x + v_seq<NT>(k - 1, n));
         id_prev = id;
         id = id_next;
       }
-      if (NT == 1) ok = ok && copy(&tm_v, &tm_vn, s.i1 - 1, id_prev, x + v_seq<NT>(n - 1, n));
+      if (NT == 1) ok = ok && copy(&tm_v, &tm_v8, &tm_vn, s.i1 - 1, id_prev, x + v_seq<NT>(n - 1, n));
       x += 2 * n;
     }
     // the last copies land before the CTA can finish (also after a wait that ran out)
@@ -453,18 +465,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       };
       auto pv = [&](int rt, uint32_t buf, uint32_t stage, bool first) {
         const uint32_t vb = r0 + stage * C::kStageBytes;
+        // a 16-key step goes to the lanes whose copy of the rows holds those keys
+        auto off_lanes = [&](int kk, bool second, uint32_t (&off)[4]) {
+          uint32_t all = 0xffffffffu;
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_bf16_ts(tmem + C::kO + rt * D, tmem + buf * kTile + kk * 8,
-                         smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128), kPv, !(first && kk == 0));
-        uint32_t off[4];
+          for (int w = 0; w < 4; ++w) {
+            off[w] = w * KS / 4 == kk * KS / 8 && !(second && !s_lo[buf * 4 + w]) ? 0u : 0xffffffffu;
+            all &= off[w];
+          }
+          return all == 0u;
+        };
 #pragma unroll
-        for (int w = 0; w < 4; ++w) off[w] = s_lo[buf * 4 + w] ? 0u : 0xffffffffu;
-        if ((off[0] & off[1] & off[2] & off[3]) == 0u) {
+        for (int kk = 0; kk < kTile / 16; ++kk) {
+          const uint32_t acc = !(first && kk % (8 / KS) == 0);
+          const uint64_t vd = smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128);
+          if constexpr (KS == 1) {
+            tc_mma_bf16_ts(tmem + C::kO + rt * D, tmem + buf * kTile + kk * 8, vd, kPv, acc);
+          } else {
+            uint32_t off[4];
+            off_lanes(kk, false, off);
+            tc_mma_bf16_ts_lanes(tmem + C::kO + rt * D, tmem + buf * kTile + kk * 8, vd, kPv, acc, off);
+          }
+        }
+        uint32_t any = 0;
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_bf16_ts_lanes(tmem + C::kO + rt * D, tmem + buf * kTile + kTile / 2 + kk * 8,
-                                 smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128), kPv, off);
+        for (int w = 0; w < 4; ++w) any |= s_lo[buf * 4 + w];
+        if (any) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            uint32_t off[4];
+            if (off_lanes(kk, true, off))
+              tc_mma_bf16_ts_lanes(tmem + C::kO + rt * D, tmem + buf * kTile + kTile / 2 + kk * 8,
+                                   smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128), kPv, 1u, off);
+          }
         }
         tc_commit(&pv_done[buf]);
       };
@@ -534,8 +567,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   } else if (warp < kProducer) {
     // ---------------- softmax: one row per thread ----------------
     if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    constexpr int CW = C::kCols;
     const int rt = warp >> 2, row = tid & 127;  // row tile, row in it
+    const int part = KS == 1 ? 0 : row / (kTile / KS);  // which copy of the rows: keys part * CW .. + CW of each tile
+    const int local = KS == 1 ? rt * kTile + row : row % (kTile / KS);  // row of the row group
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_addr = tmem + lane_base + C::kO + rt * D;
     uint32_t x = 0, seg = 0, g = 0;
     // After a wait that ran out the warp goes on without waiting: what it writes is void, but
     // the barriers between the warps stay complete and the CTA ends.
@@ -544,18 +581,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (ok) ok = mbar_wait(bar, parity, st, where);
       tc_fence_after();
     };
+    auto edge_tile = [&](int i) {  // the prefix's end, drafts, and where a window cuts
+      return i >= s.r.np || s.r.cached(i) < kTile || (a.window > 0 && s.r.base(i) < *s_maxpos - a.window + 1);
+    };
     while (walk.next(&s)) {
       const int n = s.i1 - s.i0;
       const bool two = NT == 2 && s.rows > kTile;
-      const int group = two || NT == 1 ? NT * 128 : 128;  // threads that take part in this segment's barriers
-      const int local = rt * kTile + row;                 // row of the row group
+      const int group = two ? 256 : 128;  // threads that take part in this segment's barriers
       RowView v;
       v.valid = local < s.rows;
-      const int rr = s.m * ROWS + local;
+      const int rr = s.m * C::kRows + local;
       v.i = v.valid ? rr / a.G : 0;
       const int qh = s.h * a.G + (rr - v.i * a.G), tok = s.r.t0 + v.i;
       v.p = s.r.len + v.i;
       const bool warp_live = __any_sync(0xffffffffu, v.valid);
+      bool dwindow = false;  // some pair of drafts may be a window apart
       if (a.window > 0) {
         if (v.valid && a.pos) v.p = max(__ldg(a.pos + tok), s.r.len);
         named_bar(3, NT * 128);
@@ -566,6 +606,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int top = __reduce_max_sync(0xffffffffu, v.valid ? v.p : 0);
         if (lane == 0) atomicMax(s_maxpos, top);
         named_bar(3, NT * 128);
+        dwindow = *s_maxpos - s.r.len >= a.window;
       }
       // queries: the thread's row, 16 bytes at a time, in the swizzled K-major layout
       if (warp_live) {
@@ -590,32 +631,43 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       float m_ref = -INFINITY, l = 0.f;
       bool dirty = false;
+#pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int i = s.i0 + k;
         const uint32_t gi = g + k;
         const uint32_t buf = NT == 1 ? (gi & 1) : rt;
-        const uint32_t sp = NT == 1 ? ((gi >> 1) & 1) : (gi & 1);
-        wait(&s_full[buf], sp, 242);
-        // tiles at an edge: the prefix's end, the drafts, and where a window cuts
-        const int base = (s.r.tile0 + i) << 7;
-        const bool draft = i >= s.r.np;
-        const bool edge = draft || s.r.len - base < kTile || (a.window > 0 && base < *s_maxpos - a.window + 1);
+        wait(&s_full[buf], NT == 1 ? ((gi >> 1) & 1) : (gi & 1), 242);
+        const bool edge = edge_tile(i);
         const uint32_t s_addr = tmem + lane_base + buf * kTile;
+        bool lo = false;
         if (warp_live) {
-          uint32_t sv[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
-          tmem_ld_wait();
           if (edge) {
-            uint32_t bits[4];
-            tile_bits(a, s, i, v, s_dpos, bits);
+            // unseen keys' scores become -infinity, in place
+#pragma unroll 1
+            for (int c = 0; c < CW / 32; ++c) {
+              const uint32_t addr = s_addr + part * CW + c * 32;
+              const uint32_t bits = tile_word(a, s, i, part * (CW / 32) + c, v, s_dpos, dwindow);
+              uint32_t y[32];
+              tmem_ld32(addr, y);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < kTile; ++j)
-              if (!(bits[j >> 5] >> (j & 31) & 1u)) sv[j] = 0xff800000u;  // -infinity
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1u)) y[j] = 0xff800000u;
+              tmem_st32(addr, y);
+            }
+            tmem_st_wait();
           }
+          uint32_t sv[CW];
+          auto load = [&] {
+#pragma unroll
+            for (int c = 0; c < CW / 32; ++c)
+              tmem_ld32(s_addr + part * CW + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+            tmem_ld_wait();
+          };
+          load();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
+          for (int j = 0; j < CW; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
           const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
           const bool grow = m_new > m_ref + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
@@ -623,13 +675,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             if (k > 0) {
               wait(&pv_done[NT == 1 ? (gi - 1) & 1 : rt], NT == 1 ? ((gi - 1) >> 1) & 1 : (gi - 1) & 1, 243);
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_base + C::kO + rt * D + c * 32, o);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + c * 16, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st32(tmem + lane_base + C::kO + rt * D + c * 32, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(o_addr + c * 16, o);
               }
               l *= f;
             }
@@ -640,57 +692,64 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           // holds over 1/16 of the row's sum so far that would show in the output next to its own
           // rounding, so the remainder goes along as a second part; with more keys in play it
           // averages out.  After a prefix's first tiles this is rare.
-          const bool lo = __any_sync(0xffffffffu, v.valid && ex2(m_new - mu) > l * 0.0625f);
-          if (lane == 0) s_lo[buf * 4 + (warp & 3)] = lo;
+          lo = __any_sync(0xffffffffu, v.valid && ex2(m_new - mu) > l * 0.0625f);
           // p = 2^(scale s - mu) in one fused step, whose error against the rounded mu is common to
           // the row.  Past 2^24 that error alone could overflow: there scale s is rounded first too.
           float sc = a.scale_log2;
           if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.f)) {
+#pragma unroll 1
+            for (int c = 0; c < CW / 16; ++c) {
+              uint32_t y[16];
+              tmem_ld16(s_addr + part * CW + c * 16, y);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < kTile; ++j) sv[j] = __float_as_uint(__uint_as_float(sv[j]) * sc);
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * sc);
+              tmem_st16(s_addr + part * CW + c * 16, y);
+            }
+            tmem_st_wait();
+            load();
             sc = 1.f;
           }
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          auto exps = [&](bool two_parts) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[32];
+            for (int c = 0; c < CW / 32; ++c) {
+              uint32_t p[16], p2[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float e0 = ex2(fmaf(__uint_as_float(sv[c * 64 + 2 * j]), sc, -mu));
-              const float e1 = ex2(fmaf(__uint_as_float(sv[c * 64 + 2 * j + 1]), sc, -mu));
-              sum[(2 * j) & 3] += e0;
-              sum[(2 * j + 1) & 3] += e1;
-              p[j] = pack_bf16(e0, e1);
-              sv[c * 64 + 2 * j] = __float_as_uint(e0);
-              sv[c * 64 + 2 * j + 1] = __float_as_uint(e1);
+              for (int j = 0; j < 16; ++j) {
+                const float e0 = ex2(fmaf(__uint_as_float(sv[c * 32 + 2 * j]), sc, -mu));
+                const float e1 = ex2(fmaf(__uint_as_float(sv[c * 32 + 2 * j + 1]), sc, -mu));
+                sum[(2 * j) & 3] += e0;
+                sum[(2 * j + 1) & 3] += e1;
+                p[j] = pack_bf16(e0, e1);
+                if (two_parts)
+                  p2[j] = pack_bf16(e0 - __uint_as_float(p[j] << 16), e1 - __uint_as_float(p[j] & 0xffff0000u));
+              }
+              tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
+              if (two_parts) tmem_st16(s_addr + kTile / 2 + part * (CW / 2) + c * 16, p2);
             }
-            tmem_st32(s_addr + c * 32, p);
-            if (lo) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                p[j] = pack_bf16(__uint_as_float(sv[c * 64 + 2 * j]) - __uint_as_float(p[j] << 16),
-                                 __uint_as_float(sv[c * 64 + 2 * j + 1]) - __uint_as_float(p[j] & 0xffff0000u));
-              tmem_st32(s_addr + kTile / 2 + c * 32, p);
-            }
-          }
+          };
+          if (lo)
+            exps(true);
+          else
+            exps(false);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
-        } else if (lane == 0) {
-          s_lo[buf * 4 + (warp & 3)] = 0;
         }
+        if (lane == 0) s_lo[buf * 4 + (warp & 3)] = lo;
         if (edge) {
           // values that no row sees become zero, and those that are not finite too (0 * NaN would
           // reach every row): they are added back to the rows that see them at the end
           const uint32_t at = x + v_seq<NT>(k, n);
           wait(&full[at % ST], (at / ST) & 1, 244);
           uint8_t* vt = s_ring + (at % ST) * C::kStageBytes;
-          const int hi = draft ? s.r.n - ((i - s.r.np) << 7) : s.r.len - base;
-          const int lo = draft || a.window == 0 ? 0 : s.r.len - a.window + 1 - base;
+          const int hi = s.r.cached(i), c0 = s.r.col(i), c1 = c0 + s.r.drafts(i);
+          const int first = a.window > 0 ? s.r.len - a.window + 1 - s.r.base(i) : 0;
           bool found = false;
           for (int c = tid; c < kTile * HALVES * 8; c += group) {
             const int key = (c >> 3) & (kTile - 1);
             uint4* w = reinterpret_cast<uint4*>(vt + (c << 4));
-            if (key >= hi || key < lo) {
+            if (!((key >= first && key < hi) || (key >= c0 && key < c1))) {
               *w = make_uint4(0u, 0u, 0u, 0u);
               continue;
             }
@@ -717,52 +776,102 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       // ---- the segment's end: finished rows to out, cut ones to the partial sums ----
       const uint32_t ge = g + n - 1;  // the segment's last tile
       wait(&pv_done[NT == 1 ? ge & 1 : rt], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
-      if (warp_live) {
-        const bool whole = s.i0 == 0 && s.i1 == s.r.nt;
-        const size_t prow = (size_t)(2 * blockIdx.x + (s.i0 == 0)) * ROWS + local;
-        const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+      const bool whole = s.i0 == 0 && s.i1 == s.r.nt;
+      float f = 1.f;
+      if constexpr (KS > 1) {  // join the copies of a row: M = max m_i, L = sum l_i 2^(m_i - M)
+        s_ml[row] = make_float2(m_ref, l);
+        named_bar(2, 128);
+        float M = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < KS; ++p) M = fmaxf(M, s_ml[p * (kTile / KS) + local].x);
+        const float mu = M == -INFINITY ? 0.f : M;
+        f = ex2(m_ref - mu);
+        l = 0.f;
+#pragma unroll
+        for (int p = 0; p < KS; ++p) {
+          const float2 y = s_ml[p * (kTile / KS) + local];
+          l += y.y * ex2(y.x - mu);
+        }
+        m_ref = M;
+      }
+      const size_t prow = (size_t)(2 * blockIdx.x + (s.i0 == 0)) * C::kRows + local;
+      const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+      constexpr int OW = 32 / KS;  // output columns per thread and chunk of 32
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_base + C::kO + rt * D + c * 32, o);
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (warp_live) {
+          tmem_ld32(o_addr + c * 32, o);
           tmem_ld_wait();
           if (dirty && v.valid) {
             uint32_t y[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = o[j];
-            for (int k = 0; k < n; ++k) {
-              const int i = s.i0 + k, base = (s.r.tile0 + i) << 7;
-              if (!(i >= s.r.np || s.r.len - base < kTile || (a.window > 0 && base < *s_maxpos - a.window + 1)))
-                continue;
-              uint32_t bits[4];
-              tile_bits(a, s, i, v, s_dpos, bits);
-              add_not_finite(a, s, i, bits, c * 32, D, y);
-            }
+            for (int i = s.i0; i < s.i1; ++i)
+              if (edge_tile(i))
+                for (int w = 0; w < CW / 32; ++w)
+                  add_not_finite(a, s, i, part * (CW / 32) + w,
+                                 tile_word(a, s, i, part * (CW / 32) + w, v, s_dpos, dwindow), c * 32, D, y);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = y[j];
           }
-          if (!v.valid) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + c * 32);
-            uint32_t w[16];
+        }
+        if constexpr (KS > 1) {
+          // [buffer][row][32] floats in the queries' place (every product that reads them is done)
+          uint8_t* buf = s_q + (c & 1) * 16384;
+          if (warp_live) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(buf + row * 128 + ((j ^ (row & 7)) << 4)) =
+                  make_float4(__uint_as_float(o[4 * j]) * f, __uint_as_float(o[4 * j + 1]) * f,
+                              __uint_as_float(o[4 * j + 2]) * f, __uint_as_float(o[4 * j + 3]) * f);
+          }
+          named_bar(2, 128);
+          if (warp_live) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c * 32);
+            for (int j = 0; j < OW / 4; ++j) {
+              float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              for (int p = 0; p < KS; ++p) {
+                const int r2 = p * (kTile / KS) + local;
+                const float4 z = *reinterpret_cast<const float4*>(
+                    buf + r2 * 128 + (((part * (OW / 4) + j) ^ (r2 & 7)) << 4));
+                y.x += z.x;
+                y.y += z.y;
+                y.z += z.z;
+                y.w += z.w;
+              }
+              o[4 * j] = __float_as_uint(y.x);
+              o[4 * j + 1] = __float_as_uint(y.y);
+              o[4 * j + 2] = __float_as_uint(y.z);
+              o[4 * j + 3] = __float_as_uint(y.w);
+            }
           }
         }
-        if (v.valid) {
-          if (!whole)
-            a.part_ml[prow] = make_float2(m_ref, l);
-          else if (a.lse)
-            a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+        if (!v.valid) continue;
+        if (whole) {
+          uint4* dst =
+              reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + c * 32 + part * OW);
+          uint32_t w[OW / 2];
+#pragma unroll
+          for (int j = 0; j < OW / 2; ++j)
+            w[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+#pragma unroll
+          for (int j = 0; j < OW / 8; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c * 32 + part * OW);
+#pragma unroll
+          for (int j = 0; j < OW / 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       }
+      if (v.valid && part == 0) {
+        if (!whole)
+          a.part_ml[prow] = make_float2(m_ref, l);
+        else if (a.lse)
+          a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+      }
+      // the next segment's queries overwrite the buffers that other warps may still read
+      if constexpr (KS > 1) named_bar(2, 128);
       x += 2 * n;
       g += n;
       ++seg;
@@ -860,9 +969,10 @@ int check_attn(const lmoe_attn_dims* d, const lmoe_kv_cache* c, bool memory) {
   return LMOE_OK;
 }
 
-// Two row tiles per CTA where some request can have more than 128 rows per kv head.
-int row_tiles(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
-  return d->max_request_tokens * (d->q_heads / c->kv_heads) > kTile ? 2 : 1;
+// Rows per CTA and segment, by the most rows that a request can have per kv head.
+int group_rows(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
+  const int rows = d->max_request_tokens * (d->q_heads / c->kv_heads);
+  return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
 }
 
 struct AttnWs {
@@ -870,7 +980,7 @@ struct AttnWs {
 };
 
 AttnWs attn_ws(const lmoe_attn_dims* d, const lmoe_kv_cache* c, int ctas) {
-  const size_t rows = (size_t)row_tiles(d, c) * kTile;
+  const size_t rows = group_rows(d, c);
   AttnWs w;
   size_t at = 256;  // the status word
   auto take = [&](size_t bytes) {
@@ -886,17 +996,27 @@ AttnWs attn_ws(const lmoe_attn_dims* d, const lmoe_kv_cache* c, int ctas) {
   return w;
 }
 
-template <int D, int NT>
-int run_attn(const AttnArgs& a, const CUtensorMap (&tm)[4], int max_rows, cudaStream_t s) {
-  using C = Cfg<D, NT>;
+template <int D, int NT, int KS>
+int run_attn(const AttnArgs& a, const CUtensorMap (&tm)[6], int max_rows, cudaStream_t s) {
+  using C = Cfg<D, NT, KS>;
   static std::atomic<unsigned long long> done{0};
-  int rc = allow_smem(done, tree_attn_kernel<D, NT>, C::kSmem);
+  int rc = allow_smem(done, tree_attn_kernel<D, NT, KS>, C::kSmem);
   if (rc) return rc;
-  rc = launch_pdl("tree_attn_kernel", dim3(a.ctas), dim3(C::kThreads), C::kSmem, s, tree_attn_kernel<D, NT>, a, tm[0],
-                  tm[1], tm[2], tm[3]);
+  rc = launch_pdl("tree_attn_kernel", dim3(a.ctas), dim3(C::kThreads), C::kSmem, s, tree_attn_kernel<D, NT, KS>, a,
+                  tm[0], tm[1], tm[2], tm[3], tm[4], tm[5]);
   if (rc) return rc;
   return launch_pdl("tree_attn_merge_kernel", dim3(a.ctas, (min(max_rows, C::kRows) + 7) / 8), dim3(256), 0, s,
                     tree_attn_merge_kernel<D>, a, C::kRows);
+}
+
+template <int D>
+int run_attn_rows(int rows, const AttnArgs& a, const CUtensorMap (&tm)[6], int max_rows, cudaStream_t s) {
+  switch (rows) {
+    case 32: return run_attn<D, 1, 4>(a, tm, max_rows, s);
+    case 64: return run_attn<D, 1, 2>(a, tm, max_rows, s);
+    case 128: return run_attn<D, 1, 1>(a, tm, max_rows, s);
+    default: return run_attn<D, 2, 1>(a, tm, max_rows, s);
+  }
 }
 
 }  // namespace
@@ -932,8 +1052,8 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
   const AttnWs w = attn_ws(d, c, di.sms);
   if (ws_bytes < w.total) return LMOE_EWORKSPACE;
   // tensor maps: the cache as [block][head][slot][d], copied 64 columns by one page (at most a
-  // tile) at a time; the drafts as [token][head][d], 64 columns by 8 tokens
-  CUtensorMap tm[4];
+  // tile) or by 8 slots at a time; the drafts as [token][head][d], 64 columns by 8 tokens
+  CUtensorMap tm[6];
   const uint16_t* const base[4] = {c->k, c->v, k_new, v_new};
   const uint64_t step[2] = {(uint64_t)k_stride * 2, (uint64_t)v_stride * 2};
   // a dimension of extent 1 never steps: any valid stride will do
@@ -944,6 +1064,10 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
                                  stride(c->block_stride, c->n_blocks)};
     const uint32_t box[4] = {64, (uint32_t)min(c->block_size, kTile), 1, 1};
     if (encode_tmap(&tm[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return LMOE_ECUDA;
+    const uint32_t box8[4] = {64, 8, 1, 1};
+    if (encode_tmap(&tm[4 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box8,
                     CU_TENSOR_MAP_SWIZZLE_128B))
       return LMOE_ECUDA;
     const uint64_t ndims[3] = {(uint64_t)D, (uint64_t)c->kv_heads, (uint64_t)d->n_tokens};
@@ -991,9 +1115,8 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
   a.scale_log2 = d->scale * 1.4426950408889634f;
   const int max_rows = a.max_n * a.G;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (row_tiles(d, c) == 1)
-    return D == 64 ? run_attn<64, 1>(a, tm, max_rows, s) : run_attn<128, 1>(a, tm, max_rows, s);
-  return D == 64 ? run_attn<64, 2>(a, tm, max_rows, s) : run_attn<128, 2>(a, tm, max_rows, s);
+  const int rows = group_rows(d, c);
+  return D == 64 ? run_attn_rows<64>(rows, a, tm, max_rows, s) : run_attn_rows<128>(rows, a, tm, max_rows, s);
 }
 
 }  // extern "C"
