@@ -15,13 +15,16 @@
 // CTA.  One producer warp copies K and V tiles page by page with TMA (128-byte
 // swizzle) into a ring; one thread issues tcgen05.mma: S = Q K^T (both K-major
 // from shared memory) into tensor memory, and O += P V with P read from tensor
-// memory and V as an MN-major operand straight from its pages' layout.  Warps
-// of the softmax group own 32 rows each, one row per thread: they read S, keep
-// the row's running maximum and sum in registers, write P (bf16, with a second
-// bf16 part where one key dominates a row, in place of S) and rescale O only when the maximum has grown by more than 2^8 (P is then at
-// most 2^8, which bf16 and the fp32 sums hold without loss).
-// With up to 128 rows the next tile's S is computed during the softmax of this
-// one (two S buffers); with more, two row tiles take turns.
+// memory and V as an MN-major operand straight from its pages' layout.  Two
+// softmax groups of four warps own a row per thread: they read S, keep the
+// row's running maximum and sum in registers, write P (bf16, with a second
+// bf16 part where one key dominates a row, in place of S) and rescale O only
+// when the maximum has grown by more than 2^8 (P is then at most 2^8, which
+// bf16 and the fp32 sums hold without loss).
+// Up to 128 rows per kv head: the groups take turns by segment, each with its
+// own queries and its own O, so one loads queries, joins and stores while the
+// other computes, and S of the next tile is computed during the softmax of
+// this one.  More rows: the groups take a row tile each of the same segment.
 #include <atomic>
 #include <cmath>
 
@@ -175,11 +178,11 @@ __device__ __noinline__ uint32_t tile_word(const AttnArgs& a, const Seg& s, int 
   return x;
 }
 
-// Adds the values that are not finite, of the keys that a row sees, to 32
+// Adds the values that are not finite, of the keys that a row sees, to 16
 // elements of its output: sanitize() took them out of the tile so that they
 // reach no other row.  Runs only where there was such a value.
 __device__ __noinline__ void add_not_finite(const AttnArgs& a, const Seg& s, int i, int w, uint32_t bits, int d0,
-                                            int width, uint32_t* o) {
+                                            int width, float* o) {
   for (; bits; bits &= bits - 1) {
     const int j = 32 * w + __ffs(bits) - 1;
     const uint16_t* v;
@@ -193,9 +196,9 @@ __device__ __noinline__ void add_not_finite(const AttnArgs& a, const Seg& s, int
       v = a.v_new + (size_t)(s.r.t0 + s.r.d0(i) + j - s.r.col(i)) * a.vs + s.h * width;
     }
 #pragma unroll
-    for (int d = 0; d < 32; ++d) {
+    for (int d = 0; d < 16; ++d) {
       const uint32_t x = v[d0 + d];
-      if ((x & 0x7f80u) == 0x7f80u) o[d] = __float_as_uint(__uint_as_float(o[d]) + bf16_bits_to_f32(x));
+      if ((x & 0x7f80u) == 0x7f80u) o[d] += bf16_bits_to_f32(x);
     }
   }
 }
@@ -233,24 +236,28 @@ struct Cfg {
   static constexpr int kRows = NT * kTile / KS;
   static constexpr int kCols = kTile / KS;            // keys of a tile per softmax thread
   static constexpr int kStageBytes = kTile * D * 2;   // one K or V tile
-  static constexpr int kQBytes = NT == 1 ? 32768 : NT * kTile * D * 2;  // also 2 x 16 KB for the copies' sums
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 6 : 5) : (NT == 1 ? 12 : 12);
-  static constexpr int kThreads = NT == 1 ? 192 : 384;  // softmax warps, producer, MMA (two: and two idle)
-  static constexpr int kMisc = 2048 + 1024;
-  static constexpr int kSmem = kQBytes + kStages * kStageBytes + kMisc;
+  static constexpr int kQBytes = KS > 1 ? 32768 : kTile * D * 2;  // a group's queries; with copies also their sums
+  static constexpr int kStages = D == 128 ? 5 : (KS > 1 ? 10 : 12);  // 160 KB of keys and values, or more, in flight
+  static constexpr int kThreads = 384;                // two softmax groups, producer, MMA, two idle warps
+  static constexpr int kMisc = 3072;
+  static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMisc;
   static constexpr uint32_t kO = 2 * kTile;           // first O column; S buffers at 0 and 128
+  // the join of copies: each takes D / KS columns of the sum, in passes of kPass columns
+  static constexpr int kOwn = D / KS;
+  static constexpr int kPass = KS == 4 && D == 128 ? 16 : kOwn;
+  static_assert(KS == 1 || kTile * (KS - 1) * kPass * 4 <= kQBytes, "room for the copies' sums");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// First ring position of K and V of tile i of n in a segment's order of use.
-// One row tile: K0 K1 V0 K2 V1 ... (S runs one tile ahead); two: K0 V0 K1 V1 ...
+// Ring position of K and V of the CTA's tile g of n.  The groups in turns: K0 K1 V0 K2 V1 ... (S runs one
+// tile ahead, also across segments); two row tiles: K0 V0 K1 V1 ...
 template <int NT>
-__device__ __forceinline__ uint32_t k_seq(int i) {
-  return NT == 2 ? 2 * i : (i == 0 ? 0 : 2 * i - 1);
+__device__ __forceinline__ uint32_t k_pos(uint32_t g) {
+  return NT == 2 ? 2 * g : (g == 0 ? 0 : 2 * g - 1);
 }
 template <int NT>
-__device__ __forceinline__ uint32_t v_seq(int i, int n) {
-  return NT == 2 ? 2 * i + 1 : (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+__device__ __forceinline__ uint32_t v_pos(uint32_t g, uint32_t n) {
+  return NT == 2 || g == n - 1 ? 2 * g + 1 : 2 * g + 2;
 }
 
 template <int D, int NT, int KS>
@@ -263,25 +270,24 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   constexpr int ST = C::kStages, ROWS = C::kRows, HALVES = D / 64;
   extern __shared__ __align__(1024) uint8_t smem[];  // no static shared memory: the base is 1024-byte aligned
   uint8_t* s_q = smem;
-  uint8_t* s_ring = smem + C::kQBytes;
+  uint8_t* s_ring = smem + 2 * C::kQBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(s_ring + ST * C::kStageBytes);
   uint64_t* empty = full + ST;
-  uint64_t* s_full = empty + ST;  // a tile's scores are in tensor memory: [S buffer] or [row tile]
-  uint64_t* p_full = s_full + 2;  // its probabilities are
-  uint64_t* pv_done = p_full + 2; // its product with V has been added to O (with one row tile, P can be
-                                  // a tile ahead of O: a barrier each for even and odd tiles)
-  uint64_t* q_full = pv_done + 2; // the segment's queries are in shared memory
-  uint64_t* done = q_full + 1;
+  uint64_t* s_full = empty + ST;  // [S buffer] a tile's scores are in tensor memory
+  uint64_t* p_full = s_full + 2;  // [S buffer] its probabilities are
+  uint64_t* pv_done = p_full + 2; // [S buffer] its product with V has been added to O
+  uint64_t* q_full = pv_done + 2; // [group] the segment's queries are in shared memory
+  uint64_t* s_first = q_full + 2; // [group] scores of a segment's first tile
+  uint64_t* done = s_first + 2;
   long long* s_start = reinterpret_cast<long long*>(done + 1);  // request, units into it, units in the range
   unsigned long long* s_warp = reinterpret_cast<unsigned long long*>(s_start + 3);  // [threads / 32]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_warp + 12);
-  volatile uint32_t* s_lo = tmem_slot + 1;  // [2][4] by S buffer or row tile, and warp: P has a second part
-  int* s_maxpos = reinterpret_cast<int*>(tmem_slot + 9);
-  int* s_dpos = s_maxpos + 1;     // [256] positions of the drafts (only with a window)
-  float2* s_ml = reinterpret_cast<float2*>(s_q + C::kQBytes + ST * C::kStageBytes + 2048);  // [128] of the copies
+  volatile uint32_t* s_lo = tmem_slot + 1;  // [S buffer] a byte per warp: P has a second part
+  int* s_maxpos = reinterpret_cast<int*>(tmem_slot + 3);  // [group]
+  int* s_dpos = s_maxpos + 2;  // [256] positions of the drafts, with a window ([group][128] where groups take turns)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = NT * 4, kMma = NT * 4 + 1;
+  constexpr int kProducer = 8, kMma = 9;
   Status* st = a.err + blockIdx.x;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -293,7 +299,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_full, NT * 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], NT * 4);
+      mbar_init(&s_first[i], 1);
+    }
     mbar_init(done, 1);
     fence_barrier_init();
     s_start[2] = 0;
@@ -372,10 +381,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     __syncthreads();
   }
   const uint32_t tmem = *tmem_slot;
-  // two row tiles: 384 threads start with 168 registers each; the service warps hand most of
-  // theirs to the softmax warps (56 + 2 x 224 = 3 x 168)
+  const uint32_t n_tiles = (uint32_t)s_start[2];
+  // 384 threads start with 168 registers each; with a whole tile's scores per thread the service
+  // warps hand some of theirs to the softmax warps (88 + 2 x 208 = 3 x 168)
   auto fewer = [] {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (KS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   };
   Walk<ROWS> walk(a, (int)s_start[0], s_start[1], s_start[2]);
   Seg s{};
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const uint64_t pol = policy_evict_first();
     const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a whole cached tile
     const int ppt = kTile / box;                  // pages per such tile
-    uint32_t x = 0, issued = 0;                   // ring position of the segment, copies issued
+    uint32_t issued = 0;                          // copies issued
     bool ok = true;
     // the lane's copies of tile i into ring position `at`: a whole tile page by page, a partial one and
     // the drafts 8 rows at a time; `id` is the block that holds the lane's cached rows
@@ -416,31 +426,49 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       issued = at + 1;
       return true;
     };
+    auto checked = [&](int id) {
+      if (id >= 0 && id < a.n_blocks) return id;
+      set_error(st, LMOE_EDEVICE_CHECK, 212);
+      return a.n_blocks;  // out of the cache: the copy reads zeros
+    };
     auto page = [&](int i) {  // the block of this lane's cached rows of tile i
       const int cached = s.r.cached(i), rows = cached == kTile ? box : 8;
       if (lane * rows >= cached) return 0;
       return __ldg(a.table + (size_t)s.b * a.max_blocks + ((s.r.base(i) + lane * rows) >> a.bs_shift));
     };
-    while (ok && walk.next(&s)) {
-      const int n = s.i1 - s.i0;
-      int id = page(s.i0), id_prev = 0;
-      for (int k = 0; k < n && ok; ++k) {
-        const int i = s.i0 + k;
-        const int id_next = k + 1 < n ? page(i + 1) : 0;
-        if (id < 0 || id >= a.n_blocks) {  // out of the cache: the copy reads zeros
-          set_error(st, LMOE_EDEVICE_CHECK, 212);
-          id = a.n_blocks;
+    uint32_t g = 0;
+    if constexpr (NT == 2) {
+      while (ok && walk.next(&s)) {
+        int id = page(s.i0);
+        for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
+          const int id_next = i + 1 < s.i1 ? page(i + 1) : 0;
+          id = checked(id);
+          ok = copy(&tm_k, &tm_k8, &tm_kn, i, id, k_pos<NT>(g)) && copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g, n_tiles));
+          id = id_next;
         }
-        ok = copy(&tm_k, &tm_k8, &tm_kn, i, id, x + k_seq<NT>(k));
-        if (NT == 2)
-          ok = ok && copy(&tm_v, &tm_v8, &tm_vn, i, id, x + v_seq<NT>(k, n));
-        else if (k > 0)
-          ok = ok && copy(&tm_v, &tm_v8, &tm_vn, i - 1, id_prev, x + v_seq<NT>(k - 1, n));
-        id_prev = id;
-        id = id_next;
       }
-      if (NT == 1) ok = ok && copy(&tm_v, &tm_v8, &tm_vn, s.i1 - 1, id_prev, x + v_seq<NT>(n - 1, n));
-      x += 2 * n;
+    } else {
+      // keys one tile ahead of values, also across segments
+      Seg nx{};
+      int i = 0, id = 0;  // the tile whose values are still to come
+      while (ok && walk.next(&nx)) {
+        Seg old = s;
+        s = nx;
+        int id_next = page(s.i0);
+        for (int k = s.i0; k < s.i1 && ok; ++k, ++g) {
+          const int id_k = checked(id_next);
+          id_next = k + 1 < s.i1 ? page(k + 1) : 0;
+          ok = copy(&tm_k, &tm_k8, &tm_kn, k, id_k, k_pos<NT>(g));
+          if (g > 0) {
+            if (k == s.i0) s = old;
+            ok = ok && copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g - 1, n_tiles));
+            if (k == s.i0 || k == nx.i0) s = nx;
+          }
+          i = k;
+          id = id_k;
+        }
+      }
+      if (ok && g > 0) copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g - 1, n_tiles));
     }
     // the last copies land before the CTA can finish (also after a wait that ran out)
     if (lane == 0)
@@ -451,52 +479,46 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
       constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
-      uint32_t x = 0, seg = 0, g0 = 0, g1 = 0;  // ring position, segments, tiles of row tile 0 / 1 so far
       bool ok = true;
-      const uint32_t q0 = smem_u32(s_q), r0 = smem_u32(s_ring);
-      auto qk = [&](int rt, uint32_t buf, uint32_t stage) {
-        const uint32_t kb = r0 + stage * C::kStageBytes, qb = q0 + rt * (kTile * D * 2);
+      // descriptors step by their start address (bits 0 to 13, in units of 16 bytes)
+      const uint64_t qd = smem_desc_sw128(smem_u32(s_q)), kd = smem_desc_sw128(smem_u32(s_ring));
+      const uint64_t vd = smem_desc_sw128_mn(smem_u32(s_ring), kTile * 128);
+      auto qk = [&](int grp, uint32_t buf, uint32_t stage) {
+        const uint64_t q = qd + grp * (C::kQBytes >> 4), kk0 = kd + stage * (C::kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-          tc_mma_bf16(tmem + buf * kTile, smem_desc_sw128(qb + o), smem_desc_sw128(kb + o), kQk, kk != 0);
+          const uint32_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+          tc_mma_bf16(tmem + buf * kTile, q + o, kk0 + o, kQk, kk != 0);
         }
         tc_commit(&s_full[buf]);
       };
-      auto pv = [&](int rt, uint32_t buf, uint32_t stage, bool first) {
-        const uint32_t vb = r0 + stage * C::kStageBytes;
-        // a 16-key step goes to the lanes whose copy of the rows holds those keys
-        auto off_lanes = [&](int kk, bool second, uint32_t (&off)[4]) {
-          uint32_t all = 0xffffffffu;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            off[w] = w * KS / 4 == kk * KS / 8 && !(second && !s_lo[buf * 4 + w]) ? 0u : 0xffffffffu;
-            all &= off[w];
-          }
-          return all == 0u;
-        };
+      auto pv = [&](int grp, uint32_t buf, uint32_t stage, bool first) {
+        const uint64_t v0 = vd + stage * (C::kStageBytes >> 4);
+        const uint32_t p = tmem + buf * kTile, o = tmem + C::kO + grp * D;
+        const uint32_t lo = s_lo[buf];
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk) {
           const uint32_t acc = !(first && kk % (8 / KS) == 0);
-          const uint64_t vd = smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128);
           if constexpr (KS == 1) {
-            tc_mma_bf16_ts(tmem + C::kO + rt * D, tmem + buf * kTile + kk * 8, vd, kPv, acc);
-          } else {
+            tc_mma_bf16_ts(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc);
+          } else {  // a 16-key step goes to the lanes whose copy of the rows holds those keys
             uint32_t off[4];
-            off_lanes(kk, false, off);
-            tc_mma_bf16_ts_lanes(tmem + C::kO + rt * D, tmem + buf * kTile + kk * 8, vd, kPv, acc, off);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == kk * KS / 8 ? 0u : 0xffffffffu;
+            tc_mma_bf16_ts_lanes(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc, off);
           }
         }
-        uint32_t any = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) any |= s_lo[buf * 4 + w];
-        if (any) {
-#pragma unroll
+        if (lo) {  // the second part, for the warps that wrote one
+#pragma unroll 1
           for (int kk = 0; kk < kTile / 16; ++kk) {
-            uint32_t off[4];
-            if (off_lanes(kk, true, off))
-              tc_mma_bf16_ts_lanes(tmem + C::kO + rt * D, tmem + buf * kTile + kTile / 2 + kk * 8,
-                                   smem_desc_sw128_mn(vb + kk * (16 * 128), kTile * 128), kPv, 1u, off);
+            uint32_t off[4], all = 0xffffffffu;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              off[w] = w * KS / 4 == kk * KS / 8 && (lo >> (8 * w) & 1u) ? 0u : 0xffffffffu;
+              all &= off[w];
+            }
+            if (!all)
+              tc_mma_bf16_ts_lanes(o, p + kTile / 2 + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, 1u, off);
           }
         }
         tc_commit(&pv_done[buf]);
@@ -506,37 +528,54 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         tc_fence_after();
         return true;
       };
-      while (ok && walk.next(&s)) {
-        const int n = s.i1 - s.i0;
-        const bool two = NT == 2 && s.rows > kTile;
-        if (!(ok = mbar_wait(q_full, seg & 1, st, 232))) break;
-        tc_fence_after();
-        if (!(ok = tile(x))) break;
-        if constexpr (NT == 1) {
-          qk(0, g0 & 1, x % ST);
-          tc_commit(&empty[x % ST]);
-          for (int k = 0; k < n; ++k) {
+      if constexpr (NT == 1) {
+        uint32_t g = 0, seg = 0;
+        auto first_qk = [&](uint32_t sg, uint32_t gt) {  // scores of segment sg's first tile gt
+          const uint32_t at = k_pos<1>(gt);
+          if (!mbar_wait(&q_full[sg & 1], (sg >> 1) & 1, st, 232) || !tile(at)) return false;
+          tc_fence_after();
+          qk(sg & 1, gt & 1, at % ST);
+          tc_commit(&s_first[sg & 1]);
+          tc_commit(&empty[at % ST]);
+          return true;
+        };
+        bool more = walk.next(&s);
+        if (more) ok = first_qk(0, 0);
+        while (ok && more) {
+          const int n = s.i1 - s.i0;
+          more = walk.next(&s);
+          for (int k = 0; k < n; ++k, ++g) {
             if (k + 1 < n) {
-              const uint32_t at = x + k_seq<1>(k + 1);
+              const uint32_t at = k_pos<1>(g + 1);
               if (!(ok = tile(at))) break;
-              qk(0, (g0 + k + 1) & 1, at % ST);
+              qk(seg & 1, (g + 1) & 1, at % ST);
               tc_commit(&empty[at % ST]);
+            } else if (more && !(ok = first_qk(seg + 1, g + 1))) {
+              break;
             }
-            const uint32_t g = g0 + k, at = x + v_seq<1>(k, n);
-            if (!(ok = tile(at))) break;
-            if (!(ok = mbar_wait(&p_full[g & 1], (g >> 1) & 1, st, 233))) break;
+            const uint32_t at = v_pos<1>(g, n_tiles);
+            if (!(ok = tile(at)) || !(ok = mbar_wait(&p_full[g & 1], (g >> 1) & 1, st, 233))) break;
             tc_fence_after();
-            pv(0, g & 1, at % ST, k == 0);
+            pv(seg & 1, g & 1, at % ST, k == 0);
             tc_commit(&empty[at % ST]);
           }
-        } else {
-          qk(0, 0, x % ST);
-          if (two) qk(1, 1, x % ST);
-          tc_commit(&empty[x % ST]);
-          for (int k = 0; k < n; ++k) {
-            const uint32_t va = x + v_seq<2>(k, n), ka = x + k_seq<2>(k + 1);
-            if (!(ok = tile(va))) break;
-            if (!(ok = mbar_wait(&p_full[0], (g0 + k) & 1, st, 233))) break;
+          ++seg;
+        }
+      } else {
+        uint32_t g = 0, seg = 0, g1 = 0;  // g1: tiles of row tile 1 so far
+        while (ok && walk.next(&s)) {
+          const int n = s.i1 - s.i0;
+          const bool two = s.rows > kTile;
+          uint32_t ka = k_pos<2>(g);
+          if (!(ok = mbar_wait(q_full, seg & 1, st, 232)) || !(ok = tile(ka))) break;
+          tc_fence_after();
+          qk(0, 0, ka % ST);
+          if (two) qk(1, 1, ka % ST);
+          tc_commit(&empty[ka % ST]);
+          for (int k = 0; k < n; ++k, ++g) {
+            const uint32_t va = v_pos<2>(g, n_tiles);
+            ka = k_pos<2>(g + 1);
+            if (!(ok = tile(va)) || !(ok = mbar_wait(&p_full[0], g & 1, st, 233))) break;
             tc_fence_after();
             pv(0, 0, va % ST, k == 0);
             if (k + 1 < n) {
@@ -544,7 +583,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               qk(0, 0, ka % ST);
             }
             if (two) {
-              if (!(ok = mbar_wait(&p_full[1], (g1 + k) & 1, st, 234))) break;
+              if (!(ok = mbar_wait(&p_full[1], g1++ & 1, st, 234))) break;
               tc_fence_after();
               pv(1, 1, va % ST, k == 0);
             }
@@ -554,26 +593,26 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               tc_commit(&empty[ka % ST]);
             }
           }
+          ++seg;
         }
-        if (!ok) break;
-        x += 2 * n;
-        g0 += n;
-        if (two) g1 += n;
-        ++seg;
       }
       tc_commit(done);  // every MMA issued has completed before TMEM is released
       mbar_wait(done, 0, st, 235);
     }
   } else if (warp < kProducer) {
     // ---------------- softmax: one row per thread ----------------
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (KS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     constexpr int CW = C::kCols;
-    const int rt = warp >> 2, row = tid & 127;  // row tile, row in it
+    const int grp = warp >> 2, row = tid & 127;  // group, row of its row tile
     const int part = KS == 1 ? 0 : row / (kTile / KS);  // which copy of the rows: keys part * CW .. + CW of each tile
-    const int local = KS == 1 ? rt * kTile + row : row % (kTile / KS);  // row of the row group
+    const int local = (NT == 2 ? grp * kTile : 0) + (KS == 1 ? row : row % (kTile / KS));  // row of the row group
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_addr = tmem + lane_base + C::kO + rt * D;
-    uint32_t x = 0, seg = 0, g = 0;
+    const uint32_t o_addr = tmem + lane_base + C::kO + grp * D;
+    uint8_t* const q_buf = s_q + grp * C::kQBytes;
+    int* const dpos = s_dpos + (NT == 2 ? 0 : grp * 128);
+    int* const maxpos = s_maxpos + (NT == 2 ? 0 : grp);
+    const int bar_seg = NT == 2 ? 3 : 4 + grp;    // barrier of the segment's threads
+    uint32_t seg = 0, g = 0, g_own = 0;           // segments and tiles of the CTA so far; tiles of this group
     // After a wait that ran out the warp goes on without waiting: what it writes is void, but
     // the barriers between the warps stay complete and the CTA ends.
     bool ok = true;
@@ -582,12 +621,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       tc_fence_after();
     };
     auto edge_tile = [&](int i) {  // the prefix's end, drafts, and where a window cuts
-      return i >= s.r.np || s.r.cached(i) < kTile || (a.window > 0 && s.r.base(i) < *s_maxpos - a.window + 1);
+      return i >= s.r.np || s.r.cached(i) < kTile || (a.window > 0 && s.r.base(i) < *maxpos - a.window + 1);
     };
-    while (walk.next(&s)) {
+    for (; walk.next(&s); ++seg) {
       const int n = s.i1 - s.i0;
+      if (NT == 1 && (int)(seg & 1) != grp) {
+        g += n;
+        continue;
+      }
       const bool two = NT == 2 && s.rows > kTile;
-      const int group = two ? 256 : 128;  // threads that take part in this segment's barriers
+      const int group = two ? 256 : 128;  // threads that take part in this segment's edge tiles
       RowView v;
       v.valid = local < s.rows;
       const int rr = s.m * C::kRows + local;
@@ -598,20 +641,20 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       bool dwindow = false;  // some pair of drafts may be a window apart
       if (a.window > 0) {
         if (v.valid && a.pos) v.p = max(__ldg(a.pos + tok), s.r.len);
-        named_bar(3, NT * 128);
-        for (int j = tid; j < s.r.n; j += NT * 128)
-          s_dpos[j] = a.pos ? max(__ldg(a.pos + s.r.t0 + j), s.r.len) : s.r.len + j;
-        if (tid == 0) *s_maxpos = 0;
-        named_bar(3, NT * 128);
+        named_bar(bar_seg, NT * 128);
+        for (int j = NT == 2 ? tid : row; j < s.r.n; j += NT * 128)
+          dpos[j] = a.pos ? max(__ldg(a.pos + s.r.t0 + j), s.r.len) : s.r.len + j;
+        if (row == 0) *maxpos = 0;
+        named_bar(bar_seg, NT * 128);
         const int top = __reduce_max_sync(0xffffffffu, v.valid ? v.p : 0);
-        if (lane == 0) atomicMax(s_maxpos, top);
-        named_bar(3, NT * 128);
-        dwindow = *s_maxpos - s.r.len >= a.window;
+        if (lane == 0) atomicMax(maxpos, top);
+        named_bar(bar_seg, NT * 128);
+        dwindow = *maxpos - s.r.len >= a.window;
       }
       // queries: the thread's row, 16 bytes at a time, in the swizzled K-major layout
       if (warp_live) {
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)tok * a.qs + (size_t)qh * D);
-        uint8_t* dst = s_q + rt * (kTile * D * 2) + row * 128;
+        uint8_t* dst = q_buf + row * 128;
         uint4 w[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) w[c] = v.valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -621,12 +664,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      if (NT == 2 && rt == 1 && !two) {
+      if (lane == 0) mbar_arrive(&q_full[NT == 2 ? 0 : grp]);
+      if (NT == 2 && grp == 1 && !two) {
         // no rows here: only keep in step with the segments
         wait(q_full, seg & 1, 241);
-        ++seg;
-        x += 2 * n;
+        g += n;
         continue;
       }
       float m_ref = -INFINITY, l = 0.f;
@@ -634,9 +676,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int i = s.i0 + k;
-        const uint32_t gi = g + k;
-        const uint32_t buf = NT == 1 ? (gi & 1) : rt;
-        wait(&s_full[buf], NT == 1 ? ((gi >> 1) & 1) : (gi & 1), 242);
+        const uint32_t gt = g + k, go = g_own + k;
+        const uint32_t buf = NT == 1 ? gt & 1 : grp;
+        if (NT == 1 && k == 0)
+          wait(&s_first[grp], (seg >> 1) & 1, 240);  // s_full may be phases behind until then
+        else
+          wait(&s_full[buf], NT == 1 ? (gt >> 1) & 1 : go & 1, 242);
         const bool edge = edge_tile(i);
         const uint32_t s_addr = tmem + lane_base + buf * kTile;
         bool lo = false;
@@ -646,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < CW / 32; ++c) {
               const uint32_t addr = s_addr + part * CW + c * 32;
-              const uint32_t bits = tile_word(a, s, i, part * (CW / 32) + c, v, s_dpos, dwindow);
+              const uint32_t bits = tile_word(a, s, i, part * (CW / 32) + c, v, dpos, dwindow);
               uint32_t y[32];
               tmem_ld32(addr, y);
               tmem_ld_wait();
@@ -673,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           if (__any_sync(0xffffffffu, grow)) {
             const float f = grow ? ex2(m_ref - m_new) : 1.f;
             if (k > 0) {
-              wait(&pv_done[NT == 1 ? (gi - 1) & 1 : rt], NT == 1 ? ((gi - 1) >> 1) & 1 : (gi - 1) & 1, 243);
+              wait(&pv_done[NT == 1 ? (gt - 1) & 1 : grp], NT == 1 ? ((gt - 1) >> 1) & 1 : (go - 1) & 1, 243);
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
@@ -736,17 +781,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
         }
-        if (lane == 0) s_lo[buf * 4 + (warp & 3)] = lo;
+        if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
         if (edge) {
           // values that no row sees become zero, and those that are not finite too (0 * NaN would
           // reach every row): they are added back to the rows that see them at the end
-          const uint32_t at = x + v_seq<NT>(k, n);
+          const uint32_t at = v_pos<NT>(gt, n_tiles);
           wait(&full[at % ST], (at / ST) & 1, 244);
           uint8_t* vt = s_ring + (at % ST) * C::kStageBytes;
           const int hi = s.r.cached(i), c0 = s.r.col(i), c1 = c0 + s.r.drafts(i);
           const int first = a.window > 0 ? s.r.len - a.window + 1 - s.r.base(i) : 0;
           bool found = false;
-          for (int c = tid; c < kTile * HALVES * 8; c += group) {
+          for (int c = two ? tid : row; c < kTile * HALVES * 8; c += group) {
             const int key = (c >> 3) & (kTile - 1);
             uint4* w = reinterpret_cast<uint4*>(vt + (c << 4));
             if (!((key >= first && key < hi) || (key >= c0 && key < c1))) {
@@ -767,102 +812,132 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             }
           }
           fence_proxy_async_smem();
-          dirty |= named_bar_or(group == 256 ? 1 : 2, group, found);
+          dirty |= named_bar_or(two ? 6 : 1 + grp, group, found);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       // ---- the segment's end: finished rows to out, cut ones to the partial sums ----
-      const uint32_t ge = g + n - 1;  // the segment's last tile
-      wait(&pv_done[NT == 1 ? ge & 1 : rt], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
+      const uint32_t ge = NT == 1 ? g + n - 1 : g_own + n - 1;  // the segment's last tile
+      wait(&pv_done[NT == 1 ? ge & 1 : grp], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
       const bool whole = s.i0 == 0 && s.i1 == s.r.nt;
-      float f = 1.f;
-      if constexpr (KS > 1) {  // join the copies of a row: M = max m_i, L = sum l_i 2^(m_i - M)
-        s_ml[row] = make_float2(m_ref, l);
-        named_bar(2, 128);
+      const size_t prow = (size_t)(2 * blockIdx.x + (s.i0 == 0)) * C::kRows + local;
+      // 16 columns of this thread's row of O
+      auto sums = [&](int col, float (&y)[16]) {
+        uint32_t o[16];
+        tmem_ld16(o_addr + col, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(o[j]);
+        if (dirty && v.valid) {
+          float z[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) z[j] = y[j];
+          for (int i = s.i0; i < s.i1; ++i)
+            if (edge_tile(i))
+              for (int w = 0; w < CW / 32; ++w)
+                add_not_finite(a, s, i, part * (CW / 32) + w,
+                               tile_word(a, s, i, part * (CW / 32) + w, v, dpos, dwindow), col, D, z);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = z[j];
+        }
+      };
+      auto put = [&](int col, const float (&y)[16], float inv) {
+        if (!v.valid) return;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + col);
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = pack_bf16(y[2 * j] * inv, y[2 * j + 1] * inv);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + col);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+        }
+      };
+      if constexpr (KS == 1) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        if (warp_live) {
+#pragma unroll 1
+          for (int col = 0; col < D; col += 16) {
+            float y[16];
+            sums(col, y);
+            put(col, y, inv);
+          }
+        }
+      } else {
+        // join the copies of a row: M = max m_i, L = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M).  Each copy
+        // finishes kOwn columns; the others hand theirs over through the queries' buffer (every product that
+        // reads it is done), [owner][other copy][row][kPass] with 16-byte pieces swizzled against conflicts.
+        constexpr int RP = kTile / KS, P = C::kPass, OWN = C::kOwn;
+        float2* ml = reinterpret_cast<float2*>(q_buf);
+        ml[row] = make_float2(m_ref, l);
+        named_bar(1 + grp, 128);
         float M = -INFINITY;
 #pragma unroll
-        for (int p = 0; p < KS; ++p) M = fmaxf(M, s_ml[p * (kTile / KS) + local].x);
+        for (int p = 0; p < KS; ++p) M = fmaxf(M, ml[p * RP + local].x);
         const float mu = M == -INFINITY ? 0.f : M;
-        f = ex2(m_ref - mu);
+        const float f = ex2(m_ref - mu);
         l = 0.f;
 #pragma unroll
         for (int p = 0; p < KS; ++p) {
-          const float2 y = s_ml[p * (kTile / KS) + local];
+          const float2 y = ml[p * RP + local];
           l += y.y * ex2(y.x - mu);
         }
         m_ref = M;
-      }
-      const size_t prow = (size_t)(2 * blockIdx.x + (s.i0 == 0)) * C::kRows + local;
-      const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
-      constexpr int OW = 32 / KS;  // output columns per thread and chunk of 32
+        named_bar(1 + grp, 128);
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        auto piece = [&](int owner, int from, int j) {
+          const int x = P == 16 ? (local >> 1) & 3 : local & 7;
+          return reinterpret_cast<float4*>(
+              q_buf + ((owner * (KS - 1) + (from > owner ? from - 1 : from)) * RP + local) * (P * 4) + ((j ^ x) << 4));
+        };
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (warp_live) {
-          tmem_ld32(o_addr + c * 32, o);
-          tmem_ld_wait();
-          if (dirty && v.valid) {
-            uint32_t y[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = o[j];
-            for (int i = s.i0; i < s.i1; ++i)
-              if (edge_tile(i))
-                for (int w = 0; w < CW / 32; ++w)
-                  add_not_finite(a, s, i, part * (CW / 32) + w,
-                                 tile_word(a, s, i, part * (CW / 32) + w, v, s_dpos, dwindow), c * 32, D, y);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = y[j];
-          }
-        }
-        if constexpr (KS > 1) {
-          // [buffer][row][32] floats in the queries' place (every product that reads them is done)
-          uint8_t* buf = s_q + (c & 1) * 16384;
+        for (int q = 0; q < OWN; q += P) {
+          if (q > 0) named_bar(1 + grp, 128);
           if (warp_live) {
+#pragma unroll 1
+            for (int d = 1; d < KS; ++d) {
+              const int owner = (part + d) % KS;
+#pragma unroll 1
+              for (int c = 0; c < P; c += 16) {
+                float y[16];
+                sums(owner * OWN + q + c, y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4*>(buf + row * 128 + ((j ^ (row & 7)) << 4)) =
-                  make_float4(__uint_as_float(o[4 * j]) * f, __uint_as_float(o[4 * j + 1]) * f,
-                              __uint_as_float(o[4 * j + 2]) * f, __uint_as_float(o[4 * j + 3]) * f);
-          }
-          named_bar(2, 128);
-          if (warp_live) {
-#pragma unroll
-            for (int j = 0; j < OW / 4; ++j) {
-              float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int p = 0; p < KS; ++p) {
-                const int r2 = p * (kTile / KS) + local;
-                const float4 z = *reinterpret_cast<const float4*>(
-                    buf + r2 * 128 + (((part * (OW / 4) + j) ^ (r2 & 7)) << 4));
-                y.x += z.x;
-                y.y += z.y;
-                y.z += z.z;
-                y.w += z.w;
+                for (int j = 0; j < 4; ++j)
+                  *piece(owner, part, c / 4 + j) =
+                      make_float4(y[4 * j] * f, y[4 * j + 1] * f, y[4 * j + 2] * f, y[4 * j + 3] * f);
               }
-              o[4 * j] = __float_as_uint(y.x);
-              o[4 * j + 1] = __float_as_uint(y.y);
-              o[4 * j + 2] = __float_as_uint(y.z);
-              o[4 * j + 3] = __float_as_uint(y.w);
+            }
+          }
+          named_bar(1 + grp, 128);
+          if (warp_live) {
+#pragma unroll 1
+            for (int c = 0; c < P; c += 16) {
+              float y[16];
+              sums(part * OWN + q + c, y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] *= f;
+#pragma unroll
+              for (int d = 1; d < KS; ++d) {
+                const int from = (part + d) % KS;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float4 z = *piece(part, from, c / 4 + j);
+                  y[4 * j] += z.x;
+                  y[4 * j + 1] += z.y;
+                  y[4 * j + 2] += z.z;
+                  y[4 * j + 3] += z.w;
+                }
+              }
+              put(part * OWN + q + c, y, inv);
             }
           }
         }
-        if (!v.valid) continue;
-        if (whole) {
-          uint4* dst =
-              reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + c * 32 + part * OW);
-          uint32_t w[OW / 2];
-#pragma unroll
-          for (int j = 0; j < OW / 2; ++j)
-            w[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-#pragma unroll
-          for (int j = 0; j < OW / 8; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c * 32 + part * OW);
-#pragma unroll
-          for (int j = 0; j < OW / 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        }
+        named_bar(1 + grp, 128);  // the next queries overwrite the buffer
       }
       if (v.valid && part == 0) {
         if (!whole)
@@ -870,11 +945,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         else if (a.lse)
           a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       }
-      // the next segment's queries overwrite the buffers that other warps may still read
-      if constexpr (KS > 1) named_bar(2, 128);
-      x += 2 * n;
       g += n;
-      ++seg;
+      g_own += n;
     }
   } else {
     fewer();
