@@ -213,6 +213,13 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool p) {
   return r != 0;
 }
 
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -476,7 +483,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   } else if (warp == kMma) {
     // ---------------- MMA issuer ----------------
     fewer();
-    if (lane == 0) {
+    // the whole warp walks, so that addresses stay in uniform registers; one lane issues
+    {
+      const bool leader = elect_one();
       constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
       constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
       bool ok = true;
@@ -485,43 +494,56 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       const uint64_t vd = smem_desc_sw128_mn(smem_u32(s_ring), kTile * 128);
       auto qk = [&](int grp, uint32_t buf, uint32_t stage) {
         const uint64_t q = qd + grp * (C::kQBytes >> 4), kk0 = kd + stage * (C::kStageBytes >> 4);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-          tc_mma_bf16(tmem + buf * kTile, q + o, kk0 + o, kQk, kk != 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+            tc_mma_bf16(tmem + buf * kTile, q + o, kk0 + o, kQk, kk != 0);
+          }
+          tc_commit(&s_full[buf]);
         }
-        tc_commit(&s_full[buf]);
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
       };
       auto pv = [&](int grp, uint32_t buf, uint32_t stage, bool first) {
         const uint64_t v0 = vd + stage * (C::kStageBytes >> 4);
         const uint32_t p = tmem + buf * kTile, o = tmem + C::kO + grp * D;
-        const uint32_t lo = s_lo[buf];
+        const uint32_t lo = __shfl_sync(0xffffffffu, s_lo[buf], 0);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) {
-          const uint32_t acc = !(first && kk % (8 / KS) == 0);
-          if constexpr (KS == 1) {
-            tc_mma_bf16_ts(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc);
-          } else {  // a 16-key step goes to the lanes whose copy of the rows holds those keys
-            uint32_t off[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == kk * KS / 8 ? 0u : 0xffffffffu;
-            tc_mma_bf16_ts_lanes(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc, off);
-          }
-        }
-        if (lo) {  // the second part, for the warps that wrote one
-#pragma unroll 1
           for (int kk = 0; kk < kTile / 16; ++kk) {
-            uint32_t off[4], all = 0xffffffffu;
+            const uint32_t acc = !(first && kk % (8 / KS) == 0);
+            if constexpr (KS == 1) {
+              tc_mma_bf16_ts(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc);
+            } else {  // a 16-key step goes to the lanes whose copy of the rows holds those keys
+              uint32_t off[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              off[w] = w * KS / 4 == kk * KS / 8 && (lo >> (8 * w) & 1u) ? 0u : 0xffffffffu;
-              all &= off[w];
+              for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == kk * KS / 8 ? 0u : 0xffffffffu;
+              tc_mma_bf16_ts_lanes(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc, off);
             }
-            if (!all)
-              tc_mma_bf16_ts_lanes(o, p + kTile / 2 + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, 1u, off);
           }
+          if (lo) {  // the second part, for the warps that wrote one
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+              uint32_t off[4], all = 0xffffffffu;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                off[w] = w * KS / 4 == c && (lo >> (8 * w) & 1u) ? 0u : 0xffffffffu;
+                all &= off[w];
+              }
+              if (!all) {
+#pragma unroll
+                for (int kk = c * 8 / KS; kk < (c + 1) * 8 / KS; ++kk)
+                  tc_mma_bf16_ts_lanes(o, p + kTile / 2 + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, 1u, off);
+              }
+            }
+          }
+          tc_commit(&pv_done[buf]);
         }
-        tc_commit(&pv_done[buf]);
+        __syncwarp();
       };
       auto tile = [&](uint32_t at) {  // the tile at ring position `at` has landed
         if (!mbar_wait(&full[at % ST], (at / ST) & 1, st, 231)) return false;
@@ -535,8 +557,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           if (!mbar_wait(&q_full[sg & 1], (sg >> 1) & 1, st, 232) || !tile(at)) return false;
           tc_fence_after();
           qk(sg & 1, gt & 1, at % ST);
-          tc_commit(&s_first[sg & 1]);
-          tc_commit(&empty[at % ST]);
+          commit(&s_first[sg & 1]);
+          commit(&empty[at % ST]);
           return true;
         };
         bool more = walk.next(&s);
@@ -549,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               const uint32_t at = k_pos<1>(g + 1);
               if (!(ok = tile(at))) break;
               qk(seg & 1, (g + 1) & 1, at % ST);
-              tc_commit(&empty[at % ST]);
+              commit(&empty[at % ST]);
             } else if (more && !(ok = first_qk(seg + 1, g + 1))) {
               break;
             }
@@ -557,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             if (!(ok = tile(at)) || !(ok = mbar_wait(&p_full[g & 1], (g >> 1) & 1, st, 233))) break;
             tc_fence_after();
             pv(seg & 1, g & 1, at % ST, k == 0);
-            tc_commit(&empty[at % ST]);
+            commit(&empty[at % ST]);
           }
           ++seg;
         }
@@ -571,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           tc_fence_after();
           qk(0, 0, ka % ST);
           if (two) qk(1, 1, ka % ST);
-          tc_commit(&empty[ka % ST]);
+          commit(&empty[ka % ST]);
           for (int k = 0; k < n; ++k, ++g) {
             const uint32_t va = v_pos<2>(g, n_tiles);
             ka = k_pos<2>(g + 1);
@@ -587,16 +609,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               tc_fence_after();
               pv(1, 1, va % ST, k == 0);
             }
-            tc_commit(&empty[va % ST]);
+            commit(&empty[va % ST]);
             if (k + 1 < n) {
               if (two) qk(1, 1, ka % ST);
-              tc_commit(&empty[ka % ST]);
+              commit(&empty[ka % ST]);
             }
           }
           ++seg;
         }
       }
-      tc_commit(done);  // every MMA issued has completed before TMEM is released
+      commit(done);  // every MMA issued has completed before TMEM is released
       mbar_wait(done, 0, st, 235);
     }
   } else if (warp < kProducer) {
