@@ -362,7 +362,8 @@ LMOE_API size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* dims, 
  *   mask     uint64 [T][mask_words], or NULL: every row sees the rows of its
  *            request up to its own (a chain, or plain decoding)
  *   pos      int32 [T], or NULL for lens[b] + the row's index; only a window
- *            reads it; a position below lens[b] counts as lens[b]
+ *            reads it; it counts as at least lens[b] and at most lens[b] + n - 1
+ *            for a request of n rows (the deepest place in any tree of n)
  *   out      out bf16 [T][q_heads][head_dim], contiguous
  *   lse      out fp32 [T][q_heads], or NULL
  * Scores, the running maximum and sum, and the accumulators are fp32.  For

@@ -25,6 +25,8 @@
 // own queries and its own O, so one loads queries, joins and stores while the
 // other computes, and S of the next tile is computed during the softmax of
 // this one.  More rows: the groups take a row tile each of the same segment.
+// Two further warps clean the value tiles at an edge of what rows see, so that
+// no bits of an unseen key reach a product.
 #include <atomic>
 #include <cmath>
 
@@ -59,158 +61,140 @@ struct AttnArgs {
 
 // One request's share of the line of tiles: np tiles of 128 cached positions
 // from base0 on (a page boundary at or below the first position in sight),
-// then nd tiles of drafts.  Up to 128 drafts move in behind the cached
-// positions of the last, partial tile when they fit there (at column c0, a
+// then tiles of drafts, nt in all.  Up to 128 drafts move in behind the cached
+// positions of the last, partial tile when they fit there (at column c0 > 0, a
 // multiple of 8 rows for the copies), which saves a tile of its own.
 struct Req {
-  int t0, n, len, base0, np, nt, c0, groups;
-  bool bad;
-  long long units;
+  int t0, n, len, base0, np, nt, c0;
+  int cut, full;  // tiles below cut hold positions that some row's window leaves out; from full on, not 128 positions
   __device__ __forceinline__ int base(int i) const { return base0 + (i << 7); }
-  // cached positions in tile i, the drafts in it: n_draft of them from d0 on, at columns from col on
+  // cached positions in tile i; the drafts in it, from d0 on, at columns from col on
   __device__ __forceinline__ int cached(int i) const { return i < np ? min(kTile, len - base(i)) : 0; }
   __device__ __forceinline__ int d0(int i) const { return c0 ? 0 : (i - np) << 7; }
   __device__ __forceinline__ int drafts(int i) const {
-    return i < nt - 1 && i < np ? 0 : (i < np ? (c0 ? n : 0) : min(kTile, n - ((i - np) << 7)));
+    return i >= np ? min(kTile, n - ((i - np) << 7)) : (c0 && i == np - 1 ? n : 0);
   }
   __device__ __forceinline__ int col(int i) const { return i < np ? c0 : 0; }
+  // whether some row sees only part of tile i: where a window cuts, the prefix's end, and drafts
+  __device__ __forceinline__ bool edge(int i) const { return i < cut || i >= full; }
+};
+
+struct Load {
+  int groups;  // row groups
+  bool bad;
+  long long units;
 };
 
 template <int ROWS>
-__device__ __forceinline__ Req load_req(const AttnArgs& a, int b) {
-  Req r;
+__device__ __forceinline__ Load load_req(const AttnArgs& a, int b, Req* r) {
   const int t0 = __ldg(a.offsets + b), t1 = __ldg(a.offsets + b + 1), len = __ldg(a.lens + b);
-  r.bad = t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 > a.max_n || len < 0 ||
+  Load w;
+  w.bad = t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 > a.max_n || len < 0 ||
           len > ((long long)a.max_blocks << a.bs_shift);
-  r.t0 = t0;
-  r.n = r.bad ? 0 : t1 - t0;
-  r.len = len;
+  r->t0 = t0;
+  r->n = w.bad ? 0 : t1 - t0;
+  r->len = len;
   const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;  // the first position that any row sees
-  r.base0 = lo & ~((1 << min(a.bs_shift, 7)) - 1);
-  const int held = lo < len ? len - r.base0 : 0;
-  r.np = (held >> 7) + ((held & 127) != 0);
+  r->base0 = lo & ~((1 << min(a.bs_shift, 7)) - 1);
+  const int held = lo < len ? len - r->base0 : 0;
+  r->np = (held >> 7) + ((held & 127) != 0);
+  r->full = held >> 7;
+  // the last row's window starts at len + n - window at most
+  r->cut = a.window > 0 ? (max(0, min(len, len + r->n - a.window) - r->base0) + 127) >> 7 : 0;
   const int tail = ((held & 127) + 7) & ~7;
-  r.c0 = (held & 127) != 0 && tail + r.n <= kTile ? tail : 0;
-  r.nt = r.np + (r.c0 ? 0 : (r.n + kTile - 1) >> 7);
-  r.groups = (r.n * a.G + ROWS - 1) / ROWS;
-  r.units = (long long)a.hk * r.groups * r.nt;
-  return r;
+  r->c0 = (held & 127) != 0 && tail + r->n <= kTile ? tail : 0;
+  r->nt = r->np + (r->c0 ? 0 : (r->n + kTile - 1) >> 7);
+  w.groups = (r->n * a.G + ROWS - 1) / ROWS;
+  w.units = (long long)a.hk * w.groups * r->nt;
+  return w;
 }
 
 // The part of one segment that falls into a CTA's range.
-struct Seg {
+struct alignas(16) Seg {
   Req r;
   int b, h, m;   // request, kv head, row group
-  int i0, i1;    // tiles [i0, i1) of r.nt
+  int i0, i1;    // tiles [i0, i1) of r.nt; i1 = 0 marks the end of the CTA's segments
   int rows;      // valid rows of this row group
+  int pad;
 };
+static_assert(sizeof(Seg) == 64, "four 16-byte pieces");
 
-// Walks the segments of the unit range [u, end): every role of the CTA takes the same walk.
+// Walks the segments of the CTA's unit range.
 template <int ROWS>
 struct Walk {
   const AttnArgs& a;
   int b;
   long long off, left;  // units into request b, units left in the range
-  Req r;
-  __device__ Walk(const AttnArgs& args, int b0, long long off0, long long n) : a(args), b(b0), off(off0), left(n) {
-    if (left > 0) r = load_req<ROWS>(a, b);
-  }
   __device__ bool next(Seg* s) {
     if (left <= 0) return false;
-    while (off >= r.units) {
-      off -= r.units;
+    Load w;
+    for (;;) {
+      w = load_req<ROWS>(a, b, &s->r);
+      if (off < w.units) break;
+      off -= w.units;
       ++b;
-      r = load_req<ROWS>(a, b);
     }
-    const long long k = off / r.nt;
-    s->r = r;
+    const long long k = off / s->r.nt;
     s->b = b;
-    s->h = (int)(k / r.groups);
-    s->m = (int)(k - (long long)s->h * r.groups);
-    s->i0 = (int)(off - k * r.nt);
-    s->i1 = (int)min((long long)r.nt, s->i0 + left);
-    s->rows = min(ROWS, r.n * a.G - s->m * ROWS);
+    s->h = (int)(k / w.groups);
+    s->m = (int)(k - (long long)s->h * w.groups);
+    s->i0 = (int)(off - k * s->r.nt);
+    s->i1 = (int)min((long long)s->r.nt, s->i0 + left);
+    s->rows = min(ROWS, s->r.n * a.G - s->m * ROWS);
     off += s->i1 - s->i0;
     left -= s->i1 - s->i0;
     return true;
   }
 };
 
-struct RowView {
-  bool valid;
-  int i, p;  // draft index, position
-};
+// A draft's position: between the prefix's end and the deepest place that n drafts can reach.
+__device__ __forceinline__ int draft_pos(const AttnArgs& a, int t0, int n, int len, int j) {
+  return a.pos ? min(max(__ldg(a.pos + t0 + j), len), len + n - 1) : len + j;
+}
 
-__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {  // bits [lo, hi) of a 32-bit word
-  const int a = min(max(lo, 0), 32), b = min(max(hi, 0), 32);
-  const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+__device__ __forceinline__ uint64_t range_bits(int lo, int hi) {  // bits [lo, hi) of a 64-bit word
+  const int a = min(max(lo, 0), 64), b = min(max(hi, 0), 64);
+  const uint64_t below_b = b == 64 ? ~0ull : (1ull << b) - 1ull, below_a = a == 64 ? ~0ull : (1ull << a) - 1ull;
   return below_b & ~below_a;
 }
 
-// 32 bits of a row's mask from draft j on (j may be negative; bits of drafts below 0 are 0).
-__device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int j) {
-  const int w = j >> 6, o = j & 63;  // floor
-  const uint64_t lo = w >= 0 && w < words ? __ldg(m + w) : 0ull;
-  uint64_t x = lo >> o;
-  if (o > 32 && w + 1 >= 0 && w + 1 < words) x |= __ldg(m + w + 1) << (64 - o);
-  return (uint32_t)x;
-}
-
-// What a row sees of columns 32 w .. 32 w + 31 of tile i, as bits.
-__device__ __noinline__ uint32_t tile_word(const AttnArgs& a, const Seg& s, int i, int w, const RowView& v,
-                                           const int* s_dpos, bool dwindow) {
-  if (!v.valid) return 0u;
-  const int base = s.r.base(i) + 32 * w;
-  uint32_t x = range_bits(a.window > 0 ? v.p - a.window + 1 - base : 0, s.r.cached(i) - 32 * w);
-  const int nd = s.r.drafts(i);
-  if (nd > 0) {
-    const int d0 = s.r.d0(i), c = 32 * w - s.r.col(i);  // the first column's draft is d0 + c
-    uint32_t y = range_bits(-c, nd - c);
-    if (a.mask)
-      y &= mask_bits(a.mask + (size_t)(s.r.t0 + v.i) * a.words, a.words, d0 + c);
-    else
-      y &= range_bits(0, v.i - d0 - c + 1);
-    if (dwindow)
-      for (int j = 0; j < 32; ++j)
-        if ((y >> j & 1u) && v.p - s_dpos[d0 + c + j] >= a.window) y &= ~(1u << j);
-    x |= y;
+// What draft vi (at position vp) of a segment's request sees of the 128 columns of tile i.
+__device__ __forceinline__ void edge_bits(const AttnArgs& a, const Seg* s, int i, int vi, int vp, uint64_t (&bits)[2]) {
+  const int cached = s->r.cached(i), first = a.window > 0 ? vp - a.window + 1 - s->r.base(i) : 0;
+  bits[0] = range_bits(first, cached);
+  bits[1] = range_bits(first - 64, cached - 64);
+  const int nd = s->r.drafts(i);
+  if (nd == 0) return;
+  const int d0 = s->r.d0(i), c = s->r.col(i), t0 = s->r.t0;
+  // the drafts d0 .. d0 + 127 that the row sees, moved up to column c
+  uint64_t m0, m1;
+  if (a.mask) {
+    const uint64_t* row = a.mask + (size_t)(t0 + vi) * a.words;
+    const int w = d0 >> 6;
+    m0 = w < a.words ? __ldg(row + w) : 0ull;
+    m1 = w + 1 < a.words ? __ldg(row + w + 1) : 0ull;
+  } else {
+    m0 = range_bits(0, vi - d0 + 1);
+    m1 = range_bits(0, vi - d0 - 63);
   }
-  return x;
-}
-
-// Adds the values that are not finite, of the keys that a row sees, to 16
-// elements of its output: sanitize() took them out of the tile so that they
-// reach no other row.  Runs only where there was such a value.
-__device__ __noinline__ void add_not_finite(const AttnArgs& a, const Seg& s, int i, int w, uint32_t bits, int d0,
-                                            int width, float* o) {
-  for (; bits; bits &= bits - 1) {
-    const int j = 32 * w + __ffs(bits) - 1;
-    const uint16_t* v;
-    if (j < s.r.cached(i)) {
-      const int p = s.r.base(i) + j;
-      const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (p >> a.bs_shift));
-      if (id < 0 || id >= a.n_blocks) continue;
-      v = a.v_cache + (size_t)id * a.block_stride + (size_t)s.h * a.head_stride +
-          (size_t)(p & ((1 << a.bs_shift) - 1)) * a.slot_stride;
-    } else {
-      v = a.v_new + (size_t)(s.r.t0 + s.r.d0(i) + j - s.r.col(i)) * a.vs + s.h * width;
-    }
-#pragma unroll
-    for (int d = 0; d < 16; ++d) {
-      const uint32_t x = v[d0 + d];
-      if ((x & 0x7f80u) == 0x7f80u) o[d] += bf16_bits_to_f32(x);
-    }
+  m0 &= range_bits(0, nd);
+  m1 &= range_bits(0, nd - 64);
+  const int n = s->r.n, len = s->r.len;
+  if (a.window > 0 && n > a.window) {  // some pair of drafts may be a window apart
+    for (uint64_t z = m0; z; z &= z - 1)
+      if (vp - draft_pos(a, t0, n, len, d0 + __ffsll(z) - 1) >= a.window) m0 &= ~(z & -z);
+    for (uint64_t z = m1; z; z &= z - 1)
+      if (vp - draft_pos(a, t0, n, len, d0 + 63 + __ffsll(z)) >= a.window) m1 &= ~(z & -z);
   }
-}
-
-__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(nthreads), "r"((uint32_t)p)
-      : "memory");
-  return r != 0;
+  if (c >= 64) {
+    bits[1] |= m0 << (c - 64);
+  } else if (c > 0) {
+    bits[0] |= m0 << c;
+    bits[1] |= m1 << c | m0 >> (64 - c);
+  } else {
+    bits[0] |= m0;
+    bits[1] |= m1;
+  }
 }
 
 // One lane of a converged warp, the same one each time.
@@ -222,6 +206,12 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// 16 bytes global -> shared without registers; `bytes` 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -231,6 +221,32 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// pairs of floats: one instruction for two products or sums
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
@@ -245,7 +261,7 @@ struct Cfg {
   static constexpr int kStageBytes = kTile * D * 2;   // one K or V tile
   static constexpr int kQBytes = KS > 1 ? 32768 : kTile * D * 2;  // a group's queries; with copies also their sums
   static constexpr int kStages = D == 128 ? 5 : (KS > 1 ? 10 : 12);  // 160 KB of keys and values, or more, in flight
-  static constexpr int kThreads = 384;                // two softmax groups, producer, MMA, two idle warps
+  static constexpr int kThreads = 384;                // two softmax groups, producer, MMA, two cleaning warps
   static constexpr int kMisc = 3072;
   static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMisc;
   static constexpr uint32_t kO = 2 * kTile;           // first O column; S buffers at 0 and 128
@@ -280,18 +296,23 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   uint8_t* s_ring = smem + 2 * C::kQBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(s_ring + ST * C::kStageBytes);
   uint64_t* empty = full + ST;
-  uint64_t* s_full = empty + ST;  // [S buffer] a tile's scores are in tensor memory
-  uint64_t* p_full = s_full + 2;  // [S buffer] its probabilities are
-  uint64_t* pv_done = p_full + 2; // [S buffer] its product with V has been added to O
-  uint64_t* q_full = pv_done + 2; // [group] the segment's queries are in shared memory
-  uint64_t* s_first = q_full + 2; // [group] scores of a segment's first tile
-  uint64_t* done = s_first + 2;
+  uint64_t* s_full = empty + ST;   // [S buffer] a tile's scores are in tensor memory
+  uint64_t* p_full = s_full + 2;   // [S buffer][half] its probabilities for keys 0..63, 64..127 are
+  uint64_t* pv_done = p_full + 4;  // [S buffer] its product with V has been added to O
+  uint64_t* q_full = pv_done + 2;  // [group] the segment's queries are in shared memory
+  uint64_t* s_first = q_full + 2;  // [group] scores of a segment's first tile
+  uint64_t* v_edge = s_first + 2;  // an edge tile is next to be cleaned
+  uint64_t* v_clean = v_edge + 1;  // it has been
+  uint64_t* seg_full = v_clean + 1;   // [4] a segment's record is there
+  uint64_t* seg_empty = seg_full + 4; // [4] every warp is through with it
+  uint64_t* join = seg_empty + 4;     // [group] its four warps meet (a barrier whose wait is bounded)
+  uint64_t* done = join + 2;
   long long* s_start = reinterpret_cast<long long*>(done + 1);  // request, units into it, units in the range
   unsigned long long* s_warp = reinterpret_cast<unsigned long long*>(s_start + 3);  // [threads / 32]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_warp + 12);
-  volatile uint32_t* s_lo = tmem_slot + 1;  // [S buffer] a byte per warp: P has a second part
-  int* s_maxpos = reinterpret_cast<int*>(tmem_slot + 3);  // [group]
-  int* s_dpos = s_maxpos + 2;  // [256] positions of the drafts, with a window ([group][128] where groups take turns)
+  volatile uint32_t* s_lo = tmem_slot + 1;     // [S buffer] a byte per warp: P has a second part
+  volatile uint32_t* s_dirty = tmem_slot + 3;  // [segment % 4] segment + 1 where a value was not finite
+  Seg* s_seg = reinterpret_cast<Seg*>(reinterpret_cast<uint8_t*>(full) + 1024);  // [segment % 4]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kProducer = 8, kMma = 9;
@@ -303,14 +324,21 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], KS == 1 ? 4 : 2);  // the warps that hold the half's keys
+      mbar_init(&p_full[2 * i + 1], KS == 1 ? 4 : 2);
       mbar_init(&pv_done[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], NT * 4);
+      mbar_init(&q_full[i], 4);
       mbar_init(&s_first[i], 1);
+      mbar_init(&join[i], 4);
     }
+    mbar_init(v_edge, 1);
+    mbar_init(v_clean, 2);
     mbar_init(done, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 11);  // MMA, eight softmax and two cleaning warps
+      s_dirty[i] = 0;
+    }
     fence_barrier_init();
     s_start[2] = 0;
   }
@@ -326,9 +354,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     unsigned long long mine = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
-      const Req r = load_req<ROWS>(a, b);
-      mine += r.units;
-      bad |= r.bad;
+      Req r;
+      const Load w = load_req<ROWS>(a, b, &r);
+      mine += w.units;
+      bad |= w.bad;
     }
     unsigned long long x = mine;
 #pragma unroll
@@ -351,30 +380,30 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     if (c < n) {
       // the threads whose requests hold the range's first and last unit
       const unsigned long long u0 = total * c / n, u1 = total * (c + 1) / n;
-      auto find = [&](unsigned long long u, unsigned long long* at, Req* r) {
-        *at = before;
-        int b = b0;
-        for (;; ++b) {
-          *r = load_req<ROWS>(a, b);
-          if (u < *at + r->units) return b;
-          *at += r->units;
+      Req r;
+      Load w;
+      unsigned long long at;
+      auto find = [&](unsigned long long u) {
+        at = before;
+        for (int b = b0;; ++b) {
+          w = load_req<ROWS>(a, b, &r);
+          if (u < at + w.units) return b;
+          at += w.units;
         }
       };
-      unsigned long long at;
-      Req r;
       if (u0 >= before && u0 < before + mine) {
-        s_start[0] = find(u0, &at, &r);
+        s_start[0] = find(u0);
         s_start[1] = (long long)(u0 - at);
         s_start[2] = (long long)(u1 - u0);
       }
       if (u1 - 1 >= before && u1 - 1 < before + mine) {
         // does the range's last segment start in it and end past it?  Then its last CTA is the
         // first one whose range ends at or after the segment's end
-        find(u1 - 1, &at, &r);
+        find(u1 - 1);
         const unsigned long long k = (u1 - 1 - at) / r.nt, start = at + k * r.nt, e = start + r.nt;
         int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
         if (start >= u0 && e > u1) {
-          const int h = (int)(k / r.groups), m = (int)(k % r.groups);
+          const int h = (int)(k / w.groups), m = (int)(k % w.groups);
           const int last = (int)((e * n + total - 1) / total) - 1;
           c0 = make_int4(last - (int)c + 1, r.t0, min(ROWS, r.n * a.G - m * ROWS), h);
           c1 = make_int4(m, 0, 0, 0);
@@ -394,8 +423,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   auto fewer = [] {
     if constexpr (KS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   };
-  Walk<ROWS> walk(a, (int)s_start[0], s_start[1], s_start[2]);
-  Seg s{};
+  // the record of segment `i`, once it is there; warps take the segments in order
+  auto seg_at = [&](uint32_t i) { return const_cast<const Seg*>(s_seg + (i & 3)); };
+  auto seg_wait = [&](uint32_t i) { return mbar_wait(&seg_full[i & 3], (i >> 2) & 1, st, 261); };
+  auto seg_done = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[i & 3]);
+  };
 
   if (warp == kProducer) {
     // ---------------- TMA producer: one lane per page (or 8 drafts) ----------------
@@ -404,6 +438,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a whole cached tile
     const int ppt = kTile / box;                  // pages per such tile
     uint32_t issued = 0;                          // copies issued
+    Seg s{};
     bool ok = true;
     // the lane's copies of tile i into ring position `at`: a whole tile page by page, a partial one and
     // the drafts 8 rows at a time; `id` is the block that holds the lane's cached rows
@@ -443,9 +478,21 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       if (lane * rows >= cached) return 0;
       return __ldg(a.table + (size_t)s.b * a.max_blocks + ((s.r.base(i) + lane * rows) >> a.bs_shift));
     };
-    uint32_t g = 0;
+    uint32_t g = 0, seg = 0;
+    Walk<ROWS> walk{a, (int)s_start[0], s_start[1], s_start[2]};
+    auto post = [&](const Seg& x) {
+      if (!mbar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, st, 262)) return false;
+      if (lane == 0) {
+        s_seg[seg & 3] = x;
+        mbar_arrive(&seg_full[seg & 3]);
+      }
+      __syncwarp();
+      ++seg;
+      return true;
+    };
     if constexpr (NT == 2) {
       while (ok && walk.next(&s)) {
+        if (!(ok = post(s))) break;
         int id = page(s.i0);
         for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
           const int id_next = i + 1 < s.i1 ? page(i + 1) : 0;
@@ -459,7 +506,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       Seg nx{};
       int i = 0, id = 0;  // the tile whose values are still to come
       while (ok && walk.next(&nx)) {
-        Seg old = s;
+        if (!(ok = post(nx))) break;
+        const Seg old = s;
         s = nx;
         int id_next = page(s.i0);
         for (int k = s.i0; k < s.i1 && ok; ++k, ++g) {
@@ -475,7 +523,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           id = id_k;
         }
       }
-      if (ok && g > 0) copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g - 1, n_tiles));
+      if (ok && g > 0) ok = copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g - 1, n_tiles));
+    }
+    if (ok) {
+      s.i0 = s.i1 = 0;
+      post(s);
     }
     // the last copies land before the CTA can finish (also after a wait that ran out)
     if (lane == 0)
@@ -508,113 +560,154 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         if (leader) tc_commit(bar);
         __syncwarp();
       };
-      auto pv = [&](int grp, uint32_t buf, uint32_t stage, bool first) {
+      // O += P V for 64 keys at a time, each half as soon as its probabilities are there
+      auto pv = [&](int grp, uint32_t buf, uint32_t stage, bool first, uint32_t parity) {
         const uint64_t v0 = vd + stage * (C::kStageBytes >> 4);
         const uint32_t p = tmem + buf * kTile, o = tmem + C::kO + grp * D;
-        const uint32_t lo = __shfl_sync(0xffffffffu, s_lo[buf], 0);
-        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk) {
-            const uint32_t acc = !(first && kk % (8 / KS) == 0);
-            if constexpr (KS == 1) {
-              tc_mma_bf16_ts(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc);
-            } else {  // a 16-key step goes to the lanes whose copy of the rows holds those keys
-              uint32_t off[4];
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!mbar_wait(&p_full[2 * buf + hf], parity, st, 233 + hf)) return false;
+          tc_fence_after();
+          const uint32_t lo = __shfl_sync(0xffffffffu, s_lo[buf], 0);
+          if (leader) {
 #pragma unroll
-              for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == kk * KS / 8 ? 0u : 0xffffffffu;
-              tc_mma_bf16_ts_lanes(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc, off);
+            for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
+              const uint32_t acc = !(first && kk % (8 / KS) == 0);
+              if constexpr (KS == 1) {
+                tc_mma_bf16_ts(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc);
+              } else {  // a 16-key step goes to the lanes whose copy of the rows holds those keys
+                uint32_t off[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == kk * KS / 8 ? 0u : 0xffffffffu;
+                tc_mma_bf16_ts_lanes(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc, off);
+              }
             }
-          }
-          if (lo) {  // the second part, for the warps that wrote one
+            constexpr int kParts = KS == 4 ? 2 : 1;  // copies whose keys lie in this half
 #pragma unroll
-            for (int c = 0; c < KS; ++c) {
+            for (int c = 0; c < kParts; ++c) {  // the second part, for the warps that wrote one
+              const int part = KS == 1 ? 0 : hf * kParts + c;
               uint32_t off[4], all = 0xffffffffu;
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
-                off[w] = w * KS / 4 == c && (lo >> (8 * w) & 1u) ? 0u : 0xffffffffu;
+                off[w] = w * KS / 4 == part && (lo >> (8 * w) & 1u) ? 0u : 0xffffffffu;
                 all &= off[w];
               }
               if (!all) {
 #pragma unroll
-                for (int kk = c * 8 / KS; kk < (c + 1) * 8 / KS; ++kk)
+                for (int kk = 4 * hf + c * (4 / kParts); kk < 4 * hf + (c + 1) * (4 / kParts); ++kk)
                   tc_mma_bf16_ts_lanes(o, p + kTile / 2 + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, 1u, off);
               }
             }
+            if (hf == 1) tc_commit(&pv_done[buf]);
           }
-          tc_commit(&pv_done[buf]);
+          __syncwarp();
         }
-        __syncwarp();
+        return true;
       };
       auto tile = [&](uint32_t at) {  // the tile at ring position `at` has landed
         if (!mbar_wait(&full[at % ST], (at / ST) & 1, st, 231)) return false;
         tc_fence_after();
         return true;
       };
+      // what this warp needs of a segment
+      struct Part {
+        int i0, i1, cut, full, rows;
+        __device__ __forceinline__ bool edge(int i) const { return i < cut || i >= full; }
+      };
+      Part s{}, nx{};
+      auto get = [&](uint32_t i, Part* p) {
+        if (!seg_wait(i)) return false;
+        const Seg* x = seg_at(i);
+        *p = Part{x->i0, x->i1, x->r.cut, x->r.full, x->rows};
+        seg_done(i);
+        return true;
+      };
+      uint32_t edges = 0;  // edge tiles that came back from the cleaning warps
+      auto clean = [&](const Part& p, int i) {  // hands tile i to the cleaning warps if it is an edge
+        if (p.edge(i) && leader) mbar_arrive(v_edge);
+        __syncwarp();
+      };
+      // tile i of s is clean; then it is the next tile's turn (one at a time, so that no phase is missed)
+      auto cleaned = [&](int i) {
+        if (s.edge(i) && !mbar_wait(v_clean, edges++ & 1, st, 236)) return false;
+        if (i + 1 < s.i1)
+          clean(s, i + 1);
+        else if (nx.i1 > 0)
+          clean(nx, nx.i0);
+        return true;
+      };
+      uint32_t g = 0, seg = 0;
+      ok = get(0, &s);
       if constexpr (NT == 1) {
-        uint32_t g = 0, seg = 0;
-        auto first_qk = [&](uint32_t sg, uint32_t gt) {  // scores of segment sg's first tile gt
+        auto first_qk = [&](uint32_t nr, uint32_t gt) {  // scores of segment nr's first tile gt
           const uint32_t at = k_pos<1>(gt);
-          if (!mbar_wait(&q_full[sg & 1], (sg >> 1) & 1, st, 232) || !tile(at)) return false;
+          if (!mbar_wait(&q_full[nr & 1], (nr >> 1) & 1, st, 232) || !tile(at)) return false;
           tc_fence_after();
-          qk(sg & 1, gt & 1, at % ST);
-          commit(&s_first[sg & 1]);
+          qk(nr & 1, gt & 1, at % ST);
+          commit(&s_first[nr & 1]);
           commit(&empty[at % ST]);
           return true;
         };
-        bool more = walk.next(&s);
-        if (more) ok = first_qk(0, 0);
-        while (ok && more) {
-          const int n = s.i1 - s.i0;
-          more = walk.next(&s);
-          for (int k = 0; k < n; ++k, ++g) {
-            if (k + 1 < n) {
+        if (ok && s.i1 > 0) {
+          clean(s, s.i0);
+          ok = first_qk(0, 0);
+        }
+        while (ok && s.i1 > 0) {
+          for (int i = s.i0; i < s.i1; ++i, ++g) {
+            if (i + 1 < s.i1) {
               const uint32_t at = k_pos<1>(g + 1);
               if (!(ok = tile(at))) break;
               qk(seg & 1, (g + 1) & 1, at % ST);
               commit(&empty[at % ST]);
-            } else if (more && !(ok = first_qk(seg + 1, g + 1))) {
+            } else if (!(ok = get(seg + 1, &nx)) || (nx.i1 > 0 && !(ok = first_qk(seg + 1, g + 1)))) {
               break;
             }
             const uint32_t at = v_pos<1>(g, n_tiles);
-            if (!(ok = tile(at)) || !(ok = mbar_wait(&p_full[g & 1], (g >> 1) & 1, st, 233))) break;
-            tc_fence_after();
-            pv(seg & 1, g & 1, at % ST, k == 0);
+            if (!(ok = tile(at)) || !(ok = cleaned(i))) break;
+            if (!(ok = pv(seg & 1, g & 1, at % ST, i == s.i0, (g >> 1) & 1))) break;
             commit(&empty[at % ST]);
           }
+          s = nx;
           ++seg;
         }
       } else {
-        uint32_t g = 0, seg = 0, g1 = 0;  // g1: tiles of row tile 1 so far
-        while (ok && walk.next(&s)) {
-          const int n = s.i1 - s.i0;
-          const bool two = s.rows > kTile;
-          uint32_t ka = k_pos<2>(g);
-          if (!(ok = mbar_wait(q_full, seg & 1, st, 232)) || !(ok = tile(ka))) break;
+        // queries of a segment's row tile, then its first scores; per group, the phases so far
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+        auto first_qk = [&](int grp, uint32_t at) {
+          if (!mbar_wait(&q_full[grp], nq[grp]++ & 1, st, 232) || !tile(at)) return false;
           tc_fence_after();
-          qk(0, 0, ka % ST);
-          if (two) qk(1, 1, ka % ST);
-          commit(&empty[ka % ST]);
-          for (int k = 0; k < n; ++k, ++g) {
-            const uint32_t va = v_pos<2>(g, n_tiles);
-            ka = k_pos<2>(g + 1);
-            if (!(ok = tile(va)) || !(ok = mbar_wait(&p_full[0], g & 1, st, 233))) break;
-            tc_fence_after();
-            pv(0, 0, va % ST, k == 0);
-            if (k + 1 < n) {
-              if (!(ok = tile(ka))) break;
-              qk(0, 0, ka % ST);
+          qk(grp, grp, at % ST);
+          return true;
+        };
+        if (ok && s.i1 > 0) {
+          clean(s, s.i0);
+          ok = first_qk(0, 0) && (s.rows <= kTile || first_qk(1, 0));
+          commit(&empty[0]);
+        }
+        while (ok && s.i1 > 0) {
+          for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
+            const uint32_t va = v_pos<2>(g, n_tiles), ka = k_pos<2>(g + 1);
+            const bool same = i + 1 < s.i1;
+            if (!(ok = tile(va)) || (!same && !(ok = get(seg + 1, &nx))) || !(ok = cleaned(i))) break;
+            const bool more = same || nx.i1 > 0;
+#pragma unroll
+            for (int grp = 0; grp < 2; ++grp) {
+              if (grp == 0 || s.rows > kTile) {
+                if (!(ok = pv(grp, grp, va % ST, i == s.i0, np[grp]++ & 1))) break;
+                if (grp == 1 || s.rows <= kTile) commit(&empty[va % ST]);
+              }
+              if (same) {
+                if (grp == 0 || s.rows > kTile) {
+                  if (!(ok = tile(ka))) break;
+                  qk(grp, grp, ka % ST);
+                }
+              } else if (more && (grp == 0 || nx.rows > kTile)) {
+                if (!(ok = first_qk(grp, ka))) break;
+              }
             }
-            if (two) {
-              if (!(ok = mbar_wait(&p_full[1], g1++ & 1, st, 234))) break;
-              tc_fence_after();
-              pv(1, 1, va % ST, k == 0);
-            }
-            commit(&empty[va % ST]);
-            if (k + 1 < n) {
-              if (two) qk(1, 1, ka % ST);
-              commit(&empty[ka % ST]);
-            }
+            if (ok && more) commit(&empty[ka % ST]);
           }
+          s = nx;
           ++seg;
         }
       }
@@ -631,96 +724,100 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_addr = tmem + lane_base + C::kO + grp * D;
     uint8_t* const q_buf = s_q + grp * C::kQBytes;
-    int* const dpos = s_dpos + (NT == 2 ? 0 : grp * 128);
-    int* const maxpos = s_maxpos + (NT == 2 ? 0 : grp);
-    const int bar_seg = NT == 2 ? 3 : 4 + grp;    // barrier of the segment's threads
     uint32_t seg = 0, g = 0, g_own = 0;           // segments and tiles of the CTA so far; tiles of this group
-    // After a wait that ran out the warp goes on without waiting: what it writes is void, but
-    // the barriers between the warps stay complete and the CTA ends.
+    // After a wait that ran out the warp goes on without waiting to the segment's end and leaves; what
+    // it writes is void.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
       if (ok) ok = mbar_wait(bar, parity, st, where);
       tc_fence_after();
     };
-    auto edge_tile = [&](int i) {  // the prefix's end, drafts, and where a window cuts
-      return i >= s.r.np || s.r.cached(i) < kTile || (a.window > 0 && s.r.base(i) < *maxpos - a.window + 1);
+    uint32_t meets = 0;
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&join[grp]);
+      wait(&join[grp], meets++ & 1, 246);
     };
-    for (; walk.next(&s); ++seg) {
-      const int n = s.i1 - s.i0;
-      if (NT == 1 && (int)(seg & 1) != grp) {
-        g += n;
-        continue;
-      }
-      const bool two = NT == 2 && s.rows > kTile;
-      const int group = two ? 256 : 128;  // threads that take part in this segment's edge tiles
-      RowView v;
-      v.valid = local < s.rows;
-      const int rr = s.m * C::kRows + local;
-      v.i = v.valid ? rr / a.G : 0;
-      const int qh = s.h * a.G + (rr - v.i * a.G), tok = s.r.t0 + v.i;
-      v.p = s.r.len + v.i;
-      const bool warp_live = __any_sync(0xffffffffu, v.valid);
-      bool dwindow = false;  // some pair of drafts may be a window apart
-      if (a.window > 0) {
-        if (v.valid && a.pos) v.p = max(__ldg(a.pos + tok), s.r.len);
-        named_bar(bar_seg, NT * 128);
-        for (int j = NT == 2 ? tid : row; j < s.r.n; j += NT * 128)
-          dpos[j] = a.pos ? max(__ldg(a.pos + s.r.t0 + j), s.r.len) : s.r.len + j;
-        if (row == 0) *maxpos = 0;
-        named_bar(bar_seg, NT * 128);
-        const int top = __reduce_max_sync(0xffffffffu, v.valid ? v.p : 0);
-        if (lane == 0) atomicMax(maxpos, top);
-        named_bar(bar_seg, NT * 128);
-        dwindow = *maxpos - s.r.len >= a.window;
-      }
-      // queries: the thread's row, 16 bytes at a time, in the swizzled K-major layout
-      if (warp_live) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)tok * a.qs + (size_t)qh * D);
-        uint8_t* dst = q_buf + row * 128;
-        uint4 w[D / 8];
+    // the thread's row of a segment's queries, in the swizzled K-major layout; rows past the last are zero
+    auto load_q = [&](const Seg* sg) {
+      const int r2 = sg->m * C::kRows + local;
+      const bool valid = local < sg->rows;
+      const int i = valid ? r2 / a.G : 0, h = valid ? sg->h * a.G + r2 - i * a.G : 0;
+      const uint16_t* src = a.q + (size_t)(sg->r.t0 + i) * a.qs + (size_t)h * D;
+      const uint32_t dst = smem_u32(q_buf) + row * 128;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = v.valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4)) = w[c];
-      }
+      for (int c = 0; c < D / 8; ++c)
+        cp_async16(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), src + c * 8, valid ? 16 : 0);
+    };
+    auto q_loaded = [&] {
+      cp_async_wait();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[NT == 2 ? 0 : grp]);
-      if (NT == 2 && grp == 1 && !two) {
-        // no rows here: only keep in step with the segments
-        wait(q_full, seg & 1, 241);
+      if (lane == 0) mbar_arrive(&q_full[grp]);
+    };
+    bool early = false;  // the segment's queries were loaded during the one before
+    for (;; ++seg) {
+      if (ok) ok = seg_wait(seg);
+      const Seg* const s = seg_at(seg);
+      const int i0 = s->i0, n = s->i1 - i0;
+      if (!ok || n == 0) break;
+      if (NT == 1 ? (int)(seg & 1) != grp : (grp == 1 && s->rows <= kTile)) {  // not this group's
+        seg_done(seg);
         g += n;
         continue;
       }
-      float m_ref = -INFINITY, l = 0.f;
-      bool dirty = false;
+      const int cut = s->r.cut, full_from = s->r.full;
+      const bool valid = local < s->rows;
+      const bool warp_live = __any_sync(0xffffffffu, valid);
+      if (!early) {
+        load_q(s);
+        q_loaded();
+      }
+      early = false;
+      auto draft = [&] { return valid ? (s->m * C::kRows + local) / a.G : 0; };  // the row's draft, its position
+      auto at_pos = [&](int vi) { return a.window > 0 ? draft_pos(a, s->r.t0, s->r.n, s->r.len, vi) : 0; };
+      // m_ref: the maximum that P refers to; l: the row's sum.  A tile whose maximum stays below
+      // `limit` takes the plain path: no rescaling of O, one part of P.
+      float m_ref = -INFINITY, l = 0.f, limit = valid ? -INFINITY : INFINITY;
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
-        const int i = s.i0 + k;
+        const int i = i0 + k;
         const uint32_t gt = g + k, go = g_own + k;
         const uint32_t buf = NT == 1 ? gt & 1 : grp;
         if (NT == 1 && k == 0)
           wait(&s_first[grp], (seg >> 1) & 1, 240);  // s_full may be phases behind until then
         else
           wait(&s_full[buf], NT == 1 ? (gt >> 1) & 1 : go & 1, 242);
-        const bool edge = edge_tile(i);
+        if (NT == 2 && k == n - 1 && mbar_test_wait(&seg_full[(seg + 1) & 3], ((seg + 1) >> 2) & 1)) {
+          // every product with these queries is done: the next segment's may come in
+          const Seg* nx = seg_at(seg + 1);
+          early = nx->i1 > 0 && (grp == 0 || nx->rows > kTile);
+          if (early) load_q(nx);
+        }
         const uint32_t s_addr = tmem + lane_base + buf * kTile;
+        auto p_ready = [&](int half) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * buf + half]);
+        };
         bool lo = false;
         if (warp_live) {
-          if (edge) {
+          if (i < cut || i >= full_from) {
             // unseen keys' scores become -infinity, in place
+            uint64_t bits[2];
+            const int vi = draft();
+            edge_bits(a, s, i, vi, at_pos(vi), bits);
 #pragma unroll 1
             for (int c = 0; c < CW / 32; ++c) {
-              const uint32_t addr = s_addr + part * CW + c * 32;
-              const uint32_t bits = tile_word(a, s, i, part * (CW / 32) + c, v, dpos, dwindow);
+              const int w = part * (CW / 32) + c;
+              const uint32_t x = valid ? (uint32_t)((w & 2 ? bits[1] : bits[0]) >> (32 * (w & 1))) : 0u;
               uint32_t y[32];
-              tmem_ld32(addr, y);
+              tmem_ld32(s_addr + w * 32, y);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1u)) y[j] = 0xff800000u;
-              tmem_st32(addr, y);
+                if (!(x >> j & 1u)) y[j] = 0xff800000u;
+              tmem_st32(s_addr + w * 32, y);
             }
             tmem_st_wait();
           }
@@ -734,117 +831,105 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           load();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < CW; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
-          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-          const bool grow = m_new > m_ref + 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(m_ref - m_new) : 1.f;
-            if (k > 0) {
-              wait(&pv_done[NT == 1 ? (gt - 1) & 1 : grp], NT == 1 ? ((gt - 1) >> 1) & 1 : (go - 1) & 1, 243);
+          for (int j = 0; j < CW; j += 2)
+            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
+          const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
+          float mu = m_ref == -INFINITY ? 0.f : m_ref, sc = a.scale_log2;
+          if (__any_sync(0xffffffffu, m_new > limit)) {
+            const bool grow = m_new > m_ref + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float f = grow ? ex2(m_ref - m_new) : 1.f;
+              if (k > 0) {
+                wait(&pv_done[NT == 1 ? (gt - 1) & 1 : grp], NT == 1 ? ((gt - 1) >> 1) & 1 : (go - 1) & 1, 243);
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld16(o_addr + c * 16, o);
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(o_addr + c * 16, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                  tmem_st16(o_addr + c * 16, o);
+                }
+                l *= f;
+              }
+              if (grow) m_ref = m_new;
+            }
+            mu = m_ref == -INFINITY ? 0.f : m_ref;
+            // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
+            // holds over 1/16 of the row's sum so far that would show in the output next to its own
+            // rounding, so the remainder goes along as a second part; with more keys in play it
+            // averages out.  After a prefix's first tiles this is rare.
+            lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > l * 0.0625f);
+            // p = 2^(scale s - mu) in one fused step, whose error against the rounded mu is common to
+            // the row.  Past 2^24 that error alone could overflow: there scale s is rounded first too.
+            if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.f)) {
+#pragma unroll 1
+              for (int c = 0; c < CW / 16; ++c) {
+                uint32_t y[16];
+                tmem_ld16(s_addr + part * CW + c * 16, y);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(o_addr + c * 16, o);
+                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * sc);
+                tmem_st16(s_addr + part * CW + c * 16, y);
               }
-              l *= f;
+              tmem_st_wait();
+              load();
+              sc = 1.f;
             }
-            if (grow) m_ref = m_new;
           }
-          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-          // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
-          // holds over 1/16 of the row's sum so far that would show in the output next to its own
-          // rounding, so the remainder goes along as a second part; with more keys in play it
-          // averages out.  After a prefix's first tiles this is rare.
-          lo = __any_sync(0xffffffffu, v.valid && ex2(m_new - mu) > l * 0.0625f);
-          // p = 2^(scale s - mu) in one fused step, whose error against the rounded mu is common to
-          // the row.  Past 2^24 that error alone could overflow: there scale s is rounded first too.
-          float sc = a.scale_log2;
-          if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.f)) {
-#pragma unroll 1
-            for (int c = 0; c < CW / 16; ++c) {
-              uint32_t y[16];
-              tmem_ld16(s_addr + part * CW + c * 16, y);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * sc);
-              tmem_st16(s_addr + part * CW + c * 16, y);
-            }
-            tmem_st_wait();
-            load();
-            sc = 1.f;
-          }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
+          uint64_t sum[2] = {0, 0};
+          const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
           auto exps = [&](bool two_parts) {
 #pragma unroll
             for (int c = 0; c < CW / 32; ++c) {
               uint32_t p[16], p2[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float e0 = ex2(fmaf(__uint_as_float(sv[c * 32 + 2 * j]), sc, -mu));
-                const float e1 = ex2(fmaf(__uint_as_float(sv[c * 32 + 2 * j + 1]), sc, -mu));
-                sum[(2 * j) & 3] += e0;
-                sum[(2 * j + 1) & 3] += e1;
+                float e0, e1;
+                unpair(fma2(pair(__uint_as_float(sv[c * 32 + 2 * j]), __uint_as_float(sv[c * 32 + 2 * j + 1])), sc2, mu2),
+                       e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
                 p[j] = pack_bf16(e0, e1);
                 if (two_parts)
                   p2[j] = pack_bf16(e0 - __uint_as_float(p[j] << 16), e1 - __uint_as_float(p[j] & 0xffff0000u));
               }
               tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
               if (two_parts) tmem_st16(s_addr + kTile / 2 + part * (CW / 2) + c * 16, p2);
+              if (KS == 1 && c == 1) {  // the first half's product can start
+                tmem_st_wait();
+                p_ready(0);
+              }
             }
           };
           if (lo)
             exps(true);
           else
             exps(false);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
+          p_ready(KS == 1 || part >= KS / 2 ? 1 : 0);
+          float s0, s1;
+          unpair(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          // below: no growth past 2^8, and no key over 1/16 of the sum
+          if (valid) limit = fabsf(m_ref) <= 16777216.f ? m_ref + fminf(8.f, __log2f(l) - 4.f) : -INFINITY;
+        } else {
+          if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
+          if (KS == 1) p_ready(0);
+          p_ready(KS == 1 || part >= KS / 2 ? 1 : 0);
         }
-        if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
-        if (edge) {
-          // values that no row sees become zero, and those that are not finite too (0 * NaN would
-          // reach every row): they are added back to the rows that see them at the end
-          const uint32_t at = v_pos<NT>(gt, n_tiles);
-          wait(&full[at % ST], (at / ST) & 1, 244);
-          uint8_t* vt = s_ring + (at % ST) * C::kStageBytes;
-          const int hi = s.r.cached(i), c0 = s.r.col(i), c1 = c0 + s.r.drafts(i);
-          const int first = a.window > 0 ? s.r.len - a.window + 1 - s.r.base(i) : 0;
-          bool found = false;
-          for (int c = two ? tid : row; c < kTile * HALVES * 8; c += group) {
-            const int key = (c >> 3) & (kTile - 1);
-            uint4* w = reinterpret_cast<uint4*>(vt + (c << 4));
-            if (!((key >= first && key < hi) || (key >= c0 && key < c1))) {
-              *w = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint4 y = *w;
-            uint32_t* e = &y.x;
-            bool change = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u, change = true;
-              if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0xffffu, change = true;
-            }
-            if (change) {
-              *w = y;
-              found = true;
-            }
-          }
-          fence_proxy_async_smem();
-          dirty |= named_bar_or(two ? 6 : 1 + grp, group, found);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
+        if (NT == 2 && k == n - 1 && early) q_loaded();
       }
       // ---- the segment's end: finished rows to out, cut ones to the partial sums ----
       const uint32_t ge = NT == 1 ? g + n - 1 : g_own + n - 1;  // the segment's last tile
       wait(&pv_done[NT == 1 ? ge & 1 : grp], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
-      const bool whole = s.i0 == 0 && s.i1 == s.r.nt;
-      const size_t prow = (size_t)(2 * blockIdx.x + (s.i0 == 0)) * C::kRows + local;
+      const bool whole = i0 == 0 && n == s->r.nt;
+      const int vi = draft(), vp = at_pos(vi);
+      const int qh = s->h * a.G + (valid ? s->m * C::kRows + local - vi * a.G : 0), tok = s->r.t0 + vi;
+      const bool dirty = s_dirty[seg & 3] == seg + 1;
+      const size_t prow = (size_t)(2 * blockIdx.x + (i0 == 0)) * C::kRows + local;
       // 16 columns of this thread's row of O
       auto sums = [&](int col, float (&y)[16]) {
         uint32_t o[16];
@@ -852,21 +937,36 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(o[j]);
-        if (dirty && v.valid) {
-          float z[16];
+        if (dirty && valid) {
+          // values that are not finite, of the keys that this row sees: the cleaning warps took them out
+          for (int i = i0; i < i0 + n; ++i) {
+            if (!s->r.edge(i)) continue;
+            uint64_t bits[2];
+            edge_bits(a, s, i, vi, vp, bits);
+#pragma unroll 1
+            for (int j = part * CW; j < part * CW + CW; ++j) {
+              if (!((j >= 64 ? bits[1] : bits[0]) >> (j & 63) & 1ull)) continue;
+              const uint16_t* val;
+              if (j < s->r.cached(i)) {
+                const int p = s->r.base(i) + j;
+                const int id = __ldg(a.table + (size_t)s->b * a.max_blocks + (p >> a.bs_shift));
+                if (id < 0 || id >= a.n_blocks) continue;
+                val = a.v_cache + (size_t)id * a.block_stride + (size_t)s->h * a.head_stride +
+                      (size_t)(p & ((1 << a.bs_shift) - 1)) * a.slot_stride;
+              } else {
+                val = a.v_new + (size_t)(s->r.t0 + s->r.d0(i) + j - s->r.col(i)) * a.vs + s->h * D;
+              }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) z[j] = y[j];
-          for (int i = s.i0; i < s.i1; ++i)
-            if (edge_tile(i))
-              for (int w = 0; w < CW / 32; ++w)
-                add_not_finite(a, s, i, part * (CW / 32) + w,
-                               tile_word(a, s, i, part * (CW / 32) + w, v, dpos, dwindow), col, D, z);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = z[j];
+              for (int d = 0; d < 16; ++d) {
+                const uint32_t x = val[col + d];
+                if ((x & 0x7f80u) == 0x7f80u) y[d] += bf16_bits_to_f32(x);
+              }
+            }
+          }
         }
       };
       auto put = [&](int col, const float (&y)[16], float inv) {
-        if (!v.valid) return;
+        if (!valid) return;
         if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + col);
           uint32_t w[8];
@@ -897,7 +997,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         constexpr int RP = kTile / KS, P = C::kPass, OWN = C::kOwn;
         float2* ml = reinterpret_cast<float2*>(q_buf);
         ml[row] = make_float2(m_ref, l);
-        named_bar(1 + grp, 128);
+        meet();
         float M = -INFINITY;
 #pragma unroll
         for (int p = 0; p < KS; ++p) M = fmaxf(M, ml[p * RP + local].x);
@@ -910,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           l += y.y * ex2(y.x - mu);
         }
         m_ref = M;
-        named_bar(1 + grp, 128);
+        meet();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         auto piece = [&](int owner, int from, int j) {
           const int x = P == 16 ? (local >> 1) & 3 : local & 7;
@@ -919,7 +1019,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         };
 #pragma unroll 1
         for (int q = 0; q < OWN; q += P) {
-          if (q > 0) named_bar(1 + grp, 128);
+          if (q > 0) meet();
           if (warp_live) {
 #pragma unroll 1
             for (int d = 1; d < KS; ++d) {
@@ -935,7 +1035,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               }
             }
           }
-          named_bar(1 + grp, 128);
+          meet();
           if (warp_live) {
 #pragma unroll 1
             for (int c = 0; c < P; c += 16) {
@@ -959,19 +1059,67 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             }
           }
         }
-        named_bar(1 + grp, 128);  // the next queries overwrite the buffer
+        meet();  // the next queries overwrite the buffer
       }
-      if (v.valid && part == 0) {
+      if (valid && part == 0) {
         if (!whole)
           a.part_ml[prow] = make_float2(m_ref, l);
         else if (a.lse)
           a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       }
+      seg_done(seg);
       g += n;
       g_own += n;
     }
   } else {
+    // ---------------- cleaning: two warps, the value tiles at an edge ----------------
+    // Values that no row sees become zero, and those that are not finite too (0 * NaN would
+    // reach every row): they are added back to the rows that see them at the segment's end.
     fewer();
+    uint32_t g = 0, edges = 0;
+    bool ok = true;
+    for (uint32_t seg = 0;; ++seg) {
+      if (!(ok = seg_wait(seg))) break;
+      const Seg s = *seg_at(seg);
+      seg_done(seg);
+      if (s.i1 == 0) break;
+      for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
+        if (!s.r.edge(i)) continue;
+        if (!(ok = mbar_wait(v_edge, edges++ & 1, st, 251))) break;
+        const uint32_t at = v_pos<NT>(g, n_tiles);
+        if (!(ok = mbar_wait(&full[at % ST], (at / ST) & 1, st, 252))) break;
+        uint8_t* vt = s_ring + (at % ST) * C::kStageBytes;
+        const int hi = s.r.cached(i), c0 = s.r.col(i), c1 = c0 + s.r.drafts(i);
+        const int first = a.window > 0 ? s.r.len - a.window + 1 - s.r.base(i) : 0;
+        bool found = false;
+#pragma unroll 4
+        for (int c = tid - 320; c < kTile * HALVES * 8; c += 64) {
+          const int key = (c >> 3) & (kTile - 1);
+          uint4* w = reinterpret_cast<uint4*>(vt + (c << 4));
+          if (!((key >= first && key < hi) || (key >= c0 && key < c1))) {
+            *w = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+          }
+          uint4 y = *w;
+          uint32_t* e = &y.x;
+          bool change = false;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u, change = true;
+            if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0xffffu, change = true;
+          }
+          if (change) {
+            *w = y;
+            found = true;
+          }
+        }
+        if (found) s_dirty[seg & 3] = seg + 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_clean);
+      }
+      if (!ok) break;
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -32,7 +32,8 @@ def attention(q, k_new, v_new, k, v, offsets, lens, table, mask, pos, window, sc
         at = np.arange(ln)
         blk = table[b][at // bs] if ln else np.zeros(0, int)
         pk, pv = k[blk, :, at % bs], v[blk, :, at % bs]
-        dpos = np.array([max(pos[t], ln) if pos is not None else ln + t - t0 for t in range(t0, t1)])
+        dpos = np.array([min(max(pos[t], ln), ln + t1 - t0 - 1) if pos is not None else ln + t - t0
+                         for t in range(t0, t1)])
         for t in range(t0, t1):
             p = dpos[t - t0]
             see = np.ones(ln, bool) if not window else p - at < window

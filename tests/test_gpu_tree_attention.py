@@ -172,6 +172,13 @@ def test_positions_below_the_prefix_count_as_its_end(lm):
     c.check(lm)
 
 
+@pytest.mark.parametrize("far", [3, 1000, 2**31 - 1])
+def test_positions_past_any_tree_count_as_its_deepest_place(lm, far):
+    c = Case([200, 40, 3], [6, 6, 9], window=30, seed=2)
+    c.pos[::3] = np.minimum(c.pos[::3].astype(np.int64) + far, 2**31 - 1).astype(np.int32)
+    c.check(lm)
+
+
 @pytest.mark.parametrize("mask", ["any", "none"])
 def test_masks_that_leave_rows_empty(lm, mask):
     # no prefix and no visible draft: zeros and an lse of -infinity, next to rows that do see something
