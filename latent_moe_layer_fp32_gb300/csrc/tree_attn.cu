@@ -541,6 +541,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
       constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
       bool ok = true;
+      // every wait of this warp is on the critical path: the blocking probe first
+      auto ready = [&](uint64_t* bar, uint32_t parity, int where) {
+        return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, st, where);
+      };
       // descriptors step by their start address (bits 0 to 13, in units of 16 bytes)
       const uint64_t qd = smem_desc_sw128(smem_u32(s_q)), kd = smem_desc_sw128(smem_u32(s_ring));
       const uint64_t vd = smem_desc_sw128_mn(smem_u32(s_ring), kTile * 128);
@@ -566,9 +570,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const uint32_t p = tmem + buf * kTile, o = tmem + C::kO + grp * D;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (!mbar_wait(&p_full[2 * buf + hf], parity, st, 233 + hf)) return false;
+          if (!ready(&p_full[2 * buf + hf], parity, 233 + hf)) return false;
           tc_fence_after();
-          const uint32_t lo = __shfl_sync(0xffffffffu, s_lo[buf], 0);
+          const uint32_t lo = s_lo[buf];
           if (leader) {
 #pragma unroll
             for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
@@ -604,9 +608,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
         return true;
       };
-      auto tile = [&](uint32_t at) {  // the tile at ring position `at` has landed
-        if (!mbar_wait(&full[at % ST], (at / ST) & 1, st, 231)) return false;
+      uint32_t ring = 0, ring_phase = 0;
+      auto tile = [&](uint32_t* stage) {  // the next tile of the ring has landed (they are taken in its order)
+        if (!ready(&full[ring], ring_phase, 231)) return false;
         tc_fence_after();
+        *stage = ring;
+        if (++ring == ST) {
+          ring = 0;
+          ring_phase ^= 1;
+        }
         return true;
       };
       // what this warp needs of a segment
@@ -638,14 +648,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       };
       uint32_t g = 0, seg = 0;
       ok = get(0, &s);
+      uint32_t ks = 0, vs = 0;  // stages of the keys and values in use
       if constexpr (NT == 1) {
         auto first_qk = [&](uint32_t nr, uint32_t gt) {  // scores of segment nr's first tile gt
-          const uint32_t at = k_pos<1>(gt);
-          if (!mbar_wait(&q_full[nr & 1], (nr >> 1) & 1, st, 232) || !tile(at)) return false;
-          tc_fence_after();
-          qk(nr & 1, gt & 1, at % ST);
+          if (!ready(&q_full[nr & 1], (nr >> 1) & 1, 232) || !tile(&ks)) return false;
+          qk(nr & 1, gt & 1, ks);
           commit(&s_first[nr & 1]);
-          commit(&empty[at % ST]);
+          commit(&empty[ks]);
           return true;
         };
         if (ok && s.i1 > 0) {
@@ -655,17 +664,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         while (ok && s.i1 > 0) {
           for (int i = s.i0; i < s.i1; ++i, ++g) {
             if (i + 1 < s.i1) {
-              const uint32_t at = k_pos<1>(g + 1);
-              if (!(ok = tile(at))) break;
-              qk(seg & 1, (g + 1) & 1, at % ST);
-              commit(&empty[at % ST]);
+              if (!(ok = tile(&ks))) break;
+              qk(seg & 1, (g + 1) & 1, ks);
+              commit(&empty[ks]);
             } else if (!(ok = get(seg + 1, &nx)) || (nx.i1 > 0 && !(ok = first_qk(seg + 1, g + 1)))) {
               break;
             }
-            const uint32_t at = v_pos<1>(g, n_tiles);
-            if (!(ok = tile(at)) || !(ok = cleaned(i))) break;
-            if (!(ok = pv(seg & 1, g & 1, at % ST, i == s.i0, (g >> 1) & 1))) break;
-            commit(&empty[at % ST]);
+            if (!(ok = tile(&vs)) || !(ok = cleaned(i))) break;
+            if (!(ok = pv(seg & 1, g & 1, vs, i == s.i0, (g >> 1) & 1))) break;
+            commit(&empty[vs]);
           }
           s = nx;
           ++seg;
@@ -673,39 +680,37 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       } else {
         // queries of a segment's row tile, then its first scores; per group, the phases so far
         uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-        auto first_qk = [&](int grp, uint32_t at) {
-          if (!mbar_wait(&q_full[grp], nq[grp]++ & 1, st, 232) || !tile(at)) return false;
+        auto first_qk = [&](int grp) {
+          if (!ready(&q_full[grp], nq[grp]++ & 1, 232) || (grp == 0 && !tile(&ks))) return false;
           tc_fence_after();
-          qk(grp, grp, at % ST);
+          qk(grp, grp, ks);
           return true;
         };
         if (ok && s.i1 > 0) {
           clean(s, s.i0);
-          ok = first_qk(0, 0) && (s.rows <= kTile || first_qk(1, 0));
-          commit(&empty[0]);
+          ok = first_qk(0) && (s.rows <= kTile || first_qk(1));
+          commit(&empty[ks]);
         }
         while (ok && s.i1 > 0) {
+          const bool two = s.rows > kTile;
           for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
-            const uint32_t va = v_pos<2>(g, n_tiles), ka = k_pos<2>(g + 1);
             const bool same = i + 1 < s.i1;
-            if (!(ok = tile(va)) || (!same && !(ok = get(seg + 1, &nx))) || !(ok = cleaned(i))) break;
+            if (!(ok = tile(&vs)) || (!same && !(ok = get(seg + 1, &nx))) || !(ok = cleaned(i))) break;
             const bool more = same || nx.i1 > 0;
 #pragma unroll
             for (int grp = 0; grp < 2; ++grp) {
-              if (grp == 0 || s.rows > kTile) {
-                if (!(ok = pv(grp, grp, va % ST, i == s.i0, np[grp]++ & 1))) break;
-                if (grp == 1 || s.rows <= kTile) commit(&empty[va % ST]);
+              if (grp == 0 || two) {
+                if (!(ok = pv(grp, grp, vs, i == s.i0, np[grp]++ & 1))) break;
+                if (grp == 1 || !two) commit(&empty[vs]);
               }
               if (same) {
-                if (grp == 0 || s.rows > kTile) {
-                  if (!(ok = tile(ka))) break;
-                  qk(grp, grp, ka % ST);
-                }
+                if (grp == 0 && !(ok = tile(&ks))) break;
+                if (grp == 0 || two) qk(grp, grp, ks);
               } else if (more && (grp == 0 || nx.rows > kTile)) {
-                if (!(ok = first_qk(grp, ka))) break;
+                if (!(ok = first_qk(grp))) break;
               }
             }
-            if (ok && more) commit(&empty[ka % ST]);
+            if (ok && more) commit(&empty[ks]);
           }
           s = nx;
           ++seg;
@@ -800,7 +805,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[2 * buf + half]);
         };
-        bool lo = false;
         if (warp_live) {
           if (i < cut || i >= full_from) {
             // unseen keys' scores become -infinity, in place
@@ -835,7 +839,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
           const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
           float mu = m_ref == -INFINITY ? 0.f : m_ref, sc = a.scale_log2;
-          if (__any_sync(0xffffffffu, m_new > limit)) {
+          const bool plain = !__any_sync(0xffffffffu, m_new > limit);
+          if (!plain) {
             const bool grow = m_new > m_ref + 8.f;
             if (__any_sync(0xffffffffu, grow)) {
               const float f = grow ? ex2(m_ref - m_new) : 1.f;
@@ -855,11 +860,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               if (grow) m_ref = m_new;
             }
             mu = m_ref == -INFINITY ? 0.f : m_ref;
-            // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
-            // holds over 1/16 of the row's sum so far that would show in the output next to its own
-            // rounding, so the remainder goes along as a second part; with more keys in play it
-            // averages out.  After a prefix's first tiles this is rare.
-            lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > l * 0.0625f);
             // p = 2^(scale s - mu) in one fused step, whose error against the rounded mu is common to
             // the row.  Past 2^24 that error alone could overflow: there scale s is rounded first too.
             if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.f)) {
@@ -877,44 +877,59 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               sc = 1.f;
             }
           }
-          if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
           uint64_t sum[2] = {0, 0};
           const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
-          auto exps = [&](bool two_parts) {
 #pragma unroll
-            for (int c = 0; c < CW / 32; ++c) {
-              uint32_t p[16], p2[16];
+          for (int c = 0; c < CW / 32; ++c) {
+            uint32_t p[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float e0, e1;
-                unpair(fma2(pair(__uint_as_float(sv[c * 32 + 2 * j]), __uint_as_float(sv[c * 32 + 2 * j + 1])), sc2, mu2),
-                       e0, e1);
-                e0 = ex2(e0);
-                e1 = ex2(e1);
-                sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
-                p[j] = pack_bf16(e0, e1);
-                if (two_parts)
-                  p2[j] = pack_bf16(e0 - __uint_as_float(p[j] << 16), e1 - __uint_as_float(p[j] & 0xffff0000u));
-              }
-              tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
-              if (two_parts) tmem_st16(s_addr + kTile / 2 + part * (CW / 2) + c * 16, p2);
-              if (KS == 1 && c == 1) {  // the first half's product can start
-                tmem_st_wait();
-                p_ready(0);
-              }
+            for (int j = 0; j < 16; ++j) {
+              const int x = c * 32 + 2 * j;
+              float e0, e1;
+              unpair(fma2(pair(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), sc2, mu2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+              p[j] = pack_bf16(e0, e1);
+              sv[x] = __float_as_uint(e0);
+              sv[x + 1] = __float_as_uint(e1);
             }
-          };
-          if (lo)
-            exps(true);
-          else
-            exps(false);
-          tmem_st_wait();
-          p_ready(KS == 1 || part >= KS / 2 ? 1 : 0);
+            tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
+            if (KS == 1 && c == 1 && plain) {  // the first half's product can start
+              if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
+              tmem_st_wait();
+              p_ready(0);
+            }
+          }
           float s0, s1;
           unpair(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-          // below: no growth past 2^8, and no key over 1/16 of the sum
-          if (valid) limit = fabsf(m_ref) <= 16777216.f ? m_ref + fminf(8.f, __log2f(l) - 4.f) : -INFINITY;
+          if (!plain || KS > 1) {
+            // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
+            // holds over 1/8 of the row's sum so far that would show in the output next to its own
+            // rounding, so the remainder goes along as a second part; with more keys in play it
+            // averages out.  After a prefix's first tiles this is rare.
+            const bool lo = !plain && __any_sync(0xffffffffu, valid && ex2(m_new - mu) > l * 0.125f);
+            if (lo) {
+#pragma unroll
+              for (int c = 0; c < CW / 32; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float e0 = __uint_as_float(sv[c * 32 + 2 * j]), e1 = __uint_as_float(sv[c * 32 + 2 * j + 1]);
+                  const uint32_t hi = pack_bf16(e0, e1);
+                  p[j] = pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
+                }
+                tmem_st16(s_addr + kTile / 2 + part * (CW / 2) + c * 16, p);
+              }
+            }
+            if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
+          }
+          tmem_st_wait();
+          if (KS == 1 && !plain) p_ready(0);
+          p_ready(KS == 1 || part >= KS / 2 ? 1 : 0);
+          // below: no growth past 2^8, and no key over 1/8 of the sum
+          if (valid) limit = fabsf(m_ref) <= 16777216.f ? m_ref + fminf(8.f, __log2f(l) - 3.f) : -INFINITY;
         } else {
           if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
           if (KS == 1) p_ready(0);
