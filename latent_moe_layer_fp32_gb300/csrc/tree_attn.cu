@@ -79,6 +79,11 @@ struct Req {
   __device__ __forceinline__ bool edge(int i) const { return i < cut || i >= full; }
 };
 
+// 64-bit division is a long subroutine; nearly always 32 bits will do.
+__device__ __forceinline__ unsigned long long quot(unsigned long long x, unsigned long long y) {
+  return (x | y) >> 32 ? x / y : (unsigned)x / (unsigned)y;
+}
+
 struct Load {
   int groups;  // row groups
   bool bad;
@@ -134,9 +139,9 @@ struct Walk {
       off -= w.units;
       ++b;
     }
-    const long long k = off / s->r.nt;
+    const long long k = (long long)quot(off, s->r.nt);
     s->b = b;
-    s->h = (int)(k / w.groups);
+    s->h = (int)quot(k, w.groups);
     s->m = (int)(k - (long long)s->h * w.groups);
     s->i0 = (int)(off - k * s->r.nt);
     s->i1 = (int)min((long long)s->r.nt, s->i0 + left);
@@ -261,7 +266,7 @@ struct Cfg {
   static constexpr int kStageBytes = kTile * D * 2;   // one K or V tile
   static constexpr int kQBytes = KS > 1 ? 32768 : kTile * D * 2;  // a group's queries; with copies also their sums
   static constexpr int kStages = D == 128 ? 5 : (KS > 1 ? 10 : 12);  // 160 KB of keys and values, or more, in flight
-  static constexpr int kThreads = 384;                // two softmax groups, producer, MMA, two cleaning warps
+  static constexpr int kThreads = 384;                // two softmax groups, two producers, MMA, cleaning warp
   static constexpr int kMisc = 3072;
   static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMisc;
   static constexpr uint32_t kO = 2 * kTile;           // first O column; S buffers at 0 and 128
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   Seg* s_seg = reinterpret_cast<Seg*>(reinterpret_cast<uint8_t*>(full) + 1024);  // [segment % 4]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = 8, kMma = 9;
+  constexpr int kKeys = 8, kMma = 9, kValues = 10;  // warps 0 to 7: softmax; 11: cleaning
   Status* st = a.err + blockIdx.x;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -332,11 +337,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       mbar_init(&join[i], 4);
     }
     mbar_init(v_edge, 1);
-    mbar_init(v_clean, 2);
+    mbar_init(v_clean, 1);
     mbar_init(done, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 11);  // MMA, eight softmax and two cleaning warps
+      mbar_init(&seg_empty[i], 11);  // values' producer, MMA, eight softmax warps, cleaning warp
       s_dirty[i] = 0;
     }
     fence_barrier_init();
@@ -353,11 +358,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     unsigned long long mine = 0;
     bool bad = false;
+    Req r0{};
+    Load w0{};
     for (int b = b0; b < b1; ++b) {
       Req r;
       const Load w = load_req<ROWS>(a, b, &r);
       mine += w.units;
       bad |= w.bad;
+      if (b == b0) r0 = r, w0 = w;
     }
     unsigned long long x = mine;
 #pragma unroll
@@ -379,17 +387,21 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const unsigned long long c = blockIdx.x;
     if (c < n) {
       // the threads whose requests hold the range's first and last unit
-      const unsigned long long u0 = total * c / n, u1 = total * (c + 1) / n;
-      Req r;
-      Load w;
-      unsigned long long at;
+      const unsigned long long u0 = quot(total * c, n), u1 = quot(total * (c + 1), n);
+      Req r = r0;
+      Load w = w0;
+      unsigned long long at = before;
       auto find = [&](unsigned long long u) {
-        at = before;
-        for (int b = b0;; ++b) {
-          w = load_req<ROWS>(a, b, &r);
-          if (u < at + w.units) return b;
-          at += w.units;
+        int b = b0;
+        if (b1 - b0 > 1) {
+          at = before;
+          for (;; ++b) {
+            w = load_req<ROWS>(a, b, &r);
+            if (u < at + w.units) break;
+            at += w.units;
+          }
         }
+        return b;
       };
       if (u0 >= before && u0 < before + mine) {
         s_start[0] = find(u0);
@@ -400,11 +412,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         // does the range's last segment start in it and end past it?  Then its last CTA is the
         // first one whose range ends at or after the segment's end
         find(u1 - 1);
-        const unsigned long long k = (u1 - 1 - at) / r.nt, start = at + k * r.nt, e = start + r.nt;
+        const unsigned long long k = quot(u1 - 1 - at, r.nt), start = at + k * r.nt, e = start + r.nt;
         int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
         if (start >= u0 && e > u1) {
-          const int h = (int)(k / w.groups), m = (int)(k % w.groups);
-          const int last = (int)((e * n + total - 1) / total) - 1;
+          const int h = (int)quot(k, w.groups), m = (int)(k - (unsigned long long)h * w.groups);
+          const int last = (int)quot(e * n + total - 1, total) - 1;
           c0 = make_int4(last - (int)c + 1, r.t0, min(ROWS, r.n * a.G - m * ROWS), h);
           c1 = make_int4(m, 0, 0, 0);
         }
@@ -431,107 +443,84 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     if (lane == 0) mbar_arrive(&seg_empty[i & 3]);
   };
 
-  if (warp == kProducer) {
-    // ---------------- TMA producer: one lane per page (or 8 drafts) ----------------
+  if (warp == kKeys || warp == kValues) {
+    // ---------------- TMA producers, one for K and one for V: a lane per page (or 8 rows) ----------------
     fewer();
+    const bool keys = warp == kKeys;
+    const CUtensorMap* const tp = keys ? &tm_k : &tm_v;   // whole pages, 8 rows, drafts
+    const CUtensorMap* const t8 = keys ? &tm_k8 : &tm_v8;
+    const CUtensorMap* const td = keys ? &tm_kn : &tm_vn;
     const uint64_t pol = policy_evict_first();
     const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a whole cached tile
     const int ppt = kTile / box;                  // pages per such tile
-    uint32_t issued = 0;                          // copies issued
-    Seg s{};
+    uint32_t g = 0, seg = 0, issued = 0;          // issued: past the last ring position that was issued
     bool ok = true;
-    // the lane's copies of tile i into ring position `at`: a whole tile page by page, a partial one and
-    // the drafts 8 rows at a time; `id` is the block that holds the lane's cached rows
-    auto copy = [&](const CUtensorMap* tp, const CUtensorMap* t8, const CUtensorMap* td, int i, int id, uint32_t at) {
-      const uint32_t stage = at % ST;
-      if (!mbar_wait(&empty[stage], ((at / ST) & 1) ^ 1, st, 221)) return false;
-      uint8_t* dst = s_ring + stage * C::kStageBytes;
-      const int cached = s.r.cached(i);
-      const int rows = cached == kTile ? box : 8;
-      const int nc = cached == kTile ? ppt : (cached + 7) >> 3, nd = (s.r.drafts(i) + 7) >> 3;
-      if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
-      __syncwarp();
-      if (lane < nc) {
-        const int slot = (s.r.base(i) + lane * rows) & ((1 << a.bs_shift) - 1);
-#pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf)
-          tma_load_4d(dst + hf * (kTile * 128) + lane * rows * 128, rows == 8 ? t8 : tp, hf * 64, slot, s.h, id,
-                      &full[stage], pol);
-      } else if (lane < nc + nd) {
-        const int j = (lane - nc) * 8;
-#pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf)
-          tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, td, hf * 64, s.h, s.r.t0 + s.r.d0(i) + j,
-                      &full[stage], pol);
-      }
-      __syncwarp();
-      issued = at + 1;
-      return true;
-    };
-    auto checked = [&](int id) {
-      if (id >= 0 && id < a.n_blocks) return id;
-      set_error(st, LMOE_EDEVICE_CHECK, 212);
-      return a.n_blocks;  // out of the cache: the copy reads zeros
-    };
-    auto page = [&](int i) {  // the block of this lane's cached rows of tile i
-      const int cached = s.r.cached(i), rows = cached == kTile ? box : 8;
-      if (lane * rows >= cached) return 0;
-      return __ldg(a.table + (size_t)s.b * a.max_blocks + ((s.r.base(i) + lane * rows) >> a.bs_shift));
-    };
-    uint32_t g = 0, seg = 0;
     Walk<ROWS> walk{a, (int)s_start[0], s_start[1], s_start[2]};
-    auto post = [&](const Seg& x) {
-      if (!mbar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, st, 262)) return false;
-      if (lane == 0) {
-        s_seg[seg & 3] = x;
-        mbar_arrive(&seg_full[seg & 3]);
-      }
-      __syncwarp();
-      ++seg;
-      return true;
-    };
-    if constexpr (NT == 2) {
-      while (ok && walk.next(&s)) {
-        if (!(ok = post(s))) break;
-        int id = page(s.i0);
-        for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
-          const int id_next = i + 1 < s.i1 ? page(i + 1) : 0;
-          id = checked(id);
-          ok = copy(&tm_k, &tm_k8, &tm_kn, i, id, k_pos<NT>(g)) && copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g, n_tiles));
-          id = id_next;
+    for (;; ++seg) {
+      // the keys' producer walks the range and posts each segment's record, the others read it
+      Seg s{};
+      if (keys) {
+        const bool more = walk.next(&s);
+        if (!more) s.i0 = s.i1 = 0;
+        if (!(ok = mbar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, st, 262))) break;
+        if (lane == 0) {
+          s_seg[seg & 3] = s;
+          mbar_arrive(&seg_full[seg & 3]);
         }
+        __syncwarp();
+      } else {
+        if (!(ok = seg_wait(seg))) break;
+        s = *seg_at(seg);
+        seg_done(seg);
       }
-    } else {
-      // keys one tile ahead of values, also across segments
-      Seg nx{};
-      int i = 0, id = 0;  // the tile whose values are still to come
-      while (ok && walk.next(&nx)) {
-        if (!(ok = post(nx))) break;
-        const Seg old = s;
-        s = nx;
-        int id_next = page(s.i0);
-        for (int k = s.i0; k < s.i1 && ok; ++k, ++g) {
-          const int id_k = checked(id_next);
-          id_next = k + 1 < s.i1 ? page(k + 1) : 0;
-          ok = copy(&tm_k, &tm_k8, &tm_kn, k, id_k, k_pos<NT>(g));
-          if (g > 0) {
-            if (k == s.i0) s = old;
-            ok = ok && copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g - 1, n_tiles));
-            if (k == s.i0 || k == nx.i0) s = nx;
-          }
-          i = k;
-          id = id_k;
+      if (s.i1 == 0) break;
+      const int32_t* const table = a.table + (size_t)s.b * a.max_blocks;
+      auto page = [&](int i) {  // the block of this lane's cached rows of tile i
+        const int cached = s.r.cached(i), rows = cached == kTile ? box : 8;
+        return lane * rows < cached ? __ldg(table + ((s.r.base(i) + lane * rows) >> a.bs_shift)) : 0;
+      };
+      int id_next = page(s.i0);
+      for (int i = s.i0; i < s.i1; ++i, ++g) {
+        int id = id_next;
+        if (i + 1 < s.i1) id_next = page(i + 1);
+        if (id < 0 || id >= a.n_blocks) {  // out of the cache: the copy reads zeros
+          set_error(st, LMOE_EDEVICE_CHECK, 212);
+          id = a.n_blocks;
         }
+        // a whole tile page by page, a partial one and the drafts 8 rows at a time
+        const uint32_t at = keys ? k_pos<NT>(g) : v_pos<NT>(g, n_tiles), stage = at % ST;
+        const int cached = s.r.cached(i);
+        const int rows = cached == kTile ? box : 8;
+        const int nc = cached == kTile ? ppt : (cached + 7) >> 3, nd = (s.r.drafts(i) + 7) >> 3;
+        if (!(ok = mbar_wait(&empty[stage], ((at / ST) & 1) ^ 1, st, 221))) break;
+        uint8_t* dst = s_ring + stage * C::kStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
+        __syncwarp();
+        if (lane < nc) {
+          const int slot = (s.r.base(i) + lane * rows) & ((1 << a.bs_shift) - 1);
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_4d(dst + hf * (kTile * 128) + lane * rows * 128, rows == 8 ? t8 : tp, hf * 64, slot, s.h, id,
+                        &full[stage], pol);
+        } else if (lane < nc + nd) {
+          const int j = (lane - nc) * 8;
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, td, hf * 64, s.h, s.r.t0 + s.r.d0(i) + j,
+                        &full[stage], pol);
+        }
+        __syncwarp();
+        issued = at + 1;
       }
-      if (ok && g > 0) ok = copy(&tm_v, &tm_v8, &tm_vn, i, id, v_pos<NT>(g - 1, n_tiles));
+      if (!ok) break;
     }
-    if (ok) {
-      s.i0 = s.i1 = 0;
-      post(s);
+    // this warp's last copies land before the CTA can finish (also after a wait that ran out); a stage
+    // that the other producer has filled since needs no wait
+    const uint32_t end = ok ? 2 * n_tiles : issued;
+    for (uint32_t k = g < ST ? 0 : g - ST; k < g; ++k) {
+      const uint32_t at = keys ? k_pos<NT>(k) : v_pos<NT>(k, n_tiles);
+      if (at + ST >= end) mbar_wait(&full[at % ST], (at / ST) & 1, st, 222);
     }
-    // the last copies land before the CTA can finish (also after a wait that ran out)
-    if (lane == 0)
-      for (uint32_t k = issued < ST ? 0 : issued - ST; k < issued; ++k) mbar_wait(&full[k % ST], (k / ST) & 1, st, 222);
   } else if (warp == kMma) {
     // ---------------- MMA issuer ----------------
     fewer();
@@ -719,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       commit(done);  // every MMA issued has completed before TMEM is released
       mbar_wait(done, 0, st, 235);
     }
-  } else if (warp < kProducer) {
+  } else if (warp < kKeys) {
     // ---------------- softmax: one row per thread ----------------
     if constexpr (KS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     constexpr int CW = C::kCols;
@@ -945,16 +934,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       const int qh = s->h * a.G + (valid ? s->m * C::kRows + local - vi * a.G : 0), tok = s->r.t0 + vi;
       const bool dirty = s_dirty[seg & 3] == seg + 1;
       const size_t prow = (size_t)(2 * blockIdx.x + (i0 == 0)) * C::kRows + local;
-      // 16 columns of this thread's row of O
-      auto sums = [&](int col, float (&y)[16]) {
-        uint32_t o[16];
-        tmem_ld16(o_addr + col, o);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(o[j]);
-        if (dirty && valid) {
-          // values that are not finite, of the keys that this row sees: the cleaning warps took them out
-          for (int i = i0; i < i0 + n; ++i) {
+      if (dirty && warp_live) {
+        // values that are not finite, of the keys that a row sees: the cleaning warp took them out
+#pragma unroll 1
+        for (int col = 0; col < D; col += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_addr + col, o);
+          tmem_ld_wait();
+          for (int i = i0; valid && i < i0 + n; ++i) {
             if (!s->r.edge(i)) continue;
             uint64_t bits[2];
             edge_bits(a, s, i, vi, vp, bits);
@@ -974,33 +961,47 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 #pragma unroll
               for (int d = 0; d < 16; ++d) {
                 const uint32_t x = val[col + d];
-                if ((x & 0x7f80u) == 0x7f80u) y[d] += bf16_bits_to_f32(x);
+                if ((x & 0x7f80u) == 0x7f80u) o[d] = __float_as_uint(__uint_as_float(o[d]) + bf16_bits_to_f32(x));
               }
             }
           }
+          __syncwarp();
+          tmem_st16(o_addr + col, o);
         }
+        tmem_st_wait();
+      }
+      // N columns of this thread's row of O
+      auto sums = [&](int col, auto& y) {
+        constexpr int N = sizeof(y) / 4;
+        uint32_t* o = reinterpret_cast<uint32_t*>(&y[0]);
+#pragma unroll
+        for (int c = 0; c < N; c += 16) tmem_ld16(o_addr + col + c, *reinterpret_cast<uint32_t(*)[16]>(o + c));
+        tmem_ld_wait();
       };
-      auto put = [&](int col, const float (&y)[16], float inv) {
+      auto put = [&](int col, const auto& y, float inv) {
+        constexpr int N = sizeof(y) / 4;
         if (!valid) return;
         if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + col);
-          uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = pack_bf16(y[2 * j] * inv, y[2 * j + 1] * inv);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int c = 0; c < N / 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack_bf16(y[c * 8 + 2 * j] * inv, y[c * 8 + 2 * j + 1] * inv);
+            dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         } else {
           float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + col);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          for (int j = 0; j < N / 4; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
         }
       };
       if constexpr (KS == 1) {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         if (warp_live) {
 #pragma unroll 1
-          for (int col = 0; col < D; col += 16) {
-            float y[16];
+          for (int col = 0; col < D; col += 64) {
+            float y[64];
             sums(col, y);
             put(col, y, inv);
           }
@@ -1036,42 +1037,35 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         for (int q = 0; q < OWN; q += P) {
           if (q > 0) meet();
           if (warp_live) {
-#pragma unroll 1
+#pragma unroll
             for (int d = 1; d < KS; ++d) {
               const int owner = (part + d) % KS;
-#pragma unroll 1
-              for (int c = 0; c < P; c += 16) {
-                float y[16];
-                sums(owner * OWN + q + c, y);
+              float y[P];
+              sums(owner * OWN + q, y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  *piece(owner, part, c / 4 + j) =
-                      make_float4(y[4 * j] * f, y[4 * j + 1] * f, y[4 * j + 2] * f, y[4 * j + 3] * f);
-              }
+              for (int j = 0; j < P / 4; ++j)
+                *piece(owner, part, j) = make_float4(y[4 * j] * f, y[4 * j + 1] * f, y[4 * j + 2] * f, y[4 * j + 3] * f);
             }
           }
+          float y[P];
+          if (warp_live) sums(part * OWN + q, y);
           meet();
           if (warp_live) {
-#pragma unroll 1
-            for (int c = 0; c < P; c += 16) {
-              float y[16];
-              sums(part * OWN + q + c, y);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] *= f;
+            for (int j = 0; j < P; ++j) y[j] *= f;
 #pragma unroll
-              for (int d = 1; d < KS; ++d) {
-                const int from = (part + d) % KS;
+            for (int d = 1; d < KS; ++d) {
+              const int from = (part + d) % KS;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float4 z = *piece(part, from, c / 4 + j);
-                  y[4 * j] += z.x;
-                  y[4 * j + 1] += z.y;
-                  y[4 * j + 2] += z.z;
-                  y[4 * j + 3] += z.w;
-                }
+              for (int j = 0; j < P / 4; ++j) {
+                const float4 z = *piece(part, from, j);
+                y[4 * j] += z.x;
+                y[4 * j + 1] += z.y;
+                y[4 * j + 2] += z.z;
+                y[4 * j + 3] += z.w;
               }
-              put(part * OWN + q + c, y, inv);
             }
+            put(part * OWN + q, y, inv);
           }
         }
         meet();  // the next queries overwrite the buffer
@@ -1087,9 +1081,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       g_own += n;
     }
   } else {
-    // ---------------- cleaning: two warps, the value tiles at an edge ----------------
-    // Values that no row sees become zero, and those that are not finite too (0 * NaN would
-    // reach every row): they are added back to the rows that see them at the segment's end.
+    // ---------------- cleaning: the value tiles at an edge ----------------
+    // Values that no row sees become zero (0 * NaN would reach every row), and so do those that are not
+    // finite among the keys that only some rows see: these are added back to the rows that see them at
+    // the segment's end.  A warp's access covers 4 keys of 128 bytes.
     fewer();
     uint32_t g = 0, edges = 0;
     bool ok = true;
@@ -1103,31 +1098,44 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         if (!(ok = mbar_wait(v_edge, edges++ & 1, st, 251))) break;
         const uint32_t at = v_pos<NT>(g, n_tiles);
         if (!(ok = mbar_wait(&full[at % ST], (at / ST) & 1, st, 252))) break;
-        uint8_t* vt = s_ring + (at % ST) * C::kStageBytes;
-        const int hi = s.r.cached(i), c0 = s.r.col(i), c1 = c0 + s.r.drafts(i);
-        const int first = a.window > 0 ? s.r.len - a.window + 1 - s.r.base(i) : 0;
+        uint8_t* const vt = s_ring + (at % ST) * C::kStageBytes + (lane & 7) * 16;
+        const int base = s.r.base(i), hi = s.r.cached(i), nd = s.r.drafts(i), c0 = nd ? s.r.col(i) : hi, c1 = c0 + nd;
+        // cached positions: seen by some row from `first` on, by every row from `all` on
+        const int first = a.window > 0 ? min(max(s.r.len - a.window + 1 - base, 0), hi) : 0;
+        const int all = a.window > 0 ? min(max(s.r.len + s.r.n - a.window - base, 0), hi) : 0;
         bool found = false;
-#pragma unroll 4
-        for (int c = tid - 320; c < kTile * HALVES * 8; c += 64) {
-          const int key = (c >> 3) & (kTile - 1);
-          uint4* w = reinterpret_cast<uint4*>(vt + (c << 4));
-          if (!((key >= first && key < hi) || (key >= c0 && key < c1))) {
-            *w = make_uint4(0u, 0u, 0u, 0u);
-            continue;
-          }
-          uint4 y = *w;
-          uint32_t* e = &y.x;
-          bool change = false;
+        auto zero = [&](int from, int to) {
+          for (int key = from + (lane >> 3); key < to; key += 4)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u, change = true;
-            if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0xffffu, change = true;
-          }
-          if (change) {
-            *w = y;
-            found = true;
-          }
-        }
+            for (int hf = 0; hf < HALVES; ++hf)
+              *reinterpret_cast<uint4*>(vt + hf * (kTile * 128) + key * 128) = make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto check = [&](int from, int to) {
+          for (int key = from + (lane >> 3); key < to; key += 4)
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf) {
+              uint4* const w = reinterpret_cast<uint4*>(vt + hf * (kTile * 128) + key * 128);
+              uint4 y = *w;
+              uint32_t* const e = &y.x;
+              uint32_t top = 0;  // an exponent of all ones carries into the sign's place
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top |= (e[j] & 0x7f807f80u) + 0x00800080u;
+              if (top & 0x80008000u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u;
+                  if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0xffffu;
+                }
+                *w = y;
+                found = true;
+              }
+            }
+        };
+        zero(0, first);
+        check(first, all);
+        zero(hi, c0);
+        check(c0, c1);
+        zero(c1, kTile);
         if (found) s_dirty[seg & 3] = seg + 1;
         fence_proxy_async_smem();
         __syncwarp();
@@ -1165,43 +1173,51 @@ __global__ void __launch_bounds__(256) tree_attn_merge_kernel(const AttnArgs a, 
     e.where = __shfl_sync(0xffffffffu, e.where, from);
     if (lane == 0) *a.status = e;
   }
-  const int4 c0 = a.cut[2 * blockIdx.x];
+  const int4 c0 = a.cut[2 * blockIdx.x], c1 = a.cut[2 * blockIdx.x + 1];
   const int pieces = c0.x, local = blockIdx.y * 8 + warp;
   if (pieces < 2 || local >= c0.z) return;
-  const int rr = a.cut[2 * blockIdx.x + 1].x * rows + local;
+  const int rr = c1.x * rows + local;
   const int i = rr / a.G, tok = c0.y + i, qh = c0.w * a.G + rr - i * a.G;
   auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)) * rows + local; };
+  // eight pieces' rows are under way at a time, the first ones already beside the maxima
+  constexpr int E = D / 32, U = 8;
+  float o[U][E];
+  auto fetch = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (p0 + u >= pieces) break;
+      const float* x = a.part_o + slot(p0 + u) * D + lane * E;
+      if constexpr (E == 4)
+        *reinterpret_cast<float4*>(o[u]) = *reinterpret_cast<const float4*>(x);
+      else
+        *reinterpret_cast<float2*>(o[u]) = *reinterpret_cast<const float2*>(x);
+    }
+  };
+  fetch(0);
   float M = -INFINITY;
   for (int p = lane; p < pieces; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   const float mu = M == -INFINITY ? 0.f : M;
-  constexpr int E = D / 32;
-  float acc[E] = {}, L = 0.f;
-  for (int p0 = 0; p0 < pieces; p0 += 32) {
-    float w = 0.f, lw = 0.f;
-    if (p0 + lane < pieces) {
-      const float2 ml = a.part_ml[slot(p0 + lane)];
-      w = ex2(ml.x - mu);
-      lw = w * ml.y;
-    }
-    L += warp_sum(lw);
-    const int np = min(32, pieces - p0);
-#pragma unroll 4
-    for (int p = 0; p < np; ++p) {
-      const float wp = __shfl_sync(0xffffffffu, w, p);
-      const float* o = a.part_o + slot(p0 + p) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(o);
-        acc[0] = fmaf(wp, y.x, acc[0]);
-        acc[1] = fmaf(wp, y.y, acc[1]);
-        acc[2] = fmaf(wp, y.z, acc[2]);
-        acc[3] = fmaf(wp, y.w, acc[3]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(o);
-        acc[0] = fmaf(wp, y.x, acc[0]);
-        acc[1] = fmaf(wp, y.y, acc[1]);
+  float acc[E] = {}, L = 0.f, w = 0.f;
+  for (int p0 = 0; p0 < pieces; p0 += U) {
+    if (p0 > 0) fetch(p0);
+    if (p0 % 32 == 0) {  // the weights of 32 pieces, a lane each
+      float lw = 0.f;
+      w = 0.f;
+      if (p0 + lane < pieces) {
+        const float2 ml = a.part_ml[slot(p0 + lane)];
+        w = ex2(ml.x - mu);
+        lw = w * ml.y;
       }
+      L += warp_sum(lw);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (p0 + u >= pieces) break;
+      const float wp = __shfl_sync(0xffffffffu, w, (p0 + u) & 31);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wp, o[u][e], acc[e]);
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
