@@ -54,7 +54,7 @@ struct AttnArgs {
   Status* err;     // [CTAs], joined into *status by the merge kernel
   int4* cut;       // [CTAs][2], the segment that starts in a CTA's range and ends past it
   float2* part_ml; // [2 CTAs][rows] running maximum (base 2) and sum
-  float* part_o;   // [2 CTAs][rows][D]
+  float* part_o;   // [2 CTAs][D / 4][rows][4]
   int B, T, max_n, hk, G, max_blocks, n_blocks, bs_shift, words, window, ctas;
   float scale_log2;
 };
@@ -84,13 +84,38 @@ __device__ __forceinline__ unsigned long long quot(unsigned long long x, unsigne
   return (x | y) >> 32 ? x / y : (unsigned)x / (unsigned)y;
 }
 
-struct Load {
-  int groups;  // row groups
-  bool bad;
-  long long units;
+// A wait bounded by about a second of SM clocks.  The kernel's warps run different loops of it at once and
+// wait for instructions where these do not fit the instruction cache together, so this is kept short: what
+// ran out is noted in `failed` and reported once, at the kernel's end.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int where, int& failed) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint32_t t0, t1;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(t0));
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    asm volatile("mov.u32 %0, %%clock;" : "=r"(t1));
+  } while (t1 - t0 < 0x70000000u);
+  failed = where;
+  return false;
+}
+
+// How the line of tiles is measured for the cut into equal ranges: a tile of two row tiles, of one, and
+// the end of a segment.  Of two row tiles the second comes at half the price of the first (the products
+// of one run during the softmax of the other), and a segment's end costs about a tile.
+template <int NT>
+struct Cost {
+  static constexpr int kTwo = NT == 2 ? 3 : 2, kOne = 2, kEnd = NT == 2 ? 3 : 1;
 };
 
-template <int ROWS>
+struct Load {
+  int groups;        // row groups
+  int last;          // cost of a tile of the last group
+  long long head;    // cost of a kv head
+  long long units;   // of the request
+  bool bad;
+};
+
+template <int NT, int ROWS>
 __device__ __forceinline__ Load load_req(const AttnArgs& a, int b, Req* r) {
   const int t0 = __ldg(a.offsets + b), t1 = __ldg(a.offsets + b + 1), len = __ldg(a.lens + b);
   Load w;
@@ -110,8 +135,29 @@ __device__ __forceinline__ Load load_req(const AttnArgs& a, int b, Req* r) {
   r->c0 = (held & 127) != 0 && tail + r->n <= kTile ? tail : 0;
   r->nt = r->np + (r->c0 ? 0 : (r->n + kTile - 1) >> 7);
   w.groups = (r->n * a.G + ROWS - 1) / ROWS;
-  w.units = (long long)a.hk * w.groups * r->nt;
+  w.last = r->n * a.G - (w.groups - 1) * ROWS > kTile ? Cost<NT>::kTwo : Cost<NT>::kOne;
+  w.head = w.groups == 0 ? 0
+                         : (long long)(w.groups - 1) * ((long long)r->nt * Cost<NT>::kTwo + Cost<NT>::kEnd) +
+                               (long long)r->nt * w.last + Cost<NT>::kEnd;
+  w.units = a.hk * w.head;
   return w;
+}
+
+// A segment by its place in its request's part of the line.
+struct Place {
+  int h, m, tile;   // kv head, row group, cost of a tile
+  long long start;  // where it starts
+};
+
+template <int NT>
+__device__ __forceinline__ Place place(const Load& w, int nt, long long off) {
+  Place p;
+  p.h = (int)quot(off, w.head);
+  const long long r = off - p.h * w.head, group = (long long)nt * Cost<NT>::kTwo + Cost<NT>::kEnd;
+  p.m = w.groups == 1 ? 0 : min((int)quot(r, group), w.groups - 1);
+  p.tile = p.m == w.groups - 1 ? w.last : Cost<NT>::kTwo;
+  p.start = p.h * w.head + p.m * group;
+  return p;
 }
 
 // The part of one segment that falls into a CTA's range.
@@ -124,31 +170,37 @@ struct alignas(16) Seg {
 };
 static_assert(sizeof(Seg) == 64, "four 16-byte pieces");
 
-// Walks the segments of the CTA's unit range.
-template <int ROWS>
+// Walks the segments of the CTA's range: a tile belongs to the range that it starts in.
+template <int NT, int ROWS>
 struct Walk {
   const AttnArgs& a;
   int b;
-  long long off, left;  // units into request b, units left in the range
+  long long off, end;  // where the range goes on and where it ends, from request b's start
   __device__ bool next(Seg* s) {
-    if (left <= 0) return false;
-    Load w;
-    for (;;) {
-      w = load_req<ROWS>(a, b, &s->r);
-      if (off < w.units) break;
-      off -= w.units;
-      ++b;
+    while (off < end) {
+      const Load w = load_req<NT, ROWS>(a, b, &s->r);
+      if (off >= w.units) {
+        off -= w.units;
+        end -= w.units;
+        ++b;
+        continue;
+      }
+      const int nt = s->r.nt;
+      const Place p = place<NT>(w, nt, off);
+      const int i0 = (int)quot(off - p.start + p.tile - 1, p.tile);
+      off = p.start + (long long)nt * p.tile + Cost<NT>::kEnd;
+      if (i0 >= nt) continue;
+      const int i1 = (int)min((long long)nt, (long long)quot(max(end - p.start, 0ll) + p.tile - 1, p.tile));
+      if (i1 <= i0) return false;
+      s->b = b;
+      s->h = p.h;
+      s->m = p.m;
+      s->i0 = i0;
+      s->i1 = i1;
+      s->rows = min(ROWS, s->r.n * a.G - p.m * ROWS);
+      return true;
     }
-    const long long k = (long long)quot(off, s->r.nt);
-    s->b = b;
-    s->h = (int)quot(k, w.groups);
-    s->m = (int)(k - (long long)s->h * w.groups);
-    s->i0 = (int)(off - k * s->r.nt);
-    s->i1 = (int)min((long long)s->r.nt, s->i0 + left);
-    s->rows = min(ROWS, s->r.n * a.G - s->m * ROWS);
-    off += s->i1 - s->i0;
-    left -= s->i1 - s->i0;
-    return true;
+    return false;
   }
 };
 
@@ -164,12 +216,13 @@ __device__ __forceinline__ uint64_t range_bits(int lo, int hi) {  // bits [lo, h
 }
 
 // What draft vi (at position vp) of a segment's request sees of the 128 columns of tile i.
-__device__ __forceinline__ void edge_bits(const AttnArgs& a, const Seg* s, int i, int vi, int vp, uint64_t (&bits)[2]) {
+__device__ __forceinline__ ulonglong2 edge_bits(const AttnArgs& a, const Seg* s, int i, int vi, int vp) {
+  uint64_t bits[2];
   const int cached = s->r.cached(i), first = a.window > 0 ? vp - a.window + 1 - s->r.base(i) : 0;
   bits[0] = range_bits(first, cached);
   bits[1] = range_bits(first - 64, cached - 64);
   const int nd = s->r.drafts(i);
-  if (nd == 0) return;
+  if (nd == 0) return make_ulonglong2(bits[0], bits[1]);
   const int d0 = s->r.d0(i), c = s->r.col(i), t0 = s->r.t0;
   // the drafts d0 .. d0 + 127 that the row sees, moved up to column c
   uint64_t m0, m1;
@@ -200,6 +253,7 @@ __device__ __forceinline__ void edge_bits(const AttnArgs& a, const Seg* s, int i
     bits[0] |= m0;
     bits[1] |= m1;
   }
+  return make_ulonglong2(bits[0], bits[1]);
 }
 
 // One lane of a converged warp, the same one each time.
@@ -255,6 +309,78 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Turns U 16-byte units per lane into whole pieces of rows: afterwards unit j of lane l is unit l % U of
+// lane l / U * U + j, so that U neighbouring lanes hold 16 U consecutive bytes of one row.
+template <int U>
+__device__ __forceinline__ void turn_units(uint32_t (&w)[U][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s < U; s *= 2)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (!(u & s))
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t mine = lane & s ? w[u][j] : w[u | s][j];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, mine, s);
+          if (lane & s)
+            w[u][j] = got;
+          else
+            w[u | s][j] = got;
+        }
+}
+
+// Stores 16 U bytes of each lane's row, at `row` (null: no row), U lanes to a row.
+template <int U>
+__device__ __forceinline__ void store_rows(uint32_t (&w)[U][4], void* row) {
+  const int lane = threadIdx.x & 31;
+  turn_units<U>(w);
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (lane & -U) + j));
+    if (dst) *reinterpret_cast<uint4*>(dst + (lane % U) * 16) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+  }
+}
+
+// Adds the values that are not finite, of the keys that a row sees, to the thread's row of O: the cleaning
+// warp took them out.  Runs only where there was one.
+template <int D, int CW>
+__device__ __forceinline__ void add_not_finite(const AttnArgs& a, const Seg* s, uint32_t o_addr, int part, bool valid,
+                                            int vi, int vp, int i0, int n) {
+#pragma unroll 1
+  for (int col = 0; col < D; col += 16) {
+    uint32_t o[16];
+    tmem_ld16(o_addr + col, o);
+    tmem_ld_wait();
+    for (int i = i0; valid && i < i0 + n; ++i) {
+      if (!s->r.edge(i)) continue;
+      const ulonglong2 bits = edge_bits(a, s, i, vi, vp);
+#pragma unroll 1
+      for (int j = part * CW; j < part * CW + CW; ++j) {
+        if (!((j >= 64 ? bits.y : bits.x) >> (j & 63) & 1ull)) continue;
+        const uint16_t* val;
+        if (j < s->r.cached(i)) {
+          const int p = s->r.base(i) + j;
+          const int id = __ldg(a.table + (size_t)s->b * a.max_blocks + (p >> a.bs_shift));
+          if (id < 0 || id >= a.n_blocks) continue;
+          val = a.v_cache + (size_t)id * a.block_stride + (size_t)s->h * a.head_stride +
+                (size_t)(p & ((1 << a.bs_shift) - 1)) * a.slot_stride;
+        } else {
+          val = a.v_new + (size_t)(s->r.t0 + s->r.d0(i) + j - s->r.col(i)) * a.vs + s->h * D;
+        }
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+          const uint32_t x = val[col + d];
+          if ((x & 0x7f80u) == 0x7f80u) o[d] = __float_as_uint(__uint_as_float(o[d]) + bf16_bits_to_f32(x));
+        }
+      }
+    }
+    __syncwarp();
+    tmem_st16(o_addr + col, o);
+  }
+  tmem_st_wait();
+}
+
 // D: head width.  NT: row tiles of 128 rows per CTA.  KS: with few rows (128 / KS at most) each row
 // stands KS times in the row tile, and the copies take 128 / KS of a tile's keys each, so that all four
 // softmax warps work on 32 rows or less.
@@ -277,20 +403,20 @@ struct Cfg {
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// Ring position of K and V of the CTA's tile g of n.  The groups in turns: K0 K1 V0 K2 V1 ... (S runs one
-// tile ahead, also across segments); two row tiles: K0 V0 K1 V1 ...
+// Ring position of K and V of the CTA's tile g.  The groups in turns: K0 K1 V0 K2 V1 ... (S runs one tile
+// ahead, also across segments; the place before the last V stays empty); two row tiles: K0 V0 K1 V1 ...
 template <int NT>
 __device__ __forceinline__ uint32_t k_pos(uint32_t g) {
   return NT == 2 ? 2 * g : (g == 0 ? 0 : 2 * g - 1);
 }
 template <int NT>
-__device__ __forceinline__ uint32_t v_pos(uint32_t g, uint32_t n) {
-  return NT == 2 || g == n - 1 ? 2 * g + 1 : 2 * g + 2;
+__device__ __forceinline__ uint32_t v_pos(uint32_t g) {
+  return NT == 2 ? 2 * g + 1 : 2 * g + 2;
 }
 
 template <int D, int NT, int KS>
 __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
-    tree_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
+    tree_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
                      const __grid_constant__ CUtensorMap tm_vn, const __grid_constant__ CUtensorMap tm_k8,
                      const __grid_constant__ CUtensorMap tm_v8) {
@@ -341,7 +467,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     mbar_init(done, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 11);  // values' producer, MMA, eight softmax warps, cleaning warp
+      mbar_init(&seg_empty[i], 11);  // warps 9 to 11 and the eight softmax warps
       s_dirty[i] = 0;
     }
     fence_barrier_init();
@@ -362,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     Load w0{};
     for (int b = b0; b < b1; ++b) {
       Req r;
-      const Load w = load_req<ROWS>(a, b, &r);
+      const Load w = load_req<NT, ROWS>(a, b, &r);
       mine += w.units;
       bad |= w.bad;
       if (b == b0) r0 = r, w0 = w;
@@ -383,7 +509,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       total += s_warp[w];
     }
     if (bad) set_error(st, LMOE_EDEVICE_CHECK, 211);
-    const unsigned long long n = min((unsigned long long)a.ctas, total);  // ranges, none of them empty
+    // ranges, each long enough to hold the start of a tile
+    constexpr int kLong = Cost<NT>::kTwo + Cost<NT>::kEnd;
+    const unsigned long long n = total ? max(1ull, min((unsigned long long)a.ctas, total / kLong)) : 0ull;
     const unsigned long long c = blockIdx.x;
     if (c < n) {
       // the threads whose requests hold the range's first and last unit
@@ -396,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         if (b1 - b0 > 1) {
           at = before;
           for (;; ++b) {
-            w = load_req<ROWS>(a, b, &r);
+            w = load_req<NT, ROWS>(a, b, &r);
             if (u < at + w.units) break;
             at += w.units;
           }
@@ -409,16 +537,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         s_start[2] = (long long)(u1 - u0);
       }
       if (u1 - 1 >= before && u1 - 1 < before + mine) {
-        // does the range's last segment start in it and end past it?  Then its last CTA is the
-        // first one whose range ends at or after the segment's end
+        // does the range's last segment start in it and have tiles past it?  Then its last CTA is the
+        // first one whose range ends after the start of the segment's last tile
         find(u1 - 1);
-        const unsigned long long k = quot(u1 - 1 - at, r.nt), start = at + k * r.nt, e = start + r.nt;
+        const Place p = place<NT>(w, r.nt, (long long)(u1 - 1 - at));
+        const unsigned long long start = at + p.start, in = u1 - 1 - start;
         int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
-        if (start >= u0 && e > u1) {
-          const int h = (int)quot(k, w.groups), m = (int)(k - (unsigned long long)h * w.groups);
+        if (start >= u0 && quot(in, p.tile) + 1 < (unsigned)r.nt) {
+          const unsigned long long e = start + (unsigned long long)(r.nt - 1) * p.tile + 1;  // its last tile's start
           const int last = (int)quot(e * n + total - 1, total) - 1;
-          c0 = make_int4(last - (int)c + 1, r.t0, min(ROWS, r.n * a.G - m * ROWS), h);
-          c1 = make_int4(m, 0, 0, 0);
+          c0 = make_int4(last - (int)c + 1, r.t0, min(ROWS, r.n * a.G - p.m * ROWS), p.h);
+          c1 = make_int4(p.m, 0, 0, 0);
         }
         a.cut[2 * c] = c0;
         a.cut[2 * c + 1] = c1;
@@ -429,40 +558,37 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     __syncthreads();
   }
   const uint32_t tmem = *tmem_slot;
-  const uint32_t n_tiles = (uint32_t)s_start[2];
   // 384 threads start with 168 registers each; with a whole tile's scores per thread the service
   // warps hand some of theirs to the softmax warps (88 + 2 x 208 = 3 x 168)
   auto fewer = [] {
     if constexpr (KS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   };
+  int failed = 0;  // where a wait ran out
   // the record of segment `i`, once it is there; warps take the segments in order
   auto seg_at = [&](uint32_t i) { return const_cast<const Seg*>(s_seg + (i & 3)); };
-  auto seg_wait = [&](uint32_t i) { return mbar_wait(&seg_full[i & 3], (i >> 2) & 1, st, 261); };
+  auto seg_wait = [&](uint32_t i) { return bar_wait(&seg_full[i & 3], (i >> 2) & 1, 261, failed); };
   auto seg_done = [&](uint32_t i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[i & 3]);
   };
 
   if (warp == kKeys || warp == kValues) {
-    // ---------------- TMA producers, one for K and one for V: a lane per page (or 8 rows) ----------------
+    // ---------------- TMA producers: a lane per page (or 8 rows) ----------------
     fewer();
     const bool keys = warp == kKeys;
-    const CUtensorMap* const tp = keys ? &tm_k : &tm_v;   // whole pages, 8 rows, drafts
-    const CUtensorMap* const t8 = keys ? &tm_k8 : &tm_v8;
-    const CUtensorMap* const td = keys ? &tm_kn : &tm_vn;
     const uint64_t pol = policy_evict_first();
     const int box = min(1 << a.bs_shift, kTile);  // rows per copy of a whole cached tile
     const int ppt = kTile / box;                  // pages per such tile
     uint32_t g = 0, seg = 0, issued = 0;          // issued: past the last ring position that was issued
     bool ok = true;
-    Walk<ROWS> walk{a, (int)s_start[0], s_start[1], s_start[2]};
+    Walk<NT, ROWS> walk{a, (int)s_start[0], s_start[1], s_start[1] + s_start[2]};
     for (;; ++seg) {
       // the keys' producer walks the range and posts each segment's record, the others read it
       Seg s{};
       if (keys) {
         const bool more = walk.next(&s);
         if (!more) s.i0 = s.i1 = 0;
-        if (!(ok = mbar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, st, 262))) break;
+        if (!(ok = bar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, 262, failed))) break;
         if (lane == 0) {
           s_seg[seg & 3] = s;
           mbar_arrive(&seg_full[seg & 3]);
@@ -488,38 +614,42 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           id = a.n_blocks;
         }
         // a whole tile page by page, a partial one and the drafts 8 rows at a time
-        const uint32_t at = keys ? k_pos<NT>(g) : v_pos<NT>(g, n_tiles), stage = at % ST;
         const int cached = s.r.cached(i);
         const int rows = cached == kTile ? box : 8;
         const int nc = cached == kTile ? ppt : (cached + 7) >> 3, nd = (s.r.drafts(i) + 7) >> 3;
-        if (!(ok = mbar_wait(&empty[stage], ((at / ST) & 1) ^ 1, st, 221))) break;
-        uint8_t* dst = s_ring + stage * C::kStageBytes;
-        if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
-        __syncwarp();
-        if (lane < nc) {
-          const int slot = (s.r.base(i) + lane * rows) & ((1 << a.bs_shift) - 1);
+        auto copy = [&](bool k, uint32_t at) {
+          const CUtensorMap* const tc = rows == 8 ? (k ? &tm_k8 : &tm_v8) : (k ? &tm_k : &tm_v);
+          const uint32_t stage = at % ST;
+          if (!bar_wait(&empty[stage], ((at / ST) & 1) ^ 1, 221, failed)) return false;
+          uint8_t* dst = s_ring + stage * C::kStageBytes;
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
+          __syncwarp();
+          if (lane < nc) {
+            const int slot = (s.r.base(i) + lane * rows) & ((1 << a.bs_shift) - 1);
 #pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_4d(dst + hf * (kTile * 128) + lane * rows * 128, rows == 8 ? t8 : tp, hf * 64, slot, s.h, id,
-                        &full[stage], pol);
-        } else if (lane < nc + nd) {
-          const int j = (lane - nc) * 8;
+            for (int hf = 0; hf < HALVES; ++hf)
+              tma_load_4d(dst + hf * (kTile * 128) + lane * rows * 128, tc, hf * 64, slot, s.h, id, &full[stage], pol);
+          } else if (lane < nc + nd) {
+            const int j = (lane - nc) * 8;
 #pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, td, hf * 64, s.h, s.r.t0 + s.r.d0(i) + j,
-                        &full[stage], pol);
-        }
-        __syncwarp();
-        issued = at + 1;
+            for (int hf = 0; hf < HALVES; ++hf)
+              tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, k ? &tm_kn : &tm_vn, hf * 64, s.h,
+                          s.r.t0 + s.r.d0(i) + j, &full[stage], pol);
+          }
+          __syncwarp();
+          issued = at + 1;
+          return true;
+        };
+        if (!(ok = keys ? copy(true, k_pos<NT>(g)) : copy(false, v_pos<NT>(g)))) break;
       }
       if (!ok) break;
     }
     // this warp's last copies land before the CTA can finish (also after a wait that ran out); a stage
-    // that the other producer has filled since needs no wait
-    const uint32_t end = ok ? 2 * n_tiles : issued;
+    // that has been filled again since needs no wait
+    const uint32_t end = ok ? v_pos<NT>(g - 1) + 1 : issued;
     for (uint32_t k = g < ST ? 0 : g - ST; k < g; ++k) {
-      const uint32_t at = keys ? k_pos<NT>(k) : v_pos<NT>(k, n_tiles);
-      if (at + ST >= end) mbar_wait(&full[at % ST], (at / ST) & 1, st, 222);
+      const uint32_t at = keys ? k_pos<NT>(k) : v_pos<NT>(k);
+      if (at + ST >= end) bar_wait(&full[at % ST], (at / ST) & 1, 222, failed);
     }
   } else if (warp == kMma) {
     // ---------------- MMA issuer ----------------
@@ -530,10 +660,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
       constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
       bool ok = true;
-      // every wait of this warp is on the critical path: the blocking probe first
-      auto ready = [&](uint64_t* bar, uint32_t parity, int where) {
-        return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, st, where);
-      };
+      auto ready = [&](uint64_t* bar, uint32_t parity, int where) { return bar_wait(bar, parity, where, failed); };
       // descriptors step by their start address (bits 0 to 13, in units of 16 bytes)
       const uint64_t qd = smem_desc_sw128(smem_u32(s_q)), kd = smem_desc_sw128(smem_u32(s_ring));
       const uint64_t vd = smem_desc_sw128_mn(smem_u32(s_ring), kTile * 128);
@@ -598,14 +725,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         return true;
       };
       uint32_t ring = 0, ring_phase = 0;
-      auto tile = [&](uint32_t* stage) {  // the next tile of the ring has landed (they are taken in its order)
-        if (!ready(&full[ring], ring_phase, 231)) return false;
-        tc_fence_after();
-        *stage = ring;
+      auto skip = [&] {
         if (++ring == ST) {
           ring = 0;
           ring_phase ^= 1;
         }
+      };
+      auto tile = [&](uint32_t* stage) {  // the next tile of the ring has landed (they are taken in its order)
+        if (!ready(&full[ring], ring_phase, 231)) return false;
+        tc_fence_after();
+        *stage = ring;
+        skip();
         return true;
       };
       // what this warp needs of a segment
@@ -628,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       };
       // tile i of s is clean; then it is the next tile's turn (one at a time, so that no phase is missed)
       auto cleaned = [&](int i) {
-        if (s.edge(i) && !mbar_wait(v_clean, edges++ & 1, st, 236)) return false;
+        if (s.edge(i) && !bar_wait(v_clean, edges++ & 1, 236, failed)) return false;
         if (i + 1 < s.i1)
           clean(s, i + 1);
         else if (nx.i1 > 0)
@@ -659,6 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             } else if (!(ok = get(seg + 1, &nx)) || (nx.i1 > 0 && !(ok = first_qk(seg + 1, g + 1)))) {
               break;
             }
+            if (i + 1 == s.i1 && nx.i1 == 0) skip();
             if (!(ok = tile(&vs)) || !(ok = cleaned(i))) break;
             if (!(ok = pv(seg & 1, g & 1, vs, i == s.i0, (g >> 1) & 1))) break;
             commit(&empty[vs]);
@@ -682,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
         while (ok && s.i1 > 0) {
           const bool two = s.rows > kTile;
-          for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
+          for (int i = s.i0; i < s.i1 && ok; ++i) {
             const bool same = i + 1 < s.i1;
             if (!(ok = tile(&vs)) || (!same && !(ok = get(seg + 1, &nx))) || !(ok = cleaned(i))) break;
             const bool more = same || nx.i1 > 0;
@@ -706,7 +837,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
       }
       commit(done);  // every MMA issued has completed before TMEM is released
-      mbar_wait(done, 0, st, 235);
+      bar_wait(done, 0, 235, failed);
     }
   } else if (warp < kKeys) {
     // ---------------- softmax: one row per thread ----------------
@@ -723,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     // it writes is void.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
-      if (ok) ok = mbar_wait(bar, parity, st, where);
+      if (ok) ok = bar_wait(bar, parity, where, failed);
       tc_fence_after();
     };
     uint32_t meets = 0;
@@ -797,13 +928,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         if (warp_live) {
           if (i < cut || i >= full_from) {
             // unseen keys' scores become -infinity, in place
-            uint64_t bits[2];
             const int vi = draft();
-            edge_bits(a, s, i, vi, at_pos(vi), bits);
+            const ulonglong2 bits = edge_bits(a, s, i, vi, at_pos(vi));
 #pragma unroll 1
             for (int c = 0; c < CW / 32; ++c) {
               const int w = part * (CW / 32) + c;
-              const uint32_t x = valid ? (uint32_t)((w & 2 ? bits[1] : bits[0]) >> (32 * (w & 1))) : 0u;
+              const uint32_t x = valid ? (uint32_t)((w & 2 ? bits.y : bits.x) >> (32 * (w & 1))) : 0u;
               uint32_t y[32];
               tmem_ld32(s_addr + w * 32, y);
               tmem_ld_wait();
@@ -814,22 +944,67 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             }
             tmem_st_wait();
           }
-          uint32_t sv[CW];
-          auto load = [&] {
+          // the tile's maximum
+          float mx[2] = {-INFINITY, -INFINITY};
+          {
+            uint32_t y[2][32];
+            tmem_ld32(s_addr + part * CW, y[0]);
 #pragma unroll
-            for (int c = 0; c < CW / 32; ++c)
-              tmem_ld32(s_addr + part * CW + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
-            tmem_ld_wait();
+            for (int c = 0; c < CW / 32; ++c) {
+              tmem_ld_wait();
+              if (c + 1 < CW / 32) tmem_ld32(s_addr + part * CW + (c + 1) * 32, y[(c + 1) & 1]);
+#pragma unroll
+              for (int j = 0; j < 32; j += 2)
+                mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], __uint_as_float(y[c & 1][j]), __uint_as_float(y[c & 1][j + 1]));
+            }
+          }
+          const float m_new = fmaxf(mx[0], mx[1]) * a.scale_log2;
+          uint64_t sum[2] = {0, 0};
+          // p = 2^(sc s - mu) of 32 keys, in place, and its bf16 part
+          auto exps = [&](uint32_t (&y)[32], uint32_t (&p)[16], uint64_t sc2, uint64_t mu2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float e0, e1;
+              unpair(fma2(pair(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), sc2, mu2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+              p[j] = pack_bf16(e0, e1);
+              y[2 * j] = __float_as_uint(e0);
+              y[2 * j + 1] = __float_as_uint(e1);
+            }
           };
-          load();
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < CW; j += 2)
-            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
-          const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
-          float mu = m_ref == -INFINITY ? 0.f : m_ref, sc = a.scale_log2;
           const bool plain = !__any_sync(0xffffffffu, m_new > limit);
-          if (!plain) {
+          if (plain) {
+            if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), mu2 = pair(-mu, -mu);
+            // the scores once more: P takes the place of scores that have been read
+            const uint32_t from = s_addr + part * CW, to = s_addr + part * (CW / 2);
+            uint32_t y0[32], y1[32], p[16];
+            tmem_ld32(from, y0);
+            if constexpr (CW == 32) {
+              tmem_ld_wait();
+              exps(y0, p, sc2, mu2);
+              tmem_st16(to, p);
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < CW / 32; c += 2) {
+                tmem_ld_wait();
+                tmem_ld32(from + c * 32 + 32, y1);
+                exps(y0, p, sc2, mu2);
+                tmem_st16(to + c * 16, p);
+                tmem_ld_wait();
+                if (c + 2 < CW / 32) tmem_ld32(from + c * 32 + 64, y0);
+                exps(y1, p, sc2, mu2);
+                tmem_st16(to + c * 16 + 16, p);
+                if (KS == 1 && c == 0) {  // the first half's product can start
+                  tmem_st_wait();
+                  p_ready(0);
+                }
+              }
+            }
+          } else {
             const bool grow = m_new > m_ref + 8.f;
             if (__any_sync(0xffffffffu, grow)) {
               const float f = grow ? ex2(m_ref - m_new) : 1.f;
@@ -848,64 +1023,41 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               }
               if (grow) m_ref = m_new;
             }
-            mu = m_ref == -INFINITY ? 0.f : m_ref;
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
             // p = 2^(scale s - mu) in one fused step, whose error against the rounded mu is common to
             // the row.  Past 2^24 that error alone could overflow: there scale s is rounded first too.
-            if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.f)) {
-#pragma unroll 1
-              for (int c = 0; c < CW / 16; ++c) {
-                uint32_t y[16];
-                tmem_ld16(s_addr + part * CW + c * 16, y);
-                tmem_ld_wait();
+            float sc = a.scale_log2;
+            const bool huge = __any_sync(0xffffffffu, fabsf(mu) > 16777216.f);
+            if (huge) sc = 1.f;
+            uint32_t y[CW / 32][32];
+            const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * sc);
-                tmem_st16(s_addr + part * CW + c * 16, y);
+            for (int c = 0; c < CW / 32; ++c) tmem_ld32(s_addr + part * CW + c * 32, y[c]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < CW / 32; ++c) {
+              uint32_t p[16];
+              if (huge) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[c][j] = __float_as_uint(__uint_as_float(y[c][j]) * a.scale_log2);
               }
-              tmem_st_wait();
-              load();
-              sc = 1.f;
+              exps(y[c], p, sc2, mu2);
+              tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
             }
-          }
-          uint64_t sum[2] = {0, 0};
-          const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
-#pragma unroll
-          for (int c = 0; c < CW / 32; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int x = c * 32 + 2 * j;
-              float e0, e1;
-              unpair(fma2(pair(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), sc2, mu2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
-              p[j] = pack_bf16(e0, e1);
-              sv[x] = __float_as_uint(e0);
-              sv[x + 1] = __float_as_uint(e1);
-            }
-            tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
-            if (KS == 1 && c == 1 && plain) {  // the first half's product can start
-              if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
-              tmem_st_wait();
-              p_ready(0);
-            }
-          }
-          float s0, s1;
-          unpair(add2(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
-          if (!plain || KS > 1) {
             // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
             // holds over 1/8 of the row's sum so far that would show in the output next to its own
             // rounding, so the remainder goes along as a second part; with more keys in play it
             // averages out.  After a prefix's first tiles this is rare.
-            const bool lo = !plain && __any_sync(0xffffffffu, valid && ex2(m_new - mu) > l * 0.125f);
+            float s0, s1;
+            unpair(add2(sum[0], sum[1]), s0, s1);
+            const bool lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > (l + (s0 + s1)) * 0.125f);
             if (lo) {
 #pragma unroll
               for (int c = 0; c < CW / 32; ++c) {
                 uint32_t p[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                  const float e0 = __uint_as_float(sv[c * 32 + 2 * j]), e1 = __uint_as_float(sv[c * 32 + 2 * j + 1]);
+                  const float e0 = __uint_as_float(y[c][2 * j]), e1 = __uint_as_float(y[c][2 * j + 1]);
                   const uint32_t hi = pack_bf16(e0, e1);
                   p[j] = pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
                 }
@@ -913,10 +1065,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               }
             }
             if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
+            if (KS == 1) {
+              tmem_st_wait();
+              p_ready(0);
+            }
           }
           tmem_st_wait();
-          if (KS == 1 && !plain) p_ready(0);
           p_ready(KS == 1 || part >= KS / 2 ? 1 : 0);
+          float s0, s1;
+          unpair(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
           // below: no growth past 2^8, and no key over 1/8 of the sum
           if (valid) limit = fabsf(m_ref) <= 16777216.f ? m_ref + fminf(8.f, __log2f(l) - 3.f) : -INFINITY;
         } else {
@@ -933,43 +1091,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       const int vi = draft(), vp = at_pos(vi);
       const int qh = s->h * a.G + (valid ? s->m * C::kRows + local - vi * a.G : 0), tok = s->r.t0 + vi;
       const bool dirty = s_dirty[seg & 3] == seg + 1;
-      const size_t prow = (size_t)(2 * blockIdx.x + (i0 == 0)) * C::kRows + local;
-      if (dirty && warp_live) {
-        // values that are not finite, of the keys that a row sees: the cleaning warp took them out
-#pragma unroll 1
-        for (int col = 0; col < D; col += 16) {
-          uint32_t o[16];
-          tmem_ld16(o_addr + col, o);
-          tmem_ld_wait();
-          for (int i = i0; valid && i < i0 + n; ++i) {
-            if (!s->r.edge(i)) continue;
-            uint64_t bits[2];
-            edge_bits(a, s, i, vi, vp, bits);
-#pragma unroll 1
-            for (int j = part * CW; j < part * CW + CW; ++j) {
-              if (!((j >= 64 ? bits[1] : bits[0]) >> (j & 63) & 1ull)) continue;
-              const uint16_t* val;
-              if (j < s->r.cached(i)) {
-                const int p = s->r.base(i) + j;
-                const int id = __ldg(a.table + (size_t)s->b * a.max_blocks + (p >> a.bs_shift));
-                if (id < 0 || id >= a.n_blocks) continue;
-                val = a.v_cache + (size_t)id * a.block_stride + (size_t)s->h * a.head_stride +
-                      (size_t)(p & ((1 << a.bs_shift) - 1)) * a.slot_stride;
-              } else {
-                val = a.v_new + (size_t)(s->r.t0 + s->r.d0(i) + j - s->r.col(i)) * a.vs + s->h * D;
-              }
-#pragma unroll
-              for (int d = 0; d < 16; ++d) {
-                const uint32_t x = val[col + d];
-                if ((x & 0x7f80u) == 0x7f80u) o[d] = __float_as_uint(__uint_as_float(o[d]) + bf16_bits_to_f32(x));
-              }
-            }
-          }
-          __syncwarp();
-          tmem_st16(o_addr + col, o);
-        }
-        tmem_st_wait();
-      }
+      const int slot = 2 * blockIdx.x + (i0 == 0);
+      if (dirty && warp_live) add_not_finite<D, CW>(a, s, o_addr, part, valid, vi, vp, i0, n);
       // N columns of this thread's row of O
       auto sums = [&](int col, auto& y) {
         constexpr int N = sizeof(y) / 4;
@@ -978,22 +1101,28 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         for (int c = 0; c < N; c += 16) tmem_ld16(o_addr + col + c, *reinterpret_cast<uint32_t(*)[16]>(o + c));
         tmem_ld_wait();
       };
+      // N columns of each row from col on (all lanes of the warp)
       auto put = [&](int col, const auto& y, float inv) {
         constexpr int N = sizeof(y) / 4;
-        if (!valid) return;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + col);
+          uint16_t* const dst = valid ? a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + col : nullptr;
+          uint32_t w[N / 8][4];
 #pragma unroll
-          for (int c = 0; c < N / 8; ++c) {
-            uint32_t w[4];
+          for (int u = 0; u < N / 8; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack_bf16(y[c * 8 + 2 * j] * inv, y[c * 8 + 2 * j + 1] * inv);
-            dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) w[u][j] = pack_bf16(y[u * 8 + 2 * j] * inv, y[u * 8 + 2 * j + 1] * inv);
+          if constexpr (KS == 1) {  // 128 rows' worth of 16-byte stores would queue up: 128 bytes of a row at a time
+            store_rows<N / 8>(w, dst);
+          } else if (dst) {
+#pragma unroll
+            for (int u = 0; u < N / 8; ++u)
+              *reinterpret_cast<uint4*>(dst + u * 8) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + col);
+        } else if (valid) {  // [slot][4 columns][row]: neighbouring lanes' pieces are neighbours
+          float4* const dst = reinterpret_cast<float4*>(a.part_o) + ((size_t)slot * (D / 4) + col / 4) * C::kRows + local;
 #pragma unroll
-          for (int j = 0; j < N / 4; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          for (int j = 0; j < N / 4; ++j)
+            dst[j * C::kRows] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
         }
       };
       if constexpr (KS == 1) {
@@ -1072,7 +1201,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       }
       if (valid && part == 0) {
         if (!whole)
-          a.part_ml[prow] = make_float2(m_ref, l);
+          a.part_ml[(size_t)slot * C::kRows + local] = make_float2(m_ref, l);
         else if (a.lse)
           a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       }
@@ -1095,9 +1224,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       if (s.i1 == 0) break;
       for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
         if (!s.r.edge(i)) continue;
-        if (!(ok = mbar_wait(v_edge, edges++ & 1, st, 251))) break;
-        const uint32_t at = v_pos<NT>(g, n_tiles);
-        if (!(ok = mbar_wait(&full[at % ST], (at / ST) & 1, st, 252))) break;
+        if (!(ok = bar_wait(v_edge, edges++ & 1, 251, failed))) break;
+        const uint32_t at = v_pos<NT>(g);
+        if (!(ok = bar_wait(&full[at % ST], (at / ST) & 1, 252, failed))) break;
         uint8_t* const vt = s_ring + (at % ST) * C::kStageBytes + (lane & 7) * 16;
         const int base = s.r.base(i), hi = s.r.cached(i), nd = s.r.drafts(i), c0 = nd ? s.r.col(i) : hi, c1 = c0 + nd;
         // cached positions: seen by some row from `first` on, by every row from `all` on
@@ -1144,6 +1273,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       if (!ok) break;
     }
   }
+  if (failed) set_error(st, LMOE_ETIMEOUT, failed);
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) {
@@ -1152,18 +1282,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   }
 }
 
-// Joins the pieces of each cut segment, one warp per row: block x is the CTA in
-// whose range a segment starts, its pieces lie in that CTA's tail slot and the
-// head slots of the CTAs after it.
+// Joins the pieces of each cut segment: block x is the CTA in whose range a segment starts, its pieces lie
+// in that CTA's tail slot and the head slots of the CTAs after it.  A thread joins 4 columns of a row, a
+// block 8 rows; eight pieces are under way at a time.
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum O_i 2^(m_i - M) / L
 template <int D>
-__global__ void __launch_bounds__(256) tree_attn_merge_kernel(const AttnArgs a, int rows) {
+__global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a, int rows) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {  // the call's status: the first CTA's error
+  const int4 c0 = a.cut[2 * blockIdx.x], c1 = a.cut[2 * blockIdx.x + 1];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // the call's status: the first CTA's error
     Status e{0, 0};
-    for (int c = lane; c < a.ctas; c += 32) {
+    for (int c = threadIdx.x; c < a.ctas; c += 32) {
       const Status x = a.err[c];
       if (e.code == 0) e = x;
     }
@@ -1171,60 +1301,46 @@ __global__ void __launch_bounds__(256) tree_attn_merge_kernel(const AttnArgs a, 
     const int from = hit ? __ffs(hit) - 1 : 0;
     e.code = __shfl_sync(0xffffffffu, e.code, from);
     e.where = __shfl_sync(0xffffffffu, e.where, from);
-    if (lane == 0) *a.status = e;
+    if (threadIdx.x == 0) *a.status = e;
   }
-  const int4 c0 = a.cut[2 * blockIdx.x], c1 = a.cut[2 * blockIdx.x + 1];
-  const int pieces = c0.x, local = blockIdx.y * 8 + warp;
+  const int pieces = c0.x, unit = threadIdx.x >> 3, local = blockIdx.y * 8 + (threadIdx.x & 7);
   if (pieces < 2 || local >= c0.z) return;
-  const int rr = c1.x * rows + local;
-  const int i = rr / a.G, tok = c0.y + i, qh = c0.w * a.G + rr - i * a.G;
-  auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)) * rows + local; };
-  // eight pieces' rows are under way at a time, the first ones already beside the maxima
-  constexpr int E = D / 32, U = 8;
-  float o[U][E];
+  auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
+  constexpr int U = 8;
+  float4 o[U];
   auto fetch = [&](int p0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (p0 + u >= pieces) break;
-      const float* x = a.part_o + slot(p0 + u) * D + lane * E;
-      if constexpr (E == 4)
-        *reinterpret_cast<float4*>(o[u]) = *reinterpret_cast<const float4*>(x);
-      else
-        *reinterpret_cast<float2*>(o[u]) = *reinterpret_cast<const float2*>(x);
-    }
+    for (int u = 0; u < U; ++u)
+      if (p0 + u < pieces)
+        o[u] = reinterpret_cast<const float4*>(a.part_o)[(slot(p0 + u) * (D / 4) + unit) * rows + local];
   };
   fetch(0);
   float M = -INFINITY;
-  for (int p = lane; p < pieces; p += 32) M = fmaxf(M, a.part_ml[slot(p)].x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+#pragma unroll 8
+  for (int p = 0; p < pieces; ++p) M = fmaxf(M, a.part_ml[slot(p) * rows + local].x);
   const float mu = M == -INFINITY ? 0.f : M;
-  float acc[E] = {}, L = 0.f, w = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
   for (int p0 = 0; p0 < pieces; p0 += U) {
     if (p0 > 0) fetch(p0);
-    if (p0 % 32 == 0) {  // the weights of 32 pieces, a lane each
-      float lw = 0.f;
-      w = 0.f;
-      if (p0 + lane < pieces) {
-        const float2 ml = a.part_ml[slot(p0 + lane)];
-        w = ex2(ml.x - mu);
-        lw = w * ml.y;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (p0 + u < pieces) {
+        const float2 ml = a.part_ml[slot(p0 + u) * rows + local];
+        const float w = ex2(ml.x - mu);
+        L = fmaf(w, ml.y, L);
+        acc.x = fmaf(w, o[u].x, acc.x);
+        acc.y = fmaf(w, o[u].y, acc.y);
+        acc.z = fmaf(w, o[u].z, acc.z);
+        acc.w = fmaf(w, o[u].w, acc.w);
       }
-      L += warp_sum(lw);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (p0 + u >= pieces) break;
-      const float wp = __shfl_sync(0xffffffffu, w, (p0 + u) & 31);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wp, o[u][e], acc[e]);
-    }
   }
+  const int rr = c1.x * rows + local;
+  const int i = rr / a.G, tok = c0.y + i, qh = c0.w * a.G + rr - i * a.G;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (a.lse && lane == 0)
+  *reinterpret_cast<uint2*>(a.out + ((size_t)tok * (a.hk * a.G) + qh) * D + unit * 4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && unit == 0)
     a.lse[(size_t)tok * (a.hk * a.G) + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
@@ -1278,7 +1394,7 @@ int run_attn(const AttnArgs& a, const CUtensorMap (&tm)[6], int max_rows, cudaSt
   rc = launch_pdl("tree_attn_kernel", dim3(a.ctas), dim3(C::kThreads), C::kSmem, s, tree_attn_kernel<D, NT, KS>, a,
                   tm[0], tm[1], tm[2], tm[3], tm[4], tm[5]);
   if (rc) return rc;
-  return launch_pdl("tree_attn_merge_kernel", dim3(a.ctas, (min(max_rows, C::kRows) + 7) / 8), dim3(256), 0, s,
+  return launch_pdl("tree_attn_merge_kernel", dim3(a.ctas, (min(max_rows, C::kRows) + 7) / 8), dim3(2 * D), 0, s,
                     tree_attn_merge_kernel<D>, a, C::kRows);
 }
 
