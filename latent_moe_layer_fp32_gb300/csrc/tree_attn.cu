@@ -688,34 +688,32 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         for (int hf = 0; hf < 2; ++hf) {
           if (!ready(&p_full[2 * buf + hf], parity, 233 + hf)) return false;
           tc_fence_after();
-          const uint32_t lo = s_lo[buf];
-          if (leader) {
+          const uint32_t lo = s_lo[buf], ph = p + hf * 32;
+          const uint64_t vh = v0 + hf * (64 * 128 >> 4);
+          // with copies of rows a 16-key step goes to the lanes whose copy holds those keys
+          auto lanes = [&](int kk, bool second, uint32_t (&off)[4]) {
+            const int part = KS == 1 ? 0 : KS == 2 ? hf : 2 * hf + (kk >> 1);
 #pragma unroll
-            for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
-              const uint32_t acc = !(first && kk % (8 / KS) == 0);
+            for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == part && (!second || (lo >> (8 * w) & 1u)) ? 0u : 0xffffffffu;
+          };
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t acc = !(first && (KS == 1 ? hf == 0 && kk == 0 : kk % (8 / KS) == 0));
               if constexpr (KS == 1) {
-                tc_mma_bf16_ts(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc);
-              } else {  // a 16-key step goes to the lanes whose copy of the rows holds those keys
+                tc_mma_bf16_ts(o, ph + kk * 8, vh + kk * (16 * 128 >> 4), kPv, acc);
+              } else {
                 uint32_t off[4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) off[w] = w * KS / 4 == kk * KS / 8 ? 0u : 0xffffffffu;
-                tc_mma_bf16_ts_lanes(o, p + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, acc, off);
+                lanes(kk, false, off);
+                tc_mma_bf16_ts_lanes(o, ph + kk * 8, vh + kk * (16 * 128 >> 4), kPv, acc, off);
               }
             }
-            constexpr int kParts = KS == 4 ? 2 : 1;  // copies whose keys lie in this half
-#pragma unroll
-            for (int c = 0; c < kParts; ++c) {  // the second part, for the warps that wrote one
-              const int part = KS == 1 ? 0 : hf * kParts + c;
-              uint32_t off[4], all = 0xffffffffu;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                off[w] = w * KS / 4 == part && (lo >> (8 * w) & 1u) ? 0u : 0xffffffffu;
-                all &= off[w];
-              }
-              if (!all) {
-#pragma unroll
-                for (int kk = 4 * hf + c * (4 / kParts); kk < 4 * hf + (c + 1) * (4 / kParts); ++kk)
-                  tc_mma_bf16_ts_lanes(o, p + kTile / 2 + kk * 8, v0 + kk * (16 * 128 >> 4), kPv, 1u, off);
+            if (lo) {  // the second part, for the warps that wrote one
+#pragma unroll 1
+              for (int kk = 0; kk < 4; ++kk) {
+                uint32_t off[4];
+                lanes(kk, true, off);
+                tc_mma_bf16_ts_lanes(o, ph + kTile / 2 + kk * 8, vh + kk * (16 * 128 >> 4), kPv, 1u, off);
               }
             }
             if (hf == 1) tc_commit(&pv_done[buf]);
@@ -751,90 +749,79 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         seg_done(i);
         return true;
       };
-      uint32_t edges = 0;  // edge tiles that came back from the cleaning warps
-      auto clean = [&](const Part& p, int i) {  // hands tile i to the cleaning warps if it is an edge
-        if (p.edge(i) && leader) mbar_arrive(v_edge);
+      auto clean = [&](const Part& p, int i) {  // hands tile i to the cleaning warp if it is an edge
+        if (p.edge(i) && lane == 0) mbar_arrive(v_edge);
         __syncwarp();
       };
-      // tile i of s is clean; then it is the next tile's turn (one at a time, so that no phase is missed)
-      auto cleaned = [&](int i) {
-        if (s.edge(i) && !bar_wait(v_clean, edges++ & 1, 236, failed)) return false;
-        if (i + 1 < s.i1)
-          clean(s, i + 1);
-        else if (nx.i1 > 0)
-          clean(nx, nx.i0);
-        return true;
-      };
-      uint32_t g = 0, seg = 0;
-      ok = get(0, &s);
+      uint32_t edges = 0;  // edge tiles that came back from the cleaning warp
       uint32_t ks = 0, vs = 0;  // stages of the keys and values in use
-      if constexpr (NT == 1) {
-        auto first_qk = [&](uint32_t nr, uint32_t gt) {  // scores of segment nr's first tile gt
-          if (!ready(&q_full[nr & 1], (nr >> 1) & 1, 232) || !tile(&ks)) return false;
-          qk(nr & 1, gt & 1, ks);
-          commit(&s_first[nr & 1]);
-          commit(&empty[ks]);
-          return true;
-        };
-        if (ok && s.i1 > 0) {
-          clean(s, s.i0);
-          ok = first_qk(0, 0);
-        }
-        while (ok && s.i1 > 0) {
-          for (int i = s.i0; i < s.i1; ++i, ++g) {
-            if (i + 1 < s.i1) {
-              if (!(ok = tile(&ks))) break;
-              qk(seg & 1, (g + 1) & 1, ks);
-              commit(&empty[ks]);
-            } else if (!(ok = get(seg + 1, &nx)) || (nx.i1 > 0 && !(ok = first_qk(seg + 1, g + 1)))) {
-              break;
+      uint32_t nq = 0, np = 0;  // a bit per group (or S buffer): the phase of its queries, of its P
+      // Tile by tile: the scores of the next one (of the same segment, or the next segment's first), and the
+      // product of this one with its values.
+      bool have = false;
+      int i = 0;
+      for (uint32_t seg = 0;;) {
+        const bool same = have && i + 1 < s.i1;
+        if (!same && !(ok = get(seg, &nx))) break;
+        const Part t = same ? s : nx;  // of the next tile
+        const int ti = same ? i + 1 : nx.i0;
+        const bool more = same || nx.i1 > 0;
+        if constexpr (NT == 1) {
+          // group of this segment: seg is one past it
+          const uint32_t tg = (same ? seg - 1 : seg) & 1, tb = have ? (np >> 2 & 1) ^ 1 : 0;
+          if (more) {
+            if (!same) {
+              if (!(ok = ready(&q_full[tg], nq >> tg & 1, 232))) break;
+              nq ^= 1u << tg;
             }
-            if (i + 1 == s.i1 && nx.i1 == 0) skip();
-            if (!(ok = tile(&vs)) || !(ok = cleaned(i))) break;
-            if (!(ok = pv(seg & 1, g & 1, vs, i == s.i0, (g >> 1) & 1))) break;
+            if (!(ok = tile(&ks))) break;
+            qk(tg, tb, ks);
+            if (!same) commit(&s_first[tg]);
+            commit(&empty[ks]);
+          } else if (have) {
+            skip();  // the place before the last values
+          }
+          if (have) {
+            const uint32_t buf = np >> 2 & 1;
+            if (!(ok = tile(&vs))) break;
+            if (s.edge(i) && !(ok = ready(v_clean, edges++ & 1, 236))) break;
+            if (more) clean(t, ti);
+            if (!(ok = pv((seg - 1) & 1, buf, vs, i == s.i0, np >> buf & 1))) break;
             commit(&empty[vs]);
+            np ^= 1u << buf | 4u;  // bit 2: the S buffer of the tile
+          } else if (more) {
+            clean(t, ti);
           }
-          s = nx;
-          ++seg;
-        }
-      } else {
-        // queries of a segment's row tile, then its first scores; per group, the phases so far
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-        auto first_qk = [&](int grp) {
-          if (!ready(&q_full[grp], nq[grp]++ & 1, 232) || (grp == 0 && !tile(&ks))) return false;
-          tc_fence_after();
-          qk(grp, grp, ks);
-          return true;
-        };
-        if (ok && s.i1 > 0) {
-          clean(s, s.i0);
-          ok = first_qk(0) && (s.rows <= kTile || first_qk(1));
-          commit(&empty[ks]);
-        }
-        while (ok && s.i1 > 0) {
-          const bool two = s.rows > kTile;
-          for (int i = s.i0; i < s.i1 && ok; ++i) {
-            const bool same = i + 1 < s.i1;
-            if (!(ok = tile(&vs)) || (!same && !(ok = get(seg + 1, &nx))) || !(ok = cleaned(i))) break;
-            const bool more = same || nx.i1 > 0;
-#pragma unroll
-            for (int grp = 0; grp < 2; ++grp) {
-              if (grp == 0 || two) {
-                if (!(ok = pv(grp, grp, vs, i == s.i0, np[grp]++ & 1))) break;
-                if (grp == 1 || !two) commit(&empty[vs]);
-              }
-              if (same) {
-                if (grp == 0 && !(ok = tile(&ks))) break;
-                if (grp == 0 || two) qk(grp, grp, ks);
-              } else if (more && (grp == 0 || nx.rows > kTile)) {
-                if (!(ok = first_qk(grp))) break;
-              }
+        } else {
+          if (have) {
+            if (!(ok = tile(&vs)) || (s.edge(i) && !(ok = ready(v_clean, edges++ & 1, 236)))) break;
+          }
+          if (more) clean(t, ti);  // (one at a time, so that no phase is missed)
+#pragma unroll 1
+          for (int grp = 0; grp < 2; ++grp) {
+            if (have && (grp == 0 || s.rows > kTile)) {
+              if (!(ok = pv(grp, grp, vs, i == s.i0, np >> grp & 1))) break;
+              np ^= 1u << grp;
+              if (grp == 1 || s.rows <= kTile) commit(&empty[vs]);
             }
-            if (ok && more) commit(&empty[ks]);
+            if (more && (grp == 0 || t.rows > kTile)) {
+              if (!same) {
+                if (!(ok = ready(&q_full[grp], nq >> grp & 1, 232))) break;
+                nq ^= 1u << grp;
+              }
+              if (grp == 0 && !(ok = tile(&ks))) break;
+              tc_fence_after();
+              qk(grp, grp, ks);
+            }
           }
-          s = nx;
-          ++seg;
+          if (!ok) break;
+          if (more) commit(&empty[ks]);
         }
+        if (!more) break;
+        if (!same) ++seg;
+        s = t;
+        i = ti;
+        have = true;
       }
       commit(done);  // every MMA issued has completed before TMEM is released
       bar_wait(done, 0, 235, failed);
@@ -1111,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           for (int u = 0; u < N / 8; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[u][j] = pack_bf16(y[u * 8 + 2 * j] * inv, y[u * 8 + 2 * j + 1] * inv);
-          if constexpr (KS == 1) {  // 128 rows' worth of 16-byte stores would queue up: 128 bytes of a row at a time
+          if constexpr (KS == 1) {  // 128 rows' worth of 16-byte stores would queue up: 64 bytes of a row at a time
             store_rows<N / 8>(w, dst);
           } else if (dst) {
 #pragma unroll
@@ -1129,8 +1116,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         if (warp_live) {
 #pragma unroll 1
-          for (int col = 0; col < D; col += 64) {
-            float y[64];
+          for (int col = 0; col < D; col += 32) {
+            float y[32];
             sums(col, y);
             put(col, y, inv);
           }
