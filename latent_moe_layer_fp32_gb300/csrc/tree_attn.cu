@@ -1271,7 +1271,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 
 // Joins the pieces of each cut segment: block x is the CTA in whose range a segment starts, its pieces lie
 // in that CTA's tail slot and the head slots of the CTAs after it.  A thread joins 4 columns of a row, a
-// block 8 rows; eight pieces are under way at a time.
+// block 8 rows; eight pieces are under way at a time
+// (what there is so far is rescaled for them).
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum O_i 2^(m_i - M) / L
 template <int D>
 __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a, int rows) {
@@ -1294,28 +1295,32 @@ __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a
   if (pieces < 2 || local >= c0.z) return;
   auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
   constexpr int U = 8;
-  float4 o[U];
-  auto fetch = [&](int p0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (p0 + u < pieces)
-        o[u] = reinterpret_cast<const float4*>(a.part_o)[(slot(p0 + u) * (D / 4) + unit) * rows + local];
-  };
-  fetch(0);
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int p = 0; p < pieces; ++p) M = fmaxf(M, a.part_ml[slot(p) * rows + local].x);
-  const float mu = M == -INFINITY ? 0.f : M;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
+  float M = -INFINITY, L = 0.f;
   for (int p0 = 0; p0 < pieces; p0 += U) {
-    if (p0 > 0) fetch(p0);
+    float4 o[U];
+    float2 ml[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p0 + u < pieces) {
+        ml[u] = a.part_ml[slot(p0 + u) * rows + local];
+        o[u] = reinterpret_cast<const float4*>(a.part_o)[(slot(p0 + u) * (D / 4) + unit) * rows + local];
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+    const float mu = top == -INFINITY ? 0.f : top, f = ex2(M - mu);
+    M = top;
+    L *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (p0 + u < pieces) {
-        const float2 ml = a.part_ml[slot(p0 + u) * rows + local];
-        const float w = ex2(ml.x - mu);
-        L = fmaf(w, ml.y, L);
+        const float w = ex2(ml[u].x - mu);
+        L = fmaf(w, ml[u].y, L);
         acc.x = fmaf(w, o[u].x, acc.x);
         acc.y = fmaf(w, o[u].y, acc.y);
         acc.z = fmaf(w, o[u].z, acc.z);
