@@ -24,7 +24,7 @@ __all__ = [
     "lmoe_block_forward", "norms_of", "lmoe_experts_nvfp4", "lmoe_forward_nvfp4", "nvfp4_of",
     "lmoe_status_check", "lmoe_error_string",
     "lmoe_last_launch_count", "lmoe_selftest_e2m1", "lmoe_selftest_timeout", "lmoe_profile_events", "dims_of",
-    "weights_of", "LmoeKvCache", "LmoeAttnDims", "kv_cache_of", "attn_dims_of", "lmoe_tree_masks",
+    "weights_of", "LmoeKvCache", "LmoeKvMaps", "LmoeAttnDims", "kv_cache_of", "attn_dims_of", "lmoe_tree_masks",
     "lmoe_tree_attention", "lmoe_tree_attention_workspace_bytes", "lmoe_kv_plan", "lmoe_kv_write",
 ]
 
@@ -60,7 +60,12 @@ class LmoeWsLayout(ctypes.Structure):
 class LmoeKvCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("maps", ctypes.c_void_p)]
+
+
+class LmoeKvMaps(ctypes.Structure):
+    _fields_ = [("made_for", ctypes.c_uint64 * 8), ("map", ctypes.c_uint64 * 64)]
 
 
 class LmoeAttnDims(ctypes.Structure):
@@ -126,8 +131,9 @@ def load(path: str | None = None):
     lib.lmoe_tree_attention_workspace_bytes.restype = sz
     lib.lmoe_tree_attention.argtypes = [ap, cp, vp, i64, vp, i64, vp, i64] + [vp] * 8 + [sz, vp]
     lib.lmoe_kv_plan.argtypes = [i32] * 4 + [vp] * 5 + [i32] + [vp] * 7
+    lib.lmoe_kv_maps_init.argtypes = [cp, ctypes.POINTER(LmoeKvMaps)]
     lib.lmoe_kv_write.argtypes = [cp, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz, vp]
-    for f in ("lmoe_tree_masks", "lmoe_tree_attention", "lmoe_kv_plan", "lmoe_kv_write",
+    for f in ("lmoe_tree_masks", "lmoe_kv_maps_init", "lmoe_tree_attention", "lmoe_kv_plan", "lmoe_kv_write",
               "lmoe_workspace_layout", "lmoe_route", "lmoe_pool", "lmoe_experts_mxfp4", "lmoe_norm_combine_unpool",
               "lmoe_forward", "lmoe_forward_routed", "lmoe_block_forward", "lmoe_forward_nvfp4", "lmoe_experts_nvfp4",
               "lmoe_status_check", "lmoe_last_launch_count", "lmoe_selftest_e2m1",
@@ -160,6 +166,17 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
+
+
+try:  # the current stream's address without a Stream object
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getDevice as _device
+except ImportError:  # a torch built without them
+    def _device():
+        return torch.cuda.current_device()
+
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream):
@@ -315,14 +332,53 @@ def lmoe_block_forward(dims, weights: LmoeWeights, norms: LmoeBlockNorms, x, y, 
 # speculative decoding over a paged key/value cache
 # ---------------------------------------------------------------------------------------------
 
+# These calls take a few microseconds on the GPU, so their marshalling is kept short: one test per
+# tensor, addresses passed as plain integers, the current stream asked for without a Stream object.
+
 _I64 = (torch.int64, torch.uint64)
 _BF16_ONLY = (torch.bfloat16,)
+
+
+def _arg(t, n, dtypes, what):
+    """Address of a contiguous CUDA tensor of at least n elements (None for None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor")
+    if t.dtype in dtypes and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    _ptr(t, dtypes)  # raises for all but the size
+    raise ValueError(f"{what}: expected at least {n} elements, got {t.numel()}")
+
+
+def _rows(t, heads, width, what="rows"):
+    """Address and row stride of a bf16 CUDA tensor [rows, heads, width] whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{what}: unexpected dtype {t.dtype}, want torch.bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor (the library takes device pointers)")
+    shape, st = t.shape, t.stride()
+    if len(st) != 3 or shape[1] != heads or shape[2] != width or st[2] != 1 or (heads > 1 and st[1] != width):
+        raise ValueError(f"{what}: expected [rows, {heads}, {width}] with contiguous rows, got {tuple(shape)} with "
+                         f"strides {tuple(st)}")
+    return t.data_ptr(), st[0] if shape[0] > 1 else heads * width
+
+
+def _stream_arg(stream):
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
+
+
+def _ws_arg(ws):
+    return (None, 0) if ws is None else (_arg(ws, 0, (ws.dtype,), "ws"), ws.numel() * ws.element_size())
 
 
 def kv_cache_of(k, v) -> LmoeKvCache:
     """LmoeKvCache of two bf16 tensors [n_blocks, kv_heads, block_size, head_dim] of equal
     strides; any order in memory with head_dim contiguous (a [block][slot][head][d] cache
-    is passed as its transpose(1, 2)).  The caller keeps the tensors alive."""
+    is passed as its transpose(1, 2)), with its copy descriptors.  The caller keeps the
+    tensors alive."""
     for t in (k, v):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError("expected CUDA tensors (the library takes device pointers)")
@@ -333,38 +389,17 @@ def kv_cache_of(k, v) -> LmoeKvCache:
     if k.shape != v.shape or k.stride() != v.stride():
         raise ValueError("k and v must have the same shape and strides")
     n, h, b, d = k.shape
-    return LmoeKvCache(k.data_ptr(), v.data_ptr(), n, b, h, d, k.stride(0), k.stride(1), k.stride(2))
+    cache = LmoeKvCache(k.data_ptr(), v.data_ptr(), n, b, h, d, k.stride(0), k.stride(1), k.stride(2), None)
+    maps = LmoeKvMaps()
+    _check(load().lmoe_kv_maps_init(ctypes.byref(cache), ctypes.byref(maps)), "lmoe_kv_maps_init")
+    cache.maps = ctypes.addressof(maps)
+    cache._maps = maps  # lives as long as the descriptor
+    return cache
 
 
 def attn_dims_of(n_requests, n_tokens, max_request_tokens, q_heads, max_blocks, mask_words, scale,
                  window=0) -> LmoeAttnDims:
     return LmoeAttnDims(n_requests, n_tokens, max_request_tokens, q_heads, max_blocks, mask_words, window, scale)
-
-
-def _rows(t, heads, width):
-    """Address and row stride of a bf16 [rows, heads, width] tensor whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("expected a torch tensor")
-    if t.dtype not in _BF16_ONLY:
-        raise TypeError(f"unexpected dtype {t.dtype}, want torch.bfloat16")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor (the library takes device pointers)")
-    st = t.stride()
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != width or st[2] != 1 or (heads > 1 and st[1] != width):
-        raise ValueError(f"expected [rows, {heads}, {width}] with contiguous rows, got {tuple(t.shape)} with strides "
-                         f"{tuple(st)}")
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * width
-
-
-def _sized(t, n, dtype, what):
-    p = _ptr(t, dtype)
-    if t is not None and t.numel() < n:
-        raise ValueError(f"{what}: expected at least {n} elements, got {t.numel()}")
-    return p
-
-
-def _ws(ws):
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
 
 
 def lmoe_tree_masks(token_offsets, parents, lens, mask, pos, ws=None, stream=None):
@@ -373,10 +408,12 @@ def lmoe_tree_masks(token_offsets, parents, lens, mask, pos, ws=None, stream=Non
     b, t = token_offsets.numel() - 1, parents.numel()
     if mask.dim() != 2 or mask.shape[0] != t:
         raise ValueError(f"mask: expected [{t}, mask_words], got {tuple(mask.shape)}")
-    w, nb = _ws(ws)
-    _check(load().lmoe_tree_masks(b, t, mask.shape[1], _ptr(token_offsets, _I32), _ptr(parents, _I32),
-                                  _sized(lens, b, _I32, "lens"), _ptr(mask, _I64), _sized(pos, t, _I32, "pos"), w, nb,
-                                  _stream(stream)), "lmoe_tree_masks")
+    w, nb = _ws_arg(ws)
+    rc = load().lmoe_tree_masks(b, t, mask.shape[1], _arg(token_offsets, 2, _I32, "token_offsets"),
+                                _arg(parents, 1, _I32, "parents"), _arg(lens, b, _I32, "lens"),
+                                _arg(mask, 1, _I64, "mask"), _arg(pos, t, _I32, "pos"), w, nb, _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_tree_masks")
 
 
 def lmoe_tree_attention_workspace_bytes(dims: LmoeAttnDims, cache: LmoeKvCache) -> int:
@@ -387,18 +424,20 @@ def lmoe_tree_attention(dims, cache, q, k_new, v_new, token_offsets, lens, block
                         stream=None):
     """Drafted rows over the cached prefix and the tree of drafts.  q [T, q_heads, d], k_new and
     v_new [T, kv_heads, d] may be slices of one projection; mask, pos and lse may be None."""
-    n, d = dims.n_tokens, cache.head_dim
-    (qp, qs), (kp, ks), (vp, vs) = (_rows(q, dims.q_heads, d), _rows(k_new, cache.kv_heads, d),
-                                    _rows(v_new, cache.kv_heads, d))
-    if min(q.shape[0], k_new.shape[0], v_new.shape[0]) < n:
+    n, b, hq, hk, d = dims.n_tokens, dims.n_requests, dims.q_heads, cache.kv_heads, cache.head_dim
+    qp, qs = _rows(q, hq, d, "q")
+    kp, ks = _rows(k_new, hk, d, "k_new")
+    vp, vs = _rows(v_new, hk, d, "v_new")
+    if q.shape[0] < n or k_new.shape[0] < n or v_new.shape[0] < n:
         raise ValueError(f"expected {n} rows in q, k_new and v_new")
-    _check(load().lmoe_tree_attention(
+    rc = load().lmoe_tree_attention(
         ctypes.byref(dims), ctypes.byref(cache), qp, qs, kp, ks, vp, vs,
-        _sized(token_offsets, dims.n_requests + 1, _I32, "token_offsets"), _sized(lens, dims.n_requests, _I32, "lens"),
-        _sized(block_table, dims.n_requests * dims.max_blocks, _I32, "block_table"),
-        _sized(mask, n * dims.mask_words, _I64, "mask"), _sized(pos, n, _I32, "pos"),
-        _sized(out, n * dims.q_heads * d, _BF16, "out"), _sized(lse, n * dims.q_heads, _F32, "lse"), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)), "lmoe_tree_attention")
+        _arg(token_offsets, b + 1, _I32, "token_offsets"), _arg(lens, b, _I32, "lens"),
+        _arg(block_table, b * dims.max_blocks, _I32, "block_table"), _arg(mask, n * dims.mask_words, _I64, "mask"),
+        _arg(pos, n, _I32, "pos"), _arg(out, n * hq * d, _BF16, "out"), _arg(lse, n * hq, _F32, "lse"), *_ws_arg(ws),
+        _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_tree_attention")
 
 
 def lmoe_kv_plan(block_size, lens, new_tokens, owned, block_table, ring, ring_state, lens_out, owned_out,
@@ -407,23 +446,27 @@ def lmoe_kv_plan(block_size, lens, new_tokens, owned, block_table, ring, ring_st
     b = lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError(f"block_table: expected [{b}, max_blocks], got {tuple(block_table.shape)}")
-    _check(load().lmoe_kv_plan(
-        b, int(block_size), block_table.shape[1], slots.numel(), _ptr(lens, _I32),
-        _sized(new_tokens, b, _I32, "new_tokens"), _sized(owned, b, _I32, "owned"), _ptr(block_table, _I32),
-        _ptr(ring, _I32), ring.numel(), _sized(ring_state, 2, _I32, "ring_state"),
-        _sized(lens_out, b, _I32, "lens_out"), _sized(owned_out, b, _I32, "owned_out"),
-        _sized(ring_state_out, 2, _I32, "ring_state_out"), _sized(token_offsets, b + 1, _I32, "token_offsets"),
-        _ptr(slots, _I32), _stream(stream)), "lmoe_kv_plan")
+    rc = load().lmoe_kv_plan(
+        b, block_size, block_table.shape[1], slots.numel(), _arg(lens, 1, _I32, "lens"),
+        _arg(new_tokens, b, _I32, "new_tokens"), _arg(owned, b, _I32, "owned"),
+        _arg(block_table, 1, _I32, "block_table"), _arg(ring, 1, _I32, "ring"), ring.numel(),
+        _arg(ring_state, 2, _I32, "ring_state"), _arg(lens_out, b, _I32, "lens_out"),
+        _arg(owned_out, b, _I32, "owned_out"), _arg(ring_state_out, 2, _I32, "ring_state_out"),
+        _arg(token_offsets, b + 1, _I32, "token_offsets"), _arg(slots, 1, _I32, "slots"), _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_kv_plan")
 
 
 def lmoe_kv_write(cache, k_new, v_new, src, slots, ws=None, stream=None):
     """Rows src[t] (or t, src None) of k_new and v_new [rows, kv_heads, d] into the cache's slots[t]."""
-    (kp, ks), (vp, vs) = (_rows(k_new, cache.kv_heads, cache.head_dim), _rows(v_new, cache.kv_heads, cache.head_dim))
-    n = slots.numel()
-    w, nb = _ws(ws)
-    _check(load().lmoe_kv_write(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
-                                _sized(src, n, _I32, "src"), _ptr(slots, _I32), n, w, nb, _stream(stream)),
-           "lmoe_kv_write")
+    hk, d, n = cache.kv_heads, cache.head_dim, slots.numel()
+    kp, ks = _rows(k_new, hk, d, "k_new")
+    vp, vs = _rows(v_new, hk, d, "v_new")
+    w, nb = _ws_arg(ws)
+    rc = load().lmoe_kv_write(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
+                              _arg(src, n, _I32, "src"), _arg(slots, 1, _I32, "slots"), n, w, nb, _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_kv_write")
 
 
 def lmoe_status_check(ws, stream=None) -> int:

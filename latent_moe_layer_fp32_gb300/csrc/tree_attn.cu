@@ -29,6 +29,7 @@
 // no bits of an unseen key reach a product.
 #include <atomic>
 #include <cmath>
+#include <cstring>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -1336,6 +1337,40 @@ __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a
     a.lse[(size_t)tok * (a.hk * a.G) + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
+// What a cache's copy descriptors depend on.
+void maps_key(const lmoe_kv_cache* c, uint64_t (&key)[8]) {
+  key[0] = reinterpret_cast<uintptr_t>(c->k);
+  key[1] = reinterpret_cast<uintptr_t>(c->v);
+  key[2] = (uint64_t)(uint32_t)c->n_blocks << 32 | (uint32_t)c->block_size;
+  key[3] = (uint64_t)(uint32_t)c->kv_heads << 32 | (uint32_t)c->head_dim;
+  key[4] = (uint64_t)c->block_stride;
+  key[5] = (uint64_t)c->head_stride;
+  key[6] = (uint64_t)c->slot_stride;
+  key[7] = 1;
+}
+
+// The cache as [block][head][slot][d], copied 64 columns by one page (at most a tile) at a time: K, V; and
+// by 8 slots: K, V.
+int make_maps(const lmoe_kv_cache* c, lmoe_kv_maps* m) {
+  static_assert(sizeof(m->map[0]) == sizeof(CUtensorMap), "a map's size");
+  // a dimension of extent 1 never steps: any valid stride will do
+  auto stride = [](int64_t elements, int64_t extent) { return (uint64_t)(extent > 1 ? elements : 64) * 2; };
+  const uint64_t dims[4] = {(uint64_t)c->head_dim, (uint64_t)c->block_size, (uint64_t)c->kv_heads,
+                            (uint64_t)c->n_blocks};
+  const uint64_t strides[3] = {stride(c->slot_stride, c->block_size), stride(c->head_stride, c->kv_heads),
+                               stride(c->block_stride, c->n_blocks)};
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t box[4] = {64, i < 2 ? (uint32_t)min(c->block_size, kTile) : 8u, 1, 1};
+    CUtensorMap t;
+    if (encode_tmap(&t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i & 1 ? c->v : c->k, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return LMOE_ECUDA;
+    std::memcpy(m->map[i], &t, sizeof(t));
+  }
+  maps_key(c, m->made_for);
+  return LMOE_OK;
+}
+
 bool al(const void* p, unsigned n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int check_attn(const lmoe_attn_dims* d, const lmoe_kv_cache* c, bool memory) {
@@ -1408,6 +1443,13 @@ using namespace lmoe;
 
 extern "C" {
 
+int lmoe_kv_maps_init(const lmoe_kv_cache* cache, lmoe_kv_maps* maps) {
+  const int rc = check_cache(cache, true);
+  if (rc) return rc;
+  if (!maps) return LMOE_EINVAL;
+  return make_maps(cache, maps);
+}
+
 size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
   if (check_attn(d, c, false) != LMOE_OK) return 0;
   DevInfo di;
@@ -1432,29 +1474,26 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
   if ((rc = dev_info(&di))) return rc;
   const AttnWs w = attn_ws(d, c, di.sms);
   if (ws_bytes < w.total) return LMOE_EWORKSPACE;
-  // tensor maps: the cache as [block][head][slot][d], copied 64 columns by one page (at most a
-  // tile) or by 8 slots at a time; the drafts as [token][head][d], 64 columns by 8 tokens
+  // tensor maps: those of the cache, and the drafts as [token][head][d], 64 columns by 8 tokens
   CUtensorMap tm[6];
-  const uint16_t* const base[4] = {c->k, c->v, k_new, v_new};
+  lmoe_kv_maps own;
+  const lmoe_kv_maps* maps = c->maps;
+  maps_key(c, own.made_for);
+  if (!maps || std::memcmp(maps->made_for, own.made_for, sizeof(own.made_for)) != 0) {
+    if ((rc = make_maps(c, &own))) return rc;
+    maps = &own;
+  }
+  std::memcpy(&tm[0], maps->map[0], sizeof(CUtensorMap));
+  std::memcpy(&tm[1], maps->map[1], sizeof(CUtensorMap));
+  std::memcpy(&tm[4], maps->map[2], sizeof(CUtensorMap));
+  std::memcpy(&tm[5], maps->map[3], sizeof(CUtensorMap));
+  const uint16_t* const fresh[2] = {k_new, v_new};
   const uint64_t step[2] = {(uint64_t)k_stride * 2, (uint64_t)v_stride * 2};
-  // a dimension of extent 1 never steps: any valid stride will do
-  auto stride = [](int64_t elements, int64_t extent) { return (uint64_t)(extent > 1 ? elements : 64) * 2; };
   for (int i = 0; i < 2; ++i) {
-    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)c->block_size, (uint64_t)c->kv_heads, (uint64_t)c->n_blocks};
-    const uint64_t strides[3] = {stride(c->slot_stride, c->block_size), stride(c->head_stride, c->kv_heads),
-                                 stride(c->block_stride, c->n_blocks)};
-    const uint32_t box[4] = {64, (uint32_t)min(c->block_size, kTile), 1, 1};
-    if (encode_tmap(&tm[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box,
-                    CU_TENSOR_MAP_SWIZZLE_128B))
-      return LMOE_ECUDA;
-    const uint32_t box8[4] = {64, 8, 1, 1};
-    if (encode_tmap(&tm[4 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box8,
-                    CU_TENSOR_MAP_SWIZZLE_128B))
-      return LMOE_ECUDA;
-    const uint64_t ndims[3] = {(uint64_t)D, (uint64_t)c->kv_heads, (uint64_t)d->n_tokens};
-    const uint64_t nstrides[2] = {(uint64_t)D * 2, step[i]};
-    const uint32_t nbox[3] = {64, 1, 8};
-    if (encode_tmap(&tm[2 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base[2 + i], ndims, nstrides, nbox,
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)c->kv_heads, (uint64_t)d->n_tokens};
+    const uint64_t strides[2] = {(uint64_t)D * 2, step[i]};
+    const uint32_t box[3] = {64, 1, 8};
+    if (encode_tmap(&tm[2 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, fresh[i], dims, strides, box,
                     CU_TENSOR_MAP_SWIZZLE_128B))
       return LMOE_ECUDA;
   }

@@ -339,6 +339,32 @@ def test_another_stream_and_a_graph(lm):
     assert torch.equal(c.check(lm), out)
 
 
+def test_copy_descriptors_of_another_cache_are_not_used(lm):
+    # a descriptor whose fields changed after its maps were made, and one without maps
+    c = Case([300, 90], [8, 3], hq=16, hk=2, d=128, seed=37)
+    ref = c.check(lm)
+    made = lm.kv_cache_of
+
+    def stale(k, v):
+        cache = made(torch.zeros_like(k), torch.zeros_like(v))
+        cache.k, cache.v = k.data_ptr(), v.data_ptr()
+        return cache
+
+    def bare(k, v):
+        cache = made(k, v)
+        cache.maps = None
+        return cache
+
+    class Lm:
+        def __getattr__(self, name):
+            return getattr(lm, name)
+
+    for of in (stale, bare):
+        other = Lm()
+        other.kv_cache_of = of
+        assert torch.equal(c.run(other)[0], ref)
+
+
 def test_device_checks(lm):
     # a bad request is reported and skipped, the others are computed
     c = Case([40, 50, 60], [3, 3, 3], seed=29)

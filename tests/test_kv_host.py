@@ -70,6 +70,14 @@ def test_cache_descriptors(lib):
         assert write(cache(), **bad) == EINVAL, bad
 
 
+def test_copy_descriptors_refuse(lib):
+    m = lm.LmoeKvMaps()
+    assert lib.lmoe_kv_maps_init(ctypes.byref(cache(k=0)), ctypes.byref(m)) == EINVAL
+    assert lib.lmoe_kv_maps_init(ctypes.byref(cache(head_dim=96)), ctypes.byref(m)) == EUNSUPPORTED
+    assert lib.lmoe_kv_maps_init(ctypes.byref(cache()), None) == EINVAL
+    assert lib.lmoe_kv_maps_init(None, ctypes.byref(m)) == EINVAL
+
+
 def test_workspace_bytes(lib):
     assert lm.lmoe_tree_attention_workspace_bytes(dims(), cache()) >= 8
     # only the heads and the width of the cache count
