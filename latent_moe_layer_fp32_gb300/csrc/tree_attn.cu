@@ -100,20 +100,23 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int whe
   return false;
 }
 
-// How the line of tiles is measured for the cut into equal ranges: a tile of two row tiles, of one, and
-// the end of a segment.  Of two row tiles the second comes at half the price of the first (the products
-// of one run during the softmax of the other), and a segment's end costs about a tile.
+// How the line of tiles is measured for the cut into equal ranges: a tile of two row tiles, of one, and the
+// end of a segment (its sums joined and stored, the next one's queries, masks and first tiles).  Measured:
+// the ends at two and a half tiles instead of half a one took 16 requests of 1000 to 32768 positions from
+// 136 to 126 us; of two row tiles, at 18 instead of 3, 32 requests with 33 to 64 drafts from 253 to 221 us.
+// A range has to hold the start of a tile, so with few tiles the ends count less (end_cost).
 template <int NT>
 struct Cost {
-  static constexpr int kTwo = NT == 2 ? 3 : 2, kOne = 2, kEnd = NT == 2 ? 3 : 1;
+  static constexpr int kTwo = NT == 2 ? 3 : 2, kOne = 2, kEnd = NT == 2 ? 18 : 5;
 };
 
 struct Load {
-  int groups;        // row groups
+  int groups;        // row groups: a segment each per kv head
   int last;          // cost of a tile of the last group
-  long long head;    // cost of a kv head
-  long long units;   // of the request
+  long long head;    // cost of a kv head's tiles
   bool bad;
+  // of the request, with `end` for each segment's end
+  __device__ __forceinline__ long long units(int hk, int end) const { return hk * (head + (long long)groups * end); }
 };
 
 template <int NT, int ROWS>
@@ -137,10 +140,7 @@ __device__ __forceinline__ Load load_req(const AttnArgs& a, int b, Req* r) {
   r->nt = r->np + (r->c0 ? 0 : (r->n + kTile - 1) >> 7);
   w.groups = (r->n * a.G + ROWS - 1) / ROWS;
   w.last = r->n * a.G - (w.groups - 1) * ROWS > kTile ? Cost<NT>::kTwo : Cost<NT>::kOne;
-  w.head = w.groups == 0 ? 0
-                         : (long long)(w.groups - 1) * ((long long)r->nt * Cost<NT>::kTwo + Cost<NT>::kEnd) +
-                               (long long)r->nt * w.last + Cost<NT>::kEnd;
-  w.units = a.hk * w.head;
+  w.head = w.groups == 0 ? 0 : (long long)r->nt * ((long long)(w.groups - 1) * Cost<NT>::kTwo + w.last);
   return w;
 }
 
@@ -151,13 +151,14 @@ struct Place {
 };
 
 template <int NT>
-__device__ __forceinline__ Place place(const Load& w, int nt, long long off) {
+__device__ __forceinline__ Place place(const Load& w, int nt, int end, long long off) {
   Place p;
-  p.h = (int)quot(off, w.head);
-  const long long r = off - p.h * w.head, group = (long long)nt * Cost<NT>::kTwo + Cost<NT>::kEnd;
+  const long long head = w.units(1, end);
+  p.h = (int)quot(off, head);
+  const long long r = off - p.h * head, group = (long long)nt * Cost<NT>::kTwo + end;
   p.m = w.groups == 1 ? 0 : min((int)quot(r, group), w.groups - 1);
   p.tile = p.m == w.groups - 1 ? w.last : Cost<NT>::kTwo;
-  p.start = p.h * w.head + p.m * group;
+  p.start = p.h * head + p.m * group;
   return p;
 }
 
@@ -175,21 +176,22 @@ static_assert(sizeof(Seg) == 64, "four 16-byte pieces");
 template <int NT, int ROWS>
 struct Walk {
   const AttnArgs& a;
-  int b;
+  int b, cost;         // request; of a segment's end
   long long off, end;  // where the range goes on and where it ends, from request b's start
   __device__ bool next(Seg* s) {
     while (off < end) {
       const Load w = load_req<NT, ROWS>(a, b, &s->r);
-      if (off >= w.units) {
-        off -= w.units;
-        end -= w.units;
+      const long long units = w.units(a.hk, cost);
+      if (off >= units) {
+        off -= units;
+        end -= units;
         ++b;
         continue;
       }
       const int nt = s->r.nt;
-      const Place p = place<NT>(w, nt, off);
+      const Place p = place<NT>(w, nt, cost, off);
       const int i0 = (int)quot(off - p.start + p.tile - 1, p.tile);
-      off = p.start + (long long)nt * p.tile + Cost<NT>::kEnd;
+      off = p.start + (long long)nt * p.tile + cost;
       if (i0 >= nt) continue;
       const int i1 = (int)min((long long)nt, (long long)quot(max(end - p.start, 0ll) + p.tile - 1, p.tile));
       if (i1 <= i0) return false;
@@ -440,8 +442,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   uint64_t* join = seg_empty + 4;     // [group] its four warps meet (a barrier whose wait is bounded)
   uint64_t* done = join + 2;
   long long* s_start = reinterpret_cast<long long*>(done + 1);  // request, units into it, units in the range
-  unsigned long long* s_warp = reinterpret_cast<unsigned long long*>(s_start + 3);  // [threads / 32]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_warp + 12);
+  unsigned long long* s_warp = reinterpret_cast<unsigned long long*>(s_start + 3);  // [threads / 32][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_warp + 24);
   volatile uint32_t* s_lo = tmem_slot + 1;     // [S buffer] a byte per warp: P has a second part
   volatile uint32_t* s_dirty = tmem_slot + 3;  // [segment % 4] segment + 1 where a value was not finite
   Seg* s_seg = reinterpret_cast<Seg*>(reinterpret_cast<uint8_t*>(full) + 1024);  // [segment % 4]
@@ -479,40 +481,48 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   pdl_trigger();
 
   // ---- this CTA's range of the line of tiles ----
+  int end_cost;  // of a segment's end
   if (tid == 0) *st = Status{0, 0};
   {
     const int per = (a.B + C::kThreads - 1) / C::kThreads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    unsigned long long mine = 0;
+    unsigned long long tiles = 0, segs = 0;  // of this thread's requests: the tiles' cost, the segments
     bool bad = false;
     Req r0{};
     Load w0{};
     for (int b = b0; b < b1; ++b) {
       Req r;
       const Load w = load_req<NT, ROWS>(a, b, &r);
-      mine += w.units;
+      tiles += a.hk * w.head;
+      segs += (unsigned)(a.hk * w.groups);
       bad |= w.bad;
       if (b == b0) r0 = r, w0 = w;
     }
-    unsigned long long x = mine;
+    unsigned long long x = tiles, y = segs;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const unsigned long long x1 = __shfl_up_sync(0xffffffffu, x, o), y1 = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) x += x1, y += y1;
     }
-    if (lane == 31) s_warp[warp] = x;
+    if (lane == 31) s_warp[2 * warp] = x, s_warp[2 * warp + 1] = y;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    unsigned long long before = x - mine, total = 0;
+    unsigned long long tiles_before = x - tiles, segs_before = y - segs, all_tiles = 0, all_segs = 0;
     for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w < warp) before += s_warp[w];
-      total += s_warp[w];
+      if (w < warp) tiles_before += s_warp[2 * w], segs_before += s_warp[2 * w + 1];
+      all_tiles += s_warp[2 * w];
+      all_segs += s_warp[2 * w + 1];
     }
+    // the most that leaves every CTA a range with the start of a tile
+    end_cost = (int)min((long long)Cost<NT>::kEnd,
+                        max(0ll, (long long)quot(all_tiles, a.ctas) - Cost<NT>::kTwo));
+    const unsigned long long before = tiles_before + segs_before * end_cost, mine = tiles + segs * end_cost;
+    const unsigned long long total = all_tiles + all_segs * end_cost;
     if (bad) set_error(st, LMOE_EDEVICE_CHECK, 211);
     // ranges, each long enough to hold the start of a tile
-    constexpr int kLong = Cost<NT>::kTwo + Cost<NT>::kEnd;
-    const unsigned long long n = total ? max(1ull, min((unsigned long long)a.ctas, total / kLong)) : 0ull;
+    const unsigned long long n =
+        total ? max(1ull, min((unsigned long long)a.ctas, quot(total, Cost<NT>::kTwo + end_cost))) : 0ull;
     const unsigned long long c = blockIdx.x;
     if (c < n) {
       // the threads whose requests hold the range's first and last unit
@@ -526,8 +536,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           at = before;
           for (;; ++b) {
             w = load_req<NT, ROWS>(a, b, &r);
-            if (u < at + w.units) break;
-            at += w.units;
+            const unsigned long long units = w.units(a.hk, end_cost);
+            if (u < at + units) break;
+            at += units;
           }
         }
         return b;
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         // does the range's last segment start in it and have tiles past it?  Then its last CTA is the
         // first one whose range ends after the start of the segment's last tile
         find(u1 - 1);
-        const Place p = place<NT>(w, r.nt, (long long)(u1 - 1 - at));
+        const Place p = place<NT>(w, r.nt, end_cost, (long long)(u1 - 1 - at));
         const unsigned long long start = at + p.start, in = u1 - 1 - start;
         int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
         if (start >= u0 && quot(in, p.tile) + 1 < (unsigned)r.nt) {
@@ -582,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const int ppt = kTile / box;                  // pages per such tile
     uint32_t g = 0, seg = 0, issued = 0;          // issued: past the last ring position that was issued
     bool ok = true;
-    Walk<NT, ROWS> walk{a, (int)s_start[0], s_start[1], s_start[1] + s_start[2]};
+    Walk<NT, ROWS> walk{a, (int)s_start[0], end_cost, s_start[1], s_start[1] + s_start[2]};
     for (;; ++seg) {
       // the keys' producer walks the range and posts each segment's record, the others read it
       Seg s{};
