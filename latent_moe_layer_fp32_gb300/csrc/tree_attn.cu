@@ -898,8 +898,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         q_loaded();
       }
       early = false;
-      auto draft = [&] { return valid ? (s->m * C::kRows + local) / a.G : 0; };  // the row's draft, its position
-      auto at_pos = [&](int vi) { return a.window > 0 ? draft_pos(a, s->r.t0, s->r.n, s->r.len, vi) : 0; };
+      const int vi = valid ? (s->m * C::kRows + local) / a.G : 0;  // the row's draft
+      auto at_pos = [&] { return a.window > 0 ? draft_pos(a, s->r.t0, s->r.n, s->r.len, vi) : 0; };
       // m_ref: the maximum that P refers to; l: the row's sum.  A tile whose maximum stays below
       // `limit` takes the plain path: no rescaling of O, one part of P.
       float m_ref = -INFINITY, l = 0.f, limit = valid ? -INFINITY : INFINITY;
@@ -908,6 +908,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const int i = i0 + k;
         const uint32_t gt = g + k, go = g_own + k;
         const uint32_t buf = NT == 1 ? gt & 1 : grp;
+        const bool edge = (i < cut || i >= full_from) && warp_live;
+        ulonglong2 bits = make_ulonglong2(0, 0);
+        if (edge) bits = edge_bits(a, s, i, vi, at_pos());  // (before the wait, which hides its loads)
         if (NT == 1 && k == 0)
           wait(&s_first[grp], (seg >> 1) & 1, 240);  // s_full may be phases behind until then
         else
@@ -925,10 +928,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[2 * buf + half]);
         };
         if (warp_live) {
-          if (i < cut || i >= full_from) {
+          if (edge) {
             // unseen keys' scores become -infinity, in place
-            const int vi = draft();
-            const ulonglong2 bits = edge_bits(a, s, i, vi, at_pos(vi));
 #pragma unroll 1
             for (int c = 0; c < CW / 32; ++c) {
               const int w = part * (CW / 32) + c;
@@ -1087,11 +1088,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       const uint32_t ge = NT == 1 ? g + n - 1 : g_own + n - 1;  // the segment's last tile
       wait(&pv_done[NT == 1 ? ge & 1 : grp], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
       const bool whole = i0 == 0 && n == s->r.nt;
-      const int vi = draft(), vp = at_pos(vi);
       const int qh = s->h * a.G + (valid ? s->m * C::kRows + local - vi * a.G : 0), tok = s->r.t0 + vi;
       const bool dirty = s_dirty[seg & 3] == seg + 1;
       const int slot = 2 * blockIdx.x + (i0 == 0);
-      if (dirty && warp_live) add_not_finite<D, CW>(a, s, o_addr, part, valid, vi, vp, i0, n);
+      if (dirty && warp_live) add_not_finite<D, CW>(a, s, o_addr, part, valid, vi, at_pos(), i0, n);
       // N columns of this thread's row of O
       auto sums = [&](int col, auto& y) {
         constexpr int N = sizeof(y) / 4;
@@ -1125,7 +1125,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
       };
       if constexpr (KS == 1) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
         if (warp_live) {
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
@@ -1155,7 +1155,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
         m_ref = M;
         meet();
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
         auto piece = [&](int owner, int from, int j) {
           const int x = P == 16 ? (local >> 1) & 3 : local & 7;
           return reinterpret_cast<float4*>(
@@ -1202,7 +1202,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         if (!whole)
           a.part_ml[(size_t)slot * C::kRows + local] = make_float2(m_ref, l);
         else if (a.lse)
-          a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+          a.lse[(size_t)tok * (a.hk * a.G) + qh] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
       }
       seg_done(seg);
       g += n;
