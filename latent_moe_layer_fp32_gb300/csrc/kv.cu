@@ -77,8 +77,14 @@ __global__ void __launch_bounds__(64 * W)
   }
   depth = span;
   if (i < n) {
+    uint64_t* const row = mask + (size_t)(t0 + i) * W;
+    if (W % 2 == 0 && (reinterpret_cast<uintptr_t>(mask) & 15u) == 0) {
 #pragma unroll
-    for (int w = 0; w < W; ++w) mask[(size_t)(t0 + i) * W + w] = m[w];
+      for (int w = 0; w + 1 < W; w += 2) *reinterpret_cast<ulonglong2*>(row + w) = make_ulonglong2(m[w], m[w + 1]);
+    } else {
+#pragma unroll
+      for (int w = 0; w < W; ++w) row[w] = m[w];
+    }
     pos[t0 + i] = len + depth;
   }
 }
@@ -86,7 +92,6 @@ __global__ void __launch_bounds__(64 * W)
 // ---------------------------------------------------------------------------
 // block plan
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxRequests = 8192;
 
 struct PlanArgs {
@@ -95,24 +100,14 @@ struct PlanArgs {
   int32_t *table, *ring, *lens_out, *owned_out, *ring_state_out, *offsets, *slots;
 };
 
-struct PlanReq {
-  int len, add, owned, after;  // tokens held, tokens to append (0 for an ended request), blocks held / needed in all
-  bool ends;
-};
-
-__device__ __forceinline__ PlanReq plan_req(const PlanArgs& a, int b) {
-  PlanReq r;
-  const int add = a.add[b];
-  r.ends = add < 0;
-  r.add = max(add, 0);
-  r.len = max(a.lens[b], 0);
-  r.owned = min(max(a.owned[b], 0), a.max_blocks);
-  const long long after = ((long long)r.len + r.add + a.bs - 1) / a.bs;
-  r.after = (int)min(after, (long long)a.max_blocks + 1);
-  return r;
+// ceil of (len + add) / bs, at most one past the table
+__device__ __forceinline__ int blocks_for(int len, int add, int bs, int max_blocks) {
+  const unsigned held = (unsigned)len + (unsigned)add, q = held / (unsigned)bs;
+  return (int)min(q + (held != q * (unsigned)bs), (unsigned)max_blocks + 1u);
 }
 
 // Sum of v over the threads before this one, and over all in *total.
+template <int NT>
 __device__ __forceinline__ unsigned long long scan_excl(unsigned long long v, unsigned long long* s_warp,
                                                         unsigned long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -124,112 +119,153 @@ __device__ __forceinline__ unsigned long long scan_excl(unsigned long long v, un
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  unsigned long long w = s_warp[lane];
+  unsigned long long w = lane < NT / 32 ? s_warp[lane] : 0ull;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < NT / 32; o <<= 1) {
     const unsigned long long y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
+  *total = __shfl_sync(0xffffffffu, w, NT / 32 - 1);
   const unsigned long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   __syncthreads();
   return x - v + (warp ? before : 0ull);
 }
 
+// (head + i) % size for a head and an i below size
 __device__ __forceinline__ int ring_at(int head, long long i, int size) {
-  return (int)(((long long)head + i) % size);
+  const long long x = head + i;
+  return (int)(x >= size ? x - size : x);
 }
 
-// Every CTA scans all requests (at most 8192: 8 passes of 1024 threads over
-// L2-resident lengths) and keeps three prefix sums in shared memory, then
-// takes its share of the requests (a warp each) and of the tokens (a thread
-// each, its request found by bisection).  Nothing is passed between CTAs, so
-// one launch does it.
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a) {
+// Every CTA scans all requests itself (L2-resident lengths, a run of up to 8 requests per thread, two block
+// scans) and keeps what a token needs of its request in shared memory; then it takes its share of the
+// requests (a warp each) and of the tokens (a thread each, its request found by bisection).  Nothing is
+// passed between CTAs, so one launch does it.  What bounds it is the chain of dependent loads: 4096 requests
+// with 76000 tokens take 9.8 us, 8 requests 2.8 us (with a scan per 1024 requests and lengths fetched again
+// per token: 14.9 and 4.0 us).
+template <int NT, int PER>
+__global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
   extern __shared__ int s_plan[];
   int* s_tok = s_plan;             // [B + 1] first token of each request, saturated at n_slots + 1
   int* s_pop = s_plan + a.B + 1;   // [B] blocks popped by the requests before it; -1: not served
-  int* s_push = s_pop + a.B;       // [B] blocks pushed by the requests before it
+  int* s_push = s_pop + a.B;       // [B] blocks pushed by the requests before it; -1: it does not end
+  int* s_len = s_push + a.B;       // [B] tokens held
+  int* s_own = s_len + a.B;        // [B] blocks held
   __shared__ unsigned long long s_warp[32];
   __shared__ int s_taken;
   pdl_wait();
   pdl_trigger();
+  const int b0 = threadIdx.x * PER;
+  int add[PER], len[PER], own[PER];  // all at once: one trip to memory
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool in = b0 + j < a.B;
+    add[j] = in ? a.add[b0 + j] : 0;
+    len[j] = in ? max(a.lens[b0 + j], 0) : 0;
+    own[j] = in ? min(max(a.owned[b0 + j], 0), a.max_blocks) : 0;
+  }
   const int head = a.ring_state[0], count = min(max(a.ring_state[1], 0), a.ring_size);
   const int hd = head < 0 || head >= a.ring_size ? 0 : head;
   if (threadIdx.x == 0) s_taken = 0;
-  unsigned long long tok = 0, pops = 0, pushes = 0;
-  for (int c = 0; c < a.B; c += kPlanThreads) {
-    const int b = c + threadIdx.x;
-    PlanReq r = {0, 0, 0, 0, false};
-    if (b < a.B) r = plan_req(a, b);
-    unsigned long long sum;
-    const unsigned long long t0 = tok + scan_excl((unsigned)r.add, s_warp, &sum);
-    tok += sum;
-    const bool fits = b < a.B && !r.ends && r.after <= a.max_blocks && t0 + r.add <= (unsigned long long)a.n_slots;
-    const int need = fits ? max(r.after - r.owned, 0) : 0;
-    const unsigned long long both = (unsigned long long)need << 32 | (unsigned)(r.ends ? r.owned : 0);
-    const unsigned long long at = scan_excl(both, s_warp, &sum);
-    const unsigned long long pop0 = pops + (at >> 32);
-    if (b < a.B) {
-      const bool served = fits && (need == 0 || pop0 + need <= (unsigned long long)count);
-      s_tok[b] = (int)min(t0, (unsigned long long)a.n_slots + 1);
-      s_pop[b] = served ? (int)min(pop0, (unsigned long long)0x7fffffff) : -1;
-      s_push[b] = (int)(pushes + (at & 0xffffffffu));
-      if (served && need > 0) atomicMax(&s_taken, (int)(pop0 + need));
-      if (blockIdx.x == 0) a.offsets[b] = (int)min(t0, 0x7fffffffull);
-    }
-    pops += sum >> 32;
-    pushes += sum & 0xffffffffu;
+  unsigned long long sum = 0, n_tok, n_both;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) sum += (unsigned)max(add[j], 0);
+  unsigned long long t0 = scan_excl<NT>(sum, s_warp, &n_tok);
+  // blocks asked for (high half) and given back (low half) by the requests that fit
+  unsigned long long at = t0, both = 0;
+  int need[PER];
+  unsigned fit = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int more = max(add[j], 0), after = blocks_for(len[j], more, a.bs, a.max_blocks);
+    const bool fits = add[j] >= 0 && after <= a.max_blocks && at + more <= (unsigned long long)a.n_slots;
+    need[j] = fits ? max(after - own[j], 0) : 0;
+    fit |= (unsigned)fits << j;
+    at += more;
+    both += (unsigned long long)need[j] << 32 | (unsigned)(add[j] < 0 ? own[j] : 0);
   }
+  both = scan_excl<NT>(both, s_warp, &n_both);
+  int taken = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int b = b0 + j;
+    if (b < a.B) {
+      const unsigned long long pop = both >> 32;
+      const bool served = (fit >> j & 1u) && (need[j] == 0 || pop + need[j] <= (unsigned long long)count);
+      if (served && need[j] > 0) taken = (int)(pop + need[j]);
+      s_tok[b] = (int)min(t0, (unsigned long long)a.n_slots + 1);
+      s_pop[b] = served ? (int)min(pop, 0x7fffffffull) : -1;
+      s_push[b] = add[j] < 0 ? (int)(both & 0xffffffffu) : -1;
+      s_len[b] = len[j];
+      s_own[b] = own[j];
+      if (blockIdx.x == 0) a.offsets[b] = (int)min(t0, 0x7fffffffull);
+      t0 += max(add[j], 0);
+      both += (unsigned long long)need[j] << 32 | (unsigned)(add[j] < 0 ? own[j] : 0);
+    }
+  }
+  if (taken > 0) atomicMax(&s_taken, taken);
   if (threadIdx.x == 0) {
-    s_tok[a.B] = (int)min(tok, (unsigned long long)a.n_slots + 1);
-    if (blockIdx.x == 0) a.offsets[a.B] = (int)min(tok, 0x7fffffffull);
+    s_tok[a.B] = (int)min(n_tok, (unsigned long long)a.n_slots + 1);
+    if (blockIdx.x == 0) a.offsets[a.B] = (int)min(n_tok, 0x7fffffffull);
   }
   __syncthreads();
   const int room = a.ring_size - count;  // ring entries that hold no free block
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    const int back = (int)min(pushes, (unsigned long long)room);
+    const int back = (int)min(n_both & 0xffffffffull, (unsigned long long)room);
     a.ring_state_out[0] = ring_at(hd, s_taken, a.ring_size);
     a.ring_state_out[1] = count - s_taken + back;
   }
   const int lane = threadIdx.x & 31;
-  for (int b = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5); b < a.B; b += gridDim.x * (kPlanThreads / 32)) {
-    const PlanReq r = plan_req(a, b);
+  for (int b = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); b < a.B; b += gridDim.x * (NT / 32)) {
     int32_t* row = a.table + (size_t)b * a.max_blocks;
-    if (r.ends) {
-      for (int j = lane; j < r.owned && s_push[b] + j < room; j += 32)
-        a.ring[ring_at(hd, (long long)count + s_push[b] + j, a.ring_size)] = row[j];
+    const int owned = s_own[b], push = s_push[b], pop = s_pop[b], held = s_len[b];
+    if (push >= 0) {  // it ends
+      for (int j = lane; j < owned && push + j < room; j += 32)
+        a.ring[ring_at(hd, (long long)count + push + j, a.ring_size)] = row[j];
       if (lane == 0) a.lens_out[b] = a.owned_out[b] = 0;
-      continue;
-    }
-    const bool served = s_pop[b] >= 0;
-    const int need = served ? max(r.after - r.owned, 0) : 0;
-    for (int j = lane; j < need; j += 32) row[r.owned + j] = a.ring[ring_at(hd, s_pop[b] + j, a.ring_size)];
-    if (lane == 0) {
-      a.lens_out[b] = served ? r.len + r.add : a.lens[b];
-      a.owned_out[b] = served ? r.owned + need : a.owned[b];
+    } else if (pop >= 0) {
+      const int more = s_tok[b + 1] - s_tok[b], after = max(blocks_for(held, more, a.bs, a.max_blocks), owned);
+      for (int j = lane; j < after - owned; j += 32) row[owned + j] = a.ring[ring_at(hd, pop + j, a.ring_size)];
+      if (lane == 0) {
+        a.lens_out[b] = held + more;
+        a.owned_out[b] = after;
+      }
+    } else if (lane == 0) {
+      a.lens_out[b] = a.lens[b];
+      a.owned_out[b] = a.owned[b];
     }
   }
   // a token's slot: from the table for a block held before the call, else straight from the ring
-  const int n_tok = min(s_tok[a.B], a.n_slots);
-  for (int t = blockIdx.x * kPlanThreads + threadIdx.x; t < a.n_slots; t += gridDim.x * kPlanThreads) {
+  const int last = min(s_tok[a.B], a.n_slots);
+  for (int t = blockIdx.x * NT + threadIdx.x; t < a.n_slots; t += gridDim.x * NT) {
     int slot = -1;
-    if (t < n_tok) {
+    if (t < last) {
       int lo = 0, hi = a.B - 1;  // the last request whose first token is at or before t
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (s_tok[mid] <= t) lo = mid; else hi = mid - 1;
       }
       if (s_pop[lo] >= 0) {
-        const PlanReq r = plan_req(a, lo);
-        const int p = r.len + t - s_tok[lo], blk = p / a.bs;
-        const int id = blk < r.owned ? a.table[(size_t)lo * a.max_blocks + blk]
-                                     : a.ring[ring_at(hd, (long long)s_pop[lo] + blk - r.owned, a.ring_size)];
-        slot = id * a.bs + p % a.bs;
+        const int p = s_len[lo] + t - s_tok[lo], blk = p / a.bs, owned = s_own[lo];
+        const int id = blk < owned ? a.table[(size_t)lo * a.max_blocks + blk]
+                                   : a.ring[ring_at(hd, (long long)s_pop[lo] + blk - owned, a.ring_size)];
+        slot = id * a.bs + p - blk * a.bs;
       }
     }
     a.slots[t] = slot;
   }
+}
+
+// Threads per CTA and requests per thread for B requests; a CTA per 32 requests (its warps' one round) or
+// 1024 tokens, whichever asks for more.
+template <int NT, int PER>
+int run_plan(const PlanArgs& a, int sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  const int rc = allow_smem(done, kv_plan_kernel<NT, PER>, (5 * NT * PER + 1) * 4);
+  if (rc) return rc;
+  const int want = max((a.B + NT / 32 - 1) / (NT / 32), (int)((a.n_slots + NT - 1ll) / NT));
+  return launch_pdl("kv_plan_kernel", dim3(min(want, sms)), dim3(NT), (5 * (size_t)a.B + 1) * 4, s,
+                    kv_plan_kernel<NT, PER>, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -353,14 +389,12 @@ int lmoe_kv_plan(int32_t n_requests, int32_t block_size, int32_t max_blocks, int
   int rc = dev_info(&di);
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  static std::atomic<unsigned long long> done{0};
-  if ((rc = allow_smem(done, kv_plan_kernel, (3 * kPlanMaxRequests + 1) * 4))) return rc;
   const PlanArgs a = {n_requests, block_size,  max_blocks, n_slots,  ring_size, lens,           new_tokens, owned,
                       ring_state, block_table, ring,       lens_out, owned_out, ring_state_out, token_offsets, slots};
-  // one CTA per 64 requests (two rounds of its warps) or 2048 tokens, whichever asks for more
-  const int want = max((n_requests + 63) / 64, (int)((n_slots + 2047ll) / 2048));
-  return launch_pdl("kv_plan_kernel", dim3(min(want, di.sms)), dim3(kPlanThreads), (3 * (size_t)n_requests + 1) * 4, s,
-                    kv_plan_kernel, a);
+  if (n_requests <= 256) return run_plan<256, 1>(a, di.sms, s);
+  if (n_requests <= 1024) return run_plan<1024, 1>(a, di.sms, s);
+  if (n_requests <= 4096) return run_plan<1024, 4>(a, di.sms, s);
+  return run_plan<1024, 8>(a, di.sms, s);
 }
 
 int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, int64_t k_stride, const uint16_t* v_new,
