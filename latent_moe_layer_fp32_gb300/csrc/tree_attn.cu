@@ -178,6 +178,8 @@ struct Walk {
   const AttnArgs& a;
   int b, cost;         // request; of a segment's end
   long long off, end;  // where the range goes on and where it ends, from request b's start
+  long long at;        // where request b starts in the whole line
+  long long last;      // where the last tile of the latest segment starts in it
   __device__ bool next(Seg* s) {
     while (off < end) {
       const Load w = load_req<NT, ROWS>(a, b, &s->r);
@@ -185,6 +187,7 @@ struct Walk {
       if (off >= units) {
         off -= units;
         end -= units;
+        at += units;
         ++b;
         continue;
       }
@@ -195,6 +198,7 @@ struct Walk {
       if (i0 >= nt) continue;
       const int i1 = (int)min((long long)nt, (long long)quot(max(end - p.start, 0ll) + p.tile - 1, p.tile));
       if (i1 <= i0) return false;
+      last = at + p.start + (long long)(nt - 1) * p.tile;
       s->b = b;
       s->h = p.h;
       s->m = p.m;
@@ -481,14 +485,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   pdl_trigger();
 
   // ---- this CTA's range of the line of tiles ----
-  int end_cost;  // of a segment's end
+  int end_cost;                          // of a segment's end
+  long long line, ranges, first = 0;     // the line's length, its ranges, this range's start
   if (tid == 0) *st = Status{0, 0};
   {
     const int per = (a.B + C::kThreads - 1) / C::kThreads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     unsigned long long tiles = 0, segs = 0;  // of this thread's requests: the tiles' cost, the segments
     bool bad = false;
-    Req r0{};
     Load w0{};
     for (int b = b0; b < b1; ++b) {
       Req r;
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       tiles += a.hk * w.head;
       segs += (unsigned)(a.hk * w.groups);
       bad |= w.bad;
-      if (b == b0) r0 = r, w0 = w;
+      if (b == b0) w0 = w;
     }
     unsigned long long x = tiles, y = segs;
 #pragma unroll
@@ -524,48 +528,27 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const unsigned long long n =
         total ? max(1ull, min((unsigned long long)a.ctas, quot(total, Cost<NT>::kTwo + end_cost))) : 0ull;
     const unsigned long long c = blockIdx.x;
+    ranges = (long long)n;
+    line = (long long)total;
     if (c < n) {
-      // the threads whose requests hold the range's first and last unit
-      const unsigned long long u0 = quot(total * c, n), u1 = quot(total * (c + 1), n);
-      Req r = r0;
-      Load w = w0;
-      unsigned long long at = before;
-      auto find = [&](unsigned long long u) {
-        int b = b0;
-        if (b1 - b0 > 1) {
-          at = before;
-          for (;; ++b) {
-            w = load_req<NT, ROWS>(a, b, &r);
-            const unsigned long long units = w.units(a.hk, end_cost);
-            if (u < at + units) break;
-            at += units;
-          }
-        }
-        return b;
-      };
+      const unsigned long long u0 = quot(total * c, n);
+      first = (long long)u0;
       if (u0 >= before && u0 < before + mine) {
-        s_start[0] = find(u0);
-        s_start[1] = (long long)(u0 - at);
-        s_start[2] = (long long)(u1 - u0);
-      }
-      if (u1 - 1 >= before && u1 - 1 < before + mine) {
-        // does the range's last segment start in it and have tiles past it?  Then its last CTA is the
-        // first one whose range ends after the start of the segment's last tile
-        find(u1 - 1);
-        const Place p = place<NT>(w, r.nt, end_cost, (long long)(u1 - 1 - at));
-        const unsigned long long start = at + p.start, in = u1 - 1 - start;
-        int4 c0 = make_int4(0, 0, 0, 0), c1 = c0;
-        if (start >= u0 && quot(in, p.tile) + 1 < (unsigned)r.nt) {
-          const unsigned long long e = start + (unsigned long long)(r.nt - 1) * p.tile + 1;  // its last tile's start
-          const int last = (int)quot(e * n + total - 1, total) - 1;
-          c0 = make_int4(last - (int)c + 1, r.t0, min(ROWS, r.n * a.G - p.m * ROWS), p.h);
-          c1 = make_int4(p.m, 0, 0, 0);
+        int b = b0;
+        unsigned long long at = before;
+        for (Load w = w0;; ++b) {
+          if (b > b0) {
+            Req r;
+            w = load_req<NT, ROWS>(a, b, &r);
+          }
+          const unsigned long long units = w.units(a.hk, end_cost);
+          if (u0 < at + units) break;
+          at += units;
         }
-        a.cut[2 * c] = c0;
-        a.cut[2 * c + 1] = c1;
+        s_start[0] = b;
+        s_start[1] = (long long)(u0 - at);
+        s_start[2] = (long long)(quot(total * (c + 1), n) - u0);
       }
-    } else if (tid == 0) {
-      a.cut[2 * c] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
   }
@@ -593,13 +576,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const int ppt = kTile / box;                  // pages per such tile
     uint32_t g = 0, seg = 0, issued = 0;          // issued: past the last ring position that was issued
     bool ok = true;
-    Walk<NT, ROWS> walk{a, (int)s_start[0], end_cost, s_start[1], s_start[1] + s_start[2]};
+    Walk<NT, ROWS> walk{a, (int)s_start[0], end_cost, s_start[1], s_start[1] + s_start[2], first - s_start[1], 0};
+    int4 cut0 = make_int4(0, 0, 0, 0), cut1 = cut0;  // the latest segment, if it starts in this range and ends past it
     for (;; ++seg) {
       // the keys' producer walks the range and posts each segment's record, the others read it
       Seg s{};
       if (keys) {
         const bool more = walk.next(&s);
-        if (!more) s.i0 = s.i1 = 0;
+        if (!more)
+          s.i0 = s.i1 = 0;
+        else if (s.i0 == 0 && s.i1 < s.r.nt)
+          cut0 = make_int4(1, s.r.t0, s.rows, s.h), cut1 = make_int4(s.m, 0, 0, 0);
+        else
+          cut0.x = 0;
         if (!(ok = bar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, 262, failed))) break;
         if (lane == 0) {
           s_seg[seg & 3] = s;
@@ -655,6 +644,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         if (!(ok = keys ? copy(true, k_pos<NT>(g)) : copy(false, v_pos<NT>(g)))) break;
       }
       if (!ok) break;
+    }
+    if (keys && lane == 0) {
+      // for the merge: a cut segment's last CTA is the first one whose range ends after the start of its last tile
+      if (cut0.x) cut0.x = (int)quot((walk.last + 1) * ranges + line - 1, line) - (int)blockIdx.x;
+      a.cut[2 * blockIdx.x] = cut0;
+      a.cut[2 * blockIdx.x + 1] = cut1;
     }
     // this warp's last copies land before the CTA can finish (also after a wait that ran out); a stage
     // that has been filled again since needs no wait
@@ -1283,8 +1278,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 
 // Joins the pieces of each cut segment: block x is the CTA in whose range a segment starts, its pieces lie
 // in that CTA's tail slot and the head slots of the CTAs after it.  A thread joins 4 columns of a row, a
-// block 8 rows; eight pieces are under way at a time
-// (what there is so far is rescaled for them).
+// block 8 rows; 4 pieces are under way at a time (what there is so far is
+// rescaled for them); 2, 8 and 16 were slower.
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum O_i 2^(m_i - M) / L
 template <int D>
 __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a, int rows) {
@@ -1306,7 +1301,7 @@ __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a
   const int pieces = c0.x, unit = threadIdx.x >> 3, local = blockIdx.y * 8 + (threadIdx.x & 7);
   if (pieces < 2 || local >= c0.z) return;
   auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
-  constexpr int U = 8;
+  constexpr int U = 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, L = 0.f;
   for (int p0 = 0; p0 < pieces; p0 += U) {
