@@ -618,8 +618,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const int cached = s.r.cached(i);
         const int rows = cached == kTile ? box : 8;
         const int nc = cached == kTile ? ppt : (cached + 7) >> 3, nd = (s.r.drafts(i) + 7) >> 3;
-        auto copy = [&](bool k, uint32_t at) {
-          const CUtensorMap* const tc = rows == 8 ? (k ? &tm_k8 : &tm_v8) : (k ? &tm_k : &tm_v);
+        auto copy = [&](uint32_t at) {
+          const CUtensorMap* const tc = rows == 8 ? (keys ? &tm_k8 : &tm_v8) : (keys ? &tm_k : &tm_v);
           const uint32_t stage = at % ST;
           if (!bar_wait(&empty[stage], ((at / ST) & 1) ^ 1, 221, failed)) return false;
           uint8_t* dst = s_ring + stage * C::kStageBytes;
@@ -634,14 +634,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             const int j = (lane - nc) * 8;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
-              tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, k ? &tm_kn : &tm_vn, hf * 64, s.h,
+              tma_load_3d(dst + hf * (kTile * 128) + (s.r.col(i) + j) * 128, keys ? &tm_kn : &tm_vn, hf * 64, s.h,
                           s.r.t0 + s.r.d0(i) + j, &full[stage], pol);
           }
           __syncwarp();
           issued = at + 1;
           return true;
         };
-        if (!(ok = keys ? copy(true, k_pos<NT>(g)) : copy(false, v_pos<NT>(g)))) break;
+        if (!(ok = copy(keys ? k_pos<NT>(g) : v_pos<NT>(g)))) break;
       }
       if (!ok) break;
     }
@@ -695,8 +695,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         for (int hf = 0; hf < 2; ++hf) {
           if (!ready(&p_full[2 * buf + hf], parity, 233 + hf)) return false;
           tc_fence_after();
-          const uint32_t lo = s_lo[buf], ph = p + hf * 32;
+          const uint32_t lo = s_lo[buf], ph = p + hf * 64;
           const uint64_t vh = v0 + hf * (64 * 128 >> 4);
+          // P of 16 keys each stands at 0, 8, 32 and 40 of a half's columns, the second parts 16 further on;
           // with copies of rows a 16-key step goes to the lanes whose copy holds those keys
           auto lanes = [&](int kk, bool second, uint32_t (&off)[4]) {
             const int part = KS == 1 ? 0 : KS == 2 ? hf : 2 * hf + (kk >> 1);
@@ -708,11 +709,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             for (int kk = 0; kk < 4; ++kk) {
               const uint32_t acc = !(first && (KS == 1 ? hf == 0 && kk == 0 : kk % (8 / KS) == 0));
               if constexpr (KS == 1) {
-                tc_mma_bf16_ts(o, ph + kk * 8, vh + kk * (16 * 128 >> 4), kPv, acc);
+                tc_mma_bf16_ts(o, ph + (kk >> 1) * 32 + (kk & 1) * 8, vh + kk * (16 * 128 >> 4), kPv, acc);
               } else {
                 uint32_t off[4];
                 lanes(kk, false, off);
-                tc_mma_bf16_ts_lanes(o, ph + kk * 8, vh + kk * (16 * 128 >> 4), kPv, acc, off);
+                tc_mma_bf16_ts_lanes(o, ph + (kk >> 1) * 32 + (kk & 1) * 8, vh + kk * (16 * 128 >> 4), kPv, acc, off);
               }
             }
             if (lo) {  // the second part, for the warps that wrote one
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               for (int kk = 0; kk < 4; ++kk) {
                 uint32_t off[4];
                 lanes(kk, true, off);
-                tc_mma_bf16_ts_lanes(o, ph + kTile / 2 + kk * 8, vh + kk * (16 * 128 >> 4), kPv, 1u, off);
+                tc_mma_bf16_ts_lanes(o, ph + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vh + kk * (16 * 128 >> 4), kPv, 1u, off);
               }
             }
             if (hf == 1) tc_commit(&pv_done[buf]);
@@ -923,6 +924,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[2 * buf + half]);
         };
         if (warp_live) {
+          // the tile's maximum
+          float mx[2] = {-INFINITY, -INFINITY};
+          auto most = [&](const uint32_t (&y)[32]) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+          };
           if (edge) {
             // unseen keys' scores become -infinity, in place
 #pragma unroll 1
@@ -936,21 +944,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               for (int j = 0; j < 32; ++j)
                 if (!(x >> j & 1u)) y[j] = 0xff800000u;
               tmem_st32(s_addr + w * 32, y);
+              most(y);
             }
             tmem_st_wait();
-          }
-          // the tile's maximum
-          float mx[2] = {-INFINITY, -INFINITY};
-          {
+          } else {
             uint32_t y[2][32];
             tmem_ld32(s_addr + part * CW, y[0]);
 #pragma unroll
             for (int c = 0; c < CW / 32; ++c) {
               tmem_ld_wait();
               if (c + 1 < CW / 32) tmem_ld32(s_addr + part * CW + (c + 1) * 32, y[(c + 1) & 1]);
-#pragma unroll
-              for (int j = 0; j < 32; j += 2)
-                mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], __uint_as_float(y[c & 1][j]), __uint_as_float(y[c & 1][j + 1]));
+              most(y[c & 1]);
             }
           }
           const float m_new = fmaxf(mx[0], mx[1]) * a.scale_log2;
@@ -974,25 +978,25 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
             const float mu = m_ref == -INFINITY ? 0.f : m_ref;
             const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), mu2 = pair(-mu, -mu);
-            // the scores once more: P takes the place of scores that have been read
-            const uint32_t from = s_addr + part * CW, to = s_addr + part * (CW / 2);
+            // the scores once more: P takes the place of scores that have been read, 32 keys in 16 columns
+            const uint32_t from = s_addr + part * CW;
             uint32_t y0[32], y1[32], p[16];
             tmem_ld32(from, y0);
             if constexpr (CW == 32) {
               tmem_ld_wait();
               exps(y0, p, sc2, mu2);
-              tmem_st16(to, p);
+              tmem_st16(from, p);
             } else {
 #pragma unroll 1
               for (int c = 0; c < CW / 32; c += 2) {
                 tmem_ld_wait();
                 tmem_ld32(from + c * 32 + 32, y1);
                 exps(y0, p, sc2, mu2);
-                tmem_st16(to + c * 16, p);
+                tmem_st16(from + c * 32, p);
                 tmem_ld_wait();
                 if (c + 2 < CW / 32) tmem_ld32(from + c * 32 + 64, y0);
                 exps(y1, p, sc2, mu2);
-                tmem_st16(to + c * 16 + 16, p);
+                tmem_st16(from + c * 32 + 32, p);
                 if (KS == 1 && c == 0) {  // the first half's product can start
                   tmem_st_wait();
                   p_ready(0);
@@ -1024,45 +1028,67 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             float sc = a.scale_log2;
             const bool huge = __any_sync(0xffffffffu, fabsf(mu) > 16777216.f);
             if (huge) sc = 1.f;
-            uint32_t y[CW / 32][32];
             const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
-#pragma unroll
-            for (int c = 0; c < CW / 32; ++c) tmem_ld32(s_addr + part * CW + c * 32, y[c]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < CW / 32; ++c) {
-              uint32_t p[16];
-              if (huge) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) y[c][j] = __float_as_uint(__uint_as_float(y[c][j]) * a.scale_log2);
-              }
-              exps(y[c], p, sc2, mu2);
-              tmem_st16(s_addr + part * (CW / 2) + c * 16, p);
-            }
             // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
             // holds over 1/8 of the row's sum so far that would show in the output next to its own
             // rounding, so the remainder goes along as a second part; with more keys in play it
             // averages out.  After a prefix's first tiles this is rare.
-            float s0, s1;
-            unpair(add2(sum[0], sum[1]), s0, s1);
-            const bool lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > (l + (s0 + s1)) * 0.125f);
-            if (lo) {
+            bool lo = false;
+            auto weigh = [&] {
+              float s0, s1;
+              unpair(add2(sum[0], sum[1]), s0, s1);
+              lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > (l + (s0 + s1)) * 0.125f);
+              if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
+            };
+            auto put_lo = [&](const uint32_t (&y)[32], uint32_t at) {
+              uint32_t p[16];
 #pragma unroll
-              for (int c = 0; c < CW / 32; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float e0 = __uint_as_float(y[c][2 * j]), e1 = __uint_as_float(y[c][2 * j + 1]);
-                  const uint32_t hi = pack_bf16(e0, e1);
-                  p[j] = pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
-                }
-                tmem_st16(s_addr + kTile / 2 + part * (CW / 2) + c * 16, p);
+              for (int j = 0; j < 16; ++j) {
+                const float e0 = __uint_as_float(y[2 * j]), e1 = __uint_as_float(y[2 * j + 1]);
+                const uint32_t hi = pack_bf16(e0, e1);
+                p[j] = pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
               }
-            }
-            if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
-            if (KS == 1) {
-              tmem_st_wait();
-              p_ready(0);
+              tmem_st16(at + 16, p);
+            };
+            auto scaled = [&](uint32_t (&y)[32]) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a.scale_log2);
+            };
+            const uint32_t from = s_addr + part * CW;
+            if constexpr (CW > 32) {
+              // the sum first, then P: a short loop twice over (with the tile's scores held in registers the
+              // code was so long that the warps waited for it: 208 us instead of 215 for 32 requests with 33
+              // to 64 drafts)
+#pragma unroll 1
+              for (int pass = 0; pass < 2; ++pass) {
+                sum[0] = sum[1] = 0;
+#pragma unroll 1
+                for (int c = 0; c < CW / 32; ++c) {
+                  uint32_t y[32], p[16];
+                  tmem_ld32(from + c * 32, y);
+                  tmem_ld_wait();
+                  if (huge) scaled(y);
+                  exps(y, p, sc2, mu2);
+                  if (pass == 0) continue;
+                  tmem_st16(from + c * 32, p);
+                  if (lo) put_lo(y, from + c * 32);
+                  if (KS == 1 && c == 1) {  // the first half's product can start
+                    tmem_st_wait();
+                    p_ready(0);
+                  }
+                }
+                if (pass == 0) weigh();
+              }
+            } else {  // 32 scores stay in registers (twice over: 41.8 us instead of 39.7 for 48 requests of up
+                      // to 21 rows)
+              uint32_t y[32], p[16];
+              tmem_ld32(from, y);
+              tmem_ld_wait();
+              if (huge) scaled(y);
+              exps(y, p, sc2, mu2);
+              tmem_st16(from, p);
+              weigh();
+              if (lo) put_lo(y, from);
             }
           }
           tmem_st_wait();
@@ -1105,7 +1131,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           for (int u = 0; u < N / 8; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[u][j] = pack_bf16(y[u * 8 + 2 * j] * inv, y[u * 8 + 2 * j + 1] * inv);
-          if constexpr (KS == 1) {  // 128 rows' worth of 16-byte stores would queue up: 64 bytes of a row at a time
+          if constexpr (KS == 1) {  // 128 rows' worth of 16-byte stores would queue up: 32 bytes of a row at a time
             store_rows<N / 8>(w, dst);
           } else if (dst) {
 #pragma unroll
@@ -1123,8 +1149,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);
         if (warp_live) {
 #pragma unroll 1
-          for (int col = 0; col < D; col += 32) {
-            float y[32];
+          for (int col = 0; col < D; col += 16) {
+            float y[16];
             sums(col, y);
             put(col, y, inv);
           }
