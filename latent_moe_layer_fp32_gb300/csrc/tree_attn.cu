@@ -1033,62 +1033,42 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             // holds over 1/8 of the row's sum so far that would show in the output next to its own
             // rounding, so the remainder goes along as a second part; with more keys in play it
             // averages out.  After a prefix's first tiles this is rare.
-            bool lo = false;
-            auto weigh = [&] {
-              float s0, s1;
-              unpair(add2(sum[0], sum[1]), s0, s1);
-              lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > (l + (s0 + s1)) * 0.125f);
-              if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
-            };
-            auto put_lo = [&](const uint32_t (&y)[32], uint32_t at) {
-              uint32_t p[16];
+            auto put_lo = [&](const uint32_t (&y)[32], uint32_t (&p)[16], uint32_t at) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 const float e0 = __uint_as_float(y[2 * j]), e1 = __uint_as_float(y[2 * j + 1]);
-                const uint32_t hi = pack_bf16(e0, e1);
-                p[j] = pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xffff0000u));
+                p[j] = pack_bf16(e0 - __uint_as_float(p[j] << 16), e1 - __uint_as_float(p[j] & 0xffff0000u));
               }
               tmem_st16(at + 16, p);
             };
-            auto scaled = [&](uint32_t (&y)[32]) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a.scale_log2);
-            };
-            const uint32_t from = s_addr + part * CW;
-            if constexpr (CW > 32) {
-              // the sum first, then P: a short loop twice over (with the tile's scores held in registers the
-              // code was so long that the warps waited for it: 208 us instead of 215 for 32 requests with 33
-              // to 64 drafts)
+            // With 32 scores a thread the whole sum decides.  With more the second part goes along in any
+            // case: to wait for the sum takes longer than its products (32 requests with 33 to 64 drafts:
+            // 208 us instead of 205).
+            bool lo = CW > 32;
+            if (CW > 32 && lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 1;
 #pragma unroll 1
-              for (int pass = 0; pass < 2; ++pass) {
-                sum[0] = sum[1] = 0;
-#pragma unroll 1
-                for (int c = 0; c < CW / 32; ++c) {
-                  uint32_t y[32], p[16];
-                  tmem_ld32(from + c * 32, y);
-                  tmem_ld_wait();
-                  if (huge) scaled(y);
-                  exps(y, p, sc2, mu2);
-                  if (pass == 0) continue;
-                  tmem_st16(from + c * 32, p);
-                  if (lo) put_lo(y, from + c * 32);
-                  if (KS == 1 && c == 1) {  // the first half's product can start
-                    tmem_st_wait();
-                    p_ready(0);
-                  }
-                }
-                if (pass == 0) weigh();
-              }
-            } else {  // 32 scores stay in registers (twice over: 41.8 us instead of 39.7 for 48 requests of up
-                      // to 21 rows)
+            for (int c = 0; c < CW / 32; ++c) {
+              const uint32_t at = s_addr + part * CW + c * 32;
               uint32_t y[32], p[16];
-              tmem_ld32(from, y);
+              tmem_ld32(at, y);
               tmem_ld_wait();
-              if (huge) scaled(y);
+              if (huge) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a.scale_log2);
+              }
               exps(y, p, sc2, mu2);
-              tmem_st16(from, p);
-              weigh();
-              if (lo) put_lo(y, from);
+              tmem_st16(at, p);
+              if constexpr (CW == 32) {
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > (l + (s0 + s1)) * 0.125f);
+                if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
+              }
+              if (lo) put_lo(y, p, at);
+              if (KS == 1 && c == 1) {  // the first half's product can start
+                tmem_st_wait();
+                p_ready(0);
+              }
             }
           }
           tmem_st_wait();
