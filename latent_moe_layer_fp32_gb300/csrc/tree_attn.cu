@@ -103,11 +103,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int whe
 // How the line of tiles is measured for the cut into equal ranges: a tile of two row tiles, of one, and the
 // end of a segment (its sums joined and stored, the next one's queries, masks and first tiles).  Measured:
 // the ends at two and a half tiles instead of half a one took 16 requests of 1000 to 32768 positions from
-// 136 to 126 us; of two row tiles, at 18 instead of 3, 32 requests with 33 to 64 drafts from 253 to 221 us.
+// 136 to 126 us; of two row tiles, 32 requests with 33 to 64 drafts take 201 us at 12, 202 at 18, 205 at 21
+// (and took 253 at 3 instead of 221 at 18 when an end was slower).
 // A range has to hold the start of a tile, so with few tiles the ends count less (end_cost).
 template <int NT>
 struct Cost {
-  static constexpr int kTwo = NT == 2 ? 3 : 2, kOne = 2, kEnd = NT == 2 ? 18 : 5;
+  static constexpr int kTwo = NT == 2 ? 3 : 2, kOne = 2, kEnd = NT == 2 ? 12 : 5;
 };
 
 struct Load {
@@ -911,12 +912,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           wait(&s_first[grp], (seg >> 1) & 1, 240);  // s_full may be phases behind until then
         else
           wait(&s_full[buf], NT == 1 ? (gt >> 1) & 1 : go & 1, 242);
-        if (NT == 2 && k == n - 1 && mbar_test_wait(&seg_full[(seg + 1) & 3], ((seg + 1) >> 2) & 1)) {
-          // every product with these queries is done: the next segment's may come in
-          const Seg* nx = seg_at(seg + 1);
-          early = nx->i1 > 0 && (grp == 0 || nx->rows > kTile);
-          if (early) load_q(nx);
-        }
         const uint32_t s_addr = tmem + lane_base + buf * kTile;
         auto p_ready = [&](int half) {
           tc_fence_before();
@@ -1083,10 +1078,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           if (KS == 1) p_ready(0);
           p_ready(KS == 1 || part >= KS / 2 ? 1 : 0);
         }
-        if (NT == 2 && k == n - 1 && early) q_loaded();
       }
       // ---- the segment's end: finished rows to out, cut ones to the partial sums ----
       const uint32_t ge = NT == 1 ? g + n - 1 : g_own + n - 1;  // the segment's last tile
+      if (NT == 2 && mbar_test_wait(&seg_full[(seg + 1) & 3], ((seg + 1) >> 2) & 1)) {
+        // every product with these queries is done: the next segment's may come in
+        const Seg* nx = seg_at(seg + 1);
+        early = nx->i1 > 0 && (grp == 0 || nx->rows > kTile);
+        if (early) {
+          load_q(nx);
+          q_loaded();
+        }
+      }
       wait(&pv_done[NT == 1 ? ge & 1 : grp], NT == 1 ? (ge >> 1) & 1 : ge & 1, 245);
       const bool whole = i0 == 0 && n == s->r.nt;
       const int qh = s->h * a.G + (valid ? s->m * C::kRows + local - vi * a.G : 0), tok = s->r.t0 + vi;
