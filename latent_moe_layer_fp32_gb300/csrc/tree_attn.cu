@@ -33,7 +33,7 @@
 
 #include "common.cuh"
 #include "launch.cuh"
-#include "tc.cuh"
+#include "tc_attn.cuh"
 #include "tmap.cuh"
 
 namespace lmoe {
