@@ -381,7 +381,7 @@ LMOE_API size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* dims, 
  *   lse      out fp32 [T][q_heads], or NULL
  * Scores, the running maximum and sum, and the accumulators are fp32.  For
  * the product with the values a probability is rounded to bf16, or to two
- * bf16 parts where a key holds over 1/8 of its row's sum so far.
+ * bf16 parts where a key may hold over 1/8 of its row's sum so far.
  * Reported on the device (LMOE_EDEVICE_CHECK through lmoe_status_check):
  * offsets that descend, pass n_tokens or give a request more than
  * max_request_tokens rows, and a length below 0 or past its table: the rows

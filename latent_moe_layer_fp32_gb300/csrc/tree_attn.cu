@@ -1027,20 +1027,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
             // P as one bf16 part is off by up to 2^-8 of each key's share.  Where some key of a row
             // holds over 1/8 of the row's sum so far that would show in the output next to its own
             // rounding, so the remainder goes along as a second part; with more keys in play it
-            // averages out.  After a prefix's first tiles this is rare.
-            auto put_lo = [&](const uint32_t (&y)[32], uint32_t (&p)[16], uint32_t at) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float e0 = __uint_as_float(y[2 * j]), e1 = __uint_as_float(y[2 * j + 1]);
-                p[j] = pack_bf16(e0 - __uint_as_float(p[j] << 16), e1 - __uint_as_float(p[j] & 0xffff0000u));
-              }
-              tmem_st16(at + 16, p);
-            };
-            // With 32 scores a thread the whole sum decides.  With more the second part goes along in any
-            // case: to wait for the sum takes longer than its products (32 requests with 33 to 64 drafts:
-            // 208 us instead of 205).
-            bool lo = CW > 32;
-            if (CW > 32 && lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 1;
+            // averages out.  After a prefix's first tiles this is rare.  On this path it goes along in any
+            // case: to wait for the tile's sum takes longer than its products (32 requests with 33 to 64
+            // drafts: 207 us instead of 203).
+            if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 1;
 #pragma unroll 1
             for (int c = 0; c < CW / 32; ++c) {
               const uint32_t at = s_addr + part * CW + c * 32;
@@ -1053,13 +1043,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
               }
               exps(y, p, sc2, mu2);
               tmem_st16(at, p);
-              if constexpr (CW == 32) {
-                float s0, s1;
-                unpair(add2(sum[0], sum[1]), s0, s1);
-                lo = __any_sync(0xffffffffu, valid && ex2(m_new - mu) > (l + (s0 + s1)) * 0.125f);
-                if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = lo;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float e0 = __uint_as_float(y[2 * j]), e1 = __uint_as_float(y[2 * j + 1]);
+                p[j] = pack_bf16(e0 - __uint_as_float(p[j] << 16), e1 - __uint_as_float(p[j] & 0xffff0000u));
               }
-              if (lo) put_lo(y, p, at);
+              tmem_st16(at + 16, p);
               if (KS == 1 && c == 1) {  // the first half's product can start
                 tmem_st_wait();
                 p_ready(0);
@@ -1071,7 +1060,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           float s0, s1;
           unpair(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-          // below: no growth past 2^8, and no key over 1/8 of the sum
+          // below: no growth past 2^8, and no key over 1/8 of the sum so far
           if (valid) limit = fabsf(m_ref) <= 16777216.f ? m_ref + fminf(8.f, __log2f(l) - 3.f) : -INFINITY;
         } else {
           if (lane == 0) reinterpret_cast<volatile uint8_t*>(s_lo + buf)[warp & 3] = 0;
@@ -1400,10 +1389,19 @@ int check_attn(const lmoe_attn_dims* d, const lmoe_kv_cache* c, bool memory) {
   return LMOE_OK;
 }
 
-// Rows per CTA and segment, by the most rows that a request can have per kv head.
+// Rows per CTA and segment, by the most rows that a request can have per kv head.  Below 128 copies of the
+// rows share the softmax's work, which pays where that is what bounds a tile: always with 64 columns, whose
+// tiles are half as long to copy (16 requests of 12000 positions, 64 rows: 70 us with two copies, 91 with
+// one; 64 of one token, 8 rows: 62 with two, 91 with one, 64 with four); with 128 columns up to 32 rows (64
+// requests of one token: 111 us with four copies, 114 with two, 115 with one), but not from 33 on (one user's
+// 8 drafts, 64 rows: 13.5 us with one, 14.4 with two).  More than 128 rows take two row tiles, so that K and V
+// are read once for both; at 128 rows one is better (16 requests of 1000 to 12000 positions: 62 us, 67 with
+// two).
 int group_rows(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
   const int rows = d->max_request_tokens * (d->q_heads / c->kv_heads);
-  return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  if (c->head_dim == 64 && rows <= 64) return 64;
+  if (c->head_dim == 128 && rows <= 32) return 32;
+  return rows <= 128 ? 128 : 256;
 }
 
 struct AttnWs {
@@ -1443,10 +1441,9 @@ int run_attn(const AttnArgs& a, const CUtensorMap (&tm)[6], int max_rows, cudaSt
 template <int D>
 int run_attn_rows(int rows, const AttnArgs& a, const CUtensorMap (&tm)[6], int max_rows, cudaStream_t s) {
   switch (rows) {
-    case 32: return run_attn<D, 1, 4>(a, tm, max_rows, s);
-    case 64: return run_attn<D, 1, 2>(a, tm, max_rows, s);
     case 128: return run_attn<D, 1, 1>(a, tm, max_rows, s);
-    default: return run_attn<D, 2, 1>(a, tm, max_rows, s);
+    case 256: return run_attn<D, 2, 1>(a, tm, max_rows, s);
+    default: return run_attn<D, 1, D / 32>(a, tm, max_rows, s);  // two copies of 64 columns, four of 128
   }
 }
 
