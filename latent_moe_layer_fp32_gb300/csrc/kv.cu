@@ -19,7 +19,10 @@ namespace {
 // One CTA per request, one thread per drafted row.  Ancestor sets by pointer
 // doubling: after round r a row's mask holds its nearest 2^r ancestors-or-self
 // and up points past them, so ceil(log2 n) rounds close any tree and the loop
-// ends as soon as every pointer has left the tree.
+// ends as soon as every pointer has left the tree.  A chain of dependent loads
+// and rounds bounds it: 8 drafts take 1.8 us, 1024 trees of up to 200 drafts
+// (4.1 MB) 5.5 us, two waves of CTAs.  Masks are stored 16 bytes at a time where
+// they are aligned (5.5 instead of 6.1 us).
 template <int W>
 __global__ void __launch_bounds__(64 * W)
     tree_masks_kernel(int n_tokens, const int32_t* __restrict__ offsets, const int32_t* __restrict__ parents,
@@ -256,8 +259,9 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
   }
 }
 
-// Threads per CTA and requests per thread for B requests; a CTA per 32 requests (its warps' one round) or
-// 1024 tokens, whichever asks for more.
+// Threads per CTA and requests per thread for B requests: few threads meet sooner (8 requests: 2.8 us with
+// 256, 3.7 with 1024), more than 256 requests need more of them.  A CTA per NT / 32 requests (its warps' one
+// round) or NT tokens, whichever asks for more.
 template <int NT, int PER>
 int run_plan(const PlanArgs& a, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
@@ -271,7 +275,8 @@ int run_plan(const PlanArgs& a, int sms, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // slot writes
 // ---------------------------------------------------------------------------
-// A thread moves one 16-byte piece of a row's K and the same of its V.
+// A thread moves one 16-byte piece of a row's K and the same of its V.  A prompt's write is a copy, bound by
+// HBM: 16384 tokens of 8 heads of 128 columns (134 MB moved) take 22.6 us, 5930 GB/s; 211 accepted rows 2.1 us.
 __global__ void __launch_bounds__(256)
     kv_write_kernel(const lmoe_kv_cache c, const uint16_t* __restrict__ k_new, long long ks,
                     const uint16_t* __restrict__ v_new, long long vs, int n_rows, const int32_t* __restrict__ src,

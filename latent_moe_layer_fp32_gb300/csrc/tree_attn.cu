@@ -12,21 +12,41 @@
 // maximum, sum, unnormalised output), which tree_attn_merge_kernel joins in
 // the order of the ranges, so results do not depend on timing.
 //
-// CTA.  One producer warp copies K and V tiles page by page with TMA (128-byte
-// swizzle) into a ring; one thread issues tcgen05.mma: S = Q K^T (both K-major
-// from shared memory) into tensor memory, and O += P V with P read from tensor
-// memory and V as an MN-major operand straight from its pages' layout.  Two
-// softmax groups of four warps own a row per thread: they read S, keep the
-// row's running maximum and sum in registers, write P (bf16, with a second
-// bf16 part where one key dominates a row, in place of S) and rescale O only
-// when the maximum has grown by more than 2^8 (P is then at most 2^8, which
+// CTA.  Two producer warps copy K and V tiles page by page with TMA (128-byte
+// swizzle) into a ring of 160 KB or more; one warp issues tcgen05.mma: S = Q K^T
+// (both K-major from shared memory) into tensor memory, and O += P V with P read
+// from tensor memory and V as an MN-major operand straight from its pages'
+// layout.  Two softmax groups of four warps own a row per thread: they read S,
+// keep the row's running maximum and sum in registers, write P (bf16, in place
+// of S, with a second bf16 part where one key may dominate a row) and rescale O
+// only when the maximum has grown by more than 2^8 (P is then at most 2^8, which
 // bf16 and the fp32 sums hold without loss).
 // Up to 128 rows per kv head: the groups take turns by segment, each with its
 // own queries and its own O, so one loads queries, joins and stores while the
 // other computes, and S of the next tile is computed during the softmax of
 // this one.  More rows: the groups take a row tile each of the same segment.
-// Two further warps clean the value tiles at an edge of what rows see, so that
+// A further warp cleans the value tiles at an edge of what rows see, so that
 // no bits of an unseen key reach a product.
+//
+// What bounds it, and what it takes (GB300; 64 query heads, 8 kv heads, 128
+// columns; 6784 GB/s and 1940 TFLOP/s are the measured rates of a copy and of a
+// bf16 GEMM).  Up to 128 rows, HBM: 16 requests of 12000 positions take 127 us
+// with 8 drafts each (6240 GB/s, 92%) and 133 us with 16; 64 of one token and
+// 512 to 8191 positions 111 us (6260 GB/s).  Past that the tensor cores: 64
+// drafts each take 292 to 305 us by the box (1320 to 1380 TFLOP/s).  A tile of
+// two row tiles then takes about 3050 clocks: its four products need 2048, and
+// their operands and the copies of K and V alone keep shared memory busy for as
+// many (128 bytes a clock); each group's softmax (1900) and its own two products
+// follow one another, since 512 columns of tensor memory hold no second S.  A
+// segment's end costs four such tiles or so, which is what ragged trees pay: 32
+// requests with 33 to 64 drafts over 1024 to 8192 positions take 199 us (889
+// TFLOP/s; rows that fill no row tile are 15% of that).  Small calls are a chain
+// of latencies: 8 drafts of one request over 1021 positions take 13.4 us (launch
+// and lengths 2, cut and first pages 2, copies 2, three tiles of latency 3, sums
+// stored 1.5, merge kernel 3).
+// The warps' loops together are longer than the instruction cache, so code that
+// is off the hot path costs time on it: several of the forms here were chosen
+// for being short.
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -1277,7 +1297,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 // Joins the pieces of each cut segment: block x is the CTA in whose range a segment starts, its pieces lie
 // in that CTA's tail slot and the head slots of the CTAs after it.  A thread joins 4 columns of a row, a
 // block 8 rows; 4 pieces are under way at a time (what there is so far is
-// rescaled for them); 2, 8 and 16 were slower.
+// rescaled for them): 32 requests with 33 to 64 drafts 215 us with the attention, 2: 215, 8: 219, 16: 233; one
+// request over 131071 positions 90.0 us, 2: 91.2, 8: 91.2, 16: 93.7.  Bound by the trip to L2; alone 4 to 6 us.
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum O_i 2^(m_i - M) / L
 template <int D>
 __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a, int rows) {
