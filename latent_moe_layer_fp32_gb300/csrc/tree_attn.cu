@@ -165,6 +165,13 @@ __device__ __forceinline__ Load load_req(const AttnArgs& a, int b, Req* r) {
   return w;
 }
 
+// Tiles that start below x, which lies within a segment (32 bits); a tile costs 2 or 3.
+template <int NT>
+__device__ __forceinline__ int tiles_below(long long x, int tile) {
+  const unsigned y = (unsigned)x;
+  return NT == 2 && tile == 3 ? (y + 2u) / 3u : (y + 1u) / 2u;
+}
+
 // A segment by its place in its request's part of the line.
 struct Place {
   int h, m, tile;   // kv head, row group, cost of a tile
@@ -175,9 +182,12 @@ template <int NT>
 __device__ __forceinline__ Place place(const Load& w, int nt, int end, long long off) {
   Place p;
   const long long head = w.units(1, end);
-  p.h = (int)quot(off, head);
+  // at most 256 heads: the quotient in floats is off by one at most
+  p.h = (int)__fdividef((float)off, (float)head);
+  p.h -= off < p.h * head;
+  p.h += off >= (p.h + 1) * head;
   const long long r = off - p.h * head, group = (long long)nt * Cost<NT>::kTwo + end;
-  p.m = w.groups == 1 ? 0 : min((int)quot(r, group), w.groups - 1);
+  p.m = NT == 1 || w.groups == 1 ? 0 : min((int)quot(r, group), w.groups - 1);
   p.tile = p.m == w.groups - 1 ? w.last : Cost<NT>::kTwo;
   p.start = p.h * head + p.m * group;
   return p;
@@ -214,10 +224,10 @@ struct Walk {
       }
       const int nt = s->r.nt;
       const Place p = place<NT>(w, nt, cost, off);
-      const int i0 = (int)quot(off - p.start + p.tile - 1, p.tile);
+      const int i0 = tiles_below<NT>(off - p.start, p.tile);
       off = p.start + (long long)nt * p.tile + cost;
       if (i0 >= nt) continue;
-      const int i1 = (int)min((long long)nt, (long long)quot(max(end - p.start, 0ll) + p.tile - 1, p.tile));
+      const int i1 = tiles_below<NT>(min(max(end - p.start, 0ll), (long long)nt * p.tile), p.tile);
       if (i1 <= i0) return false;
       last = at + p.start + (long long)(nt - 1) * p.tile;
       s->b = b;
@@ -1296,7 +1306,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
 
 // Joins the pieces of each cut segment: block x is the CTA in whose range a segment starts, its pieces lie
 // in that CTA's tail slot and the head slots of the CTAs after it.  A thread joins 4 columns of a row, a
-// block 8 rows; 4 pieces are under way at a time (what there is so far is
+// block 8 rows (4 or 16: 1% slower); 4 pieces are under way at a time (what there is so far is
 // rescaled for them): 32 requests with 33 to 64 drafts 215 us with the attention, 2: 215, 8: 219, 16: 233; one
 // request over 131071 positions 90.0 us, 2: 91.2, 8: 91.2, 16: 93.7.  Bound by the trip to L2; alone 4 to 6 us.
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum O_i 2^(m_i - M) / L
