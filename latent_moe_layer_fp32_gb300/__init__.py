@@ -336,6 +336,7 @@ def lmoe_block_forward(dims, weights: LmoeWeights, norms: LmoeBlockNorms, x, y, 
 # tensor, addresses passed as plain integers, the current stream asked for without a Stream object.
 
 _I64 = (torch.int64, torch.uint64)
+_INT32 = torch.int32
 _BF16_ONLY = (torch.bfloat16,)
 
 
@@ -349,6 +350,18 @@ def _arg(t, n, dtypes, what):
         return t.data_ptr()
     _ptr(t, dtypes)  # raises for all but the size
     raise ValueError(f"{what}: expected at least {n} elements, got {t.numel()}")
+
+
+def _i32(t, n, what):
+    """_arg for int32, with the shortest path for what is right (0.28 instead of 0.33 us)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is _INT32 and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _arg(t, n, _I32, what)  # says what is wrong
 
 
 def _rows(t, heads, width, what="rows"):
@@ -409,9 +422,9 @@ def lmoe_tree_masks(token_offsets, parents, lens, mask, pos, ws=None, stream=Non
     if mask.dim() != 2 or mask.shape[0] != t:
         raise ValueError(f"mask: expected [{t}, mask_words], got {tuple(mask.shape)}")
     w, nb = _ws_arg(ws)
-    rc = load().lmoe_tree_masks(b, t, mask.shape[1], _arg(token_offsets, 2, _I32, "token_offsets"),
-                                _arg(parents, 1, _I32, "parents"), _arg(lens, b, _I32, "lens"),
-                                _arg(mask, 1, _I64, "mask"), _arg(pos, t, _I32, "pos"), w, nb, _stream_arg(stream))
+    rc = load().lmoe_tree_masks(b, t, mask.shape[1], _i32(token_offsets, 2, "token_offsets"),
+                                _i32(parents, 1, "parents"), _i32(lens, b, "lens"),
+                                _arg(mask, 1, _I64, "mask"), _i32(pos, t, "pos"), w, nb, _stream_arg(stream))
     if rc:
         raise LmoeError(rc, "lmoe_tree_masks")
 
@@ -432,9 +445,9 @@ def lmoe_tree_attention(dims, cache, q, k_new, v_new, token_offsets, lens, block
         raise ValueError(f"expected {n} rows in q, k_new and v_new")
     rc = load().lmoe_tree_attention(
         ctypes.byref(dims), ctypes.byref(cache), qp, qs, kp, ks, vp, vs,
-        _arg(token_offsets, b + 1, _I32, "token_offsets"), _arg(lens, b, _I32, "lens"),
-        _arg(block_table, b * dims.max_blocks, _I32, "block_table"), _arg(mask, n * dims.mask_words, _I64, "mask"),
-        _arg(pos, n, _I32, "pos"), _arg(out, n * hq * d, _BF16, "out"), _arg(lse, n * hq, _F32, "lse"), *_ws_arg(ws),
+        _i32(token_offsets, b + 1, "token_offsets"), _i32(lens, b, "lens"),
+        _i32(block_table, b * dims.max_blocks, "block_table"), _arg(mask, n * dims.mask_words, _I64, "mask"),
+        _i32(pos, n, "pos"), _arg(out, n * hq * d, _BF16, "out"), _arg(lse, n * hq, _F32, "lse"), *_ws_arg(ws),
         _stream_arg(stream))
     if rc:
         raise LmoeError(rc, "lmoe_tree_attention")
@@ -447,12 +460,12 @@ def lmoe_kv_plan(block_size, lens, new_tokens, owned, block_table, ring, ring_st
     if block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError(f"block_table: expected [{b}, max_blocks], got {tuple(block_table.shape)}")
     rc = load().lmoe_kv_plan(
-        b, block_size, block_table.shape[1], slots.numel(), _arg(lens, 1, _I32, "lens"),
-        _arg(new_tokens, b, _I32, "new_tokens"), _arg(owned, b, _I32, "owned"),
-        _arg(block_table, 1, _I32, "block_table"), _arg(ring, 1, _I32, "ring"), ring.numel(),
-        _arg(ring_state, 2, _I32, "ring_state"), _arg(lens_out, b, _I32, "lens_out"),
-        _arg(owned_out, b, _I32, "owned_out"), _arg(ring_state_out, 2, _I32, "ring_state_out"),
-        _arg(token_offsets, b + 1, _I32, "token_offsets"), _arg(slots, 1, _I32, "slots"), _stream_arg(stream))
+        b, block_size, block_table.shape[1], slots.numel(), _i32(lens, 1, "lens"),
+        _i32(new_tokens, b, "new_tokens"), _i32(owned, b, "owned"),
+        _i32(block_table, 1, "block_table"), _i32(ring, 1, "ring"), ring.numel(),
+        _i32(ring_state, 2, "ring_state"), _i32(lens_out, b, "lens_out"),
+        _i32(owned_out, b, "owned_out"), _i32(ring_state_out, 2, "ring_state_out"),
+        _i32(token_offsets, b + 1, "token_offsets"), _i32(slots, 1, "slots"), _stream_arg(stream))
     if rc:
         raise LmoeError(rc, "lmoe_kv_plan")
 
@@ -464,7 +477,7 @@ def lmoe_kv_write(cache, k_new, v_new, src, slots, ws=None, stream=None):
     vp, vs = _rows(v_new, hk, d, "v_new")
     w, nb = _ws_arg(ws)
     rc = load().lmoe_kv_write(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
-                              _arg(src, n, _I32, "src"), _arg(slots, 1, _I32, "slots"), n, w, nb, _stream_arg(stream))
+                              _i32(src, n, "src"), _i32(slots, 1, "slots"), n, w, nb, _stream_arg(stream))
     if rc:
         raise LmoeError(rc, "lmoe_kv_write")
 

@@ -1,7 +1,9 @@
 """Tree attention over the paged cache against plain 64-bit loops.
 
-Bounds, from the arithmetic that include/lmoe.h states (u = 2^-9, bf16's unit
-roundoff; A = sum_j p_j |v_j|; S = max_j scale sum_d |q_d k_jd|):
+Bounds, from the arithmetic that include/lmoe.h states (u = 2^-9, half of bf16's
+unit roundoff: the result's own rounding may take all of 2 u, so where a few keys
+hold a row's weight P has to be finer than one bf16; A = sum_j p_j |v_j|;
+S = max_j scale sum_d |q_d k_jd|):
   scores   products are exact in fp32, head_dim additions of at most 2^-23
            relative each (truncating accumulators), the scale and the change
            of base: |ds| <= (head_dim + 8) 2^-23 S + 2^-22 |s|; exponentials
