@@ -155,6 +155,14 @@ def test_tree_sizes(lm, n, hq, hk, d):
     Case([150, 0], [n, max(0, n - 3)], hq=hq, hk=hk, d=d, seed=n).check(lm)
 
 
+@pytest.mark.parametrize("rows", [31, 32, 33, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 70])
+def test_rows_at_the_kernels_bounds(lm, rows, d, window):
+    """One query head a key head: a request's rows are its drafts.  Long, short and empty prefixes, ends in tiles."""
+    Case([700, 129, 0, 63], [rows, max(1, rows - 31), rows // 2, 1], hq=2, hk=2, d=d, window=window, seed=rows).check(lm)
+
+
 @pytest.mark.parametrize("order", ["head", "slot"])
 @pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("d", [64, 128])
