@@ -1331,20 +1331,28 @@ __global__ void __launch_bounds__(2 * D) tree_attn_merge_kernel(const AttnArgs a
   if (pieces < 2 || local >= c0.z) return;
   auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
   constexpr int U = 4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), next_o[U];
+  float2 next_ml[U];
   float M = -INFINITY, L = 0.f;
+  auto fetch = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      next_ml[u] = make_float2(-INFINITY, 0.f);
+      next_o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p0 + u < pieces) {
+        next_ml[u] = a.part_ml[slot(p0 + u) * rows + local];
+        next_o[u] = reinterpret_cast<const float4*>(a.part_o)[(slot(p0 + u) * (D / 4) + unit) * rows + local];
+      }
+    }
+  };
+  fetch(0);
+#pragma unroll 1
   for (int p0 = 0; p0 < pieces; p0 += U) {
     float4 o[U];
     float2 ml[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      ml[u] = make_float2(-INFINITY, 0.f);
-      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p0 + u < pieces) {
-        ml[u] = a.part_ml[slot(p0 + u) * rows + local];
-        o[u] = reinterpret_cast<const float4*>(a.part_o)[(slot(p0 + u) * (D / 4) + unit) * rows + local];
-      }
-    }
+    for (int u = 0; u < U; ++u) o[u] = next_o[u], ml[u] = next_ml[u];
+    if (p0 + U < pieces) fetch(p0 + U);
     float top = M;
 #pragma unroll
     for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
