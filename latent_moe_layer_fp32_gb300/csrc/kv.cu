@@ -276,7 +276,8 @@ int run_plan(const PlanArgs& a, int sms, cudaStream_t s) {
 // slot writes
 // ---------------------------------------------------------------------------
 // A thread moves one 16-byte piece of a row's K and the same of its V.  A prompt's write is a copy, bound by
-// HBM: 16384 tokens of 8 heads of 128 columns (134 MB moved) take 22.6 us, 5930 GB/s; 211 accepted rows 2.1 us.
+// HBM: 16384 tokens of 8 heads of 128 columns (134 MB moved) take 22.6 us, 5950 GB/s (22.8 with a grid of 16
+// CTAs an SM that loops; two or four pieces a thread: 22.3, but 211 accepted rows 2.4 and 3.2 us instead of 1.9).
 __global__ void __launch_bounds__(256)
     kv_write_kernel(const lmoe_kv_cache c, const uint16_t* __restrict__ k_new, long long ks,
                     const uint16_t* __restrict__ v_new, long long vs, int n_rows, const int32_t* __restrict__ src,
@@ -284,25 +285,24 @@ __global__ void __launch_bounds__(256)
                     Status* st) {
   pdl_wait();
   pdl_trigger();
-  const unsigned total = (unsigned)n_tokens * (unsigned)pieces;
-  for (unsigned x = blockIdx.x * 256u + threadIdx.x; x < total; x += gridDim.x * 256u) {
-    const unsigned t = x / (unsigned)pieces, p = x - t * (unsigned)pieces;
-    const int slot = slots[t];
-    if (slot < 0) continue;
-    const int row = src ? src[t] : (int)t;
-    const int block = slot >> bs_shift;
-    if (block >= c.n_blocks || row < 0 || row >= n_rows) {
-      set_error(st, LMOE_EDEVICE_CHECK, 221);
-      continue;
-    }
-    const unsigned h = p >> d_shift, d = (p & ((1u << d_shift) - 1)) * 8;
-    const size_t to = (size_t)block * c.block_stride + (size_t)h * c.head_stride +
-                      (size_t)(slot & ((1 << bs_shift) - 1)) * c.slot_stride + d;
-    const uint4 kv = __ldcs(reinterpret_cast<const uint4*>(k_new + (size_t)row * ks + (size_t)p * 8));
-    const uint4 vv = __ldcs(reinterpret_cast<const uint4*>(v_new + (size_t)row * vs + (size_t)p * 8));
-    *reinterpret_cast<uint4*>(c.k + to) = kv;
-    *reinterpret_cast<uint4*>(c.v + to) = vv;
+  const unsigned x = blockIdx.x * 256u + threadIdx.x;
+  if (x >= (unsigned)n_tokens * (unsigned)pieces) return;
+  const unsigned t = x / (unsigned)pieces, p = x - t * (unsigned)pieces;
+  const int slot = slots[t];
+  if (slot < 0) return;
+  const int row = src ? src[t] : (int)t;
+  const int block = slot >> bs_shift;
+  if (block >= c.n_blocks || row < 0 || row >= n_rows) {
+    set_error(st, LMOE_EDEVICE_CHECK, 221);
+    return;
   }
+  const unsigned h = p >> d_shift, d = (p & ((1u << d_shift) - 1)) * 8;
+  const size_t to = (size_t)block * c.block_stride + (size_t)h * c.head_stride +
+                    (size_t)(slot & ((1 << bs_shift) - 1)) * c.slot_stride + d;
+  const uint4 kv = __ldcs(reinterpret_cast<const uint4*>(k_new + (size_t)row * ks + (size_t)p * 8));
+  const uint4 vv = __ldcs(reinterpret_cast<const uint4*>(v_new + (size_t)row * vs + (size_t)p * 8));
+  *reinterpret_cast<uint4*>(c.k + to) = kv;
+  *reinterpret_cast<uint4*>(c.v + to) = vv;
 }
 
 bool al16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -420,7 +420,7 @@ int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, int64_t k_s
   const int pieces = (int)(row / 8);
   const long long total = (long long)n_tokens * pieces;
   if (total > 0x7fffffffll) return LMOE_EUNSUPPORTED;
-  const int grid = (int)min((total + 255) / 256, (long long)di.sms * 16);
+  const int grid = (int)((total + 255) / 256);
   return launch_pdl("kv_write_kernel", dim3(grid), dim3(256), 0, s, kv_write_kernel, *cache, k_new,
                     (long long)k_stride, v_new, (long long)v_stride, n_rows, src, slots, n_tokens, pieces,
                     log2_of(cache->block_size), log2_of(cache->head_dim / 8), st);
