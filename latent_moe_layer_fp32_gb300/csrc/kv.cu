@@ -101,6 +101,7 @@ struct PlanArgs {
   int B, bs, max_blocks, n_slots, ring_size;
   const int32_t *lens, *add, *owned, *ring_state;
   int32_t *table, *ring, *lens_out, *owned_out, *ring_state_out, *offsets, *slots;
+  bool wide;  // lens, add and owned are 16-byte aligned
 };
 
 // ceil of (len + add) / bs, at most one past the table
@@ -134,6 +135,13 @@ __device__ __forceinline__ unsigned long long scan_excl(unsigned long long v, un
   return x - v + (warp ? before : 0ull);
 }
 
+// Four ints at 16-byte aligned places (or in registers).
+__device__ __forceinline__ void copy4(int* to, const int* from) {
+  *reinterpret_cast<int4*>(to) = *reinterpret_cast<const int4*>(from);
+}
+// Ints of each per-request array in shared memory: B + 1 at least, in whole fours.
+__host__ __device__ constexpr int plan_ints(int b) { return (b + 4) & ~3; }
+
 // (head + i) % size for a head and an i below size
 __device__ __forceinline__ int ring_at(int head, long long i, int size) {
   const long long x = head + i;
@@ -143,29 +151,45 @@ __device__ __forceinline__ int ring_at(int head, long long i, int size) {
 // Every CTA scans all requests itself (L2-resident lengths, a run of up to 8 requests per thread, two block
 // scans) and keeps what a token needs of its request in shared memory; then it takes its share of the
 // requests (a warp each) and of the tokens (a thread each, its request found by bisection).  Nothing is
-// passed between CTAs, so one launch does it.  What bounds it is the chain of dependent loads: 4096 requests
-// with 76000 tokens take 9.8 us, 8 requests 2.8 us (with a scan per 1024 requests and lengths fetched again
-// per token: 14.9 and 4.0 us).
+// passed between CTAs, so one launch does it.  What bounds it is the chain of dependent loads and the shared
+// memory accesses of the scan: 4096 requests with 76000 tokens take 8.6 us, 8 requests 2.8 us (with a scan per
+// 1024 requests and lengths fetched again per token: 14.9 and 4.0 us; with a run's values moved one by one
+// instead of four at a time: 9.6 us).
 template <int NT, int PER>
 __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
-  extern __shared__ int s_plan[];
-  int* s_tok = s_plan;             // [B + 1] first token of each request, saturated at n_slots + 1
-  int* s_pop = s_plan + a.B + 1;   // [B] blocks popped by the requests before it; -1: not served
-  int* s_push = s_pop + a.B;       // [B] blocks pushed by the requests before it; -1: it does not end
-  int* s_len = s_push + a.B;       // [B] tokens held
-  int* s_own = s_len + a.B;        // [B] blocks held
+  extern __shared__ __align__(16) int s_plan[];
+  const int held_n = plan_ints(a.B);  // of each array, a multiple of 4
+  int* s_tok = s_plan;                // [B + 1] first token of each request, saturated at n_slots + 1
+  int* s_pop = s_tok + held_n;        // [B] blocks popped by the requests before it; -1: not served
+  int* s_push = s_pop + held_n;       // [B] blocks pushed by the requests before it; -1: it does not end
+  int* s_len = s_push + held_n;       // [B] tokens held
+  int* s_own = s_len + held_n;        // [B] blocks held
   __shared__ unsigned long long s_warp[32];
   __shared__ int s_taken;
   pdl_wait();
   pdl_trigger();
   const int b0 = threadIdx.x * PER;
-  int add[PER], len[PER], own[PER];  // all at once: one trip to memory
+  alignas(16) int add[PER], len[PER], own[PER];  // all at once: one trip to memory
+  if (PER % 4 == 0 && a.wide && b0 + PER <= a.B) {
+#pragma unroll
+    for (int j = 0; j < PER; j += 4) {
+      copy4(add + j, a.add + b0 + j);
+      copy4(len + j, a.lens + b0 + j);
+      copy4(own + j, a.owned + b0 + j);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const bool in = b0 + j < a.B;
+      add[j] = in ? a.add[b0 + j] : 0;
+      len[j] = in ? a.lens[b0 + j] : 0;
+      own[j] = in ? a.owned[b0 + j] : 0;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const bool in = b0 + j < a.B;
-    add[j] = in ? a.add[b0 + j] : 0;
-    len[j] = in ? max(a.lens[b0 + j], 0) : 0;
-    own[j] = in ? min(max(a.owned[b0 + j], 0), a.max_blocks) : 0;
+    len[j] = max(len[j], 0);
+    own[j] = min(max(own[j], 0), a.max_blocks);
   }
   const int head = a.ring_state[0], count = min(max(a.ring_state[1], 0), a.ring_size);
   const int hd = head < 0 || head >= a.ring_size ? 0 : head;
@@ -189,22 +213,37 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
   }
   both = scan_excl<NT>(both, s_warp, &n_both);
   int taken = 0;
+  alignas(16) int tok[PER], popped[PER], pushed[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int b = b0 + j;
-    if (b < a.B) {
-      const unsigned long long pop = both >> 32;
-      const bool served = (fit >> j & 1u) && (need[j] == 0 || pop + need[j] <= (unsigned long long)count);
-      if (served && need[j] > 0) taken = (int)(pop + need[j]);
-      s_tok[b] = (int)min(t0, (unsigned long long)a.n_slots + 1);
-      s_pop[b] = served ? (int)min(pop, 0x7fffffffull) : -1;
-      s_push[b] = add[j] < 0 ? (int)(both & 0xffffffffu) : -1;
-      s_len[b] = len[j];
-      s_own[b] = own[j];
-      if (blockIdx.x == 0) a.offsets[b] = (int)min(t0, 0x7fffffffull);
-      t0 += max(add[j], 0);
-      both += (unsigned long long)need[j] << 32 | (unsigned)(add[j] < 0 ? own[j] : 0);
-    }
+    const unsigned long long pop = both >> 32;
+    const bool served = (fit >> j & 1u) && (need[j] == 0 || pop + need[j] <= (unsigned long long)count);
+    if (served && need[j] > 0) taken = (int)(pop + need[j]);
+    tok[j] = (int)min(t0, (unsigned long long)a.n_slots + 1);
+    popped[j] = served ? (int)min(pop, 0x7fffffffull) : -1;
+    pushed[j] = add[j] < 0 ? (int)(both & 0xffffffffu) : -1;
+    if (blockIdx.x == 0 && b < a.B) a.offsets[b] = (int)min(t0, 0x7fffffffull);
+    t0 += max(add[j], 0);
+    both += (unsigned long long)need[j] << 32 | (unsigned)(add[j] < 0 ? own[j] : 0);
+  }
+  // (past the last request: nothing asked for, the total's token; the arrays have room for whole fours)
+  if constexpr (PER % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < PER; j += 4)
+      if (b0 + j < a.B) {
+        copy4(s_tok + b0 + j, tok + j);
+        copy4(s_pop + b0 + j, popped + j);
+        copy4(s_push + b0 + j, pushed + j);
+        copy4(s_len + b0 + j, len + j);
+        copy4(s_own + b0 + j, own + j);
+      }
+  } else if (b0 < a.B) {
+    s_tok[b0] = tok[0];
+    s_pop[b0] = popped[0];
+    s_push[b0] = pushed[0];
+    s_len[b0] = len[0];
+    s_own[b0] = own[0];
   }
   if (taken > 0) atomicMax(&s_taken, taken);
   if (threadIdx.x == 0) {
@@ -265,10 +304,10 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
 template <int NT, int PER>
 int run_plan(const PlanArgs& a, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  const int rc = allow_smem(done, kv_plan_kernel<NT, PER>, (5 * NT * PER + 1) * 4);
+  const int rc = allow_smem(done, kv_plan_kernel<NT, PER>, 5 * plan_ints(NT * PER) * 4);
   if (rc) return rc;
   const int want = max((a.B + NT / 32 - 1) / (NT / 32), (int)((a.n_slots + NT - 1ll) / NT));
-  return launch_pdl("kv_plan_kernel", dim3(min(want, sms)), dim3(NT), (5 * (size_t)a.B + 1) * 4, s,
+  return launch_pdl("kv_plan_kernel", dim3(min(want, sms)), dim3(NT), 5 * (size_t)plan_ints(a.B) * 4, s,
                     kv_plan_kernel<NT, PER>, a);
 }
 
@@ -395,7 +434,9 @@ int lmoe_kv_plan(int32_t n_requests, int32_t block_size, int32_t max_blocks, int
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const PlanArgs a = {n_requests, block_size,  max_blocks, n_slots,  ring_size, lens,           new_tokens, owned,
-                      ring_state, block_table, ring,       lens_out, owned_out, ring_state_out, token_offsets, slots};
+                      ring_state, block_table, ring,       lens_out, owned_out, ring_state_out, token_offsets, slots,
+                      ((reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(new_tokens) |
+                        reinterpret_cast<uintptr_t>(owned)) & 15u) == 0};
   if (n_requests <= 256) return run_plan<256, 1>(a, di.sms, s);
   if (n_requests <= 1024) return run_plan<1024, 1>(a, di.sms, s);
   if (n_requests <= 4096) return run_plan<1024, 4>(a, di.sms, s);

@@ -105,12 +105,12 @@ def plan_case(rng, B, bs, max_blocks, free, new, lens=None, slack=0, short_slots
     return bs, max_blocks, n_slots, lens, new, owned, table, ring, np.array([head, free], np.int32)
 
 
-def run_plan(lm, bs, max_blocks, n_slots, lens, new, owned, table, ring, state):
+def run_plan(lm, bs, max_blocks, n_slots, lens, new, owned, table, ring, state, off=0):
     B = len(lens)
     t, r = dev(table), dev(ring)
     o = {k: torch.full((n,), -77, dtype=torch.int32, device="cuda") for k, n in
          (("lens", B), ("owned", B), ("state", 2), ("offsets", B + 1), ("slots", n_slots))}
-    args = [dev(x) for x in (lens, new, owned)]
+    args = [dev(np.concatenate([np.full(off, -5, np.int32), x]))[off:] for x in (lens, new, owned)]
     st = dev(state)
     for _ in range(2):  # the same inputs again give the same outputs
         lm.lmoe_kv_plan(bs, *args, t, r, st, o["lens"], o["owned"], o["state"], o["offsets"], o["slots"])
@@ -134,6 +134,18 @@ def test_plan_random(lm, B, bs, max_blocks):
     check_plan(lm, plan_case(rng, B, bs, max_blocks, free=max(1, B // 2), new=new, slack=1))
     # too few slots: the last requests wait
     check_plan(lm, plan_case(rng, B, bs, max_blocks, free=2 * B + 8, new=new, short_slots=bs + 3))
+
+
+@pytest.mark.parametrize("B", [1026, 1027, 1028, 2050, 4095, 4096, 5003, 8191])
+def test_plan_any_alignment(lm, B):
+    """Arrays that start between 16-byte boundaries, and request counts that fill no whole four."""
+    rng = np.random.default_rng(B)
+    case = plan_case(rng, B, 16, 4, free=B, new=rng.integers(-1, 20, B), slack=1)
+    exp = kv_ref.plan(*case)
+    for off in (0, 1, 3):
+        got = run_plan(lm, *case, off=off)
+        for k in exp:
+            assert np.array_equal(got[k], exp[k]), (off, k)
 
 
 @pytest.mark.parametrize("new,lens,free", [([0], [0], 3), ([0], [16], 0), ([1], [16], 1), ([1], [16], 0),
