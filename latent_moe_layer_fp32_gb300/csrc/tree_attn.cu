@@ -41,7 +41,7 @@
 // segment's end costs four such tiles or so, which is what ragged trees pay: 32
 // requests with 33 to 64 drafts over 1024 to 8192 positions take 199 us (889
 // TFLOP/s; rows that fill no row tile are 15% of that).  Small calls are a chain
-// of latencies: 8 drafts of one request over 1021 positions take 13.4 us (launch
+// of latencies: 8 drafts of one request over 1021 positions take 13.2 us (launch
 // and lengths 2, cut and first pages 2, copies 2, three tiles of latency 3, sums
 // stored 1.5, merge kernel 3).
 // The warps' loops together are longer than the instruction cache, so code that
