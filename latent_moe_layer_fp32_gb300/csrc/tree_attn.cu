@@ -42,8 +42,8 @@
 // requests with 33 to 64 drafts over 1024 to 8192 positions take 199 us (889
 // TFLOP/s; rows that fill no row tile are 15% of that).  Small calls are a chain
 // of latencies: 8 drafts of one request over 1021 positions take 13.2 us (launch
-// and lengths 2, cut and first pages 2, copies 2, three tiles of latency 3, sums
-// stored 1.5, merge kernel 3).
+// and lengths 2, cut and first pages 2, copies 2, scores, softmax and product 2,
+// sums stored 1, merge kernel 3 to 4).
 // The warps' loops together are longer than the instruction cache, so code that
 // is off the hot path costs time on it: several of the forms here were chosen
 // for being short.
