@@ -431,7 +431,7 @@ struct Cfg {
   static constexpr int kQBytes = KS > 1 ? 32768 : kTile * D * 2;  // a group's queries; with copies also their sums
   static constexpr int kStages = D == 128 ? 5 : (KS > 1 ? 10 : 12);  // 160 KB of keys and values, or more, in flight
   static constexpr int kThreads = 384;                // two softmax groups, two producers, MMA, cleaning warp
-  static constexpr int kMisc = 3072;
+  static constexpr int kMisc = 3 * 1024;
   static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMisc;
   static constexpr uint32_t kO = 2 * kTile;           // first O column; S buffers at 0 and 128
   // the join of copies: each takes D / KS columns of the sum, in passes of kPass columns
