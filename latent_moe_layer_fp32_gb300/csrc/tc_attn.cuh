@@ -1,6 +1,7 @@
 // Further tensor-core forms, those that attention needs beside tc.cuh's: a B
 // operand that is M/N-major in shared memory (values as they lie in a cache),
-// products into some of the accumulator's lanes only, 16-column loads.
+// products into some of the accumulator's lanes only, 16-column loads, an L2
+// policy for tiles that are read again.
 #pragma once
 
 #include "tc.cuh"
@@ -15,6 +16,13 @@ __host__ __device__ constexpr uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 constexpr uint32_t kIdescBMnMajor = 1u << 16;  // B is MN-major
+
+// L2 policy for copies of what will be read again.
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 
 // TMEM -> registers: 32 lanes x 32 bits, 16 consecutive columns.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
