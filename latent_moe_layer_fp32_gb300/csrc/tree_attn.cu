@@ -120,6 +120,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int whe
   return false;
 }
 
+// Whether phase `parity` of `bar` has completed, the same answer in every lane (all 32 ask).  The phase may
+// complete between two lanes' probes; an answer that steers the whole warp has to be one for all of them.
+__device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+}
+
 // How the line of tiles is measured for the cut into equal ranges: a tile of two row tiles, of one, and the
 // end of a segment (its sums joined and stored, the next one's queries, masks and first tiles).  Measured:
 // the ends at two and a half tiles instead of half a one took 16 requests of 1000 to 32768 positions from
@@ -1105,7 +1111,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       }
       // ---- the segment's end: finished rows to out, cut ones to the partial sums ----
       const uint32_t ge = NT == 1 ? g + n - 1 : g_own + n - 1;  // the segment's last tile
-      if (NT == 2 && mbar_test_wait(&seg_full[(seg + 1) & 3], ((seg + 1) >> 2) & 1)) {
+      if (NT == 2 && bar_test(&seg_full[(seg + 1) & 3], ((seg + 1) >> 2) & 1)) {
         // every product with these queries is done: the next segment's may come in
         const Seg* nx = seg_at(seg + 1);
         early = nx->i1 > 0 && (grp == 0 || nx->rows > kTile);

@@ -306,6 +306,17 @@ def test_many_tiles_in_a_row(lm, n, d):
         assert torch.equal(c.run(lm)[0], ref)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_segments_of_one_and_two_row_tiles_in_a_row(lm, d):
+    # more than 128 rows a key head: at a segment's end both groups, or one of them, fetch the next one's queries
+    # if its record is there by then, and else later: the same bits either way
+    rng = np.random.default_rng(41)
+    c = Case(rng.integers(0, 900, 24), rng.integers(9, 48, 24), hq=16, hk=2, d=d, seed=41)
+    ref = c.check(lm)
+    for _ in range(20):
+        assert torch.equal(c.run(lm)[0], ref)
+
+
 def test_offsets_past_32_bits(lm):
     c = Case([200], [4], hq=16, hk=8, d=128, bs=64, seed=19)
     blocks = 36000  # more than 2^31 elements and 2^32 bytes per tensor
