@@ -107,7 +107,11 @@ __device__ __forceinline__ unsigned long long quot(unsigned long long x, unsigne
 
 // A wait bounded by about a second of SM clocks.  The kernel's warps run different loops of it at once and
 // wait for instructions where these do not fit the instruction cache together, so this is kept short: what
-// ran out is noted in `failed` and reported once, at the kernel's end.
+// ran out is noted in `failed` and reported once, at the kernel's end.  Each lane answers for itself, and at
+// the limit two lanes' answers may differ.  So a warp leaves a loop only by a vote; half a warp that had left
+// would have the other half wait for it at the next warp-wide step.  With votes at every wait of the issuing
+// warp wide trees took 204 us instead of 199, so that one votes once a tile (a window layer: 41.1 us, 39.4
+// without any vote; the other cases the same).
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int where, int& failed) {
   if (mbar_try_wait(bar, parity)) return true;
   uint32_t t0, t1;
@@ -118,6 +122,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int whe
   } while (t1 - t0 < 0x70000000u);
   failed = where;
   return false;
+}
+
+// bar_wait with one answer for the whole warp (all 32 lanes wait).
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, int where, int& failed) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, where, failed));
 }
 
 // Whether phase `parity` of `bar` has completed, the same answer in every lane (all 32 ask).  The phase may
@@ -595,13 +604,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   auto fewer = [] {
     if constexpr (KS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   };
-  int failed = 0;  // where a wait ran out
+  int failed = 0;  // where a wait of this lane ran out
+  auto gave_up = [&] { return __any_sync(0xffffffffu, failed != 0) != 0; };
   // the record of segment `i`, once it is there; warps take the segments in order
   auto seg_at = [&](uint32_t i) { return const_cast<const Seg*>(s_seg + (i & 3)); };
   auto seg_wait = [&](uint32_t i) { return bar_wait(&seg_full[i & 3], (i >> 2) & 1, 261, failed); };
   auto seg_done = [&](uint32_t i) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&seg_empty[i & 3]);
+    if (lane == 0 && failed == 0) mbar_arrive(&seg_empty[i & 3]);  // (never for a record that did not come)
   };
 
   if (warp == kKeys || warp == kValues) {
@@ -626,14 +636,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           cut0 = make_int4(1, s.r.t0, s.rows, s.h), cut1 = make_int4(s.m, 0, 0, 0);
         else
           cut0.x = 0;
-        if (!(ok = bar_wait(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, 262, failed))) break;
+        if (!(ok = bar_wait_warp(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, 262, failed))) break;
         if (lane == 0) {
           s_seg[seg & 3] = s;
           mbar_arrive(&seg_full[seg & 3]);
         }
         __syncwarp();
       } else {
-        if (!(ok = seg_wait(seg))) break;
+        if (!(ok = __all_sync(0xffffffffu, seg_wait(seg)))) break;
         s = *seg_at(seg);
         seg_done(seg);
       }
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         auto copy = [&](uint32_t at) {
           const CUtensorMap* const tc = rows == 8 ? (keys ? &tm_k8 : &tm_v8) : (keys ? &tm_k : &tm_v);
           const uint32_t stage = at % ST;
-          if (!bar_wait(&empty[stage], ((at / ST) & 1) ^ 1, 221, failed)) return false;
+          if (!bar_wait_warp(&empty[stage], ((at / ST) & 1) ^ 1, 221, failed)) return false;
           uint8_t* dst = s_ring + stage * C::kStageBytes;
           if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
           __syncwarp();
@@ -708,8 +718,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       const bool leader = elect_one();
       constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
       constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
-      bool ok = true;
-      auto ready = [&](uint64_t* bar, uint32_t parity, int where) { return bar_wait(bar, parity, where, failed); };
+      // a tile goes on after a wait that ran out, on whatever there is; the vote at the next one ends the loop
+      auto ready = [&](uint64_t* bar, uint32_t parity, int where) { bar_wait(bar, parity, where, failed); };
       // descriptors step by their start address (bits 0 to 13, in units of 16 bytes)
       const uint64_t qd = smem_desc_sw128(smem_u32(s_q)), kd = smem_desc_sw128(smem_u32(s_ring));
       const uint64_t vd = smem_desc_sw128_mn(smem_u32(s_ring), kTile * 128);
@@ -725,8 +735,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
         __syncwarp();
       };
+      // (after a wait that ran out no stage is given back: a copy may still be on its way into it)
       auto commit = [&](uint64_t* bar) {
-        if (leader) tc_commit(bar);
+        if (leader && failed == 0) tc_commit(bar);
         __syncwarp();
       };
       // O += P V for 64 keys at a time, each half as soon as its probabilities are there
@@ -735,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const uint32_t p = tmem + buf * kTile, o = tmem + C::kO + grp * D;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (!ready(&p_full[2 * buf + hf], parity, 233 + hf)) return false;
+          ready(&p_full[2 * buf + hf], parity, 233 + hf);
           tc_fence_after();
           const uint32_t lo = s_lo[buf], ph = p + hf * 64;
           const uint64_t vh = v0 + hf * (64 * 128 >> 4);
@@ -770,7 +781,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           }
           __syncwarp();
         }
-        return true;
       };
       uint32_t ring = 0, ring_phase = 0;
       auto skip = [&] {
@@ -780,11 +790,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         }
       };
       auto tile = [&](uint32_t* stage) {  // the next tile of the ring has landed (they are taken in its order)
-        if (!ready(&full[ring], ring_phase, 231)) return false;
+        ready(&full[ring], ring_phase, 231);
         tc_fence_after();
         *stage = ring;
         skip();
-        return true;
       };
       // what this warp needs of a segment
       struct Part {
@@ -793,11 +802,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       };
       Part s{}, nx{};
       auto get = [&](uint32_t i, Part* p) {
-        if (!seg_wait(i)) return false;
+        seg_wait(i);
         const Seg* x = seg_at(i);
         *p = Part{x->i0, x->i1, x->r.cut, x->r.full, x->rows};
         seg_done(i);
-        return true;
       };
       auto clean = [&](const Part& p, int i) {  // hands tile i to the cleaning warp if it is an edge
         if (p.edge(i) && lane == 0) mbar_arrive(v_edge);
@@ -812,7 +820,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       int i = 0;
       for (uint32_t seg = 0;;) {
         const bool same = have && i + 1 < s.i1;
-        if (!same && !(ok = get(seg, &nx))) break;
+        if (!same) get(seg, &nx);
+        if (gave_up()) break;
         const Part t = same ? s : nx;  // of the next tile
         const int ti = same ? i + 1 : nx.i0;
         const bool more = same || nx.i1 > 0;
@@ -821,10 +830,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           const uint32_t tg = (same ? seg - 1 : seg) & 1, tb = have ? (np >> 2 & 1) ^ 1 : 0;
           if (more) {
             if (!same) {
-              if (!(ok = ready(&q_full[tg], nq >> tg & 1, 232))) break;
+              ready(&q_full[tg], nq >> tg & 1, 232);
               nq ^= 1u << tg;
             }
-            if (!(ok = tile(&ks))) break;
+            tile(&ks);
             qk(tg, tb, ks);
             if (!same) commit(&s_first[tg]);
             commit(&empty[ks]);
@@ -833,10 +842,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           }
           if (have) {
             const uint32_t buf = np >> 2 & 1;
-            if (!(ok = tile(&vs))) break;
-            if (s.edge(i) && !(ok = ready(v_clean, edges++ & 1, 236))) break;
+            tile(&vs);
+            if (s.edge(i)) ready(v_clean, edges++ & 1, 236);
             if (more) clean(t, ti);
-            if (!(ok = pv((seg - 1) & 1, buf, vs, i == s.i0, np >> buf & 1))) break;
+            pv((seg - 1) & 1, buf, vs, i == s.i0, np >> buf & 1);
             commit(&empty[vs]);
             np ^= 1u << buf | 4u;  // bit 2: the S buffer of the tile
           } else if (more) {
@@ -844,27 +853,27 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           }
         } else {
           if (have) {
-            if (!(ok = tile(&vs)) || (s.edge(i) && !(ok = ready(v_clean, edges++ & 1, 236)))) break;
+            tile(&vs);
+            if (s.edge(i)) ready(v_clean, edges++ & 1, 236);
           }
           if (more) clean(t, ti);  // (one at a time, so that no phase is missed)
 #pragma unroll 1
           for (int grp = 0; grp < 2; ++grp) {
             if (have && (grp == 0 || s.rows > kTile)) {
-              if (!(ok = pv(grp, grp, vs, i == s.i0, np >> grp & 1))) break;
+              pv(grp, grp, vs, i == s.i0, np >> grp & 1);
               np ^= 1u << grp;
               if (grp == 1 || s.rows <= kTile) commit(&empty[vs]);
             }
             if (more && (grp == 0 || t.rows > kTile)) {
               if (!same) {
-                if (!(ok = ready(&q_full[grp], nq >> grp & 1, 232))) break;
+                ready(&q_full[grp], nq >> grp & 1, 232);
                 nq ^= 1u << grp;
               }
-              if (grp == 0 && !(ok = tile(&ks))) break;
+              if (grp == 0) tile(&ks);
               tc_fence_after();
               qk(grp, grp, ks);
             }
           }
-          if (!ok) break;
           if (more) commit(&empty[ks]);
         }
         if (!more) break;
@@ -873,7 +882,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         i = ti;
         have = true;
       }
-      commit(done);  // every MMA issued has completed before TMEM is released
+      if (leader) tc_commit(done);  // every MMA issued has completed before TMEM is released
+      __syncwarp();
       bar_wait(done, 0, 235, failed);
     }
   } else if (warp < kKeys) {
@@ -920,6 +930,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     bool early = false;  // the segment's queries were loaded during the one before
     for (;; ++seg) {
       if (ok) ok = seg_wait(seg);
+      ok = __all_sync(0xffffffffu, ok);
       const Seg* const s = seg_at(seg);
       const int i0 = s->i0, n = s->i1 - i0;
       if (!ok || n == 0) break;
@@ -1249,17 +1260,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     // the segment's end.  A warp's access covers 4 keys of 128 bytes.
     fewer();
     uint32_t g = 0, edges = 0;
-    bool ok = true;
     for (uint32_t seg = 0;; ++seg) {
-      if (!(ok = seg_wait(seg))) break;
+      seg_wait(seg);
+      if (gave_up()) break;
       const Seg s = *seg_at(seg);
       seg_done(seg);
       if (s.i1 == 0) break;
-      for (int i = s.i0; i < s.i1 && ok; ++i, ++g) {
+      for (int i = s.i0; i < s.i1; ++i, ++g) {
         if (!s.r.edge(i)) continue;
-        if (!(ok = bar_wait(v_edge, edges++ & 1, 251, failed))) break;
+        bar_wait(v_edge, edges++ & 1, 251, failed);
         const uint32_t at = v_pos<NT>(g);
-        if (!(ok = bar_wait(&full[at % ST], (at / ST) & 1, 252, failed))) break;
+        bar_wait(&full[at % ST], (at / ST) & 1, 252, failed);
         uint8_t* const vt = s_ring + (at % ST) * C::kStageBytes + (lane & 7) * 16;
         const int base = s.r.base(i), hi = s.r.cached(i), nd = s.r.drafts(i), c0 = nd ? s.r.col(i) : hi, c1 = c0 + nd;
         // cached positions: seen by some row from `first` on, by every row from `all` on
@@ -1303,7 +1314,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(v_clean);
       }
-      if (!ok) break;
     }
   }
   if (failed) set_error(st, LMOE_ETIMEOUT, failed);

@@ -24,3 +24,16 @@ def test_one_shot_probes_are_voted_on():
     assert asked
     for before in asked:
         assert before.endswith("__all_sync(0xffffffffu, "), before
+
+
+def test_a_warp_leaves_a_loop_only_by_a_vote():
+    # a wait may run out for one lane and not for another: no loop ends on one lane's answer
+    code = re.sub(r"//[^\n]*", "", open(SRC).read())
+    code = code[code.index("tree_attn_kernel(const"):code.index("tree_attn_merge_kernel(const")]
+    ways_out = [x for x in code.splitlines() if re.search(r"\b(break|return false);", x)
+                and re.search(r"\bok\b|\bfailed\b|_wait|gave_up|ready\(|copy\(", x)]
+    assert len(ways_out) >= 6
+    for x in ways_out:
+        # `copy` ends with a vote of its own; the other two test an `ok` that has been voted on
+        assert re.search(r"__all_sync\(0xffffffffu|bar_wait_warp\(|gave_up\(\)|copy\(|if \(!ok\) break;|!ok \|\| n == 0", x), x
+    assert re.search(r"if \(ok\) ok = seg_wait\(seg\);\s*ok = __all_sync\(0xffffffffu, ok\);", code)
