@@ -382,6 +382,9 @@ LMOE_API size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* dims, 
  * Scores, the running maximum and sum, and the accumulators are fp32.  For
  * the product with the values a probability is rounded to bf16, or to two
  * bf16 parts where a key may hold over 1/8 of its row's sum so far.
+ * The device-side waits are bounded by 2 to 4 seconds, plus 8192 clocks for
+ * every 128 positions that a row of the block table has room for
+ * (LMOE_ETIMEOUT through lmoe_status_check).
  * Reported on the device (LMOE_EDEVICE_CHECK through lmoe_status_check):
  * offsets that descend, pass n_tokens or give a request more than
  * max_request_tokens rows, and a length below 0 or past its table: the rows

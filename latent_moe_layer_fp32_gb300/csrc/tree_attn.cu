@@ -77,6 +77,7 @@ struct AttnArgs {
   float2* part_ml; // [2 CTAs][rows] running maximum (base 2) and sum
   float* part_o;   // [2 CTAs][D / 4][rows][4]
   int B, T, max_n, hk, G, max_blocks, n_blocks, bs_shift, words, window, ctas;
+  uint32_t wait_limit;  // of bar_wait
   float scale_log2;
 };
 
@@ -105,28 +106,30 @@ __device__ __forceinline__ unsigned long long quot(unsigned long long x, unsigne
   return (x | y) >> 32 ? x / y : (unsigned)x / (unsigned)y;
 }
 
-// A wait bounded by about a second of SM clocks.  The kernel's warps run different loops of it at once and
-// wait for instructions where these do not fit the instruction cache together, so this is kept short: what
-// ran out is noted in `failed` and reported once, at the kernel's end.  Each lane answers for itself, and at
-// the limit two lanes' answers may differ.  So a warp leaves a loop only by a vote; half a warp that had left
-// would have the other half wait for it at the next warp-wide step.  With votes at every wait of the issuing
-// warp wide trees took 204 us instead of 199, so that one votes once a tile (a window layer: 41.1 us, 39.4
-// without any vote; the other cases the same).
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int where, int& failed) {
+// A wait bounded in SM clocks, counted in units of 2^32 (about two seconds): it runs out when the count has
+// passed more than `limit` of them.  Some waits last as long as a CTA's part of a segment, so the limit grows
+// with the longest request that the call admits (wait_limit).  The kernel's warps run different loops of it at
+// once and wait for instructions where these do not fit the instruction cache together, so this is kept short:
+// what ran out is noted in `failed` and reported once, at the kernel's end.  Each lane answers for itself, and
+// at the limit two lanes' answers may differ.  So a warp leaves a loop only by a vote; half a warp that had
+// left would have the other half wait for it at the next warp-wide step.  With votes at every wait of the
+// issuing warp wide trees took 204 us instead of 199, so that one votes once a tile (a window layer: 41.1 us,
+// 39.4 without any vote; the other cases the same).
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int where, int& failed, uint32_t limit) {
   if (mbar_try_wait(bar, parity)) return true;
   uint32_t t0, t1;
-  asm volatile("mov.u32 %0, %%clock;" : "=r"(t0));
+  asm volatile("mov.u32 %0, %%clock_hi;" : "=r"(t0));
   do {
     if (mbar_try_wait(bar, parity)) return true;
-    asm volatile("mov.u32 %0, %%clock;" : "=r"(t1));
-  } while (t1 - t0 < 0x70000000u);
+    asm volatile("mov.u32 %0, %%clock_hi;" : "=r"(t1));
+  } while (t1 - t0 <= limit);
   failed = where;
   return false;
 }
 
 // bar_wait with one answer for the whole warp (all 32 lanes wait).
-__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, int where, int& failed) {
-  return __all_sync(0xffffffffu, bar_wait(bar, parity, where, failed));
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, int where, int& failed, uint32_t limit) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, where, failed, limit));
 }
 
 // Whether phase `parity` of `bar` has completed, the same answer in every lane (all 32 ask).  The phase may
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
   auto gave_up = [&] { return __any_sync(0xffffffffu, failed != 0) != 0; };
   // the record of segment `i`, once it is there; warps take the segments in order
   auto seg_at = [&](uint32_t i) { return const_cast<const Seg*>(s_seg + (i & 3)); };
-  auto seg_wait = [&](uint32_t i) { return bar_wait(&seg_full[i & 3], (i >> 2) & 1, 261, failed); };
+  auto seg_wait = [&](uint32_t i) { return bar_wait(&seg_full[i & 3], (i >> 2) & 1, 261, failed, a.wait_limit); };
   auto seg_done = [&](uint32_t i) {
     __syncwarp();
     if (lane == 0 && failed == 0) mbar_arrive(&seg_empty[i & 3]);  // (never for a record that did not come)
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
           cut0 = make_int4(1, s.r.t0, s.rows, s.h), cut1 = make_int4(s.m, 0, 0, 0);
         else
           cut0.x = 0;
-        if (!(ok = bar_wait_warp(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, 262, failed))) break;
+        if (!(ok = bar_wait_warp(&seg_empty[seg & 3], ((seg >> 2) & 1) ^ 1, 262, failed, a.wait_limit))) break;
         if (lane == 0) {
           s_seg[seg & 3] = s;
           mbar_arrive(&seg_full[seg & 3]);
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         auto copy = [&](uint32_t at) {
           const CUtensorMap* const tc = rows == 8 ? (keys ? &tm_k8 : &tm_v8) : (keys ? &tm_k : &tm_v);
           const uint32_t stage = at % ST;
-          if (!bar_wait_warp(&empty[stage], ((at / ST) & 1) ^ 1, 221, failed)) return false;
+          if (!bar_wait_warp(&empty[stage], ((at / ST) & 1) ^ 1, 221, failed, a.wait_limit)) return false;
           uint8_t* dst = s_ring + stage * C::kStageBytes;
           if (lane == 0) mbar_arrive_expect_tx(&full[stage], (nc * rows + nd * 8) * (128 * HALVES));
           __syncwarp();
@@ -708,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     const uint32_t end = ok ? v_pos<NT>(g - 1) + 1 : issued;
     for (uint32_t k = g < ST ? 0 : g - ST; k < g; ++k) {
       const uint32_t at = keys ? k_pos<NT>(k) : v_pos<NT>(k);
-      if (at + ST >= end) bar_wait(&full[at % ST], (at / ST) & 1, 222, failed);
+      if (at + ST >= end) bar_wait(&full[at % ST], (at / ST) & 1, 222, failed, a.wait_limit);
     }
   } else if (warp == kMma) {
     // ---------------- MMA issuer ----------------
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       constexpr uint32_t kQk = idesc_bf16_f32(128, kTile);
       constexpr uint32_t kPv = idesc_bf16_f32(128, D) | kIdescBMnMajor;
       // a tile goes on after a wait that ran out, on whatever there is; the vote at the next one ends the loop
-      auto ready = [&](uint64_t* bar, uint32_t parity, int where) { bar_wait(bar, parity, where, failed); };
+      auto ready = [&](uint64_t* bar, uint32_t parity, int where) { bar_wait(bar, parity, where, failed, a.wait_limit); };
       // descriptors step by their start address (bits 0 to 13, in units of 16 bytes)
       const uint64_t qd = smem_desc_sw128(smem_u32(s_q)), kd = smem_desc_sw128(smem_u32(s_ring));
       const uint64_t vd = smem_desc_sw128_mn(smem_u32(s_ring), kTile * 128);
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       }
       if (leader) tc_commit(done);  // every MMA issued has completed before TMEM is released
       __syncwarp();
-      bar_wait(done, 0, 235, failed);
+      bar_wait(done, 0, 235, failed, a.wait_limit);
     }
   } else if (warp < kKeys) {
     // ---------------- softmax: one row per thread ----------------
@@ -901,7 +904,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
     // it writes is void.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
-      if (ok) ok = bar_wait(bar, parity, where, failed);
+      if (ok) ok = bar_wait(bar, parity, where, failed, a.wait_limit);
       tc_fence_after();
     };
     uint32_t meets = 0;
@@ -1268,9 +1271,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       if (s.i1 == 0) break;
       for (int i = s.i0; i < s.i1; ++i, ++g) {
         if (!s.r.edge(i)) continue;
-        bar_wait(v_edge, edges++ & 1, 251, failed);
+        bar_wait(v_edge, edges++ & 1, 251, failed, a.wait_limit);
         const uint32_t at = v_pos<NT>(g);
-        bar_wait(&full[at % ST], (at / ST) & 1, 252, failed);
+        bar_wait(&full[at % ST], (at / ST) & 1, 252, failed, a.wait_limit);
         uint8_t* const vt = s_ring + (at % ST) * C::kStageBytes + (lane & 7) * 16;
         const int base = s.r.base(i), hi = s.r.cached(i), nd = s.r.drafts(i), c0 = nd ? s.r.col(i) : hi, c1 = c0 + nd;
         // cached positions: seen by some row from `first` on, by every row from `all` on
@@ -1464,6 +1467,12 @@ int group_rows(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
   return rows <= 128 ? 128 : 256;
 }
 
+// Limit of the kernel's waits: 2 to 4 seconds, and further 8192 clocks (some three times what one takes) for
+// each tile of the longest request that the block table has room for.
+uint32_t wait_limit(const lmoe_attn_dims* d, const lmoe_kv_cache* c) {
+  return 1 + (uint32_t)(((uint64_t)d->max_blocks * c->block_size / kTile * 8192) >> 32);
+}
+
 struct AttnWs {
   size_t err, cut, ml, o, total;
 };
@@ -1604,6 +1613,7 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
   a.words = d->mask_words;
   a.window = d->window;
   a.ctas = di.sms;
+  a.wait_limit = wait_limit(d, c);
   a.scale_log2 = d->scale * 1.4426950408889634f;
   const int max_rows = a.max_n * a.G;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -386,6 +386,19 @@ def test_copy_descriptors_of_another_cache_are_not_used(lm):
         assert torch.equal(c.run(other)[0], ref)
 
 
+def test_waits_as_long_as_a_long_request(lm):
+    """A key head for each SM and a hundred million positions (four pages by turns): every CTA works through one
+    segment of 780,000 tiles, well over a second, in which its cleaning warp waits for the last one.  That is no
+    wait that ran out.  (Its status is looked at; 64-bit loops over as many keys would take minutes.)"""
+    heads = torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case([4 * 256], [17], hq=8 * heads, hk=heads, d=128, bs=256, seed=53, spare=0)
+    c.table = np.tile(c.table[:, :4], (1, 97657))
+    c.lens = np.array([c.table.shape[1] * 256], np.int32)
+    assert c.lens[0] // 128 > 780000
+    out, ls = c.run(lm)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(ls).all()
+
+
 def test_device_checks(lm):
     # a bad request is reported and skipped, the others are computed
     c = Case([40, 50, 60], [3, 3, 3], seed=29)
