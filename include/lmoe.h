@@ -401,8 +401,9 @@ LMOE_API int lmoe_tree_attention(const lmoe_attn_dims* dims, const lmoe_kv_cache
  * Request b holds lens[b] tokens in owned[b] blocks and gets new_tokens[b]
  * more (below 0: the request ends).  In request order:
  *   need = max(0, ceil((lens + new) / block_size) - owned);
- *   b is served iff its blocks fit its table row, its tokens fit slots[] and
- *   the needs of the requests up to it (those that fit) fit the free count;
+ *   b is served iff its blocks fit its table row, its tokens fit slots[], its
+ *   length stays below 2^31 and the needs of the requests up to it (those that
+ *   fit) fit the free count;
  *   a served request's new blocks come from the ring's head, an ended
  *   request's blocks go to its tail (they are free for the next call).
  *   block_table  int32 [B][max_blocks], in place: entries owned .. owned +

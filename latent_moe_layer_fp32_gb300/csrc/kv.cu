@@ -104,10 +104,11 @@ struct PlanArgs {
   bool wide;  // lens, add and owned are 16-byte aligned
 };
 
-// ceil of (len + add) / bs, at most one past the table
+// ceil of (len + add) / bs, at most one past the table; a sum past 31 bits fits no table (lengths and positions
+// are int32)
 __device__ __forceinline__ int blocks_for(int len, int add, int bs, int max_blocks) {
   const unsigned held = (unsigned)len + (unsigned)add, q = held / (unsigned)bs;
-  return (int)min(q + (held != q * (unsigned)bs), (unsigned)max_blocks + 1u);
+  return held > 0x7fffffffu ? max_blocks + 1 : (int)min(q + (held != q * (unsigned)bs), (unsigned)max_blocks + 1u);
 }
 
 // Sum of v over the threads before this one, and over all in *total.

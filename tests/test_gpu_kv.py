@@ -172,6 +172,24 @@ def test_plan_overflowing_sums(lm):
     assert (got["slots"] >= 0).all()
 
 
+def test_plan_lengths_past_31_bits(lm):
+    # a request whose length would pass 31 bits is not served, its neighbours are; positions up to there are exact
+    top, bs = 2**31 - 1, 1 << 30
+    table = np.array([[0, 1, -9, -9], [1, 0, -9, -9], [1, 1, -9, -9]], np.int32)
+    got = run_plan(lm, bs, 4, 16, np.array([top - 4, top - 19, top - 3], np.int32), np.array([10, 3, 3], np.int32),
+                   np.array([2, 2, 2], np.int32), table, np.array([5, 6, 7, 8], np.int32), np.array([0, 4], np.int32))
+    assert got["lens"].tolist() == [top - 4, top - 16, top] and got["owned"].tolist() == [2, 2, 2]
+    assert got["offsets"].tolist() == [0, 10, 13, 16] and got["state"].tolist() == [0, 4]
+    first = top - 19 - bs  # in the second block of its table, which is block 0; the next request's is block 1
+    assert got["slots"].tolist() == [-1] * 10 + [first, first + 1, first + 2] + [top - 3, top - 2, top - 1]
+    assert np.array_equal(got["block_table"], table)
+    # more table than positions, more owned than held: still not served
+    got = run_plan(lm, 1 << 29, 100, 16, np.array([top], np.int32), np.array([16], np.int32),
+                   np.array([60], np.int32), np.zeros((1, 100), np.int32), np.array([5], np.int32),
+                   np.array([0, 1], np.int32))
+    assert got["lens"].tolist() == [top] and got["owned"].tolist() == [60] and got["slots"].tolist() == [-1] * 16
+
+
 # ---------------------------------------------------------------------------------------------
 # writes
 # ---------------------------------------------------------------------------------------------
