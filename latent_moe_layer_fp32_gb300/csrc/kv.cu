@@ -160,7 +160,7 @@ template <int NT, int PER>
 __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
   extern __shared__ __align__(16) int s_plan[];
   const int held_n = plan_ints(a.B);  // of each array, a multiple of 4
-  int* s_tok = s_plan;                // [B + 1] first token of each request, saturated at n_slots + 1
+  int* s_tok = s_plan;                // [B + 1] first token of each request, at most n_slots
   int* s_pop = s_tok + held_n;        // [B] blocks popped by the requests before it; -1: not served
   int* s_push = s_pop + held_n;       // [B] blocks pushed by the requests before it; -1: it does not end
   int* s_len = s_push + held_n;       // [B] tokens held
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
     const unsigned long long pop = both >> 32;
     const bool served = (fit >> j & 1u) && (need[j] == 0 || pop + need[j] <= (unsigned long long)count);
     if (served && need[j] > 0) taken = (int)(pop + need[j]);
-    tok[j] = (int)min(t0, (unsigned long long)a.n_slots + 1);
+    tok[j] = (int)min(t0, (unsigned long long)a.n_slots);
     popped[j] = served ? (int)min(pop, 0x7fffffffull) : -1;
     pushed[j] = add[j] < 0 ? (int)(both & 0xffffffffu) : -1;
     if (blockIdx.x == 0 && b < a.B) a.offsets[b] = (int)min(t0, 0x7fffffffull);
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
   }
   if (taken > 0) atomicMax(&s_taken, taken);
   if (threadIdx.x == 0) {
-    s_tok[a.B] = (int)min(n_tok, (unsigned long long)a.n_slots + 1);
+    s_tok[a.B] = (int)min(n_tok, (unsigned long long)a.n_slots);
     if (blockIdx.x == 0) a.offsets[a.B] = (int)min(n_tok, 0x7fffffffull);
   }
   __syncthreads();
@@ -279,8 +279,10 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
     }
   }
   // a token's slot: from the table for a block held before the call, else straight from the ring
-  const int last = min(s_tok[a.B], a.n_slots);
-  for (int t = blockIdx.x * NT + threadIdx.x; t < a.n_slots; t += gridDim.x * NT) {
+  const int last = s_tok[a.B];
+  // (unsigned: a step past the last slot may pass 31 bits)
+  for (unsigned x = blockIdx.x * NT + threadIdx.x; x < (unsigned)a.n_slots; x += gridDim.x * NT) {
+    const int t = (int)x;
     int slot = -1;
     if (t < last) {
       int lo = 0, hi = a.B - 1;  // the last request whose first token is at or before t

@@ -190,6 +190,18 @@ def test_plan_lengths_past_31_bits(lm):
     assert got["lens"].tolist() == [top] and got["owned"].tolist() == [60] and got["slots"].tolist() == [-1] * 16
 
 
+def test_plan_as_many_slots_as_there_can_be(lm):
+    n = 2**31 - 1  # 8.6 GB
+    slots = torch.zeros(n, dtype=torch.int32, device="cuda")
+    lens, new, owned, state = (dev(np.array(x, np.int32)) for x in ([3, 0], [5, 2], [1, 0], [0, 2]))
+    table, ring = dev(np.array([[4, -9], [-9, -9]], np.int32)), dev(np.array([7, 8], np.int32))
+    o = [torch.zeros(m, dtype=torch.int32, device="cuda") for m in (2, 2, 2, 3)]
+    lm.lmoe_kv_plan(16, lens, new, owned, table, ring, state, *o, slots)
+    assert slots[:7].tolist() == [67, 68, 69, 70, 71, 112, 113]
+    assert int(slots[7:].max()) == -1 and int(slots[7:].min()) == -1
+    assert [x.tolist() for x in o] == [[8, 2], [1, 1], [1, 1], [0, 5, 7]]
+
+
 # ---------------------------------------------------------------------------------------------
 # writes
 # ---------------------------------------------------------------------------------------------
