@@ -415,7 +415,10 @@ LMOE_API int lmoe_tree_attention(const lmoe_attn_dims* dims, const lmoe_kv_cache
  *   ring_state_out  out int32 [2]
  *   token_offsets   out int32 [B + 1], sums of new_tokens
  *   slots    out int32 [n_slots]: the slot of each new token in ragged order,
- *            -1 for tokens of requests not served and past the last token
+ *            -1 for tokens of requests not served and past the last token, and
+ *            where a block number is negative or its slot passes 31 bits (no
+ *            cache has such a one; the cache's own block count is not known
+ *            here, so lmoe_kv_write checks against it)
  * Outputs other than block_table and ring must not overlap the inputs
  * (LMOE_EINVAL where two are the same pointer).  Called again on the same
  * inputs it writes the same values. */

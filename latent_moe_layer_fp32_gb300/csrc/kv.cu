@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(NT) kv_plan_kernel(const PlanArgs a) {
         const int p = s_len[lo] + t - s_tok[lo], blk = p / a.bs, owned = s_own[lo];
         const int id = blk < owned ? a.table[(size_t)lo * a.max_blocks + blk]
                                    : a.ring[ring_at(hd, (long long)s_pop[lo] + blk - owned, a.ring_size)];
-        slot = id * a.bs + p - blk * a.bs;
+        const long long at = (long long)id * a.bs + (p - blk * a.bs);
+        slot = id >= 0 && at <= 0x7fffffff ? (int)at : -1;
       }
     }
     a.slots[t] = slot;

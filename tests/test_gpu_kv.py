@@ -190,6 +190,18 @@ def test_plan_lengths_past_31_bits(lm):
     assert got["lens"].tolist() == [top] and got["owned"].tolist() == [60] and got["slots"].tolist() == [-1] * 16
 
 
+@pytest.mark.parametrize("block,bs,slot", [(2047, 1 << 20, 2047 << 20), (2048, 1 << 20, -1), (5000, 1 << 20, -1),
+                                           (1 << 28, 16, -1), (2**31 - 1, 16, -1), (-1, 16, -1), (-2**31, 16, -1)])
+def test_plan_slots_past_31_bits(lm, block, bs, slot):
+    # a block number from the ring, and one from the table, whose slot is no int32 (or that is none): -1, not another slot
+    for lens, table, ring in ((0, -9, block), (bs - 5, block, -9)):
+        got = run_plan(lm, bs, 1, 3, np.array([lens], np.int32), np.array([3], np.int32),
+                       np.array([1 if lens else 0], np.int32), np.array([[table]], np.int32),
+                       np.array([ring], np.int32), np.array([0, 1], np.int32))
+        at = lens if slot >= 0 else 0
+        assert got["slots"].tolist() == ([slot + at, slot + at + 1, slot + at + 2] if slot >= 0 else [-1] * 3)
+
+
 def test_plan_as_many_slots_as_there_can_be(lm):
     n = 2**31 - 1  # 8.6 GB
     slots = torch.zeros(n, dtype=torch.int32, device="cuda")
