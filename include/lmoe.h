@@ -437,7 +437,10 @@ LMOE_API int lmoe_kv_plan(int32_t n_requests, int32_t block_size, int32_t max_bl
  *   ws       optional, as for lmoe_tree_masks: a slot past the cache or a row
  *            outside [0, n_rows) is reported there; it is passed over in any
  *            case
- * Slots must differ from one another. */
+ * Slots must differ from one another, and so must the cache's rows: in the
+ * order of their strides, the dimensions block, head and slot (those of more
+ * than one) each step past all that the ones below span (else LMOE_EINVAL;
+ * reading, lmoe_tree_attention takes rows that overlap). */
 LMOE_API int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, int64_t k_stride, const uint16_t* v_new,
                            int64_t v_stride, int32_t n_rows, const int32_t* src, const int32_t* slots,
                            int32_t n_tokens, void* ws, size_t ws_bytes, lmoe_stream_t stream);

@@ -4,6 +4,7 @@
 //
 // All three move few bytes, so what bounds them is the launch and the chain of
 // dependent loads, except the write of a prompt, which is a copy.
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -352,6 +353,22 @@ bool al16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p
 bool al8(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool al4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether no two rows of the cache share an element: in the order of their strides, each dimension steps past
+// all that the ones below it span.
+bool rows_apart(const lmoe_kv_cache* c) {
+  struct {
+    int64_t stride, extent;
+  } dim[3] = {{c->block_stride, c->n_blocks}, {c->head_stride, c->kv_heads}, {c->slot_stride, c->block_size}};
+  std::sort(dim, dim + 3, [](const auto& x, const auto& y) { return x.stride < y.stride; });
+  int64_t span = c->head_dim;
+  for (const auto& x : dim) {
+    if (x.extent == 1) continue;  // it never steps
+    if (x.stride < span || x.stride > (INT64_MAX - span) / (x.extent - 1)) return false;
+    span += x.stride * (x.extent - 1);
+  }
+  return true;
+}
+
 int log2_of(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;
@@ -381,7 +398,7 @@ int check_cache(const lmoe_kv_cache* c, bool memory) {
   const int64_t st[3] = {c->block_stride, c->head_stride, c->slot_stride};
   for (int64_t x : st)
     if (x < 0 || x % 8) return LMOE_EINVAL;
-  // rows of one block do not overlap
+  // heads, slots and blocks next to one another do not overlap (rows_apart tells for all of them)
   if (c->slot_stride < c->head_dim || (c->kv_heads > 1 && c->head_stride < c->head_dim) ||
       (c->n_blocks > 1 && c->block_stride < c->head_dim))
     return LMOE_EINVAL;
@@ -453,6 +470,7 @@ int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, int64_t k_s
   calls_begin();
   int rc = check_cache(cache, true);
   if (rc) return rc;
+  if (!rows_apart(cache)) return LMOE_EINVAL;  // (distinct slots would be written over one another)
   const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
   if (!al16(k_new) || !al16(v_new) || k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || n_rows < 1 ||
       n_tokens < 1 || n_tokens > (1 << 20) || (!src && n_tokens > n_rows) || (src && !al4(src)) || !al4(slots))

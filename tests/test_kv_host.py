@@ -70,6 +70,25 @@ def test_cache_descriptors(lib):
         assert write(cache(), **bad) == EINVAL, bad
 
 
+def test_write_refuses_rows_that_overlap(lib):
+    """cache(): 8 blocks of 2 heads of 16 slots of 64.  A refused call returns before it looks for a device; one
+    whose layout is accepted ends at the workspace (no bytes of it), or for want of a device, and launches nothing."""
+    def write(**kw):
+        return lib.lmoe_kv_write(ctypes.byref(cache(**kw)), P, 128, P, 128, 4, P, P, 4, P, 0, None)
+
+    # (block, head, slot) strides
+    for block, head, slot in ((2048, 64, 64), (64, 1024, 64), (2048, 1024, 1024), (1024, 1024, 64), (2040, 1024, 64),
+                              (2048, 1016, 64), (2048, 64, 120), (256, 64, 256), (4096, 2048, 136), (1984, 64, 128),
+                              (2**62, 2**62, 64)):
+        assert write(block_stride=block, head_stride=head, slot_stride=slot) == EINVAL, (block, head, slot)
+    # either order, padded, one inside the other; dimensions of one do not count
+    for kw in (dict(), dict(head_stride=64, slot_stride=128), dict(head_stride=72, slot_stride=136, block_stride=2176),
+               dict(block_stride=1024, head_stride=8192), dict(block_stride=128, head_stride=64, slot_stride=1024),
+               dict(block_stride=1 << 40), dict(head_stride=1024 + 8, block_stride=2056),
+               dict(n_blocks=1, block_stride=0), dict(kv_heads=1, head_stride=0, block_stride=1024)):
+        assert write(**kw) != EINVAL, kw
+
+
 def test_copy_descriptors_refuse(lib):
     m = lm.LmoeKvMaps()
     assert lib.lmoe_kv_maps_init(ctypes.byref(cache(k=0)), ctypes.byref(m)) == EINVAL
