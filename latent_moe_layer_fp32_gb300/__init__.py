@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import weakref
 
 import torch
 
@@ -63,9 +64,21 @@ class LmoeKvCache(ctypes.Structure):
                 ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
                 ("maps", ctypes.c_void_p)]
 
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name == "maps":  # whoever takes the address over shares the descriptors behind it
+            super().__setattr__("_maps", _live_maps.get(value))
+
 
 class LmoeKvMaps(ctypes.Structure):
     _fields_ = [("made_for", ctypes.c_uint64 * 8), ("map", ctypes.c_uint64 * 64)]
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        _live_maps[ctypes.addressof(self)] = self
+
+
+_live_maps = weakref.WeakValueDictionary()  # address -> LmoeKvMaps
 
 
 class LmoeAttnDims(ctypes.Structure):
@@ -405,8 +418,7 @@ def kv_cache_of(k, v) -> LmoeKvCache:
     cache = LmoeKvCache(k.data_ptr(), v.data_ptr(), n, b, h, d, k.stride(0), k.stride(1), k.stride(2), None)
     maps = LmoeKvMaps()
     _check(load().lmoe_kv_maps_init(ctypes.byref(cache), ctypes.byref(maps)), "lmoe_kv_maps_init")
-    cache.maps = ctypes.addressof(maps)
-    cache._maps = maps  # lives as long as the descriptor
+    cache.maps = ctypes.addressof(maps)  # they live as long as a descriptor that has their address
     return cache
 
 

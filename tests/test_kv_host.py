@@ -97,6 +97,30 @@ def test_copy_descriptors_refuse(lib):
     assert lib.lmoe_kv_maps_init(None, ctypes.byref(m)) == EINVAL
 
 
+def test_copy_descriptors_live_as_long_as_a_cache_descriptor_uses_them(lib):
+    import copy
+    import gc
+    import weakref
+
+    def fields(c):
+        return [getattr(c, n) for n, _ in lm.LmoeKvCache._fields_]
+
+    for take in (lambda c: lm.LmoeKvCache(*fields(c)), lambda c: lm.LmoeKvCache(**dict(zip("k v maps".split(),
+                 (c.k, c.v, c.maps)))), lambda c: setattr(new := cache(), "maps", c.maps) or new):
+        first, maps = cache(), lm.LmoeKvMaps()
+        first.maps = ctypes.addressof(maps)
+        alive = weakref.ref(maps)
+        second = take(first)
+        del first, maps
+        gc.collect()
+        assert alive() is not None and second.maps == ctypes.addressof(alive())
+        second.maps = None
+        gc.collect()
+        assert alive() is None and second.maps is None
+    with pytest.raises(ValueError):  # ctypes itself refuses to copy what holds addresses
+        copy.copy(cache())
+
+
 def test_workspace_bytes(lib):
     assert lm.lmoe_tree_attention_workspace_bytes(dims(), cache()) >= 8
     # only the heads and the width of the cache count
