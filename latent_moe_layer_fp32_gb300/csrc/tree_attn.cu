@@ -173,7 +173,7 @@ __device__ __forceinline__ Load load_req(const AttnArgs& a, int b, Req* r) {
   r->np = (held >> 7) + ((held & 127) != 0);
   r->full = held >> 7;
   // the last row's window starts at len + n - window at most
-  r->cut = a.window > 0 ? (max(0, min(len, len + r->n - a.window) - r->base0) + 127) >> 7 : 0;
+  r->cut = a.window > 0 ? (max(0, len - r->base0 + min(0, r->n - a.window)) + 127) >> 7 : 0;
   const int tail = ((held & 127) + 7) & ~7;
   r->c0 = (held & 127) != 0 && tail + r->n <= kTile ? tail : 0;
   r->nt = r->np + (r->c0 ? 0 : (r->n + kTile - 1) >> 7);
@@ -260,9 +260,10 @@ struct Walk {
   }
 };
 
-// A draft's position: between the prefix's end and the deepest place that n drafts can reach.
-__device__ __forceinline__ int draft_pos(const AttnArgs& a, int t0, int n, int len, int j) {
-  return a.pos ? min(max(__ldg(a.pos + t0 + j), len), len + n - 1) : len + j;
+// A draft's position past the prefix's end (the position itself may pass 31 bits): at most the deepest place
+// that n drafts can reach.
+__device__ __forceinline__ int draft_depth(const AttnArgs& a, int t0, int n, int len, int j) {
+  return a.pos ? min(max(__ldg(a.pos + t0 + j), len) - len, n - 1) : j;
 }
 
 __device__ __forceinline__ uint64_t range_bits(int lo, int hi) {  // bits [lo, hi) of a 64-bit word
@@ -271,10 +272,10 @@ __device__ __forceinline__ uint64_t range_bits(int lo, int hi) {  // bits [lo, h
   return below_b & ~below_a;
 }
 
-// What draft vi (at position vp) of a segment's request sees of the 128 columns of tile i.
-__device__ __forceinline__ ulonglong2 edge_bits(const AttnArgs& a, const Seg* s, int i, int vi, int vp) {
+// What draft vi (vd positions past the prefix) of a segment's request sees of the 128 columns of tile i.
+__device__ __forceinline__ ulonglong2 edge_bits(const AttnArgs& a, const Seg* s, int i, int vi, int vd) {
   uint64_t bits[2];
-  const int cached = s->r.cached(i), first = a.window > 0 ? vp - a.window + 1 - s->r.base(i) : 0;
+  const int cached = s->r.cached(i), first = a.window > 0 ? vd - a.window + 1 + (s->r.len - s->r.base(i)) : 0;
   bits[0] = range_bits(first, cached);
   bits[1] = range_bits(first - 64, cached - 64);
   const int nd = s->r.drafts(i);
@@ -296,9 +297,9 @@ __device__ __forceinline__ ulonglong2 edge_bits(const AttnArgs& a, const Seg* s,
   const int n = s->r.n, len = s->r.len;
   if (a.window > 0 && n > a.window) {  // some pair of drafts may be a window apart
     for (uint64_t z = m0; z; z &= z - 1)
-      if (vp - draft_pos(a, t0, n, len, d0 + __ffsll(z) - 1) >= a.window) m0 &= ~(z & -z);
+      if (vd - draft_depth(a, t0, n, len, d0 + __ffsll(z) - 1) >= a.window) m0 &= ~(z & -z);
     for (uint64_t z = m1; z; z &= z - 1)
-      if (vp - draft_pos(a, t0, n, len, d0 + 63 + __ffsll(z)) >= a.window) m1 &= ~(z & -z);
+      if (vd - draft_depth(a, t0, n, len, d0 + 63 + __ffsll(z)) >= a.window) m1 &= ~(z & -z);
   }
   if (c >= 64) {
     bits[1] |= m0 << (c - 64);
@@ -402,7 +403,7 @@ __device__ __forceinline__ void store_rows(uint32_t (&w)[U][4], void* row) {
 // warp took them out.  Runs only where there was one.
 template <int D, int CW>
 __device__ __forceinline__ void add_not_finite(const AttnArgs& a, const Seg* s, uint32_t o_addr, int part, bool valid,
-                                            int vi, int vp, int i0, int n) {
+                                            int vi, int vd, int i0, int n) {
 #pragma unroll 1
   for (int col = 0; col < D; col += 16) {
     uint32_t o[16];
@@ -410,7 +411,7 @@ __device__ __forceinline__ void add_not_finite(const AttnArgs& a, const Seg* s, 
     tmem_ld_wait();
     for (int i = i0; valid && i < i0 + n; ++i) {
       if (!s->r.edge(i)) continue;
-      const ulonglong2 bits = edge_bits(a, s, i, vi, vp);
+      const ulonglong2 bits = edge_bits(a, s, i, vi, vd);
 #pragma unroll 1
       for (int j = part * CW; j < part * CW + CW; ++j) {
         if (!((j >= 64 ? bits.y : bits.x) >> (j & 63) & 1ull)) continue;
@@ -951,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       }
       early = false;
       const int vi = valid ? (s->m * C::kRows + local) / a.G : 0;  // the row's draft
-      auto at_pos = [&] { return a.window > 0 ? draft_pos(a, s->r.t0, s->r.n, s->r.len, vi) : 0; };
+      auto depth = [&] { return a.window > 0 ? draft_depth(a, s->r.t0, s->r.n, s->r.len, vi) : 0; };
       // m_ref: the maximum that P refers to; l: the row's sum.  A tile whose maximum stays below
       // `limit` takes the plain path: no rescaling of O, one part of P.
       float m_ref = -INFINITY, l = 0.f, limit = valid ? -INFINITY : INFINITY;
@@ -962,7 +963,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         const uint32_t buf = NT == 1 ? gt & 1 : grp;
         const bool edge = (i < cut || i >= full_from) && warp_live;
         ulonglong2 bits = make_ulonglong2(0, 0);
-        if (edge) bits = edge_bits(a, s, i, vi, at_pos());  // (before the wait, which hides its loads)
+        if (edge) bits = edge_bits(a, s, i, vi, depth());  // (before the wait, which hides its loads)
         if (NT == 1 && k == 0)
           wait(&s_first[grp], (seg >> 1) & 1, 240);  // s_full may be phases behind until then
         else
@@ -1139,7 +1140,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
       const int qh = s->h * a.G + (valid ? s->m * C::kRows + local - vi * a.G : 0), tok = s->r.t0 + vi;
       const bool dirty = s_dirty[seg & 3] == seg + 1;
       const int slot = 2 * blockIdx.x + (i0 == 0);
-      if (dirty && warp_live) add_not_finite<D, CW>(a, s, o_addr, part, valid, vi, at_pos(), i0, n);
+      if (dirty && warp_live) add_not_finite<D, CW>(a, s, o_addr, part, valid, vi, depth(), i0, n);
       // N columns of this thread's row of O
       auto sums = [&](int col, auto& y) {
         constexpr int N = sizeof(y) / 4;
@@ -1277,8 +1278,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, KS>::kThreads, 1)
         uint8_t* const vt = s_ring + (at % ST) * C::kStageBytes + (lane & 7) * 16;
         const int base = s.r.base(i), hi = s.r.cached(i), nd = s.r.drafts(i), c0 = nd ? s.r.col(i) : hi, c1 = c0 + nd;
         // cached positions: seen by some row from `first` on, by every row from `all` on
-        const int first = a.window > 0 ? min(max(s.r.len - a.window + 1 - base, 0), hi) : 0;
-        const int all = a.window > 0 ? min(max(s.r.len + s.r.n - a.window - base, 0), hi) : 0;
+        const int first = a.window > 0 ? min(max(s.r.len - base - a.window + 1, 0), hi) : 0;
+        const int all = a.window > 0 ? min(max(s.r.len - base + (s.r.n - a.window), 0), hi) : 0;
         bool found = false;
         auto zero = [&](int from, int to) {
           for (int key = from + (lane >> 3); key < to; key += 4)

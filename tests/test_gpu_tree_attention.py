@@ -189,6 +189,11 @@ def test_positions_past_any_tree_count_as_its_deepest_place(lm, far):
     c.check(lm)
 
 
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 200])
+def test_windows_as_wide_as_there_can_be(lm, window):
+    Case([300, 0, 128], [5, 3, 70], window=window, seed=61).check(lm)
+
+
 @pytest.mark.parametrize("mask", ["any", "none"])
 def test_masks_that_leave_rows_empty(lm, mask):
     # no prefix and no visible draft: zeros and an lse of -infinity, next to rows that do see something
@@ -327,6 +332,30 @@ def test_offsets_past_32_bits(lm):
             x[int(n)] = y[int(o)]
     ref = c.check(lm)
     c.k, c.v, c.table = big[0], big[1], new
+    out, _ = c.run(lm)
+    assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("flat", [False, True])
+@pytest.mark.parametrize("n,window,below", [(9, 40, 3), (60, 40, 3), (200, 150, 20), (60, 40, 61), (200, 300, 100),
+                                            (3, 1, 1)])
+def test_positions_past_31_bits(lm, n, window, below, flat):
+    """The drafts of a request whose cached positions end just below 2^31: where they stand in a chain passes 31
+    bits, what they see does not (flat: alternatives for one place, so no position does).  The same bits as for a
+    short request with the same last pages."""
+    c = Case([512 - below], [n], bs=256, window=window, mask=None, pos=False, seed=59, hk=1, hq=2, spare=1)
+    if flat:
+        c.mask = np.zeros((n, c.words), np.uint64)
+        for i in range(n):
+            c.mask[i, i // 64] = np.uint64(1 << i % 64)
+        c.pos = np.full(n, 512 - below, np.int32)
+    ref = c.check(lm)
+    last = c.table[0, :2].copy()
+    c.table = np.full((1, 1 << 23), c.blocks - 1, np.int32)
+    c.table[0, -2:] = last
+    c.lens = np.array([2**31 - below], np.int32)
+    if flat:
+        c.pos = np.full(n, 2**31 - below, np.int32)
     out, _ = c.run(lm)
     assert torch.equal(out, ref)
 
