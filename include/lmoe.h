@@ -332,7 +332,7 @@ typedef struct {
   int32_t max_blocks;         /* row length of block_table */
   int32_t mask_words;         /* 64-bit words per row of the mask, 1 .. 4 */
   int32_t window;             /* tokens in sight, the row's own included; 0 = all */
-  float scale;                /* of the scores, > 0, e.g. 1/sqrt(head_dim) */
+  float scale;                /* of the scores, > 0 and at most 2.35e38, e.g. 1/sqrt(head_dim) */
 } lmoe_attn_dims;
 
 /* Tree masks: for row i of a request, mask bit j (word j / 64, bit j % 64) is

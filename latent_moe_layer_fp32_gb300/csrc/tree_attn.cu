@@ -61,6 +61,7 @@ namespace lmoe {
 namespace {
 
 constexpr int kTile = 128;  // keys per tile, rows per row tile
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
   const uint16_t* q;
@@ -1448,7 +1449,8 @@ int check_attn(const lmoe_attn_dims* d, const lmoe_kv_cache* c, bool memory) {
   if (d->n_requests < 1 || d->n_requests > 8192 || d->n_tokens < 1 || d->n_tokens > (1 << 20) ||
       d->max_request_tokens < 1 || d->max_request_tokens > 256 || d->q_heads < 1 || d->q_heads % c->kv_heads ||
       d->q_heads / c->kv_heads > 128 || d->max_blocks < 1 || d->max_blocks > (1 << 24) || d->mask_words < 1 ||
-      d->mask_words > 4 || d->window < 0 || !(d->scale > 0.f) || !(d->scale < INFINITY))
+      d->mask_words > 4 || d->window < 0 || !(d->scale > 0.f) ||
+      !(d->scale * kLog2e < INFINITY))
     return LMOE_EINVAL;
   return LMOE_OK;
 }
@@ -1615,7 +1617,7 @@ int lmoe_tree_attention(const lmoe_attn_dims* d, const lmoe_kv_cache* c, const u
   a.window = d->window;
   a.ctas = di.sms;
   a.wait_limit = wait_limit(d, c);
-  a.scale_log2 = d->scale * 1.4426950408889634f;
+  a.scale_log2 = d->scale * kLog2e;
   const int max_rows = a.max_n * a.G;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rows = group_rows(d, c);

@@ -51,6 +51,14 @@ def test_tree_attention_refuses(lib):
     assert lib.lmoe_tree_attention(None, ctypes.byref(cache()), *[P] * 2, *[P] * 14, None) == EINVAL
 
 
+def test_tree_attention_refuses_a_scale_that_has_no_base_2_form(lib):
+    # scores are taken to base 2: scale * log2(e) has to be finite
+    for scale in (2.36e38, 3e38, 3.4e38):
+        assert attend(lib, d=dims(scale=scale), ws_bytes=0) == EINVAL
+    for scale in (1e-45, 1e-30, 1.0, 2.35e38):  # (goes on to the workspace, of which there is nothing)
+        assert attend(lib, d=dims(scale=scale), ws_bytes=0) != EINVAL
+
+
 def test_cache_descriptors(lib):
     def write(c, **kw):
         a = dict(k=P, ks=128, v=P, vs=128, rows=4, src=P, slots=P, n=4, ws=None, ws_bytes=0)
