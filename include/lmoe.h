@@ -381,7 +381,11 @@ LMOE_API size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* dims, 
  *   lse      out fp32 [T][q_heads], or NULL
  * Scores, the running maximum and sum, and the accumulators are fp32.  For
  * the product with the values a probability is rounded to bf16, or to two
- * bf16 parts where a key may hold over 1/8 of its row's sum so far.
+ * bf16 parts where a key may hold over 1/8 of its row's sum so far; the sums
+ * keep it unrounded.  So out is off by up to 2^-8 of sum_j p_j |v_j| (by
+ * 0.002 of its norm on random rows), and by its own rounding to bf16.  The
+ * tensor cores' accumulators round towards zero: 0.4% are lost where one SM
+ * adds up a million positions of a key head, 1.2% at eight million.
  * The device-side waits are bounded by 2 to 4 seconds, plus 8192 clocks for
  * every 128 positions that a row of the block table has room for
  * (LMOE_ETIMEOUT through lmoe_status_check).

@@ -212,6 +212,90 @@ def test_score_ranges(lm, qscale):
     Case([900, 130], [5, 2], qscale=qscale, d=128, seed=7).check(lm)
 
 
+def one_hot_case(power, order, ties, d, n=3, length=700, heads=4, seed=67):
+    """Scores that are whole numbers up to 255 times 2^power, exact in fp32 (one product of two powers of two and a
+    small integer each, the rest zero), so that a row's softmax is the mean of the keys that tie for the largest
+    (or, for queries of the other sign, the smallest) number.  `order`: where the numbers rise, along the keys of the
+    prefix and then of the drafts; `ties`: how many keys share the first place."""
+    c = Case([length], [n], hq=heads, hk=1, d=d, seed=seed, mask="none", scale=2.0**-4)
+    c.mask |= np.uint64(1)  # every row sees the prefix and draft 0
+    rng = np.random.default_rng(seed)
+    total = length + 1
+    num = np.sort(rng.integers(20, 230, total))
+    num = {"rising": num, "falling": num[::-1], "mixed": rng.permutation(num)}[order].copy()
+    first, last = rng.permutation(total)[:ties], rng.permutation(total)[:ties]
+    num[first] = 255
+    num[np.setdiff1d(last, first)[:ties]] = 1
+    last = np.flatnonzero(num == 1)
+    v = rng.integers(1, 100, (total, d)) * rng.choice([-1, 1], (total, d))
+    # |score| = num * 2^power, split over q, k and the scale of 2^-4
+    hi = power // 2 + 4
+    q = torch.zeros(n, heads, d)
+    q[:, :, 5] = 2.0**hi
+    q[:, 1::2, 5] = -2.0**hi
+    k = torch.zeros(total, d)
+    k[:, 5] = torch.from_numpy(num.astype(np.float32)) * 2.0**(power - hi + 4)
+    c.q.copy_(q)
+    c.kn.zero_()
+    c.vn.zero_()
+    at = torch.arange(length, device="cuda")
+    blk = dev(c.table[0]).long()[at // c.bs]
+    c.k[blk, 0, at % c.bs] = k[:length].bfloat16().cuda()
+    c.v[blk, 0, at % c.bs] = torch.from_numpy(v[:length].astype(np.float32)).bfloat16().cuda()
+    c.kn[0, 0] = k[length].bfloat16().cuda()
+    c.vn[0, 0] = torch.from_numpy(v[length].astype(np.float32)).bfloat16().cuda()
+    out, lse = np.zeros((n, heads, d)), np.zeros((n, heads))
+    for h in range(heads):
+        win = last if h % 2 else first
+        out[:, h] = v[win].mean(axis=0)
+        lse[:, h] = (-1 if h % 2 else 255) * 2.0**power + np.log(len(win))
+    return c, out, lse
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("power,ties,d", [(8, 1, 64), (14, 2, 128), (15, 1, 64), (16, 4, 64), (17, 1, 128), (20, 3, 64),
+                                          (40, 2, 128), (80, 1, 64), (110, 4, 64)])
+def test_the_largest_score_takes_all(lm, power, ties, d, order):
+    """Scores of 2^8 to 2^118 whose largest stand at least 2^power above the rest (a factor of 1.1: far more than
+    fp32's rounding of them).  The weights are exact, so out is the mean of the winners' values with the roundings of
+    1 / ties (2 units of 2^-23), the product with it (2^-24) and bf16 (2^-8 with its neighbourhood); lse has the
+    roundings of scale * log2(e), the product with it, ln(2), the product with that, and a sum: 2^-21 |lse| + 2^-19."""
+    c, out, lse = one_hot_case(power, order, ties, d)
+    got, ls = c.run(lm)
+    got, ls = got.float().cpu().numpy().astype(np.float64), ls.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - out) <= (2.0**-8 + 2.0**-20) * np.abs(out) + 2.0**-20).all(), np.abs(got - out).max()
+    assert (np.abs(ls - lse) <= 2.0**-21 * np.abs(lse) + 2.0**-19).all()
+
+
+@pytest.mark.parametrize("d,group,n", [(64, 1, 1), (128, 1, 2), (128, 16, 3), (64, 40, 2), (128, 16, 10)])
+def test_probabilities_that_round_badly(lm, d, group, n):
+    """Keys of one weight that lies just above halfway between two bf16 numbers and is rounded down, all with the same
+    value, behind a first tile of heavier keys: every probability's rounding (2^-8 of it at most) goes the same way.
+    With the result's own rounding (2^-8) the bound is (2^-7 + 2^-12 + 4 e) A, where A is what they weigh.  Enough
+    requests that a CTA works through whole ones (a cut starts anew, with a second bf16 part of its probabilities)."""
+    B, hk, bs = 40, 8, 64
+    c = Case([640] * B, [n] * B, hq=hk * group, hk=hk, d=d, bs=bs, mask="none", seed=71, scale=1.0, spare=0)
+    parts, rest = [], np.log(0.5 + 2.0**-9) - 1e-5
+    for _ in range(3):
+        parts.append(float(torch.tensor(rest).bfloat16()))
+        rest -= parts[-1]
+    c.q.zero_()
+    c.q[:, :, :3] = 1.0
+    c.k.zero_()
+    c.v.zero_()
+    late = dev(c.table)[:, 128 // bs:].long().flatten()
+    c.k[late, :, :, :3] = torch.tensor(parts).bfloat16().cuda()
+    c.v[late] = (1 + torch.arange(d) / 128.0).bfloat16().cuda()
+    out, _ = c.run(lm)
+    got = out.float().cpu().numpy().astype(np.float64)
+    w = np.exp(sum(parts))
+    share = 512 * w / (128 + 512 * w)
+    ref = share * (1 + np.arange(d) / 128.0)  # = A: the values are positive
+    e = (d + 16) * 2.0**-23 * 1.0 + 2.0**-20  # (products of 1 and the parts: below 1 in all)
+    off = np.abs(got - ref) / ref
+    assert (off <= 2.0**-7 + 2.0**-12 + 4 * e).all(), off.max()
+
+
 def test_rising_and_falling_maxima(lm):
     # the running maximum moves in every tile (rising), or only in the first (falling)
     for sign in (1.0, -1.0):
