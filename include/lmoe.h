@@ -337,7 +337,8 @@ typedef struct {
 
 /* Tree masks: for row i of a request, mask bit j (word j / 64, bit j % 64) is
  * set iff row j of the same request is i itself or an ancestor of i, and
- * pos[i] = lens[b] + the number of i's ancestors among the drafts.
+ * pos[i] = lens[b] + the number of i's ancestors among the drafts (which has
+ * to stay below 2^31).
  *   parents  int32 [T], the parent's row inside the request, below the row's
  *            own, or -1 for a child of the cached prefix
  *   lens     int32 [B], cached tokens, or NULL for none
@@ -384,8 +385,8 @@ LMOE_API size_t lmoe_tree_attention_workspace_bytes(const lmoe_attn_dims* dims, 
  * bf16 parts where a key may hold over 1/8 of its row's sum so far; the sums
  * keep it unrounded.  So out is off by up to 2^-8 of sum_j p_j |v_j| (by
  * 0.002 of its norm on random rows), and by its own rounding to bf16.  The
- * tensor cores' accumulators round towards zero: 0.4% are lost where one SM
- * adds up a million positions of a key head, 1.2% at eight million.
+ * tensor cores' accumulators round towards zero: up to 0.4% are lost where
+ * one SM adds up a million positions of a key head, in proportion beyond.
  * The device-side waits are bounded by 2 to 4 seconds, plus 8192 clocks for
  * every 128 positions that a row of the block table has room for
  * (LMOE_ETIMEOUT through lmoe_status_check).

@@ -22,8 +22,10 @@ namespace {
 // and up points past them, so ceil(log2 n) rounds close any tree and the loop
 // ends as soon as every pointer has left the tree.  A chain of dependent loads
 // and rounds bounds it: 8 drafts take 1.8 us, 1024 trees of up to 200 drafts
-// (4.1 MB) 5.5 us, two waves of CTAs.  Masks are stored 16 bytes at a time where
-// they are aligned (5.5 instead of 6.1 us).
+// (4.1 MB) 5.5 us.  Those are one wave (eight CTAs fit an SM); their warps wait at
+// the rounds' barriers first, next for the parents' loads, and shared memory is
+// busy for half of the time that an SM works.  Masks are stored 16 bytes at a time
+// where they are aligned (5.5 instead of 6.1 us).
 template <int W>
 __global__ void __launch_bounds__(64 * W)
     tree_masks_kernel(int n_tokens, const int32_t* __restrict__ offsets, const int32_t* __restrict__ parents,

@@ -32,18 +32,21 @@
 // columns; 6784 GB/s and 1940 TFLOP/s are the measured rates of a copy and of a
 // bf16 GEMM).  Up to 128 rows, HBM: 16 requests of 12000 positions take 127 us
 // with 8 drafts each (6240 GB/s, 92%) and 133 us with 16; 64 of one token and
-// 512 to 8191 positions 111 us (6260 GB/s).  Past that the tensor cores: 64
-// drafts each take 292 to 305 us by the box (1320 to 1380 TFLOP/s).  A tile of
+// 512 to 8191 positions 110 us (6320 GB/s).  Past that the tensor cores: 64
+// drafts each take 291 to 305 us by the box (1320 to 1380 TFLOP/s).  A tile of
 // two row tiles then takes about 3050 clocks: its four products need 2048, and
 // their operands and the copies of K and V alone keep shared memory busy for as
 // many (128 bytes a clock); each group's softmax (1900) and its own two products
 // follow one another, since 512 columns of tensor memory hold no second S.  A
 // segment's end costs four such tiles or so, which is what ragged trees pay: 32
-// requests with 33 to 64 drafts over 1024 to 8192 positions take 199 us (889
-// TFLOP/s; rows that fill no row tile are 15% of that).  Small calls are a chain
-// of latencies: 8 drafts of one request over 1021 positions take 13.2 us (launch
-// and lengths 2, cut and first pages 2, copies 2, scores, softmax and product 2,
-// sums stored 1, merge kernel 3 to 4).
+// requests with 33 to 64 drafts over 1024 to 8192 positions take 198 us (889
+// TFLOP/s; rows that fill no row tile are 15% of that; 205 called from Python).
+// Small calls are a chain of latencies: 8 drafts of one request over 1021
+// positions take 13.1 us in a graph.  By the slowest CTA, from the end of the
+// launch before: lengths summed at 1.2 us, ranges known at 2.1, first page numbers
+// at 3.3, first scores at 5.3, softmax done at 6.8, product at 7.1, sums stored at
+// 7.8, all CTAs over at 8.2; the merge kernel starts at 9.1, has read the pieces
+// at 11.2, joined them at 12.3 and stored at 12.5.
 // The warps' loops together are longer than the instruction cache, so code that
 // is off the hot path costs time on it: several of the forms here were chosen
 // for being short.
@@ -114,8 +117,8 @@ __device__ __forceinline__ unsigned long long quot(unsigned long long x, unsigne
 // what ran out is noted in `failed` and reported once, at the kernel's end.  Each lane answers for itself, and
 // at the limit two lanes' answers may differ.  So a warp leaves a loop only by a vote; half a warp that had
 // left would have the other half wait for it at the next warp-wide step.  With votes at every wait of the
-// issuing warp wide trees took 204 us instead of 199, so that one votes once a tile (a window layer: 41.1 us,
-// 39.4 without any vote; the other cases the same).
+// issuing warp wide trees took 204 us instead of 199, so that one votes once a tile (a window layer: 40.5 us,
+// 39.2 without any vote; the other cases the same).
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int where, int& failed, uint32_t limit) {
   if (mbar_try_wait(bar, parity)) return true;
   uint32_t t0, t1;
