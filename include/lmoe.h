@@ -450,6 +450,148 @@ LMOE_API int lmoe_kv_write(const lmoe_kv_cache* cache, const uint16_t* k_new, in
                            int64_t v_stride, int32_t n_rows, const int32_t* src, const int32_t* slots,
                            int32_t n_tokens, void* ws, size_t ws_bytes, lmoe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A decode step over an 8-bit paged cache.  Between a layer's projection and
+ * its output, for one new token a request:
+ *
+ *   lmoe_qk_norm_rope          the projection's query and key heads, normed and
+ *                              turned by the token's position
+ *   lmoe_kv_write_fp8          the token's key and value rows into the cache
+ *   lmoe_decode_attention_fp8  the query over all that its request holds
+ *   lmoe_kv_read_fp8           rows out of the cache, for calls that take bf16
+ *
+ * Decoding is bound by the bytes of the cache, so 8 bits an element instead
+ * of 16 halve its time and double the tokens that a cache holds.  Block tables
+ * and slots are those of lmoe_kv_plan.
+ * ------------------------------------------------------------------------- */
+
+/* Norm and rotation of heads: rows x of head_dim elements become
+ *   y = x * rsqrt(mean(x^2) + eps) * gain        (norm = 1; else y = x)
+ * and, for i < rot_dim / 2, with the pair (a, b) = (y[i], y[i + rot_dim / 2])
+ * or, interleaved, (y[2 i], y[2 i + 1]),
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),
+ *   t = pos[axis[i]][token] * inv_freq[i];
+ * elements from rot_dim on are not turned. */
+typedef struct {
+  int32_t n_tokens;    /* 1 .. 1048576 */
+  int32_t q_heads;     /* 0 .. 1024 */
+  int32_t k_heads;     /* 0 .. 1024; one of the two at least 1 */
+  int32_t head_dim;    /* a multiple of 8, 8 .. 256 */
+  int32_t rot_dim;     /* a multiple of 8, 0 .. head_dim */
+  int32_t n_axes;      /* axes of a position, 1 .. 4 */
+  int32_t interleaved; /* 0 or 1 */
+  int32_t norm;        /* 0 or 1 */
+  float eps;           /* >= 0 */
+} lmoe_rope_dims;
+
+/*   q, k     bf16 [T][heads][head_dim], q_stride and k_stride elements from
+ *            token to token (multiples of 8: slices of a fused projection
+ *            fit), 16-byte aligned; not read, and may be NULL, with no heads
+ *   q_gain, k_gain  bf16 [head_dim], 8-byte aligned, or NULL for ones; only
+ *            a norm reads them
+ *   pos      int32 [n_axes][T]; any value, also below 0
+ *   inv_freq fp32 [rot_dim / 2], of magnitude below 1024 (a larger or
+ *            non-finite one gives angles without meaning)
+ *   axis     int32 [rot_dim / 2], the axis of each frequency, or NULL for axis
+ *            0; a pair whose axis is outside [0, n_axes) is not turned
+ *   q_out, k_out  out bf16, shaped and strided as the inputs are, with
+ *            strides of their own; may be q and k themselves (with their
+ *            strides), else they overlap no input
+ * pos and inv_freq may be NULL with rot_dim 0.  The angle is the exact product
+ * of position and frequency, taken modulo a turn in 64-bit fixed point, so far
+ * positions lose nothing; sums and products are fp32 (squares of magnitudes
+ * above 1e18 overflow there), and y is rounded to bf16 once. */
+LMOE_API int lmoe_qk_norm_rope(const lmoe_rope_dims* dims, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                               int64_t k_stride, const uint16_t* q_gain, const uint16_t* k_gain, const int32_t* pos,
+                               const float* inv_freq, const int32_t* axis, uint16_t* q_out, int64_t q_out_stride,
+                               uint16_t* k_out, int64_t k_out_stride, lmoe_stream_t stream);
+
+/* The 8-bit cache of one layer: E4M3 codes (OCP FP8), the element (block, head,
+ * slot, d) at block * block_stride + head * head_stride + slot * slot_stride + d
+ * bytes, and one E8M0 scale byte for every (block, head, slot), contiguous in
+ * this order: element = code * 2^(scale - 127); a scale of 255 makes its whole
+ * row NaN.  Strides are multiples of 16; k, v, k_scale and v_scale are 16-byte
+ * aligned.  block_size, head_dim and kv_heads as for lmoe_kv_cache. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int32_t n_blocks;
+  int32_t block_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int64_t block_stride;
+  int64_t head_stride;
+  int64_t slot_stride;
+} lmoe_kv_cache_fp8;
+
+/* lmoe_kv_write into an 8-bit cache (arguments as there).  The row of a token
+ * and head gets the scale 2^e with the smallest e >= -127 for which its largest
+ * magnitude is at most 448 * 2^e, and each element the code nearest to
+ * x / 2^e (ties to even): off by at most 2^-4 of itself, or by 2^(e - 10) where
+ * |x| < 2^(e - 6).  A row with an infinity or a NaN gets the scale 255 and codes
+ * 0x7F: it reads back as NaN. */
+LMOE_API int lmoe_kv_write_fp8(const lmoe_kv_cache_fp8* cache, const uint16_t* k_new, int64_t k_stride,
+                               const uint16_t* v_new, int64_t v_stride, int32_t n_rows, const int32_t* src,
+                               const int32_t* slots, int32_t n_tokens, void* ws, size_t ws_bytes,
+                               lmoe_stream_t stream);
+
+/* Rows of requests out of the cache: row token_offsets[b] + i of k_out and
+ * v_out gets position first[b] + i of request b, for every row up to
+ * token_offsets[b + 1] - 1; rows outside all requests are left as they were.
+ *   token_offsets  int32 [B + 1], ascending
+ *   first    int32 [B], or NULL for 0: positions before it are skipped
+ *   block_table    int32 [B][max_blocks]
+ *   k_out, v_out   out bf16 [n_tokens][kv_heads][head_dim], strides k_stride
+ *            and v_stride (multiples of 8)
+ *   ws       optional, as for lmoe_tree_masks: rows whose request's offsets
+ *            descend or pass n_tokens, whose position is below 0 or past the
+ *            table, or whose block is outside the cache are reported there
+ *            and left as they were in any case
+ * Values are exact (an E4M3 code times a power of two is a bf16 value), but for
+ * those outside bf16's range, which round as any fp32 value does. */
+LMOE_API int lmoe_kv_read_fp8(const lmoe_kv_cache_fp8* cache, int32_t n_requests, int32_t n_tokens,
+                              int32_t max_blocks, const int32_t* token_offsets, const int32_t* first,
+                              const int32_t* block_table, uint16_t* k_out, int64_t k_stride, uint16_t* v_out,
+                              int64_t v_stride, void* ws, size_t ws_bytes, lmoe_stream_t stream);
+
+typedef struct {
+  int32_t n_requests; /* B, 1 .. 8192 */
+  int32_t q_heads;    /* a multiple of the cache's kv_heads, at most 128 per kv head */
+  int32_t max_blocks; /* row length of block_table, 1 .. 2^24 */
+  int32_t window;     /* positions in sight, the token's own included; 0 = all */
+  float scale;        /* of the scores, > 0 and at most 2.35e38, e.g. 1/sqrt(head_dim) */
+} lmoe_decode_dims;
+
+/* Workspace size of lmoe_decode_attention_fp8 (0 if dims or cache are invalid;
+ * of the cache only kv_heads and head_dim count).  256-byte aligned device
+ * memory, no initialisation needed. */
+LMOE_API size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims* dims,
+                                                          const lmoe_kv_cache_fp8* cache);
+
+/* Attention of each request's newest token, whose own row is in the cache
+ * already, over the lens[b] positions that the request holds, or the last
+ * `window` of them.  Query head h reads kv head h / (q_heads / kv_heads):
+ *   out[b][h] = sum_j p_j v_j,  p = softmax of scale * (q . k_j);
+ *   lse[b][h] = ln sum_j exp(scale * (q . k_j)).
+ * A request with no positions gets out = 0 and lse = -infinity.  Slots that
+ * are not in sight have no effect, whatever they hold.
+ *   q        bf16 [B][q_heads][head_dim], q_stride elements from token to token
+ *   lens     int32 [B], at most max_blocks * block_size
+ *   block_table  int32 [B][max_blocks]
+ *   out      out bf16 [B][q_heads][head_dim], contiguous
+ *   lse      out fp32 [B][q_heads], or NULL
+ * Pointers are 16-byte aligned, lens, block_table and lse 4-byte.
+ * Reported on the device (LMOE_EDEVICE_CHECK through lmoe_status_check): a
+ * length below 0 or past its table (the request's rows are not written), a
+ * block number outside the cache (they hold no meaning).  Nothing is read out
+ * of bounds. */
+LMOE_API int lmoe_decode_attention_fp8(const lmoe_decode_dims* dims, const lmoe_kv_cache_fp8* cache,
+                                       const uint16_t* q, int64_t q_stride, const int32_t* lens,
+                                       const int32_t* block_table, uint16_t* out, float* lse, void* ws,
+                                       size_t ws_bytes, lmoe_stream_t stream);
+
 /* Synchronises `stream`, reads the device status word of `ws` and returns it
  * (LMOE_OK, LMOE_ETIMEOUT or LMOE_EDEVICE_CHECK), or LMOE_ECUDA if the
  * stream itself reports an error.  `ws` is a device pointer. */

@@ -27,6 +27,9 @@ __all__ = [
     "lmoe_last_launch_count", "lmoe_selftest_e2m1", "lmoe_selftest_timeout", "lmoe_profile_events", "dims_of",
     "weights_of", "LmoeKvCache", "LmoeKvMaps", "LmoeAttnDims", "kv_cache_of", "attn_dims_of", "lmoe_tree_masks",
     "lmoe_tree_attention", "lmoe_tree_attention_workspace_bytes", "lmoe_kv_plan", "lmoe_kv_write",
+    "LmoeRopeDims", "LmoeKvCacheFp8", "LmoeDecodeDims", "rope_dims_of", "kv_cache_fp8_of", "decode_dims_of",
+    "lmoe_qk_norm_rope", "lmoe_kv_write_fp8", "lmoe_kv_read_fp8", "lmoe_decode_attention_fp8",
+    "lmoe_decode_attention_fp8_workspace_bytes",
 ]
 
 LMOE_OK, LMOE_EINVAL, LMOE_EUNSUPPORTED, LMOE_ECUDA, LMOE_ETIMEOUT, LMOE_EDEVICE_CHECK, LMOE_EWORKSPACE = \
@@ -84,6 +87,23 @@ _live_maps = weakref.WeakValueDictionary()  # address -> LmoeKvMaps
 class LmoeAttnDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_requests", "n_tokens", "max_request_tokens", "q_heads", "max_blocks",
                                               "mask_words", "window")] + [("scale", ctypes.c_float)]
+
+
+class LmoeRopeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "q_heads", "k_heads", "head_dim", "rot_dim", "n_axes",
+                                              "interleaved", "norm")] + [("eps", ctypes.c_float)]
+
+
+class LmoeKvCacheFp8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+
+
+class LmoeDecodeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_requests", "q_heads", "max_blocks", "window")] + \
+        [("scale", ctypes.c_float)]
 
 
 class LmoeError(RuntimeError):
@@ -146,7 +166,15 @@ def load(path: str | None = None):
     lib.lmoe_kv_plan.argtypes = [i32] * 4 + [vp] * 5 + [i32] + [vp] * 7
     lib.lmoe_kv_maps_init.argtypes = [cp, ctypes.POINTER(LmoeKvMaps)]
     lib.lmoe_kv_write.argtypes = [cp, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz, vp]
-    for f in ("lmoe_tree_masks", "lmoe_kv_maps_init", "lmoe_tree_attention", "lmoe_kv_plan", "lmoe_kv_write",
+    rp, c8, d8 = ctypes.POINTER(LmoeRopeDims), ctypes.POINTER(LmoeKvCacheFp8), ctypes.POINTER(LmoeDecodeDims)
+    lib.lmoe_qk_norm_rope.argtypes = [rp, vp, i64, vp, i64] + [vp] * 5 + [vp, i64, vp, i64, vp]
+    lib.lmoe_kv_write_fp8.argtypes = [c8, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz, vp]
+    lib.lmoe_kv_read_fp8.argtypes = [c8, i32, i32, i32, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]
+    lib.lmoe_decode_attention_fp8_workspace_bytes.argtypes = [d8, c8]
+    lib.lmoe_decode_attention_fp8_workspace_bytes.restype = sz
+    lib.lmoe_decode_attention_fp8.argtypes = [d8, c8, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    for f in ("lmoe_qk_norm_rope", "lmoe_kv_write_fp8", "lmoe_kv_read_fp8", "lmoe_decode_attention_fp8",
+              "lmoe_tree_masks", "lmoe_kv_maps_init", "lmoe_tree_attention", "lmoe_kv_plan", "lmoe_kv_write",
               "lmoe_workspace_layout", "lmoe_route", "lmoe_pool", "lmoe_experts_mxfp4", "lmoe_norm_combine_unpool",
               "lmoe_forward", "lmoe_forward_routed", "lmoe_block_forward", "lmoe_forward_nvfp4", "lmoe_experts_nvfp4",
               "lmoe_status_check", "lmoe_last_launch_count", "lmoe_selftest_e2m1",
@@ -492,6 +520,112 @@ def lmoe_kv_write(cache, k_new, v_new, src, slots, ws=None, stream=None):
                               _i32(src, n, "src"), _i32(slots, 1, "slots"), n, w, nb, _stream_arg(stream))
     if rc:
         raise LmoeError(rc, "lmoe_kv_write")
+
+
+def rope_dims_of(n_tokens, q_heads, k_heads, head_dim, rot_dim=None, n_axes=1, interleaved=False, norm=True,
+                 eps=1e-6) -> LmoeRopeDims:
+    """rot_dim None: the whole head is turned."""
+    return LmoeRopeDims(n_tokens, q_heads, k_heads, head_dim, head_dim if rot_dim is None else rot_dim, n_axes,
+                        bool(interleaved), bool(norm), eps)
+
+
+def lmoe_qk_norm_rope(dims, q, k, q_gain, k_gain, pos, inv_freq, axis, q_out, k_out, stream=None):
+    """Norm and rotation of q [T, q_heads, d] and k [T, k_heads, d], bf16 and perhaps slices of one projection;
+    gains bf16 [d] or None, pos int32 [n_axes, T], inv_freq fp32 [rot_dim / 2], axis int32 [rot_dim / 2] or None.
+    q_out and k_out may be q and k themselves; with no heads a side is None."""
+    t, d, half, sides = dims.n_tokens, dims.head_dim, dims.rot_dim // 2, []
+    for x, heads, what in ((q, dims.q_heads, "q"), (k, dims.k_heads, "k"), (q_out, dims.q_heads, "q_out"),
+                           (k_out, dims.k_heads, "k_out")):
+        if heads == 0:
+            sides.append((None, 0))
+            continue
+        sides.append(_rows(x, heads, d, what))
+        if x.shape[0] < t:
+            raise ValueError(f"{what}: expected {t} rows, got {x.shape[0]}")
+    rc = load().lmoe_qk_norm_rope(
+        ctypes.byref(dims), *sides[0], *sides[1], _arg(q_gain, d, _BF16_ONLY, "q_gain"),
+        _arg(k_gain, d, _BF16_ONLY, "k_gain"), _i32(pos, dims.n_axes * t, "pos"), _arg(inv_freq, half, _F32, "inv_freq"),
+        _i32(axis, half, "axis"), *sides[2], *sides[3], _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_qk_norm_rope")
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def kv_cache_fp8_of(k, v, k_scale, v_scale) -> LmoeKvCacheFp8:
+    """LmoeKvCacheFp8 of two E4M3 tensors [n_blocks, kv_heads, block_size, head_dim] (uint8 or float8_e4m3fn) of
+    equal strides, any order in memory with head_dim contiguous, and their contiguous scale bytes
+    [n_blocks, kv_heads, block_size].  The caller keeps the tensors alive."""
+    for t in (k, v):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("expected CUDA tensors (the library takes device pointers)")
+        if t.dtype not in _CODES:
+            raise TypeError(f"unexpected dtype {t.dtype}, want one of {_CODES}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError("expected [n_blocks, kv_heads, block_size, head_dim] with head_dim contiguous")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    n, h, b, d = k.shape
+    for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if isinstance(t, torch.Tensor) and tuple(t.shape) != (n, h, b):
+            raise ValueError(f"{what}: expected {[n, h, b]}, got {list(t.shape)}")
+    return LmoeKvCacheFp8(k.data_ptr(), v.data_ptr(), _arg(k_scale, n * h * b, _SCALES, "k_scale"),
+                          _arg(v_scale, n * h * b, _SCALES, "v_scale"), n, b, h, d, k.stride(0), k.stride(1),
+                          k.stride(2))
+
+
+def lmoe_kv_write_fp8(cache, k_new, v_new, src, slots, ws=None, stream=None):
+    """lmoe_kv_write into an 8-bit cache: rows src[t] (or t, src None) of bf16 k_new and v_new
+    [rows, kv_heads, d] as codes and scales in the cache's slots[t]."""
+    hk, d, n = cache.kv_heads, cache.head_dim, slots.numel()
+    kp, ks = _rows(k_new, hk, d, "k_new")
+    vp, vs = _rows(v_new, hk, d, "v_new")
+    w, nb = _ws_arg(ws)
+    rc = load().lmoe_kv_write_fp8(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
+                                  _i32(src, n, "src"), _i32(slots, 1, "slots"), n, w, nb, _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_kv_write_fp8")
+
+
+def lmoe_kv_read_fp8(cache, token_offsets, first, block_table, k_out, v_out, ws=None, stream=None):
+    """Positions first[b] (0, first None) and on of every request as rows token_offsets[b] .. token_offsets[b + 1] - 1
+    of bf16 k_out and v_out [rows, kv_heads, d]."""
+    hk, d, b = cache.kv_heads, cache.head_dim, token_offsets.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] != b:
+        raise ValueError(f"block_table: expected [{b}, max_blocks], got {tuple(block_table.shape)}")
+    kp, ks = _rows(k_out, hk, d, "k_out")
+    vp, vs = _rows(v_out, hk, d, "v_out")
+    w, nb = _ws_arg(ws)
+    rc = load().lmoe_kv_read_fp8(ctypes.byref(cache), b, min(k_out.shape[0], v_out.shape[0]), block_table.shape[1],
+                                 _i32(token_offsets, 2, "token_offsets"), _i32(first, b, "first"),
+                                 _i32(block_table, 1, "block_table"), kp, ks, vp, vs, w, nb, _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_kv_read_fp8")
+
+
+def decode_dims_of(n_requests, q_heads, max_blocks, scale, window=0) -> LmoeDecodeDims:
+    return LmoeDecodeDims(n_requests, q_heads, max_blocks, window, scale)
+
+
+def lmoe_decode_attention_fp8_workspace_bytes(dims: LmoeDecodeDims, cache: LmoeKvCacheFp8) -> int:
+    return int(load().lmoe_decode_attention_fp8_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache)))
+
+
+def lmoe_decode_attention_fp8(dims, cache, q, lens, block_table, out, lse, ws, stream=None):
+    """One new token a request, q [B, q_heads, d] (perhaps a slice of a projection), over the lens[b] positions
+    that the 8-bit cache holds of it; lse may be None."""
+    b, hq, d = dims.n_requests, dims.q_heads, cache.head_dim
+    qp, qs = _rows(q, hq, d, "q")
+    if q.shape[0] < b:
+        raise ValueError(f"expected {b} rows in q")
+    rc = load().lmoe_decode_attention_fp8(
+        ctypes.byref(dims), ctypes.byref(cache), qp, qs, _i32(lens, b, "lens"),
+        _i32(block_table, b * dims.max_blocks, "block_table"), _arg(out, b * hq * d, _BF16_ONLY, "out"),
+        _arg(lse, b * hq, _F32, "lse"), *_ws_arg(ws), _stream_arg(stream))
+    if rc:
+        raise LmoeError(rc, "lmoe_decode_attention_fp8")
 
 
 def lmoe_status_check(ws, stream=None) -> int:

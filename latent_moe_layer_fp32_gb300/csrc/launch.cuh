@@ -46,5 +46,10 @@ int optional_status(void* ws, size_t ws_bytes, cudaStream_t s, Status** st);
 // LMOE_OK, LMOE_EINVAL or LMOE_EUNSUPPORTED for a cache descriptor; with
 // `memory` false only its head count and width are looked at
 int check_cache(const lmoe_kv_cache* c, bool memory);
+int check_cache_fp8(const lmoe_kv_cache_fp8* c, bool memory);
+// Whether no two rows of a cache share an element: in the order of their strides, each dimension steps past all
+// that the ones below it span.
+bool rows_apart(int64_t block_stride, int64_t n_blocks, int64_t head_stride, int64_t kv_heads, int64_t slot_stride,
+                int64_t block_size, int64_t head_dim);
 
 }  // namespace lmoe
