@@ -512,6 +512,7 @@ LMOE_API int lmoe_qk_norm_rope(const lmoe_rope_dims* dims, const uint16_t* q, in
  * this order: element = code * 2^(scale - 127); a scale of 255 makes its whole
  * row NaN.  Strides are multiples of 16; k, v, k_scale and v_scale are 16-byte
  * aligned.  block_size, head_dim and kv_heads as for lmoe_kv_cache. */
+typedef struct lmoe_kv_maps_fp8 lmoe_kv_maps_fp8;
 typedef struct {
   uint8_t* k;
   uint8_t* v;
@@ -524,7 +525,18 @@ typedef struct {
   int64_t block_stride;
   int64_t head_stride;
   int64_t slot_stride;
+  const lmoe_kv_maps_fp8* maps; /* from lmoe_kv_maps_fp8_init, or NULL */
 } lmoe_kv_cache_fp8;
+
+/* The copy descriptors of an 8-bit cache, as lmoe_kv_maps is for
+ * lmoe_kv_cache: in the caller's host memory, encoded once for many calls of
+ * lmoe_decode_attention_fp8 (the only one that uses them; it encodes its own
+ * where these were not made for the very fields of the descriptor). */
+struct lmoe_kv_maps_fp8 {
+  uint64_t made_for[8];
+  uint64_t map[2][16];
+};
+LMOE_API int lmoe_kv_maps_fp8_init(const lmoe_kv_cache_fp8* cache, lmoe_kv_maps_fp8* maps);
 
 /* lmoe_kv_write into an 8-bit cache (arguments as there).  The row of a token
  * and head gets the scale 2^e with the smallest e >= -127 for which its largest
@@ -586,7 +598,8 @@ LMOE_API size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims
  * Reported on the device (LMOE_EDEVICE_CHECK through lmoe_status_check): a
  * length below 0 or past its table (the request's rows are not written), a
  * block number outside the cache (they hold no meaning).  Nothing is read out
- * of bounds. */
+ * of bounds.  Each wait for a copy is bounded by about a second (LMOE_ETIMEOUT
+ * through lmoe_status_check). */
 LMOE_API int lmoe_decode_attention_fp8(const lmoe_decode_dims* dims, const lmoe_kv_cache_fp8* cache,
                                        const uint16_t* q, int64_t q_stride, const int32_t* lens,
                                        const int32_t* block_table, uint16_t* out, float* lse, void* ws,

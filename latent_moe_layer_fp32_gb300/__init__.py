@@ -27,7 +27,7 @@ __all__ = [
     "lmoe_last_launch_count", "lmoe_selftest_e2m1", "lmoe_selftest_timeout", "lmoe_profile_events", "dims_of",
     "weights_of", "LmoeKvCache", "LmoeKvMaps", "LmoeAttnDims", "kv_cache_of", "attn_dims_of", "lmoe_tree_masks",
     "lmoe_tree_attention", "lmoe_tree_attention_workspace_bytes", "lmoe_kv_plan", "lmoe_kv_write",
-    "LmoeRopeDims", "LmoeKvCacheFp8", "LmoeDecodeDims", "rope_dims_of", "kv_cache_fp8_of", "decode_dims_of",
+    "LmoeRopeDims", "LmoeKvCacheFp8", "LmoeKvMapsFp8", "LmoeDecodeDims", "rope_dims_of", "kv_cache_fp8_of", "decode_dims_of",
     "lmoe_qk_norm_rope", "lmoe_kv_write_fp8", "lmoe_kv_read_fp8", "lmoe_decode_attention_fp8",
     "lmoe_decode_attention_fp8_workspace_bytes",
 ]
@@ -98,7 +98,20 @@ class LmoeKvCacheFp8(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("maps", ctypes.c_void_p)]
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name == "maps":  # as for LmoeKvCache
+            super().__setattr__("_maps", _live_maps.get(value))
+
+
+class LmoeKvMapsFp8(ctypes.Structure):
+    _fields_ = [("made_for", ctypes.c_uint64 * 8), ("map", ctypes.c_uint64 * 32)]
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        _live_maps[ctypes.addressof(self)] = self
 
 
 class LmoeDecodeDims(ctypes.Structure):
@@ -168,12 +181,13 @@ def load(path: str | None = None):
     lib.lmoe_kv_write.argtypes = [cp, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz, vp]
     rp, c8, d8 = ctypes.POINTER(LmoeRopeDims), ctypes.POINTER(LmoeKvCacheFp8), ctypes.POINTER(LmoeDecodeDims)
     lib.lmoe_qk_norm_rope.argtypes = [rp, vp, i64, vp, i64] + [vp] * 5 + [vp, i64, vp, i64, vp]
+    lib.lmoe_kv_maps_fp8_init.argtypes = [c8, ctypes.POINTER(LmoeKvMapsFp8)]
     lib.lmoe_kv_write_fp8.argtypes = [c8, vp, i64, vp, i64, i32, vp, vp, i32, vp, sz, vp]
     lib.lmoe_kv_read_fp8.argtypes = [c8, i32, i32, i32, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]
     lib.lmoe_decode_attention_fp8_workspace_bytes.argtypes = [d8, c8]
     lib.lmoe_decode_attention_fp8_workspace_bytes.restype = sz
     lib.lmoe_decode_attention_fp8.argtypes = [d8, c8, vp, i64, vp, vp, vp, vp, vp, sz, vp]
-    for f in ("lmoe_qk_norm_rope", "lmoe_kv_write_fp8", "lmoe_kv_read_fp8", "lmoe_decode_attention_fp8",
+    for f in ("lmoe_qk_norm_rope", "lmoe_kv_maps_fp8_init", "lmoe_kv_write_fp8", "lmoe_kv_read_fp8", "lmoe_decode_attention_fp8",
               "lmoe_tree_masks", "lmoe_kv_maps_init", "lmoe_tree_attention", "lmoe_kv_plan", "lmoe_kv_write",
               "lmoe_workspace_layout", "lmoe_route", "lmoe_pool", "lmoe_experts_mxfp4", "lmoe_norm_combine_unpool",
               "lmoe_forward", "lmoe_forward_routed", "lmoe_block_forward", "lmoe_forward_nvfp4", "lmoe_experts_nvfp4",
@@ -557,7 +571,7 @@ _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 def kv_cache_fp8_of(k, v, k_scale, v_scale) -> LmoeKvCacheFp8:
     """LmoeKvCacheFp8 of two E4M3 tensors [n_blocks, kv_heads, block_size, head_dim] (uint8 or float8_e4m3fn) of
     equal strides, any order in memory with head_dim contiguous, and their contiguous scale bytes
-    [n_blocks, kv_heads, block_size].  The caller keeps the tensors alive."""
+    [n_blocks, kv_heads, block_size]; with its copy descriptors.  The caller keeps the tensors alive."""
     for t in (k, v):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError("expected CUDA tensors (the library takes device pointers)")
@@ -571,9 +585,13 @@ def kv_cache_fp8_of(k, v, k_scale, v_scale) -> LmoeKvCacheFp8:
     for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if isinstance(t, torch.Tensor) and tuple(t.shape) != (n, h, b):
             raise ValueError(f"{what}: expected {[n, h, b]}, got {list(t.shape)}")
-    return LmoeKvCacheFp8(k.data_ptr(), v.data_ptr(), _arg(k_scale, n * h * b, _SCALES, "k_scale"),
-                          _arg(v_scale, n * h * b, _SCALES, "v_scale"), n, b, h, d, k.stride(0), k.stride(1),
-                          k.stride(2))
+    cache = LmoeKvCacheFp8(k.data_ptr(), v.data_ptr(), _arg(k_scale, n * h * b, _SCALES, "k_scale"),
+                           _arg(v_scale, n * h * b, _SCALES, "v_scale"), n, b, h, d, k.stride(0), k.stride(1),
+                           k.stride(2), None)
+    maps = LmoeKvMapsFp8()
+    _check(load().lmoe_kv_maps_fp8_init(ctypes.byref(cache), ctypes.byref(maps)), "lmoe_kv_maps_fp8_init")
+    cache.maps = ctypes.addressof(maps)  # they live as long as a descriptor that has their address
+    return cache
 
 
 def lmoe_kv_write_fp8(cache, k_new, v_new, src, slots, ws=None, stream=None):

@@ -2,9 +2,12 @@
 // (include/lmoe.h has the contract).
 #include <algorithm>
 #include <atomic>
+#include <cstring>
+#include <utility>
 
 #include "common.cuh"
 #include "launch.cuh"
+#include "tmap.cuh"
 
 namespace lmoe {
 
@@ -13,9 +16,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTile = 32;        // keys of a tile
-constexpr int kStages = 3;       // tiles of a warp's ring
 constexpr float kShift = 14.f;   // P stands in f16 as p * 2^14, see below
 
 struct DecodeArgs {
@@ -41,14 +42,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {  // the low two
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-  return h;
+// Four codes as two pairs of f16.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n cvt.rn.f16x2.e4m3x2 %0, x;\n cvt.rn.f16x2.e4m3x2 %1, y;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+template <int DST>
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {  // the rest is zero
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(DST)
+               : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -59,10 +69,18 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+template <int OFF>
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(OFF)
+               : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(OFF)
                : "memory");
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -91,93 +109,111 @@ struct Sum {
   __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 };
 
-// The tiles that a request's positions in sight take, and where the first one begins.
+// The tiles of KT keys that a request's positions in sight take, and where the first one begins.
+template <int KT>
 struct Span {
   int lo, len, n;
-  __device__ __forceinline__ int p0(int tile) const { return (lo & ~(kTile - 1)) + tile * kTile; }
+  __device__ __forceinline__ int p0(int tile) const { return (lo & ~(KT - 1)) + tile * KT; }
 };
 
-__device__ __forceinline__ Span span_of(const DecodeArgs& a, int len) {
-  Span s;
+template <int KT>
+__device__ __forceinline__ Span<KT> span_of(const DecodeArgs& a, int len) {
+  Span<KT> s;
   s.len = len;
   s.lo = a.window && len > a.window ? len - a.window : 0;
   const bool fine = len > 0 && ((unsigned)(len - 1) >> a.bs_shift) < (unsigned)a.max_blocks;
-  s.n = fine ? (int)(((unsigned)(len - 1) >> 5) - ((unsigned)s.lo >> 5)) + 1 : 0;
+  s.n = fine ? (int)((unsigned)(len - 1) / KT - (unsigned)s.lo / KT) + 1 : 0;
   return s;
 }
 
-// A warp's walk over the line of tiles: request by request, in it segment (key head and query group) by segment.
+// A warp's walk over the line of tiles: request by request, in it key head by key head, in it group by group of
+// query rows.
+template <int KT>
 struct Walk {
-  int b, seg, tile;
-  Span s;
+  int b, h, group, tile;
+  Span<KT> s;
   long long left;
 
-  __device__ __forceinline__ void next(const DecodeArgs& a, int segs) {
+  __device__ __forceinline__ void next(const DecodeArgs& a) {
     if (--left <= 0) return;
     if (++tile < s.n) return;
     tile = 0;
-    if (++seg < segs) return;
-    seg = 0;
+    if (++group < a.groups) return;
+    group = 0;
+    if (++h < a.c.kv_heads) return;
+    h = 0;
     do {
-      s = span_of(a, a.lens[++b]);
+      s = span_of<KT>(a, a.lens[++b]);
     } while (s.n == 0);  // (there are tiles left, so there is such a request)
   }
 };
 
-struct Tile {      // what is kept of a tile until it is computed
-  int b, seg;
-  int lo, hi;      // rows in sight
-  int from;        // its segment starts with it (1), before it in this range (2) or before the range (0)
-  int rest;        // tiles of its segment after it
-};
-
-// N8: groups of eight query rows that a key's codes are used for.
+// N8: groups of eight query rows that a key's codes are used for; W warps; S tiles of KT keys in a warp's ring.
 template <int D, int N8>
 struct Cfg {
+  static constexpr int W = N8 == 1 ? 12 : 8, KT = kTile, S = N8 == 1 ? 2 : 3;
+  static constexpr int kThreads = 32 * W;
   static constexpr int kRows = 8 * N8;
   static constexpr int kChunks = D / 16;  // 16-byte pieces of a row
-  static constexpr int kCodes = kTile * D;
-  static constexpr int kStage = 2 * kCodes + 2 * kTile;
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kCodes = KT * D;
+  static constexpr int kStage = 2 * kCodes;
+  static constexpr int kRing = W * S * kStage;
   static constexpr int kPiece = kRows * D;  // floats of a piece's output
-  static constexpr int kSmem = kRing;
-  static_assert(kWarps * (kPiece * 4 + kRows * 8) <= kRing, "the last pieces take the ring's place");
+  static constexpr int kSmem = kRing + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
+  static_assert(W * (kPiece * 4 + kRows * 8) <= kRing, "the last pieces take the ring's place");
+  static_assert(KT == 16 || KT == 32, "a lane a key");
 };
 
-// Where 16-byte piece c of row r stands in a tile: rows that are read together lie in different banks.
+// The 16-byte piece c of a tile's row r stands at r * D + ((c ^ swizzle(r)) << 4): the eight rows of one 8x8 matrix
+// lie in different banks.
 template <int D>
-__device__ __forceinline__ uint32_t place(int r, int c) {
-  return D == 128 ? r * 128 + ((c ^ ((r & 1) << 2 | (r >> 1 & 3))) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
+__device__ __forceinline__ uint32_t swizzle(int r) {
+  return D == 128 ? r & 7 : r >> 1 & 3;
+}
+
+// A loop over constants: the body gets them as types.
+template <typename F, int... I>
+__device__ __forceinline__ void unrolled_by(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  unrolled_by(f, std::make_integer_sequence<int, N>());
 }
 
 template <int D, int N8>
-__global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<D, N8>;
-  extern __shared__ __align__(128) uint8_t s_ring[];
-  __shared__ unsigned long long s_scan[kWarps];
-  __shared__ int s_b[kWarps];
-  __shared__ unsigned long long s_at[kWarps];
-  __shared__ Tile s_tile[kWarps][4];
-  __shared__ int2 s_seg[kWarps][2];  // segments of a warp's pieces: put down on the way, at its range's end
-  __shared__ int2 s_flags[kWarps];
-  __shared__ int s_rest;
-  __shared__ int s_err;
+  constexpr int W = C::W, KT = C::KT, MT = KT / 16;
+  extern __shared__ uint8_t s_dynamic[];
+  uint8_t* const s_ring = s_dynamic + (-smem_u32(s_dynamic) & 1023u);
+  __shared__ uint64_t s_full[W][C::S];
+  __shared__ float4 s_key[W][KT];  // of a tile's keys: the key's scale, 0 or -infinity, the value's exponent
+  __shared__ __align__(16) uint8_t s_scale[W][C::S][2 * KT];  // of the ring's tiles: K's, V's
+  __shared__ unsigned long long s_scan[W], s_at[W];
+  __shared__ int s_b[W];
+  __shared__ int4 s_seg[W][2];  // a warp's pieces, put down on the way and at its range's end: {request, head, group, flags}
+  __shared__ int s_rest, s_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int segs = a.c.kv_heads * a.groups, hq = a.c.kv_heads * a.G;
+  const int hq = a.c.kv_heads * a.G;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) s_err = 0;
+  if (threadIdx.x == 0) s_err = s_rest = 0;
+  if (lane < C::S) mbar_init(&s_full[warp][lane], 1);
+  fence_barrier_init();
 
   // ---- the line of tiles, and this warp's part of it ----
   unsigned long long total, n_ctas, hi;
   long long todo;
   {
-    const int run = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
+    const int run = (a.B + C::kThreads - 1) / C::kThreads, b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
+    const unsigned segs = (unsigned)(a.c.kv_heads * a.groups);
     unsigned long long mine = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const int len = a.lens[b];
-      const Span s = span_of(a, len);
+      const Span<KT> s = span_of<KT>(a, len);
       bad |= len != 0 && s.n == 0;
       mine += s.n;
     }
@@ -192,22 +228,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
     __syncthreads();
     unsigned long long before = x - mine;
     total = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < warp) before += s_scan[w];
       total += s_scan[w];
     }
     if (bad) atomicCAS(&s_err, 0, 241);
     // as many CTAs as have a tile for each warp
-    n_ctas = min((unsigned long long)a.ctas, (total + kWarps - 1) / kWarps);
+    n_ctas = min((unsigned long long)a.ctas, (total + W - 1) / W);
     const unsigned long long c = blockIdx.x, lo = c < n_ctas ? total * c / n_ctas : total;
     hi = c < n_ctas ? total * (c + 1) / n_ctas : total;
-    for (int w = 0; w < kWarps; ++w) {
-      const unsigned long long at = lo + (hi - lo) * w / kWarps;
+    for (int w = 0; w < W; ++w) {
+      const unsigned long long at = lo + (hi - lo) * w / W;
       if (at >= before && at < before + mine) {
         unsigned long long skip = at - before;
         int b = b0;
         for (;; ++b) {
-          const unsigned long long there = (unsigned long long)span_of(a, a.lens[b]).n * segs;
+          const unsigned long long there = (unsigned long long)span_of<KT>(a, a.lens[b]).n * segs;
           if (skip < there) break;
           skip -= there;
         }
@@ -215,103 +251,121 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
         s_at[w] = skip;
       }
     }
-    todo = (long long)((hi - lo) * (warp + 1) / kWarps - (hi - lo) * warp / kWarps);
+    todo = (long long)((hi - lo) * (warp + 1) / W - (hi - lo) * warp / W);
   }
   // requests without positions
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (a.lens[b] != 0) continue;
-    for (int i = threadIdx.x; i < hq * D / 8; i += kThreads)
+    for (int i = threadIdx.x; i < hq * D / 8; i += C::kThreads)
       reinterpret_cast<uint4*>(a.out + (size_t)b * hq * D)[i] = make_uint4(0, 0, 0, 0);
     if (a.lse)
-      for (int i = threadIdx.x; i < hq; i += kThreads) a.lse[(size_t)b * hq + i] = -INFINITY;
+      for (int i = threadIdx.x; i < hq; i += C::kThreads) a.lse[(size_t)b * hq + i] = -INFINITY;
   }
   __syncthreads();
 
-  Walk walk;
+  Walk<KT> walk;
   walk.left = todo;
-  bool started = false;  // whether the current segment of the walk starts in this range
-  if (walk.left > 0) {
+  if (todo > 0) {
     walk.b = s_b[warp];
-    walk.s = span_of(a, a.lens[walk.b]);
+    walk.s = span_of<KT>(a, a.lens[walk.b]);
     const unsigned long long at = s_at[warp];
-    walk.seg = (int)(at / (unsigned)walk.s.n);
-    walk.tile = (int)(at - (unsigned long long)walk.seg * walk.s.n);
+    const int seg = (int)(at / (unsigned)walk.s.n);
+    walk.tile = (int)(at - (unsigned long long)seg * walk.s.n);
+    walk.h = seg / a.groups;
+    walk.group = seg - walk.h * a.groups;
   }
-  uint8_t* const ring = s_ring + warp * kStages * C::kStage;
-  const uint32_t ring32 = smem_u32(ring);
+  Walk<KT> ahead = walk;  // walks in front and looks pages up
+  const uint32_t ring32 = smem_u32(s_ring + warp * C::S * C::kStage), scale32 = smem_u32(s_scale[warp]);
 
   // ---- a tile's way: its pages are looked up, its rows copied, its products formed ----
   int page = 0;  // block number of the page that holds this lane's half of the looked-up tile
   int look_h = 0, look_in = 0, look_lo = 0, look_hi = 0;
-  int n_look = 0, n_copy = 0;
-  auto look = [&] {  // (walk.left > 0)
-    const int p0 = walk.s.p0(walk.tile);
-    look_lo = max(walk.s.lo - p0, 0);
-    look_hi = min(walk.s.len - p0, kTile);
-    look_h = walk.seg / a.groups;
+  bool looked = false;
+  int to_stage = 0;
+  auto look = [&] {
+    looked = ahead.left > 0;
+    if (!looked) return;
+    const int p0 = ahead.s.p0(ahead.tile);
+    look_lo = max(ahead.s.lo - p0, 0);
+    look_hi = min(ahead.s.len - p0, KT);
+    look_h = ahead.h;
     look_in = p0;
-    const int p = min(max(p0 + (lane & 16), p0 + look_lo), p0 + look_hi - 1);
-    page = a.table[(size_t)walk.b * a.max_blocks + (p >> a.bs_shift)];
-    if (walk.tile == 0) started = true;
-    if (lane == 0) {
-      Tile d;
-      d.b = walk.b;
-      d.seg = walk.seg;
-      d.lo = look_lo;
-      d.hi = look_hi;
-      d.from = walk.tile == 0 ? 1 : started ? 2 : 0;
-      d.rest = walk.s.n - 1 - walk.tile;
-      s_tile[warp][n_look & 3] = d;
-    }
-    if (walk.tile + 1 == walk.s.n) started = false;
-    ++n_look;
-    walk.next(a, segs);
+    const int p = min(max(p0 + (lane & (KT - 16)), p0 + look_lo), p0 + look_hi - 1);
+    page = a.table[(size_t)ahead.b * a.max_blocks + (p >> a.bs_shift)];
+    ahead.next(a);
   };
-  const size_t lane_off = (size_t)(lane / C::kChunks) * a.c.slot_stride + (lane % C::kChunks) * 16;
   constexpr int kStep = 32 / C::kChunks;  // rows that one copy instruction takes
+  const int row = lane / C::kChunks, chunk = lane % C::kChunks;
+  const size_t lane_off = (size_t)row * a.c.slot_stride + chunk * 16;
+  const size_t step = (size_t)kStep * a.c.slot_stride;
+  // (a step of four rows turns the swizzle's bit 2, a step of eight none)
+  const uint32_t lane_to = row * D + ((chunk ^ swizzle<D>(row)) << 4);
+  const uint64_t once = a.groups == 1 ? policy_evict_first() : policy_evict_normal();
+  const int box = min(1 << a.bs_shift, KT);  // rows that a bulk copy takes
+  // a bit for each place of the ring: its tile came in bulk, and has not been waited for; the parity of its next
+  // bulk copy; it was last written by lanes
+  uint32_t bulk = 0, parity = 0, by_lanes = 0;
   auto copy = [&] {  // the tile that was looked up
-    const uint32_t dst = ring32 + (n_copy % kStages) * C::kStage;
-    const int mask = (1 << a.bs_shift) - 1;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      int block = __shfl_sync(0xffffffffu, page, half * 16);
-      const bool any = look_lo < half * 16 + 16 && look_hi > half * 16;
-      bool ok = true;
-      if (block < 0 || block >= a.c.n_blocks) {
-        if (any && lane == 0) atomicCAS(&s_err, 0, 242);
-        block = 0;
-        ok = false;
+    const uint32_t to = ring32 + to_stage * C::kStage, bit = 1u << to_stage, mask = (1u << a.bs_shift) - 1;
+    const bool fine = __all_sync(0xffffffffu, (unsigned)page < (unsigned)a.c.n_blocks);
+    if (look_lo == 0 && look_hi == KT && fine) {
+      // all its rows are in sight: K and V in bulk, a lane a page
+      if (by_lanes & bit) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      by_lanes &= ~bit;
+      bulk |= bit;
+      __syncwarp();
+      uint64_t* const bar = &s_full[warp][to_stage];
+      if (lane == 0) mbar_arrive_expect_tx(bar, C::kStage);
+      __syncwarp();
+      const int r = (lane & 16);
+      if ((lane & 15) == 0 && r < KT && (r == 0 || box == 16)) {
+        const int in = (look_in + r) & mask;
+        uint8_t* const dst = s_ring + (to - smem_u32(s_ring)) + r * D;
+        tma_load_4d(dst, &k_map, 0, in, look_h, page, bar, once);
+        tma_load_4d(dst + C::kCodes, &v_map, 0, in, look_h, page, bar, once);
       }
-      const int in = (look_in + half * 16) & mask;
-      const size_t off = (size_t)block * a.c.block_stride + (size_t)look_h * a.c.head_stride +
-                         (size_t)in * a.c.slot_stride + lane_off;
-#pragma unroll
-      for (int i = 0; i < 16 / kStep; ++i) {
-        const int r = half * 16 + i * kStep + lane / C::kChunks;
-        const uint32_t to = dst + place<D>(r, lane % C::kChunks);
-        const uint32_t bytes = ok && r >= look_lo && r < look_hi ? 16 : 0;
-        const size_t from = bytes ? off + (size_t)(i * kStep) * a.c.slot_stride : 0;
-        copy16(to, a.c.k + from, bytes);
-        copy16(to + C::kCodes, a.c.v + from, bytes);
-      }
-      // four scale bytes a lane: eight lanes for each half, the first four K
-      if ((lane >> 3) == half) {
-        const int r = half * 16 + (lane & 3) * 4;
-        const uint32_t bytes = ok && r + 4 > look_lo && r < look_hi ? 4 : 0;
-        const size_t from =
-            bytes ? ((((size_t)block * a.c.kv_heads + look_h) << a.bs_shift) + in + (lane & 3) * 4) : 0;
-        const bool v = lane & 4;
-        copy4(dst + 2 * C::kCodes + (v ? kTile : 0) + r, (v ? a.c.v_scale : a.c.k_scale) + from, bytes);
-      }
+    } else {
+      by_lanes |= bit;
+      const uint32_t dst = to + lane_to, dst2 = kStep == 4 ? dst ^ 64 : dst;
+      unrolled<MT>([&](auto half) {
+        constexpr int kHalf = half * 16 * D;
+        int block = __shfl_sync(0xffffffffu, page, half * 16);
+        int lo = look_lo - half * 16, n = look_hi - look_lo;  // rows in sight, from the half's first
+        if (block < 0 || block >= a.c.n_blocks) {
+          if (lane == 0 && lo < 16 && lo + n > 0) atomicCAS(&s_err, 0, 242);
+          block = 0;
+          n = 0;
+        }
+        const size_t off = (size_t)block * a.c.block_stride + (size_t)look_h * a.c.head_stride +
+                           (size_t)((look_in + half * 16) & mask) * a.c.slot_stride + lane_off;
+        const uint8_t *kp = a.c.k + off, *vp = a.c.v + off;
+        unrolled<16 / kStep>([&](auto i) {
+          const uint32_t bytes = (unsigned)(i * kStep + row - lo) < (unsigned)n ? 16 : 0;
+          copy16<kHalf + i * kStep * D>(i % 2 ? dst2 : dst, bytes ? kp : a.c.k, bytes);
+          copy16<kHalf + i * kStep * D + C::kCodes>(i % 2 ? dst2 : dst, bytes ? vp : a.c.v, bytes);
+          kp += step;
+          vp += step;
+        });
+      });
     }
-    ++n_copy;
+    // four scale bytes a lane: eight lanes for each half, the first four K
+    const int half = lane >> 3 & 1, r = half * 16 + (lane & 3) * 4;
+    const int block = __shfl_sync(0xffffffffu, page, half * 16);
+    if (lane < KT / 2) {
+      const uint32_t bytes = r + 4 > look_lo && r < look_hi && (unsigned)block < (unsigned)a.c.n_blocks ? 4 : 0;
+      const size_t from =
+          bytes ? ((((size_t)block * a.c.kv_heads + look_h) << a.bs_shift) + ((look_in + r) & mask)) : 0;
+      const bool v = lane & 4;
+      copy4(scale32 + to_stage * 2 * KT + (v ? KT : 0) + r, (v ? a.c.v_scale : a.c.k_scale) + from, bytes);
+    }
+    to_stage = to_stage == C::S - 1 ? 0 : to_stage + 1;
   };
 
-  if (walk.left > 0) look();
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (n_copy < n_look) {
+  look();
+  for (int i = 0; i < C::S - 1; ++i) {
+    if (looked) {
       copy();
-      if (walk.left > 0) look();
+      look();
     }
     copies_end();
   }
@@ -322,7 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
   // this warp's pieces, put down on the way (x) and at its range's end (y): 1 there is one, 2 its segment started
   // before the range, 4 it ended
   int2 flags = make_int2(0, 0);
-  int bank = 0;
+  int stage = 0;
+  bool fresh = true, whole = false;  // the segment has no tile here yet; its first tile is in this range
+  // this lane's row of a 16-key matrix pair, and its half of two pieces
+  const uint32_t lane_at = (lane & 15) * D + (((lane >> 4) ^ swizzle<D>(lane & 15)) << 4);
 
   // the accumulators as outputs: put(row, column, the value and the next column's), and sums(row, M, L)
   auto results = [&](auto&& put, auto&& sums) {
@@ -343,54 +400,67 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
       }
   };
 
-  for (; todo > 0; --todo) {
-    copies_wait<kStages - 2>();
+  bool ok = true;
+  while (walk.left > 0) {
+    copies_wait<C::S - 2>();
+    if (bulk >> stage & 1) {
+      // (one answer for the whole warp)
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], parity >> stage & 1, nullptr, 0));
+      if (!ok) break;
+      bulk ^= 1u << stage;
+      parity ^= 1u << stage;
+    }
     __syncwarp();
-    const Tile d = s_tile[warp][bank & 3];
+    const uint32_t st32 = ring32 + stage * C::kStage + lane_at;
+    const bool last = walk.tile == walk.s.n - 1;
+    if (lane < KT) {
+      const uint32_t kb = s_scale[warp][stage][lane], vb = s_scale[warp][stage][KT + lane];
+      float4 key = make_float4(e8m0_to_f32(kb), 0.f, vb == 255 ? NAN : (float)vb - 127.f, 0.f);
+      if (last || walk.tile == 0) {
+        const int p = walk.s.p0(walk.tile) + lane;
+        if (p < walk.s.lo || (unsigned)p >= (unsigned)walk.s.len) key = make_float4(0.f, -INFINITY, 0.f, 0.f);
+      }
+      s_key[warp][lane] = key;
+    }
     __syncwarp();
     // (the ring's oldest place is free: its tile was computed before the last __syncwarp)
-    if (n_copy < n_look) {
+    if (looked) {
       copy();
-      if (walk.left > 0) look();
+      look();
     }
     copies_end();
-    const uint8_t* const st = ring + (bank % kStages) * C::kStage;
-    const uint32_t st32 = ring32 + (bank % kStages) * C::kStage;
-    ++bank;
-    const int h = d.seg / a.groups, row0 = (d.seg - h * a.groups) * C::kRows;  // rows of the head's G
+    stage = stage == C::S - 1 ? 0 : stage + 1;
+    const int h = walk.h, row0 = walk.group * C::kRows;  // rows of the head's G
     const int rows = min(C::kRows, a.G - row0);
-    if (d.from == 1 || bank == 1) {  // a segment's first tile here
+    if (fresh) {
+      fresh = false;
+      whole = walk.tile == 0;
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
         const int r = n * 8 + g;
-        const uint16_t* const src = a.q + (long long)d.b * a.qs + (size_t)(h * a.G + row0 + r) * D + t * 16;
-        uint4 w[D / 64][2];
+        const uint16_t* const src = a.q + (long long)walk.b * a.qs + (size_t)(h * a.G + row0 + r) * D + t * 4;
+        uint2 w[C::kChunks];
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            w[i][j] = r < rows ? reinterpret_cast<const uint4*>(src + i * 64)[j] : make_uint4(0, 0, 0, 0);
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i][j].x & 0x7fff7fffu, w[i][j].y & 0x7fff7fffu),
-                                         __vmaxu2(w[i][j].z & 0x7fff7fffu, w[i][j].w & 0x7fff7fffu)));
-          }
+        for (int i = 0; i < C::kChunks; ++i) {
+          w[i] = r < rows ? *reinterpret_cast<const uint2*>(src + i * 16) : make_uint2(0, 0);
+          top = __vmaxu2(top, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+        }
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = act_exponent(top << 16);
         const float up = ldexpf(1.f, e);
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
+        for (int i = 0; i < C::kChunks; ++i) {
+          const uint32_t x[2] = {w[i].x, w[i].y};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t x[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const __half2 hv = __floats2half2_rn(__uint_as_float(x[m] << 16) * up,
-                                                   __uint_as_float(x[m] & 0xffff0000u) * up);
-              qf[n][i * 4 + j * 2 + m / 2][m & 1] = *reinterpret_cast<const uint32_t*>(&hv);
-            }
+          for (int m = 0; m < 2; ++m) {
+            const __half2 hv = __floats2half2_rn(__uint_as_float(x[m] << 16) * up,
+                                                 __uint_as_float(x[m] & 0xffff0000u) * up);
+            qf[n][i][m] = *reinterpret_cast<const uint32_t*>(&hv);
           }
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int ej = __shfl_sync(0xffffffffu, e, (2 * t + j) * 4);
@@ -406,46 +476,39 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
     }
 
     // ---- scores: S[key][row] = codes . queries ----
-    float s[2][N8][4];
+    float s[MT][N8][4];
+    unrolled<C::kChunks / 2>([&](auto pair) {
+      constexpr int c = 2 * pair;
+      unrolled<MT>([&](auto mt) {
+        uint32_t r[4];  // keys g and g + 8, columns 4 t .. 4 t + 3 of piece c; the same of c + 1
+        ldmatrix<mt * 16 * D>(r, st32 ^ (c << 4));
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
+        for (int x = 0; x < 2; ++x) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(r[2 * x], a0, a2);
+          e4m3x4_to_f16x4(r[2 * x + 1], a1, a3);
 #pragma unroll
-      for (int n = 0; n < N8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[mt][n][j] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(st + place<D>(mt * 16 + g, i * 4 + t));
-        const uint4 y = *reinterpret_cast<const uint4*>(st + place<D>(mt * 16 + g + 8, i * 4 + t));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t a0 = e4m3x2_to_f16x2(xs[m]), a2 = e4m3x2_to_f16x2(xs[m] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(ys[m]), a3 = e4m3x2_to_f16x2(ys[m] >> 16);
-#pragma unroll
-          for (int n = 0; n < N8; ++n) mma_f16(s[mt][n], a0, a1, a2, a3, qf[n][i * 4 + m][0], qf[n][i * 4 + m][1]);
+          for (int n = 0; n < N8; ++n) {
+            if (c + x == 0) mma_f16_zero(s[mt][n], a0, a1, a2, a3, qf[n][0][0], qf[n][0][1]);
+            else mma_f16(s[mt][n], a0, a1, a2, a3, qf[n][c + x][0], qf[n][c + x][1]);
+          }
         }
-      }
-    }
-    // ---- to base 2, with the keys' scales; the same with the values' scales for the products with them ----
-    float so[2][N8][4];
-    const bool edge = d.lo > 0 || d.hi < kTile;
+      });
+    });
+    // ---- to base 2, with the keys' scales; the same with the values' exponents for the products with them ----
+    float so[MT][N8][4];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = mt * 16 + k * 8 + g;
-        const float ks = e8m0_to_f32(st[2 * C::kCodes + r]);
-        const uint32_t vb = st[2 * C::kCodes + kTile + r];
-        const float vs = vb == 255 ? NAN : (float)vb - 127.f;
-        const bool see = !edge || (r >= d.lo && r < d.hi);
+        const float4 key = s_key[warp][mt * 16 + k * 8 + g];
 #pragma unroll
         for (int n = 0; n < N8; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& x = s[mt][n][k * 2 + j];
-            x = see ? x * q_scale[n][j] * ks : -INFINITY;
-            so[mt][n][k * 2 + j] = see ? x + vs : -INFINITY;
+            x = fmaf(x * q_scale[n][j], key.x, key.y);
+            so[mt][n][k * 2 + j] = x + key.z;
           }
       }
     // ---- running maxima ----
@@ -455,8 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
     for (int n = 0; n < N8; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        top[n][j] = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]), fmaxf(s[1][n][j], s[1][n][2 + j]));
-        top_o[n][j] = fmaxf(fmaxf(so[0][n][j], so[0][n][2 + j]), fmaxf(so[1][n][j], so[1][n][2 + j]));
+        top[n][j] = fmaxf(s[0][n][j], s[0][n][2 + j]);
+        top_o[n][j] = fmaxf(so[0][n][j], so[0][n][2 + j]);
+#pragma unroll
+        for (int mt = 1; mt < MT; ++mt) {
+          top[n][j] = fmaxf(top[n][j], fmaxf(s[mt][n][j], s[mt][n][2 + j]));
+          top_o[n][j] = fmaxf(top_o[n][j], fmaxf(so[mt][n][j], so[mt][n][2 + j]));
+        }
         more |= top[n][j] > M[n][j] || top_o[n][j] > Mo[n][j];
       }
     if (__any_sync(0xffffffffu, more)) {
@@ -482,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
         }
     }
     // ---- probabilities: their sums in fp32, and as f16 fragments ----
-    uint32_t pf[2][N8][2];
+    uint32_t pf[MT][N8][2];
 #pragma unroll
     for (int n = 0; n < N8; ++n) {
       float mu[2], mo[2];
@@ -492,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
         mo[j] = (Mo[n][j] == -INFINITY ? 0.f : Mo[n][j]) - kShift;
       }
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float p[2];
@@ -506,72 +574,82 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
         }
     }
     // ---- products with the values: O[d][row] ----
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int c = 0; c < C::kChunks; c += 2) {
+    unrolled<MT>([&](auto mt) {
+      unrolled<C::kChunks / 2>([&](auto pair) {
+        constexpr int c = 2 * pair;
         uint32_t r[4];
-        ldmatrix_x4_trans(r, st32 + C::kCodes + place<D>(mt * 16 + (lane & 15), c + (lane >> 4)));
+        ldmatrix_trans<C::kCodes + mt * 16 * D>(r, st32 ^ (c << 4));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           // a word holds two keys by two columns: by columns, and each column's pair is a fragment's
-          const uint32_t w0 = __byte_perm(r[2 * x], 0, 0x3120), w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
-          const uint32_t a0 = e4m3x2_to_f16x2(w0), a1 = e4m3x2_to_f16x2(w0 >> 16);
-          const uint32_t a2 = e4m3x2_to_f16x2(w1), a3 = e4m3x2_to_f16x2(w1 >> 16);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(__byte_perm(r[2 * x], 0, 0x3120), a0, a1);
+          e4m3x4_to_f16x4(__byte_perm(r[2 * x + 1], 0, 0x3120), a2, a3);
 #pragma unroll
           for (int n = 0; n < N8; ++n) mma_f16(o[c + x][n], a0, a1, a2, a3, pf[mt][n][0], pf[mt][n][1]);
         }
-      }
+      });
+    });
 
     // ---- the segment's end, or the range's ----
-    if (d.rest == 0 && d.from != 0) {
+    if (last && whole) {
       results(
           [&](int r, int col, float x, float y) {
             if (r < rows)
-              *reinterpret_cast<uint32_t*>(a.out + ((size_t)d.b * hq + h * a.G + row0 + r) * D + col) = pack_bf16(x, y);
+              *reinterpret_cast<uint32_t*>(a.out + ((size_t)walk.b * hq + h * a.G + row0 + r) * D + col) = pack_bf16(x, y);
           },
           [&](int r, float m, float l) {
             if (r < rows && a.lse)
-              a.lse[(size_t)d.b * hq + h * a.G + row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+              a.lse[(size_t)walk.b * hq + h * a.G + row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           });
-    } else if (d.rest == 0 && todo > 1) {  // started before this range: a piece
-      const size_t at = (size_t)blockIdx.x * kWarps + warp;
+    } else if (last && walk.left > 1) {  // started before this range: a piece
+      const size_t at = (size_t)blockIdx.x * W + warp;
       results([&](int r, int col, float x, float y) {
         *reinterpret_cast<float2*>(a.warp_o + at * C::kPiece + r * D + col) = make_float2(x, y);
       }, [&](int r, float m, float l) { a.warp_ml[at * C::kRows + r] = make_float2(m, l); });
       flags.x = 1 | 2 | 4;
-      if (lane == 0) s_seg[warp][0] = make_int2(d.b, d.seg);
-    } else if (todo == 1) {
-      flags.y = 1 | (d.from == 0 ? 2 : 0) | (d.rest == 0 ? 4 : 0);
+      if (lane == 0) s_seg[warp][0] = make_int4(walk.b, h, row0, 0);
+    } else if (walk.left == 1) {
+      flags.y = 1 | (whole ? 0 : 2) | (last ? 4 : 0);
       if (lane == 0) {
-        s_seg[warp][1] = make_int2(d.b, d.seg);
-        if (warp == kWarps - 1) s_rest = d.rest;
+        s_seg[warp][1] = make_int4(walk.b, h, row0, 0);
+        if (warp == W - 1) s_rest = walk.s.n - 1 - walk.tile;
       }
     }
+    fresh = last;
+    walk.next(a);
   }
 
   // ---- the pieces of the warps joined, in the order of the line ----
   copies_wait<0>();
+  if (!ok) {  // a copy did not come: its CTA's results hold no meaning; the others in flight are waited for as long
+    if (lane == 0) atomicExch(&s_err, 251);
+    for (int i = 0; i < C::S; ++i)
+      if (bulk >> i & 1) mbar_wait(&s_full[warp][i], parity >> i & 1, nullptr, 0);
+  }
   __syncthreads();  // the ring's place is free
   float* const z_o = reinterpret_cast<float*>(s_ring);
-  float2* const z_ml = reinterpret_cast<float2*>(z_o + kWarps * C::kPiece);
+  float2* const z_ml = reinterpret_cast<float2*>(z_o + W * C::kPiece);
   if (flags.y)
     results([&](int r, int col, float x, float y) {
       *reinterpret_cast<float2*>(z_o + warp * C::kPiece + r * D + col) = make_float2(x, y);
     }, [&](int r, float m, float l) { z_ml[warp * C::kRows + r] = make_float2(m, l); });
-  if (lane == 0) s_flags[warp] = flags;
+  if (lane == 0) {
+    s_seg[warp][0].w = flags.x;
+    s_seg[warp][1].w = flags.y;
+  }
   __syncthreads();
   int4 rec = make_int4(0, 0, -1, s_err);
-  for (int e = threadIdx.x; e < C::kPiece / 4; e += kThreads) {
+  for (int e = threadIdx.x; e < C::kPiece / 4; e += C::kThreads) {
     const int r = e / (D / 4);
     Sum sum;
     bool open = false, outer = false;  // outer: the segment started before this CTA's range
-    auto end = [&](int2 seg, bool ended) {
-      const int h = seg.y / a.groups, row = (seg.y - h * a.groups) * C::kRows + r;
+    auto end = [&](int4 seg, bool ended) {
+      const int row = seg.z + r;
       const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
       if (!outer && ended) {
         if (row < a.G) {
-          const size_t at = (size_t)seg.x * hq + h * a.G + row;
+          const size_t at = (size_t)seg.x * hq + seg.y * a.G + row;
           *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
               make_uint2(pack_bf16(sum.o.x * inv, sum.o.y * inv), pack_bf16(sum.o.z * inv, sum.o.w * inv));
           if (a.lse && e % (D / 4) == 0) a.lse[at] = sum.lse();
@@ -581,28 +659,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(const DecodeAr
         reinterpret_cast<float4*>(a.o + at * C::kPiece)[e] =
             make_float4(sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
         if (e % (D / 4) == 0) a.ml[at * C::kRows + r] = make_float2(sum.m, sum.l);
-        if (!outer) rec = make_int4(seg.x, seg.y, (int)(((hi + s_rest) * n_ctas - 1) / total), rec.w);
+        if (!outer) rec = make_int4(seg.x, seg.y << 8 | seg.z / 8, (int)min(((hi + s_rest) * n_ctas - 1) / total, n_ctas - 1), rec.w);
       }
       open = false;
     };
-    int2 seg = make_int2(0, 0);
-    for (int w = 0; w < kWarps; ++w) {
-      const int2 f = s_flags[w];
-      if (f.x) {
+    int4 last = make_int4(0, 0, 0, 0);
+    for (int w = 0; w < W; ++w) {
+      const int4 way = s_seg[w][0], fin = s_seg[w][1];
+      if (way.w) {
         if (!open) sum = Sum(), outer = true;
-        const size_t at = (size_t)blockIdx.x * kWarps + w;
+        const size_t at = (size_t)blockIdx.x * W + w;
         sum.add(a.warp_ml[at * C::kRows + r], reinterpret_cast<const float4*>(a.warp_o + at * C::kPiece)[e]);
-        end(s_seg[w][0], true);
+        end(way, true);
       }
-      if (f.y) {
-        if (!open) sum = Sum(), outer = (f.y & 2) != 0, open = true;
-        seg = s_seg[w][1];
+      if (fin.w) {
+        if (!open) sum = Sum(), outer = (fin.w & 2) != 0, open = true;
         sum.add(z_ml[w * C::kRows + r], reinterpret_cast<const float4*>(z_o + w * C::kPiece)[e]);
-        if (f.y & 4) end(seg, true);
+        last = fin;
+        if (fin.w & 4) end(fin, true);
       }
     }
-    if (open) end(seg, false);
+    if (open) end(last, false);
   }
+  if (rec.w > 250) rec.z = -1;
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
@@ -621,12 +700,12 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
     for (int i = threadIdx.x; i < a.ctas; i += blockDim.x)
       if (const int e = a.rec[i].w) atomicMax(&s_err, e);
     __syncthreads();
-    if (threadIdx.x == 0) *a.status = Status{s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
+    if (threadIdx.x == 0) *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
   }
   const int4 rec = a.rec[blockIdx.x];
   if (rec.z < 0) return;
   const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4);
-  const int h = rec.y / a.groups, row = (rec.y - h * a.groups) * C::kRows + r;
+  const int h = rec.y >> 8, row = (rec.y & 255) * 8 + r;
   if (row >= a.G) return;
   Sum sum;
   for (int p0 = blockIdx.x; p0 <= rec.z; p0 += U) {
@@ -663,12 +742,47 @@ int check_decode(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8* c, bool mem
   return LMOE_OK;
 }
 
+// What a cache's copy descriptors depend on.
+void maps_key(const lmoe_kv_cache_fp8* c, uint64_t (&key)[8]) {
+  key[0] = reinterpret_cast<uintptr_t>(c->k);
+  key[1] = reinterpret_cast<uintptr_t>(c->v);
+  key[2] = (uint64_t)(uint32_t)c->n_blocks << 32 | (uint32_t)c->block_size;
+  key[3] = (uint64_t)(uint32_t)c->kv_heads << 32 | (uint32_t)c->head_dim;
+  key[4] = (uint64_t)c->block_stride;
+  key[5] = (uint64_t)c->head_stride;
+  key[6] = (uint64_t)c->slot_stride;
+  key[7] = 1;
+}
+
+// K and V as [block][head][slot][d], copied by a page, or by a tile's rows of one.
+int make_maps(const lmoe_kv_cache_fp8* c, lmoe_kv_maps_fp8* m) {
+  static_assert(sizeof(m->map[0]) == sizeof(CUtensorMap), "a map's size");
+  // a dimension of extent 1 never steps: any valid stride will do
+  auto stride = [](int64_t bytes, int64_t extent) { return (uint64_t)(extent > 1 ? bytes : 64); };
+  const uint64_t dims[4] = {(uint64_t)c->head_dim, (uint64_t)c->block_size, (uint64_t)c->kv_heads,
+                            (uint64_t)c->n_blocks};
+  const uint64_t strides[3] = {stride(c->slot_stride, c->block_size), stride(c->head_stride, c->kv_heads),
+                               stride(c->block_stride, c->n_blocks)};
+  const uint32_t box[4] = {(uint32_t)c->head_dim, (uint32_t)std::min(c->block_size, kTile), 1, 1};
+  for (int i = 0; i < 2; ++i) {
+    CUtensorMap t;
+    if (encode_tmap(&t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? c->v : c->k, dims, strides, box,
+                    c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return LMOE_ECUDA;
+    std::memcpy(m->map[i], &t, sizeof(t));
+  }
+  maps_key(c, m->made_for);
+  return LMOE_OK;
+}
+
 // Query heads of a kv head that one reading of its keys serves, in eights.
 int eights(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8* c) { return d->q_heads / c->kv_heads <= 8 ? 1 : 2; }
 
 struct DecodeWs {
   size_t rec, ml, o, warp_ml, warp_o, total;
 };
+
+constexpr int kMostWarps = 16;
 
 DecodeWs decode_ws(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8* c, int ctas) {
   const size_t rows = 8 * (size_t)eights(d, c), row = c->head_dim * sizeof(float);
@@ -682,19 +796,20 @@ DecodeWs decode_ws(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8* c, int ct
   w.rec = take(sizeof(int4) * ctas);
   w.ml = take(2 * ctas * rows * sizeof(float2));
   w.o = take(2 * ctas * rows * row);
-  w.warp_ml = take(kWarps * ctas * rows * sizeof(float2));
-  w.warp_o = take(kWarps * ctas * rows * row);
+  w.warp_ml = take(kMostWarps * ctas * rows * sizeof(float2));
+  w.warp_o = take(kMostWarps * ctas * rows * row);
   w.total = at;
   return w;
 }
 
 template <int D, int N8>
-int run_decode(const DecodeArgs& a, cudaStream_t s) {
+int run_decode(const DecodeArgs& a, const CUtensorMap (&tm)[2], cudaStream_t s) {
   using C = Cfg<D, N8>;
   static std::atomic<unsigned long long> done{0};
   int rc = allow_smem(done, decode_attn_kernel<D, N8>, C::kSmem);
   if (rc) return rc;
-  rc = launch_pdl("decode_attn_kernel", dim3(a.ctas), dim3(kThreads), C::kSmem, s, decode_attn_kernel<D, N8>, a);
+  rc = launch_pdl("decode_attn_kernel", dim3(a.ctas), dim3(C::kThreads), C::kSmem, s, decode_attn_kernel<D, N8>, a,
+                  tm[0], tm[1]);
   if (rc) return rc;
   constexpr int kUnits = C::kPiece / 4, kBlock = kUnits < 256 ? kUnits : 256;
   return launch_pdl("decode_merge_kernel", dim3(a.ctas, kUnits / kBlock), dim3(kBlock), 0, s,
@@ -708,6 +823,13 @@ int run_decode(const DecodeArgs& a, cudaStream_t s) {
 using namespace lmoe;
 
 extern "C" {
+
+int lmoe_kv_maps_fp8_init(const lmoe_kv_cache_fp8* cache, lmoe_kv_maps_fp8* maps) {
+  const int rc = check_cache_fp8(cache, true);
+  if (rc) return rc;
+  if (!maps) return LMOE_EINVAL;
+  return make_maps(cache, maps);
+}
 
 size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8* c) {
   if (check_decode(d, c, false) != LMOE_OK) return 0;
@@ -754,8 +876,17 @@ int lmoe_decode_attention_fp8(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8
   while ((1 << a.bs_shift) < c->block_size) ++a.bs_shift;
   a.ctas = di.sms;
   a.scale_log2 = d->scale * kLog2e;
-  if (c->head_dim == 64) return n8 == 1 ? run_decode<64, 1>(a, s) : run_decode<64, 2>(a, s);
-  return n8 == 1 ? run_decode<128, 1>(a, s) : run_decode<128, 2>(a, s);
+  lmoe_kv_maps_fp8 own;
+  const lmoe_kv_maps_fp8* maps = c->maps;
+  maps_key(c, own.made_for);
+  if (!maps || std::memcmp(maps->made_for, own.made_for, sizeof(own.made_for)) != 0) {
+    if ((rc = make_maps(c, &own))) return rc;
+    maps = &own;
+  }
+  CUtensorMap tm[2];
+  std::memcpy(tm, maps->map, sizeof(tm));
+  if (c->head_dim == 64) return n8 == 1 ? run_decode<64, 1>(a, tm, s) : run_decode<64, 2>(a, tm, s);
+  return n8 == 1 ? run_decode<128, 1>(a, tm, s) : run_decode<128, 2>(a, tm, s);
 }
 
 }  // extern "C"
