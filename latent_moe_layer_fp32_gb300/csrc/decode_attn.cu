@@ -109,6 +109,20 @@ struct Sum {
   __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 };
 
+// x / y; a 32-bit division where that is enough, as 64-bit ones take hundreds of clocks.
+__device__ __forceinline__ unsigned long long quot(unsigned long long x, unsigned long long y) {
+  return (x | y) >> 32 ? x / y : (unsigned long long)((unsigned)x / (unsigned)y);
+}
+
+// An even cut of n things into parts.
+struct Cut {
+  unsigned long long each, more;  // `more` parts have one more
+  __device__ __forceinline__ Cut(unsigned long long n, unsigned parts) : each(quot(n, parts)), more(n - each * parts) {}
+  __device__ __forceinline__ unsigned long long first(unsigned i) const {
+    return i * each + min((unsigned long long)i, more);
+  }
+};
+
 // The tiles of KT keys that a request's positions in sight take, and where the first one begins.
 template <int KT>
 struct Span {
@@ -160,7 +174,7 @@ struct Cfg {
   static constexpr int kRing = W * S * kStage;
   static constexpr int kPiece = kRows * D;  // floats of a piece's output
   static constexpr int kSmem = kRing + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
-  static_assert(W * (kPiece * 4 + kRows * 8) <= kRing, "the last pieces take the ring's place");
+  static_assert(kPiece * 4 <= S * kStage, "a warp's last piece takes its ring's place");
   static_assert(KT == 16 || KT == 32, "a lane a key");
 };
 
@@ -194,17 +208,22 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   __shared__ unsigned long long s_scan[W], s_at[W];
   __shared__ int s_b[W];
   __shared__ int4 s_seg[W][2];  // a warp's pieces, put down on the way and at its range's end: {request, head, group, flags}
-  __shared__ int s_rest, s_err;
+  __shared__ float2 s_ml[W][C::kRows];
+  __shared__ int s_last, s_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hq = a.c.kv_heads * a.G;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) s_err = s_rest = 0;
+  if (threadIdx.x == 0) s_err = s_last = 0;
+  if (lane < 2) s_seg[warp][lane] = make_int4(0, 0, 0, 0);
+  auto piece_at = [&](int w) { return reinterpret_cast<float*>(s_ring + w * C::S * C::kStage); };
   if (lane < C::S) mbar_init(&s_full[warp][lane], 1);
   fence_barrier_init();
 
   // ---- the line of tiles, and this warp's part of it ----
-  unsigned long long total, n_ctas, hi;
+  unsigned long long total, hi;
+  unsigned n_ctas;
+  bool at_end;  // the range is not empty and ends with the CTA's
   long long todo;
   {
     const int run = (a.B + C::kThreads - 1) / C::kThreads, b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
@@ -234,11 +253,21 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     }
     if (bad) atomicCAS(&s_err, 0, 241);
     // as many CTAs as have a tile for each warp
-    n_ctas = min((unsigned long long)a.ctas, (total + W - 1) / W);
-    const unsigned long long c = blockIdx.x, lo = c < n_ctas ? total * c / n_ctas : total;
-    hi = c < n_ctas ? total * (c + 1) / n_ctas : total;
+    n_ctas = (unsigned)min((unsigned long long)a.ctas, (total + W - 1) / W);
+    const unsigned c = blockIdx.x;
+    unsigned long long lo = total;
+    hi = total;
+    if (c < n_ctas) {
+      const Cut ctas(total, n_ctas);
+      lo = ctas.first(c);
+      hi = ctas.first(c + 1);
+    }
+    const Cut warps(hi - lo, W);
+    todo = (long long)(warps.each + ((unsigned)warp < warps.more));
+    at_end = todo > 0 && lo + warps.first(warp + 1) == hi;
+    unsigned long long at = lo;
+#pragma unroll 1
     for (int w = 0; w < W; ++w) {
-      const unsigned long long at = lo + (hi - lo) * w / W;
       if (at >= before && at < before + mine) {
         unsigned long long skip = at - before;
         int b = b0;
@@ -250,8 +279,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
         s_b[w] = b;
         s_at[w] = skip;
       }
+      at += warps.each + ((unsigned)w < warps.more);
     }
-    todo = (long long)((hi - lo) * (warp + 1) / W - (hi - lo) * warp / W);
   }
   // requests without positions
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -269,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     walk.b = s_b[warp];
     walk.s = span_of<KT>(a, a.lens[walk.b]);
     const unsigned long long at = s_at[warp];
-    const int seg = (int)(at / (unsigned)walk.s.n);
+    const int seg = (int)quot(at, walk.s.n);
     walk.tile = (int)(at - (unsigned long long)seg * walk.s.n);
     walk.h = seg / a.groups;
     walk.group = seg - walk.h * a.groups;
@@ -373,32 +402,10 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   uint32_t qf[N8][D / 16][2];  // the queries' fragments, as f16 times a power of two of each row's
   float q_scale[N8][2];        // what makes a product with them a score to base 2, for this lane's two columns
   float o[C::kChunks][N8][4], M[N8][2], Mo[N8][2], L[N8][2];
-  // this warp's pieces, put down on the way (x) and at its range's end (y): 1 there is one, 2 its segment started
-  // before the range, 4 it ended
-  int2 flags = make_int2(0, 0);
   int stage = 0;
   bool fresh = true, whole = false;  // the segment has no tile here yet; its first tile is in this range
   // this lane's row of a 16-key matrix pair, and its half of two pieces
   const uint32_t lane_at = (lane & 15) * D + (((lane >> 4) ^ swizzle<D>(lane & 15)) << 4);
-
-  // the accumulators as outputs: put(row, column, the value and the next column's), and sums(row, M, L)
-  auto results = [&](auto&& put, auto&& sums) {
-#pragma unroll
-    for (int n = 0; n < N8; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float sum = L[n][j];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        // O 2^(Mo - M - kShift) / L; the power in two halves, each in range
-        const float f = M[n][j] == -INFINITY ? 0.f : ex2(0.5f * (Mo[n][j] - M[n][j] - kShift));
-        const float f2 = sum == 0.f ? 0.f : f / sum;
-        const int r = n * 8 + 2 * t + j;
-        if (g == 0) sums(r, M[n][j], sum);
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) put(r, c * 16 + 2 * g, o[c][n][j] * f * f2, o[c][n][2 + j] * f * f2);
-      }
-  };
 
   bool ok = true;
   while (walk.left > 0) {
@@ -592,28 +599,47 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     });
 
     // ---- the segment's end, or the range's ----
-    if (last && whole) {
-      results(
-          [&](int r, int col, float x, float y) {
-            if (r < rows)
-              *reinterpret_cast<uint32_t*>(a.out + ((size_t)walk.b * hq + h * a.G + row0 + r) * D + col) = pack_bf16(x, y);
-          },
-          [&](int r, float m, float l) {
-            if (r < rows && a.lse)
-              a.lse[(size_t)walk.b * hq + h * a.G + row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-          });
-    } else if (last && walk.left > 1) {  // started before this range: a piece
-      const size_t at = (size_t)blockIdx.x * W + warp;
-      results([&](int r, int col, float x, float y) {
-        *reinterpret_cast<float2*>(a.warp_o + at * C::kPiece + r * D + col) = make_float2(x, y);
-      }, [&](int r, float m, float l) { a.warp_ml[at * C::kRows + r] = make_float2(m, l); });
-      flags.x = 1 | 2 | 4;
-      if (lane == 0) s_seg[warp][0] = make_int4(walk.b, h, row0, 0);
-    } else if (walk.left == 1) {
-      flags.y = 1 | (whole ? 0 : 2) | (last ? 4 : 0);
-      if (lane == 0) {
-        s_seg[warp][1] = make_int4(walk.b, h, row0, 0);
-        if (warp == W - 1) s_rest = walk.s.n - 1 - walk.tile;
+    if (last || walk.left == 1) {
+      const bool done = last && whole, on_way = last && walk.left > 1;
+      // a piece: its columns in fp32 (in the ring, whose every tile has been used, unless the range goes on), and
+      // each row's maximum and sum
+      float* const po = on_way ? a.warp_o + ((size_t)blockIdx.x * W + warp) * C::kPiece : piece_at(warp);
+      float2* const ml = on_way ? a.warp_ml + ((size_t)blockIdx.x * W + warp) * C::kRows : s_ml[warp];
+      const size_t first_row = (size_t)walk.b * hq + h * a.G + row0;
+#pragma unroll
+      for (int n = 0; n < N8; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float sum = L[n][j];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          // O 2^(Mo - M - kShift) / L; the power in two halves, each in range
+          const float f = M[n][j] == -INFINITY ? 0.f : ex2(0.5f * (Mo[n][j] - M[n][j] - kShift));
+          const float f2 = sum == 0.f ? 0.f : f / sum;
+          const int r = n * 8 + 2 * t + j;
+          if (!done) {
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              *reinterpret_cast<float2*>(po + r * D + c * 16 + 2 * g) =
+                  make_float2(o[c][n][j] * f * f2, o[c][n][2 + j] * f * f2);
+            if (g == 0) ml[r] = make_float2(M[n][j], sum);
+          } else if (r < rows) {
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              *reinterpret_cast<uint32_t*>(a.out + (first_row + r) * D + c * 16 + 2 * g) =
+                  pack_bf16(o[c][n][j] * f * f2, o[c][n][2 + j] * f * f2);
+            if (a.lse && g == 0) a.lse[first_row + r] = sum == 0.f ? -INFINITY : (M[n][j] + log2f(sum)) * kLn2;
+          }
+        }
+      if (!done && lane == 0) {
+        // 1 there is one, 2 its segment started before the range, 4 it ended in it
+        s_seg[warp][on_way ? 0 : 1] = make_int4(walk.b, h, row0, 1 | (whole ? 0 : 2) | (last ? 4 : 0));
+        if (at_end && !last) {  // the CTA that the segment ends in
+          const unsigned long long end = hi + (unsigned)(walk.s.n - 2 - walk.tile);
+          const Cut ctas(total, n_ctas);
+          const unsigned long long big = ctas.more * (ctas.each + 1);
+          s_last = (int)(end < big ? quot(end, ctas.each + 1) : ctas.more + quot(end - big, ctas.each));
+        }
       }
     }
     fresh = last;
@@ -627,59 +653,59 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     for (int i = 0; i < C::S; ++i)
       if (bulk >> i & 1) mbar_wait(&s_full[warp][i], parity >> i & 1, nullptr, 0);
   }
-  __syncthreads();  // the ring's place is free
-  float* const z_o = reinterpret_cast<float*>(s_ring);
-  float2* const z_ml = reinterpret_cast<float2*>(z_o + W * C::kPiece);
-  if (flags.y)
-    results([&](int r, int col, float x, float y) {
-      *reinterpret_cast<float2*>(z_o + warp * C::kPiece + r * D + col) = make_float2(x, y);
-    }, [&](int r, float m, float l) { z_ml[warp * C::kRows + r] = make_float2(m, l); });
-  if (lane == 0) {
-    s_seg[warp][0].w = flags.x;
-    s_seg[warp][1].w = flags.y;
-  }
   __syncthreads();
   int4 rec = make_int4(0, 0, -1, s_err);
+  // pieces by warps, two bits a warp: put down on the way, at the range's end.  One that was put down on the way ends
+  // its segment; so a segment's pieces are those of a run of warps' ends, and perhaps one on the next one's way.
+  const int what = lane < 2 * W ? s_seg[lane >> 1][lane & 1].w : 0;
+  const unsigned there = __ballot_sync(0xffffffffu, what != 0), ends = __ballot_sync(0xffffffffu, (what & 4) != 0);
   for (int e = threadIdx.x; e < C::kPiece / 4; e += C::kThreads) {
     const int r = e / (D / 4);
-    Sum sum;
-    bool open = false, outer = false;  // outer: the segment started before this CTA's range
-    auto end = [&](int4 seg, bool ended) {
-      const int row = seg.z + r;
-      const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+    unsigned left = there;
+#pragma unroll 1
+    while (left) {
+      const int i0 = __ffs(left) - 1, i1 = ends & left ? __ffs(ends & left) - 1 : 31 - __clz(left);
+      left &= ~0u << i1 << 1;
+      const int w0 = i0 >> 1, w1 = (i1 - 1) >> 1;  // whose ends' pieces they are (none, if w1 < w0)
+      const bool way = (i1 & 1) == 0;
+      const int4 seg = s_seg[i0 >> 1][i0 & 1];
+      const bool outer = (seg.w & 2) != 0, ended = ends >> i1 & 1;  // outer: it started before this CTA's range
+      float2 way_ml = make_float2(-INFINITY, 0.f);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (way) {
+        const size_t at = (size_t)blockIdx.x * W + (i1 >> 1);
+        way_ml = a.warp_ml[at * C::kRows + r];
+        acc = reinterpret_cast<const float4*>(a.warp_o + at * C::kPiece)[e];
+      }
+      float m = way_ml.x;
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w) m = fmaxf(m, s_ml[w][r].x);
+      const float mu = m == -INFINITY ? 0.f : m;
+      float l = ex2(way_ml.x - mu) * way_ml.y;
+      acc = make_float4(acc.x * l, acc.y * l, acc.z * l, acc.w * l);
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w) {
+        const float2 ml = s_ml[w][r];
+        const float4 x = reinterpret_cast<const float4*>(piece_at(w))[e];
+        const float f = ex2(ml.x - mu) * ml.y;
+        l += f;
+        acc = make_float4(fmaf(f, x.x, acc.x), fmaf(f, x.y, acc.y), fmaf(f, x.z, acc.z), fmaf(f, x.w, acc.w));
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float4 x = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (!outer && ended) {
-        if (row < a.G) {
-          const size_t at = (size_t)seg.x * hq + seg.y * a.G + row;
-          *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
-              make_uint2(pack_bf16(sum.o.x * inv, sum.o.y * inv), pack_bf16(sum.o.z * inv, sum.o.w * inv));
-          if (a.lse && e % (D / 4) == 0) a.lse[at] = sum.lse();
+        if (seg.z + r < a.G) {
+          const size_t at = (size_t)seg.x * hq + seg.y * a.G + seg.z + r;
+          *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+          if (a.lse && e % (D / 4) == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
       } else {
         const size_t at = (size_t)blockIdx.x * 2 + !outer;
-        reinterpret_cast<float4*>(a.o + at * C::kPiece)[e] =
-            make_float4(sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
-        if (e % (D / 4) == 0) a.ml[at * C::kRows + r] = make_float2(sum.m, sum.l);
-        if (!outer) rec = make_int4(seg.x, seg.y << 8 | seg.z / 8, (int)min(((hi + s_rest) * n_ctas - 1) / total, n_ctas - 1), rec.w);
-      }
-      open = false;
-    };
-    int4 last = make_int4(0, 0, 0, 0);
-    for (int w = 0; w < W; ++w) {
-      const int4 way = s_seg[w][0], fin = s_seg[w][1];
-      if (way.w) {
-        if (!open) sum = Sum(), outer = true;
-        const size_t at = (size_t)blockIdx.x * W + w;
-        sum.add(a.warp_ml[at * C::kRows + r], reinterpret_cast<const float4*>(a.warp_o + at * C::kPiece)[e]);
-        end(way, true);
-      }
-      if (fin.w) {
-        if (!open) sum = Sum(), outer = (fin.w & 2) != 0, open = true;
-        sum.add(z_ml[w * C::kRows + r], reinterpret_cast<const float4*>(z_o + w * C::kPiece)[e]);
-        last = fin;
-        if (fin.w & 4) end(fin, true);
+        reinterpret_cast<float4*>(a.o + at * C::kPiece)[e] = x;
+        if (e % (D / 4) == 0) a.ml[at * C::kRows + r] = make_float2(m, l);
+        if (!outer) rec = make_int4(seg.x, seg.y << 8 | seg.z / 8, s_last, rec.w);
       }
     }
-    if (open) end(last, false);
   }
   if (rec.w > 250) rec.z = -1;
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
@@ -702,22 +728,25 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
     __syncthreads();
     if (threadIdx.x == 0) *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
   }
-  const int4 rec = a.rec[blockIdx.x];
-  if (rec.z < 0) return;
   const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4);
-  const int h = rec.y >> 8, row = (rec.y & 255) * 8 + r;
-  if (row >= a.G) return;
-  Sum sum;
-  for (int p0 = blockIdx.x; p0 <= rec.z; p0 += U) {
-    float2 ml[U];
-    float4 o[U];
+  float2 ml[U];
+  float4 o[U];
+  auto fetch = [&](int p0, int end) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int p = min(p0 + u, rec.z);
+      const int p = min(p0 + u, end);
       const size_t at = (size_t)p * 2 + (p == (int)blockIdx.x);
       ml[u] = a.ml[at * C::kRows + r];
       o[u] = reinterpret_cast<const float4*>(a.o + at * C::kPiece)[e];
     }
+  };
+  fetch(blockIdx.x, a.ctas - 1);  // (before it is known how many there are, or whether any)
+  const int4 rec = a.rec[blockIdx.x];
+  const int h = rec.y >> 8, row = (rec.y & 255) * 8 + r;
+  if (rec.z < 0 || row >= a.G) return;
+  Sum sum;
+  for (int p0 = blockIdx.x; p0 <= rec.z; p0 += U) {
+    if (p0 > (int)blockIdx.x) fetch(p0, rec.z);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (p0 + u <= rec.z) sum.add(ml[u], o[u]);
