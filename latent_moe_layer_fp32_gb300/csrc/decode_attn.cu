@@ -17,6 +17,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 constexpr int kTile = 32;        // keys of a tile
+constexpr int kEnd = 3;          // what a segment's end costs, in tiles
 constexpr float kShift = 14.f;   // P stands in f16 as p * 2^14, see below
 
 struct DecodeArgs {
@@ -141,16 +142,20 @@ __device__ __forceinline__ Span<KT> span_of(const DecodeArgs& a, int len) {
 }
 
 // A warp's walk over the line of tiles: request by request, in it key head by key head, in it group by group of
-// query rows.
+// query rows.  Behind each of these segments the line has room for what its end costs, as many tiles as `end`.
 template <int KT>
 struct Walk {
-  int b, h, group, tile;
+  int b, h, group, tile, end;
   Span<KT> s;
-  long long left;
+  long long left;  // of the range, from the tile on
 
+  __device__ __forceinline__ bool last() const { return tile == s.n - 1; }  // of its segment
+  __device__ __forceinline__ long long after() const { return left - (last() ? 1 + end : 1); }
   __device__ __forceinline__ void next(const DecodeArgs& a) {
-    if (--left <= 0) return;
-    if (++tile < s.n) return;
+    left = after();
+    if (++tile >= s.n && left > 0) segment(a);
+  }
+  __device__ __forceinline__ void segment(const DecodeArgs& a) {
     tile = 0;
     if (++group < a.groups) return;
     group = 0;
@@ -158,7 +163,7 @@ struct Walk {
     h = 0;
     do {
       s = span_of<KT>(a, a.lens[++b]);
-    } while (s.n == 0);  // (there are tiles left, so there is such a request)
+    } while (s.n == 0);  // (there is something left of the range, so there is such a request)
   }
 };
 
@@ -206,6 +211,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   __shared__ float4 s_key[W][KT];  // of a tile's keys: the key's scale, 0 or -infinity, the value's exponent
   __shared__ __align__(16) uint8_t s_scale[W][C::S][2 * KT];  // of the ring's tiles: K's, V's
   __shared__ unsigned long long s_scan[W], s_at[W];
+  __shared__ unsigned s_live[W];
   __shared__ int s_b[W];
   __shared__ int4 s_seg[W][2];  // a warp's pieces, put down on the way and at its range's end: {request, head, group, flags}
   __shared__ float2 s_ml[W][C::kRows];
@@ -223,37 +229,50 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   // ---- the line of tiles, and this warp's part of it ----
   unsigned long long total, hi;
   unsigned n_ctas;
-  bool at_end;  // the range is not empty and ends with the CTA's
-  long long todo;
+  Walk<KT> walk;
+  bool at_end;  // this warp's range ends with the CTA's
   {
     const int run = (a.B + C::kThreads - 1) / C::kThreads, b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
     const unsigned segs = (unsigned)(a.c.kv_heads * a.groups);
-    unsigned long long mine = 0;
+    unsigned long long tiles = 0;
+    unsigned live = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const int len = a.lens[b];
       const Span<KT> s = span_of<KT>(a, len);
       bad |= len != 0 && s.n == 0;
-      mine += s.n;
+      tiles += s.n;
+      live += s.n != 0;
     }
-    mine *= segs;
-    unsigned long long x = mine;
+    unsigned long long x = tiles;
+    unsigned y = live;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const unsigned long long x1 = __shfl_up_sync(0xffffffffu, x, o);
+      const unsigned y1 = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) x += x1, y += y1;
     }
-    if (lane == 31) s_scan[warp] = x;
+    if (lane == 31) {
+      s_scan[warp] = x;
+      s_live[warp] = y;
+    }
     __syncthreads();
-    unsigned long long before = x - mine;
-    total = 0;
+    unsigned long long tiles_before = x - tiles, all = 0;
+    unsigned live_before = y - live, all_live = 0;
     for (int w = 0; w < W; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
+      if (w < warp) tiles_before += s_scan[w], live_before += s_live[w];
+      all += s_scan[w];
+      all_live += s_live[w];
     }
     if (bad) atomicCAS(&s_err, 0, 241);
+    all *= segs;
+    // what a segment's end weighs: no more than a warp has tiles
+    walk.end = (int)min((unsigned long long)kEnd, quot(all, (unsigned)(a.ctas * W)));
+    total = all + (unsigned long long)all_live * segs * walk.end;
+    const unsigned long long before = tiles_before * segs + (unsigned long long)live_before * segs * walk.end;
+    const unsigned long long mine = tiles * segs + (unsigned long long)live * segs * walk.end;
     // as many CTAs as have a tile for each warp
-    n_ctas = (unsigned)min((unsigned long long)a.ctas, (total + W - 1) / W);
+    n_ctas = (unsigned)min((unsigned long long)a.ctas, (all + W - 1) / W);
     const unsigned c = blockIdx.x;
     unsigned long long lo = total;
     hi = total;
@@ -263,8 +282,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
       hi = ctas.first(c + 1);
     }
     const Cut warps(hi - lo, W);
-    todo = (long long)(warps.each + ((unsigned)warp < warps.more));
-    at_end = todo > 0 && lo + warps.first(warp + 1) == hi;
+    walk.left = (long long)(warps.each + ((unsigned)warp < warps.more));
+    at_end = lo + warps.first(warp + 1) == hi;
     unsigned long long at = lo;
 #pragma unroll 1
     for (int w = 0; w < W; ++w) {
@@ -272,7 +291,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
         unsigned long long skip = at - before;
         int b = b0;
         for (;; ++b) {
-          const unsigned long long there = (unsigned long long)span_of<KT>(a, a.lens[b]).n * segs;
+          const int n = span_of<KT>(a, a.lens[b]).n;
+          const unsigned long long there = n ? (unsigned long long)(n + walk.end) * segs : 0;
           if (skip < there) break;
           skip -= there;
         }
@@ -292,16 +312,18 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   }
   __syncthreads();
 
-  Walk<KT> walk;
-  walk.left = todo;
-  if (todo > 0) {
+  if (walk.left > 0) {
     walk.b = s_b[warp];
     walk.s = span_of<KT>(a, a.lens[walk.b]);
     const unsigned long long at = s_at[warp];
-    const int seg = (int)quot(at, walk.s.n);
-    walk.tile = (int)(at - (unsigned long long)seg * walk.s.n);
+    const int size = walk.s.n + walk.end, seg = (int)quot(at, size);
+    walk.tile = (int)(at - (unsigned long long)seg * size);
     walk.h = seg / a.groups;
     walk.group = seg - walk.h * a.groups;
+    if (walk.tile >= walk.s.n) {  // behind a segment's tiles
+      walk.left -= size - walk.tile;
+      if (walk.left > 0) walk.segment(a);
+    }
   }
   Walk<KT> ahead = walk;  // walks in front and looks pages up
   const uint32_t ring32 = smem_u32(s_ring + warp * C::S * C::kStage), scale32 = smem_u32(s_scale[warp]);
@@ -318,6 +340,12 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     look_lo = max(ahead.s.lo - p0, 0);
     look_hi = min(ahead.s.len - p0, KT);
     look_h = ahead.h;
+    if (ahead.tile == 0) {  // its segment's queries will be wanted soon: 128 bytes a lane
+      const int r = ahead.group * C::kRows + lane * 64 / D;
+      if (r < a.G && lane * 64 < C::kPiece)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + (long long)ahead.b * a.qs +
+                                                      (size_t)(ahead.h * a.G + r) * D + lane * 64 % D));
+    }
     look_in = p0;
     const int p = min(max(p0 + (lane & (KT - 16)), p0 + look_lo), p0 + look_hi - 1);
     page = a.table[(size_t)ahead.b * a.max_blocks + (p >> a.bs_shift)];
@@ -409,6 +437,19 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
 
   bool ok = true;
   while (walk.left > 0) {
+    const int h = walk.h, row0 = walk.group * C::kRows;  // rows of the head's G
+    const int rows = min(C::kRows, a.G - row0);
+    uint2 w[N8][C::kChunks];
+    if (fresh) {  // the segment's queries, on their way while its first tile is waited for
+#pragma unroll
+      for (int n = 0; n < N8; ++n) {
+        const int r = n * 8 + g;
+        const uint16_t* const src = a.q + (long long)walk.b * a.qs + (size_t)(h * a.G + row0 + r) * D + t * 4;
+#pragma unroll
+        for (int i = 0; i < C::kChunks; ++i)
+          w[n][i] = r < rows ? *reinterpret_cast<const uint2*>(src + i * 16) : make_uint2(0, 0);
+      }
+    }
     copies_wait<C::S - 2>();
     if (bulk >> stage & 1) {
       // (one answer for the whole warp)
@@ -419,7 +460,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     }
     __syncwarp();
     const uint32_t st32 = ring32 + stage * C::kStage + lane_at;
-    const bool last = walk.tile == walk.s.n - 1;
+    const bool last = walk.last(), final = walk.after() <= 0;  // of the segment, of the range
     if (lane < KT) {
       const uint32_t kb = s_scale[warp][stage][lane], vb = s_scale[warp][stage][KT + lane];
       float4 key = make_float4(e8m0_to_f32(kb), 0.f, vb == 255 ? NAN : (float)vb - 127.f, 0.f);
@@ -437,22 +478,15 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     }
     copies_end();
     stage = stage == C::S - 1 ? 0 : stage + 1;
-    const int h = walk.h, row0 = walk.group * C::kRows;  // rows of the head's G
-    const int rows = min(C::kRows, a.G - row0);
     if (fresh) {
       fresh = false;
       whole = walk.tile == 0;
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
-        const int r = n * 8 + g;
-        const uint16_t* const src = a.q + (long long)walk.b * a.qs + (size_t)(h * a.G + row0 + r) * D + t * 4;
-        uint2 w[C::kChunks];
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < C::kChunks; ++i) {
-          w[i] = r < rows ? *reinterpret_cast<const uint2*>(src + i * 16) : make_uint2(0, 0);
-          top = __vmaxu2(top, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
-        }
+        for (int i = 0; i < C::kChunks; ++i)
+          top = __vmaxu2(top, __vmaxu2(w[n][i].x & 0x7fff7fffu, w[n][i].y & 0x7fff7fffu));
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
         const float up = ldexpf(1.f, e);
 #pragma unroll
         for (int i = 0; i < C::kChunks; ++i) {
-          const uint32_t x[2] = {w[i].x, w[i].y};
+          const uint32_t x[2] = {w[n][i].x, w[n][i].y};
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             const __half2 hv = __floats2half2_rn(__uint_as_float(x[m] << 16) * up,
@@ -599,8 +633,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     });
 
     // ---- the segment's end, or the range's ----
-    if (last || walk.left == 1) {
-      const bool done = last && whole, on_way = last && walk.left > 1;
+    if (last || final) {
+      const bool done = last && whole, on_way = last && !final;
       // a piece: its columns in fp32 (in the ring, whose every tile has been used, unless the range goes on), and
       // each row's maximum and sum
       float* const po = on_way ? a.warp_o + ((size_t)blockIdx.x * W + warp) * C::kPiece : piece_at(warp);
@@ -635,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
         // 1 there is one, 2 its segment started before the range, 4 it ended in it
         s_seg[warp][on_way ? 0 : 1] = make_int4(walk.b, h, row0, 1 | (whole ? 0 : 2) | (last ? 4 : 0));
         if (at_end && !last) {  // the CTA that the segment ends in
-          const unsigned long long end = hi + (unsigned)(walk.s.n - 2 - walk.tile);
+          const unsigned long long end = hi - walk.left + (unsigned)(walk.s.n - 1 - walk.tile);
           const Cut ctas(total, n_ctas);
           const unsigned long long big = ctas.more * (ctas.each + 1);
           s_last = (int)(end < big ? quot(end, ctas.each + 1) : ctas.more + quot(end - big, ctas.each));
