@@ -16,7 +16,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-constexpr int kTile = 32;        // keys of a tile
 constexpr int kEnd = 3;          // what a segment's end costs, in tiles
 constexpr float kShift = 14.f;   // P stands in f16 as p * 2^14, see below
 
@@ -95,6 +94,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two fp32 values in one register pair.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 apart(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Pieces of a row joined: maximum, sum, and the outputs (of four columns) times it.
 struct Sum {
   float m = -INFINITY, l = 0.f;
@@ -170,7 +197,7 @@ struct Walk {
 // N8: groups of eight query rows that a key's codes are used for; W warps; S tiles of KT keys in a warp's ring.
 template <int D, int N8>
 struct Cfg {
-  static constexpr int W = N8 == 1 ? 12 : 8, KT = kTile, S = N8 == 1 ? 2 : 3;
+  static constexpr int W = D == 128 || N8 == 2 ? 8 : 12, KT = 4096 / D, S = D == 128 || N8 == 2 ? 3 : 2;
   static constexpr int kThreads = 32 * W;
   static constexpr int kRows = 8 * N8;
   static constexpr int kChunks = D / 16;  // 16-byte pieces of a row
@@ -180,7 +207,7 @@ struct Cfg {
   static constexpr int kPiece = kRows * D;  // floats of a piece's output
   static constexpr int kSmem = kRing + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
   static_assert(kPiece * 4 <= S * kStage, "a warp's last piece takes its ring's place");
-  static_assert(KT == 16 || KT == 32, "a lane a key");
+  static_assert(KT == 32 || KT == 64, "whole warps of keys");
 };
 
 // The 16-byte piece c of a tile's row r stands at r * D + ((c ^ swizzle(r)) << 4): the eight rows of one 8x8 matrix
@@ -329,7 +356,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   const uint32_t ring32 = smem_u32(s_ring + warp * C::S * C::kStage), scale32 = smem_u32(s_scale[warp]);
 
   // ---- a tile's way: its pages are looked up, its rows copied, its products formed ----
-  int page = 0;  // block number of the page that holds this lane's half of the looked-up tile
+  constexpr int kLanes = 32 / MT;  // a group of lanes for each 16 keys
+  int page = 0;                    // block number of the page that holds this lane's 16 keys of the looked-up tile
   int look_h = 0, look_in = 0, look_lo = 0, look_hi = 0;
   bool looked = false;
   int to_stage = 0;
@@ -347,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
                                                       (size_t)(ahead.h * a.G + r) * D + lane * 64 % D));
     }
     look_in = p0;
-    const int p = min(max(p0 + (lane & (KT - 16)), p0 + look_lo), p0 + look_hi - 1);
+    const int p = min(max(p0 + lane / kLanes * 16, p0 + look_lo), p0 + look_hi - 1);
     page = a.table[(size_t)ahead.b * a.max_blocks + (p >> a.bs_shift)];
     ahead.next(a);
   };
@@ -374,8 +402,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
       uint64_t* const bar = &s_full[warp][to_stage];
       if (lane == 0) mbar_arrive_expect_tx(bar, C::kStage);
       __syncwarp();
-      const int r = (lane & 16);
-      if ((lane & 15) == 0 && r < KT && (r == 0 || box == 16)) {
+      const int r = lane / kLanes * 16;
+      if (lane % kLanes == 0 && r % box == 0) {
         const int in = (look_in + r) & mask;
         uint8_t* const dst = s_ring + (to - smem_u32(s_ring)) + r * D;
         tma_load_4d(dst, &k_map, 0, in, look_h, page, bar, once);
@@ -384,30 +412,30 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     } else {
       by_lanes |= bit;
       const uint32_t dst = to + lane_to, dst2 = kStep == 4 ? dst ^ 64 : dst;
-      unrolled<MT>([&](auto half) {
-        constexpr int kHalf = half * 16 * D;
-        int block = __shfl_sync(0xffffffffu, page, half * 16);
-        int lo = look_lo - half * 16, n = look_hi - look_lo;  // rows in sight, from the half's first
+      unrolled<MT>([&](auto part) {
+        constexpr int kPart = part * 16 * D;
+        int block = __shfl_sync(0xffffffffu, page, part * kLanes);
+        int lo = look_lo - part * 16, n = look_hi - look_lo;  // rows in sight, from the part's first
         if (block < 0 || block >= a.c.n_blocks) {
           if (lane == 0 && lo < 16 && lo + n > 0) atomicCAS(&s_err, 0, 242);
           block = 0;
           n = 0;
         }
         const size_t off = (size_t)block * a.c.block_stride + (size_t)look_h * a.c.head_stride +
-                           (size_t)((look_in + half * 16) & mask) * a.c.slot_stride + lane_off;
+                           (size_t)((look_in + part * 16) & mask) * a.c.slot_stride + lane_off;
         const uint8_t *kp = a.c.k + off, *vp = a.c.v + off;
         unrolled<16 / kStep>([&](auto i) {
           const uint32_t bytes = (unsigned)(i * kStep + row - lo) < (unsigned)n ? 16 : 0;
-          copy16<kHalf + i * kStep * D>(i % 2 ? dst2 : dst, bytes ? kp : a.c.k, bytes);
-          copy16<kHalf + i * kStep * D + C::kCodes>(i % 2 ? dst2 : dst, bytes ? vp : a.c.v, bytes);
+          copy16<kPart + i * kStep * D>(i % 2 ? dst2 : dst, bytes ? kp : a.c.k, bytes);
+          copy16<kPart + i * kStep * D + C::kCodes>(i % 2 ? dst2 : dst, bytes ? vp : a.c.v, bytes);
           kp += step;
           vp += step;
         });
       });
     }
-    // four scale bytes a lane: eight lanes for each half, the first four K
-    const int half = lane >> 3 & 1, r = half * 16 + (lane & 3) * 4;
-    const int block = __shfl_sync(0xffffffffu, page, half * 16);
+    // four scale bytes a lane: eight lanes for each 16 keys, the first four K
+    const int part = (lane >> 3) & (MT - 1), r = part * 16 + (lane & 3) * 4;
+    const int block = __shfl_sync(0xffffffffu, page, part * kLanes);
     if (lane < KT / 2) {
       const uint32_t bytes = r + 4 > look_lo && r < look_hi && (unsigned)block < (unsigned)a.c.n_blocks ? 4 : 0;
       const size_t from =
@@ -461,14 +489,15 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     __syncwarp();
     const uint32_t st32 = ring32 + stage * C::kStage + lane_at;
     const bool last = walk.last(), final = walk.after() <= 0;  // of the segment, of the range
-    if (lane < KT) {
-      const uint32_t kb = s_scale[warp][stage][lane], vb = s_scale[warp][stage][KT + lane];
+#pragma unroll
+    for (int i = lane; i < KT; i += 32) {
+      const uint32_t kb = s_scale[warp][stage][i], vb = s_scale[warp][stage][KT + i];
       float4 key = make_float4(e8m0_to_f32(kb), 0.f, vb == 255 ? NAN : (float)vb - 127.f, 0.f);
       if (last || walk.tile == 0) {
-        const int p = walk.s.p0(walk.tile) + lane;
+        const int p = walk.s.p0(walk.tile) + i;
         if (p < walk.s.lo || (unsigned)p >= (unsigned)walk.s.len) key = make_float4(0.f, -INFINITY, 0.f, 0.f);
       }
-      s_key[warp][lane] = key;
+      s_key[warp][i] = key;
     }
     __syncwarp();
     // (the ring's oldest place is free: its tile was computed before the last __syncwarp)
@@ -543,14 +572,14 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float4 key = s_key[warp][mt * 16 + k * 8 + g];
+        const Pair ks = pair(key.x, key.x), see = pair(key.y, key.y), vs = pair(key.z, key.z);
 #pragma unroll
-        for (int n = 0; n < N8; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float& x = s[mt][n][k * 2 + j];
-            x = fmaf(x * q_scale[n][j], key.x, key.y);
-            so[mt][n][k * 2 + j] = x + key.z;
-          }
+        for (int n = 0; n < N8; ++n) {
+          float *const x = &s[mt][n][k * 2], *const y = &so[mt][n][k * 2];
+          const Pair p = fma2(mul2(pair(x[0], x[1]), pair(q_scale[n][0], q_scale[n][1])), ks, see);
+          const float2 u = apart(p), v = apart(add2(p, vs));
+          x[0] = u.x, x[1] = u.y, y[0] = v.x, y[1] = v.y;
+        }
       }
     // ---- running maxima ----
     bool more = false;
@@ -597,22 +626,24 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
       float mu[2], mo[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        mu[j] = M[n][j] == -INFINITY ? 0.f : M[n][j];
-        mo[j] = (Mo[n][j] == -INFINITY ? 0.f : Mo[n][j]) - kShift;
+        mu[j] = M[n][j] == -INFINITY ? 0.f : -M[n][j];
+        mo[j] = kShift - (Mo[n][j] == -INFINITY ? 0.f : Mo[n][j]);
       }
+      const Pair mu2 = pair(mu[0], mu[1]), mo2 = pair(mo[0], mo[1]);
+      Pair sum = pair(L[n][0], L[n][1]);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float p[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            L[n][j] += ex2(s[mt][n][k * 2 + j] - mu[j]);
-            p[j] = ex2(so[mt][n][k * 2 + j] - mo[j]);
-          }
-          const __half2 hv = __floats2half2_rn(p[0], p[1]);
+          const float *const x = &s[mt][n][k * 2], *const y = &so[mt][n][k * 2];
+          const float2 u = apart(add2(pair(x[0], x[1]), mu2)), v = apart(add2(pair(y[0], y[1]), mo2));
+          sum = add2(sum, pair(ex2(u.x), ex2(u.y)));
+          const __half2 hv = __floats2half2_rn(ex2(v.x), ex2(v.y));
           pf[mt][n][k] = transposed(*reinterpret_cast<const uint32_t*>(&hv));
         }
+      const float2 l = apart(sum);
+      L[n][0] = l.x;
+      L[n][1] = l.y;
     }
     // ---- products with the values: O[d][row] ----
     unrolled<MT>([&](auto mt) {
@@ -826,7 +857,7 @@ int make_maps(const lmoe_kv_cache_fp8* c, lmoe_kv_maps_fp8* m) {
                             (uint64_t)c->n_blocks};
   const uint64_t strides[3] = {stride(c->slot_stride, c->block_size), stride(c->head_stride, c->kv_heads),
                                stride(c->block_stride, c->n_blocks)};
-  const uint32_t box[4] = {(uint32_t)c->head_dim, (uint32_t)std::min(c->block_size, kTile), 1, 1};
+  const uint32_t box[4] = {(uint32_t)c->head_dim, (uint32_t)std::min(c->block_size, 4096 / c->head_dim), 1, 1};
   for (int i = 0; i < 2; ++i) {
     CUtensorMap t;
     if (encode_tmap(&t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? c->v : c->k, dims, strides, box,
