@@ -5,7 +5,8 @@
 // HBM bounds it.  A lane holds two runs of four elements of a head: with the
 // halves of a head as pairs, four of the first half and the four that they are
 // turned with; with neighbours as pairs, eight in a row.  So a pair never leaves
-// its lane and the norm is the only thing that lanes exchange.
+// its lane, the norm is the only thing that lanes exchange, and the cosines and
+// sines of a token are eight registers.
 #include <algorithm>
 
 #include "common.cuh"
@@ -16,8 +17,9 @@ namespace lmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // tokens of a CTA
-constexpr int kBatch = 4;       // heads that a lane has under way
+constexpr int kBatch = 4;  // units that a warp has under way
+constexpr int kResident = 3;
+constexpr int kCtas = 3;   // CTAs of an SM
 
 struct RopeArgs {
   const uint16_t *q, *k;
@@ -26,138 +28,180 @@ struct RopeArgs {
   const int32_t *pos, *axis;
   const float* freq;
   long long qs, ks, qos, kos;
-  int T, hq, heads, d, rot, axes;
-  int tpc, hpc;  // tokens and heads of a CTA
+  int T, hq, hk, d, rot, axes;
+  int uq, units;   // units of a token's queries, and all of its units
+  int warps;       // among which the units of all tokens are cut
   int norm;
   float eps;
 };
 
-// 2^64 turns of one position's step, f / (2 pi), modulo a turn: the product of f (24 bits) with 1 / (2 pi) in
-// two doubles, of which the first part's whole turns are dropped.  Then pos * step wraps by itself.
+// One position's step f / (2 pi) in units of 2^-64 turns, modulo a turn, so that pos * step wraps by itself: f is
+// m 2^-e with a whole m below 2^24, and m * 2^128 / (2 pi) shifted right by 64 + e.  (In double precision the steps
+// of a launch took the SM's two lanes for it 9 us.)
 __device__ __forceinline__ uint64_t turn_step(float f) {
-  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
-  const double x = f, p = x * kHi, rest = fma(x, kLo, fma(x, kHi, -p));
-  return (uint64_t)__double2ll_rn((p - rint(p)) * 0x1p64) + (uint64_t)__double2ll_rn(rest * 0x1p64);
+  constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
+  const uint32_t bits = __float_as_uint(f), x = bits >> 23 & 255;
+  const uint32_t m = (bits & 0x7fffffu) | (x ? 0x800000u : 0u);
+  const int e = 150 - (int)max(x, 1u);  // (below 0 from 2^24 on)
+  const uint64_t w1 = m * kHi, more = __umul64hi(m, kLo), low = w1 + more;
+  const uint64_t w2 = __umul64hi(m, kHi) + (low < w1);
+  const uint64_t r = e <= 0 ? low : e < 64 ? low >> e | w2 << (64 - e) : e < 128 ? w2 >> (e - 64) : 0;
+  return bits >> 31 ? 0 - r : r;
 }
 
-__device__ __forceinline__ float2 unpack(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+// Two fp32 values in one register pair.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ float2 apart(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair unpack(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack(Pair p) {
+  const float2 f = apart(p);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ Pair swapped(Pair p) {
+  const float2 f = apart(p);
+  return pair(f.y, f.x);
+}
 
-// LP lanes a head; PAIRS: neighbours are pairs (else the halves' elements).
+// LP lanes a head, so that a unit is 32 / LP heads; PAIRS: neighbours are pairs (else the halves' elements).  The
+// units of all tokens, a token's queries first, are cut evenly over the warps.
 template <int LP, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
-  constexpr int S = kThreads / LP;  // heads that a CTA has in hand at a time
-  __shared__ __align__(16) float s_cos[kMaxTokens * 128], s_sin[kMaxTokens * 128];
+__global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int NP = 32 / LP;
   pdl_wait();
   pdl_trigger();
-  const int t0 = blockIdx.x * a.tpc, h0 = blockIdx.y * a.hpc;
-  const int nt = min(a.tpc, a.T - t0), nh = min(a.hpc, a.heads - h0), items = nt * nh;
-  const int slot = threadIdx.x / LP, j = threadIdx.x % LP;
+  const int lane = threadIdx.x & 31, sub = lane / LP, j = lane % LP, half = a.rot / 2;
+  const int id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const unsigned all = (unsigned)a.T * (unsigned)a.units;
+  const unsigned each = all / (unsigned)a.warps, more = all - each * (unsigned)a.warps;
+  unsigned u = (unsigned)id * each + min((unsigned)id, more), left = id < a.warps ? each + ((unsigned)id < more) : 0;
   const bool in = 8 * j < a.d, turned = 8 * j < a.rot;
-  const int o1 = !PAIRS && turned ? 4 * j : 8 * j, o2 = !PAIRS && turned ? a.rot / 2 + 4 * j : 8 * j + 4;
-  const int half = a.rot / 2;
+  const int o1 = !PAIRS && turned ? 4 * j : 8 * j, o2 = !PAIRS && turned ? half + 4 * j : 8 * j + 4;
 
-  for (int base = slot; base - slot < items; base += S * kBatch) {
-    uint2 x1[kBatch], x2[kBatch];
-    int tok[kBatch], head[kBatch];
+  // this lane's frequencies and gains
+  uint64_t step[4];
+  int ax[4];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = base + u * S;
-      x1[u] = x2[u] = make_uint2(0, 0);
-      tok[u] = a.tpc == 1 ? 0 : (int)((unsigned)i / (unsigned)nh);
-      head[u] = h0 + i - tok[u] * nh;
-      if (i < items && in) {
-        const long long t = t0 + tok[u];
-        const uint16_t* const row = head[u] < a.hq ? a.q + t * a.qs + (long long)head[u] * a.d
-                                                   : a.k + t * a.ks + (long long)(head[u] - a.hq) * a.d;
-        if constexpr (PAIRS) {
-          const uint4 w = *reinterpret_cast<const uint4*>(row + o1);
-          x1[u] = make_uint2(w.x, w.y);
-          x2[u] = make_uint2(w.z, w.w);
-        } else {
-          x1[u] = *reinterpret_cast<const uint2*>(row + o1);
-          x2[u] = *reinterpret_cast<const uint2*>(row + o2);
-        }
+  for (int e = 0; e < 4; ++e) {
+    const int f = 4 * j + e;
+    ax[e] = turned && a.axis ? a.axis[f] : 0;
+    if ((unsigned)ax[e] >= (unsigned)a.axes) ax[e] = -1;
+    step[e] = turned && ax[e] >= 0 ? turn_step(a.freq[f]) : 0;
+    ax[e] = max(ax[e], 0);
+  }
+  uint2 gain[2][2];
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const uint16_t* const g = side ? a.k_gain : a.q_gain;
+    const bool there = a.norm && g && in;
+    gain[side][0] = there ? *reinterpret_cast<const uint2*>(g + o1) : make_uint2(0x3f803f80u, 0x3f803f80u);
+    gain[side][1] = there ? *reinterpret_cast<const uint2*>(g + o2) : make_uint2(0x3f803f80u, 0x3f803f80u);
+  }
+  const float inv_d = 1.f / (float)a.d;
+
+  while (left > 0) {
+    const unsigned t = u / (unsigned)a.units;
+    const int first = (int)(u - t * (unsigned)a.units), n = min((unsigned)(a.units - first), left);
+    u += n;
+    left -= n;
+    float c[4], s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = 1.f;
+      s[e] = 0.f;
+      if (turned) {
+        const long long p = a.pos[(size_t)ax[e] * a.T + t];
+        sincospif((float)(int32_t)((uint64_t)p * step[e] >> 32) * 0x1p-31f, &s[e], &c[e]);
       }
     }
-    if (base == slot) {  // while the first rows are on their way: cosine and sine of the CTA's tokens
-      for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = (int)((unsigned)i / (unsigned)half), f = i - t * half;
-        const int ax = a.axis ? a.axis[f] : 0;
-        float s = 0.f, c = 1.f;
-        if (ax >= 0 && ax < a.axes) {
-          const long long p = a.pos[(size_t)ax * a.T + t0 + t];
-          const uint64_t phase = (uint64_t)p * turn_step(a.freq[f]);
-          sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+    // the token's units from `first` on, queries (side 0) or keys
+    auto rows = [&](int side, int begin, int end, int heads, const uint16_t* src, uint16_t* dst) {
+      const Pair g[4] = {unpack(gain[side][0].x), unpack(gain[side][0].y), unpack(gain[side][1].x),
+                         unpack(gain[side][1].y)};
+      for (int b = begin; b < end; b += kBatch) {
+        uint2 x1[kBatch], x2[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = (b + i) * NP + sub;
+          x1[i] = x2[i] = make_uint2(0, 0);
+          if (b + i < end && h < heads && in) {
+            const uint16_t* const row = src + (size_t)h * a.d;
+            if constexpr (PAIRS) {
+              const uint4 w = *reinterpret_cast<const uint4*>(row + o1);
+              x1[i] = make_uint2(w.x, w.y);
+              x2[i] = make_uint2(w.z, w.w);
+            } else {
+              x1[i] = *reinterpret_cast<const uint2*>(row + o1);
+              x2[i] = *reinterpret_cast<const uint2*>(row + o2);
+            }
+          }
         }
-        s_cos[i] = c;
-        s_sin[i] = s;
-      }
-      __syncthreads();
-    }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = base + u * S;
-      float v[8];
-      const uint32_t w[4] = {x1[u].x, x1[u].y, x2[u].x, x2[u].y};
+        for (int i = 0; i < kBatch; ++i) {
+          if (b + i >= end) break;
+          Pair v[4] = {unpack(x1[i].x), unpack(x1[i].y), unpack(x2[i].x), unpack(x2[i].y)};
+          if (a.norm) {
+            Pair q2 = mul2(v[0], v[0]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack(w[e]);
-        v[2 * e] = f.x;
-        v[2 * e + 1] = f.y;
-      }
-      if (a.norm) {
-        float sum = 0.f;
+            for (int e = 1; e < 4; ++e) q2 = fma2(v[e], v[e], q2);
+            const float2 q = apart(q2);
+            float sum = q.x + q.y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+            for (int o = LP / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
 #pragma unroll
-        for (int o = LP / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float r = rsqrtf(sum / (float)a.d + a.eps);
-        const uint16_t* const gain = head[u] < a.hq ? a.q_gain : a.k_gain;
+            for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], pair(r, r)), g[e]);
+          }
+          if constexpr (PAIRS) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= r;
-        if (gain && in) {
-          const uint2 g1 = *reinterpret_cast<const uint2*>(gain + o1), g2 = *reinterpret_cast<const uint2*>(gain + o2);
-          const uint32_t gw[4] = {g1.x, g1.y, g2.x, g2.y};
+            for (int e = 0; e < 4; ++e)
+              v[e] = fma2(v[e], pair(c[e], c[e]), mul2(swapped(v[e]), pair(-s[e], s[e])));
+          } else if (turned) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 g = unpack(gw[e]);
-            v[2 * e] *= g.x;
-            v[2 * e + 1] *= g.y;
+            for (int e = 0; e < 2; ++e) {
+              const Pair cc = pair(c[2 * e], c[2 * e + 1]), ss = pair(s[2 * e], s[2 * e + 1]);
+              const Pair minus = pair(-s[2 * e], -s[2 * e + 1]), x = v[e], y = v[2 + e];
+              v[e] = fma2(x, cc, mul2(y, minus));
+              v[2 + e] = fma2(y, cc, mul2(x, ss));
+            }
+          }
+          const int h = (b + i) * NP + sub;
+          if (h < heads && in) {
+            uint16_t* const row = dst + (size_t)h * a.d;
+            if constexpr (PAIRS) {
+              *reinterpret_cast<uint4*>(row + o1) = make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3]));
+            } else {
+              *reinterpret_cast<uint2*>(row + o1) = make_uint2(pack(v[0]), pack(v[1]));
+              *reinterpret_cast<uint2*>(row + o2) = make_uint2(pack(v[2]), pack(v[3]));
+            }
           }
         }
       }
-      if (i < items && in) {
-        if (turned) {
-          const float4 c4 = *reinterpret_cast<const float4*>(s_cos + tok[u] * half + 4 * j);
-          const float4 s4 = *reinterpret_cast<const float4*>(s_sin + tok[u] * half + 4 * j);
-          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float &p = v[PAIRS ? 2 * e : e], &r = v[PAIRS ? 2 * e + 1 : 4 + e];
-            const float x = p, y = r;
-            p = x * c[e] - y * s[e];
-            r = y * c[e] + x * s[e];
-          }
-        }
-        const long long t = t0 + tok[u];
-        uint16_t* const row = head[u] < a.hq ? a.q_out + t * a.qos + (long long)head[u] * a.d
-                                             : a.k_out + t * a.kos + (long long)(head[u] - a.hq) * a.d;
-        const uint2 y1 = make_uint2(pack(v[0], v[1]), pack(v[2], v[3]));
-        const uint2 y2 = make_uint2(pack(v[4], v[5]), pack(v[6], v[7]));
-        if constexpr (PAIRS) {
-          *reinterpret_cast<uint4*>(row + o1) = make_uint4(y1.x, y1.y, y2.x, y2.y);
-        } else {
-          *reinterpret_cast<uint2*>(row + o1) = y1;
-          *reinterpret_cast<uint2*>(row + o2) = y2;
-        }
-      }
-    }
+    };
+    if (first < a.uq) rows(0, first, min(a.uq, first + n), a.hq, a.q + (size_t)t * a.qs, a.q_out + (size_t)t * a.qos);
+    if (first + n > a.uq)
+      rows(1, max(first - a.uq, 0), first + n - a.uq, a.hk, a.k + (size_t)t * a.ks, a.k_out + (size_t)t * a.kos);
   }
 }
 
@@ -165,15 +209,11 @@ bool al(const void* p, unsigned n) { return p != nullptr && (reinterpret_cast<ui
 
 template <int LP>
 int run_rope(RopeArgs a, bool pairs, int sms, cudaStream_t s) {
-  constexpr int S = kThreads / LP;
-  // a CTA takes what its lanes can have under way at once: some tokens of few heads, or a token of many
-  a.tpc = std::max(1, std::min(std::min(kMaxTokens, S * kBatch / a.heads), a.T / (4 * sms)));
-  const int gx = (a.T + a.tpc - 1) / a.tpc;
-  // few tokens: their heads on several CTAs, down to one for each of a CTA's places
-  const int split = std::max(1, std::min((a.heads + S - 1) / S, 2 * sms / gx));
-  a.hpc = (a.heads + split - 1) / split;
-  const dim3 grid(gx, (a.heads + a.hpc - 1) / a.hpc);
-  return launch_pdl("qk_norm_rope_kernel", grid, dim3(kThreads), 0, s,
+  constexpr int NP = 32 / LP, kWarps = kThreads / 32;
+  a.uq = (a.hq + NP - 1) / NP;
+  a.units = a.uq + (a.hk + NP - 1) / NP;
+  a.warps = (int)std::min((long long)a.T * a.units, (long long)sms * kCtas * kWarps);
+  return launch_pdl("qk_norm_rope_kernel", dim3((a.warps + kWarps - 1) / kWarps), dim3(kThreads), 0, s,
                     pairs ? qk_norm_rope_kernel<LP, true> : qk_norm_rope_kernel<LP, false>, a);
 }
 
@@ -228,7 +268,7 @@ extern "C" int lmoe_qk_norm_rope(const lmoe_rope_dims* d, const uint16_t* q, int
   a.kos = k_out_stride;
   a.T = d->n_tokens;
   a.hq = d->q_heads;
-  a.heads = d->q_heads + d->k_heads;
+  a.hk = d->k_heads;
   a.d = d->head_dim;
   a.rot = d->rot_dim;
   a.axes = d->n_axes;
