@@ -18,8 +18,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // units that a warp has under way
-constexpr int kResident = 3;
-constexpr int kCtas = 3;   // CTAs of an SM
+constexpr int kResident = 2;
+constexpr int kCtas = 2;   // CTAs of an SM   // CTAs of an SM
 
 struct RopeArgs {
   const uint16_t *q, *k;
@@ -120,88 +120,104 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
   }
   const float inv_d = 1.f / (float)a.d;
 
-  while (left > 0) {
-    const unsigned t = u / (unsigned)a.units;
-    const int first = (int)(u - t * (unsigned)a.units), n = min((unsigned)(a.units - first), left);
-    u += n;
-    left -= n;
-    float c[4], s[4];
+  // a batch is up to kBatch units of one token's queries (side 0) or keys; the next one's rows are on their way while
+  // one is worked on, and with a token's first its positions
+  struct Batch {
+    unsigned t;
+    int side, first, n;  // first unit of the side
+    int pos[4];
+    uint2 x[kBatch][2];
+  };
+  Batch next;
+  next.t = u / (unsigned)a.units;
+  int unit = (int)(u - next.t * (unsigned)a.units);  // of the token, the next to be fetched
+  next.n = 0;
+  auto fetch = [&] {
+    if (unit == a.units) unit = 0, ++next.t;
+    next.side = unit >= a.uq;
+    next.first = next.side ? unit - a.uq : unit;
+    next.n = (int)min((unsigned)min(kBatch, (next.side ? a.units : a.uq) - unit), left);
+    if (next.n == 0) return;
+    unit += next.n;
+    left -= next.n;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[e] = 1.f;
-      s[e] = 0.f;
-      if (turned) {
-        const long long p = a.pos[(size_t)ax[e] * a.T + t];
-        sincospif((float)(int32_t)((uint64_t)p * step[e] >> 32) * 0x1p-31f, &s[e], &c[e]);
+    for (int e = 0; e < 4; ++e) next.pos[e] = turned ? a.pos[(size_t)ax[e] * a.T + next.t] : 0;
+    const int heads = next.side ? a.hk : a.hq;
+    const uint16_t* const src = next.side ? a.k + (size_t)next.t * a.ks : a.q + (size_t)next.t * a.qs;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = (next.first + i) * NP + sub;
+      next.x[i][0] = next.x[i][1] = make_uint2(0, 0);
+      if (i < next.n && h < heads && in) {
+        const uint16_t* const row = src + (size_t)h * a.d;
+        if constexpr (PAIRS) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + o1);
+          next.x[i][0] = make_uint2(w.x, w.y);
+          next.x[i][1] = make_uint2(w.z, w.w);
+        } else {
+          next.x[i][0] = *reinterpret_cast<const uint2*>(row + o1);
+          next.x[i][1] = *reinterpret_cast<const uint2*>(row + o2);
+        }
       }
     }
-    // the token's units from `first` on, queries (side 0) or keys
-    auto rows = [&](int side, int begin, int end, int heads, const uint16_t* src, uint16_t* dst) {
-      const Pair g[4] = {unpack(gain[side][0].x), unpack(gain[side][0].y), unpack(gain[side][1].x),
-                         unpack(gain[side][1].y)};
-      for (int b = begin; b < end; b += kBatch) {
-        uint2 x1[kBatch], x2[kBatch];
+  };
+  fetch();
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {};
+  unsigned at = ~0u;  // the token of the cosines
+  while (next.n > 0) {
+    const Batch now = next;
+    fetch();
+    if (now.t != at) {
+      at = now.t;
+      if (turned) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int h = (b + i) * NP + sub;
-          x1[i] = x2[i] = make_uint2(0, 0);
-          if (b + i < end && h < heads && in) {
-            const uint16_t* const row = src + (size_t)h * a.d;
-            if constexpr (PAIRS) {
-              const uint4 w = *reinterpret_cast<const uint4*>(row + o1);
-              x1[i] = make_uint2(w.x, w.y);
-              x2[i] = make_uint2(w.z, w.w);
-            } else {
-              x1[i] = *reinterpret_cast<const uint2*>(row + o1);
-              x2[i] = *reinterpret_cast<const uint2*>(row + o2);
-            }
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          sincospif((float)(int32_t)((uint64_t)(long long)now.pos[e] * step[e] >> 32) * 0x1p-31f, &s[e], &c[e]);
+      }
+    }
+    const uint2 g1 = now.side ? gain[1][0] : gain[0][0], g2 = now.side ? gain[1][1] : gain[0][1];
+    const Pair g[4] = {unpack(g1.x), unpack(g1.y), unpack(g2.x), unpack(g2.y)};
+    const int heads = now.side ? a.hk : a.hq;
+    uint16_t* const dst = now.side ? a.k_out + (size_t)now.t * a.kos : a.q_out + (size_t)now.t * a.qos;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          if (b + i >= end) break;
-          Pair v[4] = {unpack(x1[i].x), unpack(x1[i].y), unpack(x2[i].x), unpack(x2[i].y)};
-          if (a.norm) {
-            Pair q2 = mul2(v[0], v[0]);
+    for (int i = 0; i < kBatch; ++i) {
+      if (i >= now.n) break;
+      Pair v[4] = {unpack(now.x[i][0].x), unpack(now.x[i][0].y), unpack(now.x[i][1].x), unpack(now.x[i][1].y)};
+      if (a.norm) {
+        Pair q2 = mul2(v[0], v[0]);
 #pragma unroll
-            for (int e = 1; e < 4; ++e) q2 = fma2(v[e], v[e], q2);
-            const float2 q = apart(q2);
-            float sum = q.x + q.y;
+        for (int e = 1; e < 4; ++e) q2 = fma2(v[e], v[e], q2);
+        const float2 q = apart(q2);
+        float sum = q.x + q.y;
 #pragma unroll
-            for (int o = LP / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
+        for (int o = LP / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], pair(r, r)), g[e]);
-          }
-          if constexpr (PAIRS) {
+        for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], pair(r, r)), g[e]);
+      }
+      if constexpr (PAIRS) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = fma2(v[e], pair(c[e], c[e]), mul2(swapped(v[e]), pair(-s[e], s[e])));
-          } else if (turned) {
+        for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], pair(c[e], c[e]), mul2(swapped(v[e]), pair(-s[e], s[e])));
+      } else if (turned) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const Pair cc = pair(c[2 * e], c[2 * e + 1]), ss = pair(s[2 * e], s[2 * e + 1]);
-              const Pair minus = pair(-s[2 * e], -s[2 * e + 1]), x = v[e], y = v[2 + e];
-              v[e] = fma2(x, cc, mul2(y, minus));
-              v[2 + e] = fma2(y, cc, mul2(x, ss));
-            }
-          }
-          const int h = (b + i) * NP + sub;
-          if (h < heads && in) {
-            uint16_t* const row = dst + (size_t)h * a.d;
-            if constexpr (PAIRS) {
-              *reinterpret_cast<uint4*>(row + o1) = make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3]));
-            } else {
-              *reinterpret_cast<uint2*>(row + o1) = make_uint2(pack(v[0]), pack(v[1]));
-              *reinterpret_cast<uint2*>(row + o2) = make_uint2(pack(v[2]), pack(v[3]));
-            }
-          }
+        for (int e = 0; e < 2; ++e) {
+          const Pair cc = pair(c[2 * e], c[2 * e + 1]), ss = pair(s[2 * e], s[2 * e + 1]);
+          const Pair minus = pair(-s[2 * e], -s[2 * e + 1]), x = v[e], y = v[2 + e];
+          v[e] = fma2(x, cc, mul2(y, minus));
+          v[2 + e] = fma2(y, cc, mul2(x, ss));
         }
       }
-    };
-    if (first < a.uq) rows(0, first, min(a.uq, first + n), a.hq, a.q + (size_t)t * a.qs, a.q_out + (size_t)t * a.qos);
-    if (first + n > a.uq)
-      rows(1, max(first - a.uq, 0), first + n - a.uq, a.hk, a.k + (size_t)t * a.ks, a.k_out + (size_t)t * a.kos);
+      const int h = (now.first + i) * NP + sub;
+      if (h < heads && in) {
+        uint16_t* const row = dst + (size_t)h * a.d;
+        if constexpr (PAIRS) {
+          *reinterpret_cast<uint4*>(row + o1) = make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3]));
+        } else {
+          *reinterpret_cast<uint2*>(row + o1) = make_uint2(pack(v[0]), pack(v[1]));
+          *reinterpret_cast<uint2*>(row + o2) = make_uint2(pack(v[2]), pack(v[3]));
+        }
+      }
+    }
   }
 }
 
