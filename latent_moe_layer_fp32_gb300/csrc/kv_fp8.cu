@@ -29,17 +29,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return c;
 }
 
-// Eight bf16 values (one lane's part of a row) and the row's largest magnitude (its 15 bits) -> codes, and the
-// scale byte.  The magnitude is 1.m * 2^(E - 127) with 7 bits of m, and 448 = 1.75 * 2^8: e = E - 135, one more
-// where 1.m > 1.75 (m > 96); the scale byte is e + 127.
-__device__ __forceinline__ uint2 codes_of(const uint4& x, uint32_t top, uint32_t* scale) {
-  if (top >= 0x7f80u) {  // an infinity or a NaN
-    *scale = 255;
-    return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-  }
-  const int byte = max((int)(top >> 7) - 8 + ((top & 127u) > 96u), 0);
-  const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);  // 2^-e
-  *scale = byte;
+// A row's scale byte from its largest magnitude (15 bits of a bf16).  The magnitude is 1.m * 2^(E - 127) with 7 bits
+// of m, and 448 = 1.75 * 2^8: e = E - 135, one more where 1.m > 1.75 (m > 96); the byte is e + 127.  255 for an
+// infinity or a NaN.
+__device__ __forceinline__ uint32_t scale_of(uint32_t top) {
+  return top >= 0x7f80u ? 255u : (uint32_t)max((int)(top >> 7) - 8 + ((top & 127u) > 96u), 0);
+}
+
+// Eight bf16 values -> codes.
+__device__ __forceinline__ uint2 codes_of(const uint4& x, uint32_t scale) {
+  if (scale == 255) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  const float inv = __uint_as_float((254u - scale) << 23);  // 2^-e
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
@@ -57,8 +57,8 @@ __device__ __forceinline__ uint32_t top_of(const uint4& x) {
 // ---------------------------------------------------------------------------
 // write
 // ---------------------------------------------------------------------------
-// A thread takes eight elements of a row's K and the same of its V; the LP
-// lanes of a row find its largest magnitude together.
+// A thread takes 16 elements of a row's K and the same of its V; the LP lanes
+// of a row find its largest magnitude together.
 template <int LP>
 __global__ void __launch_bounds__(256)
     kv_write_fp8_kernel(const lmoe_kv_cache_fp8 c, const uint16_t* __restrict__ k_new, long long ks,
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_trigger();
   const unsigned x = blockIdx.x * 256u + threadIdx.x, pieces = (unsigned)c.kv_heads * LP;
-  const unsigned t = x / pieces, p = x - t * pieces, h = p / LP, d = (p % LP) * 8;
+  const unsigned t = x / pieces, p = x - t * pieces, h = p / LP, d = (p % LP) * 16;
   bool live = t < (unsigned)n_tokens;
   int slot = -1, row = 0;
   if (live) {
@@ -79,21 +79,26 @@ __global__ void __launch_bounds__(256)
       live = false;
     }
   }
-  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+  uint4 kx[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, vx[2] = {kx[0], kx[0]};
   if (live) {
-    kx = __ldcs(reinterpret_cast<const uint4*>(k_new + (size_t)row * ks + (size_t)p * 8));
-    vx = __ldcs(reinterpret_cast<const uint4*>(v_new + (size_t)row * vs + (size_t)p * 8));
+    const uint4* const kp = reinterpret_cast<const uint4*>(k_new + (size_t)row * ks + (size_t)p * 16);
+    const uint4* const vp = reinterpret_cast<const uint4*>(v_new + (size_t)row * vs + (size_t)p * 16);
+    kx[0] = __ldcs(kp);
+    kx[1] = __ldcs(kp + 1);
+    vx[0] = __ldcs(vp);
+    vx[1] = __ldcs(vp + 1);
   }
-  uint32_t top = top_of(kx) | top_of(vx) << 16;  // both rows' at once
+  uint32_t top = max(top_of(kx[0]), top_of(kx[1])) | max(top_of(vx[0]), top_of(vx[1])) << 16;  // both rows' at once
 #pragma unroll
   for (int o = LP / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (!live) return;
-  uint32_t k_scale, v_scale;
-  const uint2 kc = codes_of(kx, top & 0xffffu, &k_scale), vc = codes_of(vx, top >> 16, &v_scale);
+  const uint32_t k_scale = scale_of(top & 0xffffu), v_scale = scale_of(top >> 16);
+  const uint2 k0 = codes_of(kx[0], k_scale), k1 = codes_of(kx[1], k_scale);
+  const uint2 v0 = codes_of(vx[0], v_scale), v1 = codes_of(vx[1], v_scale);
   const size_t block = (size_t)(slot >> bs_shift), in = (size_t)(slot & ((1 << bs_shift) - 1));
   const size_t to = block * c.block_stride + h * c.head_stride + in * c.slot_stride + d;
-  *reinterpret_cast<uint2*>(c.k + to) = kc;
-  *reinterpret_cast<uint2*>(c.v + to) = vc;
+  *reinterpret_cast<uint4*>(c.k + to) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+  *reinterpret_cast<uint4*>(c.v + to) = make_uint4(v0.x, v0.y, v1.x, v1.y);
   if (d == 0) {
     const size_t at = ((block * c.kv_heads + h) << bs_shift) + in;
     c.k_scale[at] = (uint8_t)k_scale;
@@ -233,7 +238,7 @@ int lmoe_kv_write_fp8(const lmoe_kv_cache_fp8* cache, const uint16_t* k_new, int
       n_rows < 1 || n_tokens < 1 || n_tokens > (1 << 20) || (!src && n_tokens > n_rows) || (src && !al(src, 4)) ||
       !al(slots, 4))
     return LMOE_EINVAL;
-  const long long total = (long long)n_tokens * (row / 8);
+  const long long total = (long long)n_tokens * (row / 16);
   if (total > 0x7fffffffll) return LMOE_EUNSUPPORTED;
   DevInfo di;
   if ((rc = dev_info(&di))) return rc;
@@ -241,7 +246,7 @@ int lmoe_kv_write_fp8(const lmoe_kv_cache_fp8* cache, const uint16_t* k_new, int
   Status* st;
   if ((rc = optional_status(ws, ws_bytes, s, &st))) return rc;
   return launch_pdl("kv_write_fp8_kernel", dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s,
-                    cache->head_dim == 64 ? kv_write_fp8_kernel<8> : kv_write_fp8_kernel<16>, *cache, k_new,
+                    cache->head_dim == 64 ? kv_write_fp8_kernel<4> : kv_write_fp8_kernel<8>, *cache, k_new,
                     (long long)k_stride, v_new, (long long)v_stride, n_rows, src, slots, n_tokens,
                     log2_of(cache->block_size), st);
 }
