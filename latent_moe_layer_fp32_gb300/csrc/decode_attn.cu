@@ -16,7 +16,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-constexpr int kEnd = 3;          // what a segment's end costs, in tiles
+constexpr int kEnd = 2;          // what a segment's end costs, in tiles
 constexpr float kShift = 14.f;   // P stands in f16 as p * 2^14, see below
 
 struct DecodeArgs {
@@ -794,24 +794,27 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
     if (threadIdx.x == 0) *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
   }
   const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4);
-  float2 ml[U];
-  float4 o[U];
-  auto fetch = [&](int p0, int end) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int p = min(p0 + u, end);
-      const size_t at = (size_t)p * 2 + (p == (int)blockIdx.x);
-      ml[u] = a.ml[at * C::kRows + r];
-      o[u] = reinterpret_cast<const float4*>(a.o + at * C::kPiece)[e];
-    }
+  auto piece = [&](int p, float2& ml, float4& o) {
+    const size_t at = (size_t)p * 2 + (p == (int)blockIdx.x);
+    ml = a.ml[at * C::kRows + r];
+    o = reinterpret_cast<const float4*>(a.o + at * C::kPiece)[e];
   };
-  fetch(blockIdx.x, a.ctas - 1);  // (before it is known how many there are, or whether any)
+  // two pieces, as most have, before it is known whether there are any
+  float2 ml0, ml1;
+  float4 o0, o1;
+  piece(blockIdx.x, ml0, o0);
+  piece(min((int)blockIdx.x + 1, a.ctas - 1), ml1, o1);
   const int4 rec = a.rec[blockIdx.x];
   const int h = rec.y >> 8, row = (rec.y & 255) * 8 + r;
   if (rec.z < 0 || row >= a.G) return;
   Sum sum;
-  for (int p0 = blockIdx.x; p0 <= rec.z; p0 += U) {
-    if (p0 > (int)blockIdx.x) fetch(p0, rec.z);
+  sum.add(ml0, o0);
+  sum.add(ml1, o1);
+  for (int p0 = blockIdx.x + 2; p0 <= rec.z; p0 += U) {
+    float2 ml[U];
+    float4 o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) piece(min(p0 + u, rec.z), ml[u], o[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (p0 + u <= rec.z) sum.add(ml[u], o[u]);
