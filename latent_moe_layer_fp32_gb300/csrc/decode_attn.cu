@@ -206,6 +206,7 @@ struct Cfg {
   static constexpr int kRing = W * S * kStage;
   static constexpr int kPiece = kRows * D;  // floats of a piece's output
   static constexpr int kSmem = kRing + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
+  static_assert(8192 <= 32 * kThreads, "the most requests: no run has more than a warp's lanes");
   static_assert(kPiece * 4 <= S * kStage, "a warp's last piece takes its ring's place");
   static_assert(KT == 32 || KT == 64, "whole warps of keys");
 };
@@ -237,9 +238,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   __shared__ uint64_t s_full[W][C::S];
   __shared__ float4 s_key[W][KT];  // of a tile's keys: the key's scale, 0 or -infinity, the value's exponent
   __shared__ __align__(16) uint8_t s_scale[W][C::S][2 * KT];  // of the ring's tiles: K's, V's
-  __shared__ unsigned long long s_scan[W], s_at[W];
+  __shared__ unsigned long long s_scan[W], s_before[C::kThreads];
   __shared__ unsigned s_live[W];
-  __shared__ int s_b[W];
   __shared__ int4 s_seg[W][2];  // a warp's pieces, put down on the way and at its range's end: {request, head, group, flags}
   __shared__ float2 s_ml[W][C::kRows];
   __shared__ int s_last, s_err;
@@ -296,8 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     // what a segment's end weighs: no more than a warp has tiles
     walk.end = (int)min((unsigned long long)kEnd, quot(all, (unsigned)(a.ctas * W)));
     total = all + (unsigned long long)all_live * segs * walk.end;
-    const unsigned long long before = tiles_before * segs + (unsigned long long)live_before * segs * walk.end;
-    const unsigned long long mine = tiles * segs + (unsigned long long)live * segs * walk.end;
+    s_before[threadIdx.x] = (tiles_before + (unsigned long long)live_before * walk.end) * segs;
     // as many CTAs as have a tile for each warp
     n_ctas = (unsigned)min((unsigned long long)a.ctas, (all + W - 1) / W);
     const unsigned c = blockIdx.x;
@@ -309,47 +308,40 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
       hi = ctas.first(c + 1);
     }
     const Cut warps(hi - lo, W);
+    const unsigned long long at = lo + warps.first(warp);
     walk.left = (long long)(warps.each + ((unsigned)warp < warps.more));
     at_end = lo + warps.first(warp + 1) == hi;
-    unsigned long long at = lo;
-#pragma unroll 1
-    for (int w = 0; w < W; ++w) {
-      if (at >= before && at < before + mine) {
-        unsigned long long skip = at - before;
-        int b = b0;
-        for (;; ++b) {
-          const int n = span_of<KT>(a, a.lens[b]).n;
-          const unsigned long long there = n ? (unsigned long long)(n + walk.end) * segs : 0;
-          if (skip < there) break;
-          skip -= there;
+    __syncthreads();
+    if (walk.left > 0) {
+      // the last run of requests that begins at or before this warp's range, and in it the request: a lane each
+      int owner = -1;
+#pragma unroll
+      for (int i = 0; i < W; ++i) owner += __popc(__ballot_sync(0xffffffffu, s_before[i * 32 + lane] <= at));
+      unsigned long long skip = at - s_before[owner];
+      walk.b = owner * run;
+      if (run > 1) {
+        const int b = walk.b + lane;
+        const int n = lane < run && b < a.B ? span_of<KT>(a, a.lens[b]).n : 0;
+        const unsigned long long mine = n ? (unsigned long long)(n + walk.end) * segs : 0;
+        unsigned long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
         }
-        s_b[w] = b;
-        s_at[w] = skip;
+        const int i = __ffs(__ballot_sync(0xffffffffu, x > skip)) - 1;
+        skip -= __shfl_sync(0xffffffffu, x - mine, i);
+        walk.b += i;
       }
-      at += warps.each + ((unsigned)w < warps.more);
-    }
-  }
-  // requests without positions
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (a.lens[b] != 0) continue;
-    for (int i = threadIdx.x; i < hq * D / 8; i += C::kThreads)
-      reinterpret_cast<uint4*>(a.out + (size_t)b * hq * D)[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int i = threadIdx.x; i < hq; i += C::kThreads) a.lse[(size_t)b * hq + i] = -INFINITY;
-  }
-  __syncthreads();
-
-  if (walk.left > 0) {
-    walk.b = s_b[warp];
-    walk.s = span_of<KT>(a, a.lens[walk.b]);
-    const unsigned long long at = s_at[warp];
-    const int size = walk.s.n + walk.end, seg = (int)quot(at, size);
-    walk.tile = (int)(at - (unsigned long long)seg * size);
-    walk.h = seg / a.groups;
-    walk.group = seg - walk.h * a.groups;
-    if (walk.tile >= walk.s.n) {  // behind a segment's tiles
-      walk.left -= size - walk.tile;
-      if (walk.left > 0) walk.segment(a);
+      walk.s = span_of<KT>(a, a.lens[walk.b]);
+      const int size = walk.s.n + walk.end, seg = (int)quot(skip, size);
+      walk.tile = (int)(skip - (unsigned long long)seg * size);
+      walk.h = seg / a.groups;
+      walk.group = seg - walk.h * a.groups;
+      if (walk.tile >= walk.s.n) {  // behind a segment's tiles
+        walk.left -= size - walk.tile;
+        if (walk.left > 0) walk.segment(a);
+      }
     }
   }
   Walk<KT> ahead = walk;  // walks in front and looks pages up
@@ -453,6 +445,15 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
       look();
     }
     copies_end();
+  }
+
+  // requests without positions (while the first tiles are on their way)
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (a.lens[b] != 0) continue;
+    for (int i = threadIdx.x; i < hq * D / 8; i += C::kThreads)
+      reinterpret_cast<uint4*>(a.out + (size_t)b * hq * D)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = threadIdx.x; i < hq; i += C::kThreads) a.lse[(size_t)b * hq + i] = -INFINITY;
   }
 
   uint32_t qf[N8][D / 16][2];  // the queries' fragments, as f16 times a power of two of each row's
