@@ -447,15 +447,6 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     copies_end();
   }
 
-  // requests without positions (while the first tiles are on their way)
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (a.lens[b] != 0) continue;
-    for (int i = threadIdx.x; i < hq * D / 8; i += C::kThreads)
-      reinterpret_cast<uint4*>(a.out + (size_t)b * hq * D)[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int i = threadIdx.x; i < hq; i += C::kThreads) a.lse[(size_t)b * hq + i] = -INFINITY;
-  }
-
   uint32_t qf[N8][D / 16][2];  // the queries' fragments, as f16 times a power of two of each row's
   float q_scale[N8][2];        // what makes a product with them a score to base 2, for this lane's two columns
   float o[C::kChunks][N8][4], M[N8][2], Mo[N8][2], L[N8][2];
@@ -782,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
 template <int D, int N8>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
   using C = Cfg<D, N8>;
-  constexpr int U = 8;  // pieces under way
+  constexpr int U = 4;  // pieces under way
   __shared__ int s_err;
   pdl_wait();
   pdl_trigger();
@@ -794,37 +785,47 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
     __syncthreads();
     if (threadIdx.x == 0) *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
   }
-  const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4);
-  auto piece = [&](int p, float2& ml, float4& o) {
-    const size_t at = (size_t)p * 2 + (p == (int)blockIdx.x);
-    ml = a.ml[at * C::kRows + r];
-    o = reinterpret_cast<const float4*>(a.o + at * C::kPiece)[e];
+  const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4), hq = a.c.kv_heads * a.G;
+  auto fetch = [&](float2 (&ml)[U], float4 (&o)[U], int p0, int end) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = min(p0 + u, end);
+      const size_t at = (size_t)p * 2 + (p == (int)blockIdx.x);
+      ml[u] = a.ml[at * C::kRows + r];
+      o[u] = reinterpret_cast<const float4*>(a.o + at * C::kPiece)[e];
+    }
   };
-  // two pieces, as most have, before it is known whether there are any
-  float2 ml0, ml1;
-  float4 o0, o1;
-  piece(blockIdx.x, ml0, o0);
-  piece(min((int)blockIdx.x + 1, a.ctas - 1), ml1, o1);
+  // the first pieces before it is known whether there are any
+  float2 ml[U];
+  float4 o[U];
+  fetch(ml, o, blockIdx.x, a.ctas - 1);
   const int4 rec = a.rec[blockIdx.x];
+  int len = (int)blockIdx.x < a.B && blockIdx.y == 0 ? a.lens[blockIdx.x] : 1;
   const int h = rec.y >> 8, row = (rec.y & 255) * 8 + r;
-  if (rec.z < 0 || row >= a.G) return;
-  Sum sum;
-  sum.add(ml0, o0);
-  sum.add(ml1, o1);
-  for (int p0 = blockIdx.x + 2; p0 <= rec.z; p0 += U) {
-    float2 ml[U];
-    float4 o[U];
+  if (rec.z >= 0 && row < a.G) {
+    Sum sum;
+    for (int p0 = blockIdx.x; p0 <= rec.z; p0 += U) {
+      if (p0 > (int)blockIdx.x) fetch(ml, o, p0, rec.z);
 #pragma unroll
-    for (int u = 0; u < U; ++u) piece(min(p0 + u, rec.z), ml[u], o[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (p0 + u <= rec.z) sum.add(ml[u], o[u]);
+      for (int u = 0; u < U; ++u)
+        if (p0 + u <= rec.z) sum.add(ml[u], o[u]);
+    }
+    const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+    const size_t at = (size_t)rec.x * hq + h * a.G + row;
+    *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
+        make_uint2(pack_bf16(sum.o.x * inv, sum.o.y * inv), pack_bf16(sum.o.z * inv, sum.o.w * inv));
+    if (a.lse && e % (D / 4) == 0) a.lse[at] = sum.lse();
   }
-  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
-  const size_t at = (size_t)rec.x * a.c.kv_heads * a.G + h * a.G + row;
-  *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
-      make_uint2(pack_bf16(sum.o.x * inv, sum.o.y * inv), pack_bf16(sum.o.z * inv, sum.o.w * inv));
-  if (a.lse && e % (D / 4) == 0) a.lse[at] = sum.lse();
+  // requests without positions
+  for (int b = blockIdx.x; b < a.B && blockIdx.y == 0;) {
+    if (len == 0) {
+      for (int i = threadIdx.x; i < hq * D / 8; i += blockDim.x)
+        reinterpret_cast<uint4*>(a.out + (size_t)b * hq * D)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = threadIdx.x; i < hq; i += blockDim.x) a.lse[(size_t)b * hq + i] = -INFINITY;
+    }
+    if ((b += gridDim.x) < a.B) len = a.lens[b];
+  }
 }
 
 bool al(const void* p, unsigned n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
