@@ -197,7 +197,7 @@ struct Walk {
 // N8: groups of eight query rows that a key's codes are used for; W warps; S tiles of KT keys in a warp's ring.
 template <int D, int N8>
 struct Cfg {
-  static constexpr int W = D == 128 || N8 == 2 ? 8 : 12, KT = 4096 / D, S = D == 128 || N8 == 2 ? 3 : 2;
+  static constexpr int W = D == 64 && N8 == 1 ? 12 : 8, KT = 4096 / D, S = D == 128 && N8 == 1 ? 3 : 2;
   static constexpr int kThreads = 32 * W;
   static constexpr int kRows = 8 * N8;
   static constexpr int kChunks = D / 16;  // 16-byte pieces of a row
@@ -205,7 +205,10 @@ struct Cfg {
   static constexpr int kStage = 2 * kCodes;
   static constexpr int kRing = W * S * kStage;
   static constexpr int kPiece = kRows * D;  // floats of a piece's output
-  static constexpr int kSmem = kRing + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
+  // with 16 query rows, their fragments stand in shared memory: registers are what bounds the number of warps
+  static constexpr bool kQueriesInSmem = N8 == 2;
+  static constexpr int kQueries = kQueriesInSmem ? W * N8 * kChunks * 32 * 8 : 0;
+  static constexpr int kSmem = kRing + kQueries + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
   static_assert(8192 <= 32 * kThreads, "the most requests: no run has more than a warp's lanes");
   static_assert(kPiece * 4 <= S * kStage, "a warp's last piece takes its ring's place");
   static_assert(KT == 32 || KT == 64, "whole warps of keys");
@@ -447,7 +450,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     copies_end();
   }
 
-  uint32_t qf[N8][D / 16][2];  // the queries' fragments, as f16 times a power of two of each row's
+  uint2 qf[C::kQueriesInSmem ? 1 : N8][C::kChunks];  // the queries' fragments, as f16 times a power of two of each row's
+  uint2* const s_q = reinterpret_cast<uint2*>(s_ring + C::kRing) + warp * N8 * C::kChunks * 32 + lane;  // or here
   float q_scale[N8][2];        // what makes a product with them a score to base 2, for this lane's two columns
   float o[C::kChunks][N8][4], M[N8][2], Mo[N8][2], L[N8][2];
   int stage = 0;
@@ -516,12 +520,15 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
 #pragma unroll
         for (int i = 0; i < C::kChunks; ++i) {
           const uint32_t x[2] = {w[n][i].x, w[n][i].y};
+          uint32_t y[2];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             const __half2 hv = __floats2half2_rn(__uint_as_float(x[m] << 16) * up,
                                                  __uint_as_float(x[m] & 0xffff0000u) * up);
-            qf[n][i][m] = *reinterpret_cast<const uint32_t*>(&hv);
+            y[m] = *reinterpret_cast<const uint32_t*>(&hv);
           }
+          if constexpr (C::kQueriesInSmem) s_q[(n * C::kChunks + i) * 32] = make_uint2(y[0], y[1]);
+          else qf[n][i] = make_uint2(y[0], y[1]);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -541,6 +548,14 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     float s[MT][N8][4];
     unrolled<C::kChunks / 2>([&](auto pair) {
       constexpr int c = 2 * pair;
+      uint2 q[N8][2];
+#pragma unroll
+      for (int n = 0; n < N8; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if constexpr (C::kQueriesInSmem) q[n][x] = s_q[(n * C::kChunks + c + x) * 32];
+          else q[n][x] = qf[n][c + x];
+        }
       unrolled<MT>([&](auto mt) {
         uint32_t r[4];  // keys g and g + 8, columns 4 t .. 4 t + 3 of piece c; the same of c + 1
         ldmatrix<mt * 16 * D>(r, st32 ^ (c << 4));
@@ -551,8 +566,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
           e4m3x4_to_f16x4(r[2 * x + 1], a1, a3);
 #pragma unroll
           for (int n = 0; n < N8; ++n) {
-            if (c + x == 0) mma_f16_zero(s[mt][n], a0, a1, a2, a3, qf[n][0][0], qf[n][0][1]);
-            else mma_f16(s[mt][n], a0, a1, a2, a3, qf[n][c + x][0], qf[n][c + x][1]);
+            if (c + x == 0) mma_f16_zero(s[mt][n], a0, a1, a2, a3, q[n][x].x, q[n][x].y);
+            else mma_f16(s[mt][n], a0, a1, a2, a3, q[n][x].x, q[n][x].y);
           }
         }
       });
