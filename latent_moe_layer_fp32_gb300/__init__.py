@@ -393,6 +393,7 @@ def lmoe_block_forward(dims, weights: LmoeWeights, norms: LmoeBlockNorms, x, y, 
 _I64 = (torch.int64, torch.uint64)
 _INT32 = torch.int32
 _BF16_ONLY = (torch.bfloat16,)
+_BF16_DTYPE = torch.bfloat16
 
 
 def _arg(t, n, dtypes, what):
@@ -536,6 +537,21 @@ def lmoe_kv_write(cache, k_new, v_new, src, slots, ws=None, stream=None):
         raise LmoeError(rc, "lmoe_kv_write")
 
 
+def _rows_of(n, t, heads, width, what):
+    """_rows of a tensor of at least n rows, with the shortest path for what is right."""
+    try:
+        if t.dtype is _BF16_DTYPE and t.is_cuda:
+            (rows, h, w), (step, head, one) = t.shape, t.stride()
+            if rows >= n and h == heads and w == width and one == 1 and (head == width or heads == 1):
+                return t.data_ptr(), step if rows > 1 else heads * width
+    except (AttributeError, ValueError):
+        pass
+    at = _rows(t, heads, width, what)  # says what is wrong
+    if t.shape[0] < n:
+        raise ValueError(f"{what}: expected at least {n} rows, got {t.shape[0]}")
+    return at
+
+
 def rope_dims_of(n_tokens, q_heads, k_heads, head_dim, rot_dim=None, n_axes=1, interleaved=False, norm=True,
                  eps=1e-6) -> LmoeRopeDims:
     """rot_dim None: the whole head is turned."""
@@ -547,19 +563,19 @@ def lmoe_qk_norm_rope(dims, q, k, q_gain, k_gain, pos, inv_freq, axis, q_out, k_
     """Norm and rotation of q [T, q_heads, d] and k [T, k_heads, d], bf16 and perhaps slices of one projection;
     gains bf16 [d] or None, pos int32 [n_axes, T], inv_freq fp32 [rot_dim / 2], axis int32 [rot_dim / 2] or None.
     q_out and k_out may be q and k themselves; with no heads a side is None."""
-    t, d, half, sides = dims.n_tokens, dims.head_dim, dims.rot_dim // 2, []
-    for x, heads, what in ((q, dims.q_heads, "q"), (k, dims.k_heads, "k"), (q_out, dims.q_heads, "q_out"),
-                           (k_out, dims.k_heads, "k_out")):
-        if heads == 0:
-            sides.append((None, 0))
-            continue
-        sides.append(_rows(x, heads, d, what))
-        if x.shape[0] < t:
-            raise ValueError(f"{what}: expected {t} rows, got {x.shape[0]}")
+    t, hq, hk, d, half = dims.n_tokens, dims.q_heads, dims.k_heads, dims.head_dim, dims.rot_dim // 2
+    qp = kp = qo = ko = None
+    qs = ks = qos = kos = 0
+    if hq:
+        qp, qs = _rows_of(t, q, hq, d, "q")
+        qo, qos = _rows_of(t, q_out, hq, d, "q_out")
+    if hk:
+        kp, ks = _rows_of(t, k, hk, d, "k")
+        ko, kos = _rows_of(t, k_out, hk, d, "k_out")
     rc = load().lmoe_qk_norm_rope(
-        ctypes.byref(dims), *sides[0], *sides[1], _arg(q_gain, d, _BF16_ONLY, "q_gain"),
-        _arg(k_gain, d, _BF16_ONLY, "k_gain"), _i32(pos, dims.n_axes * t, "pos"), _arg(inv_freq, half, _F32, "inv_freq"),
-        _i32(axis, half, "axis"), *sides[2], *sides[3], _stream_arg(stream))
+        ctypes.byref(dims), qp, qs, kp, ks, _arg(q_gain, d, _BF16_ONLY, "q_gain"), _arg(k_gain, d, _BF16_ONLY, "k_gain"),
+        _i32(pos, dims.n_axes * t, "pos"), _arg(inv_freq, half, _F32, "inv_freq"), _i32(axis, half, "axis"), qo, qos, ko,
+        kos, _stream_arg(stream))
     if rc:
         raise LmoeError(rc, "lmoe_qk_norm_rope")
 
@@ -635,9 +651,7 @@ def lmoe_decode_attention_fp8(dims, cache, q, lens, block_table, out, lse, ws, s
     """One new token a request, q [B, q_heads, d] (perhaps a slice of a projection), over the lens[b] positions
     that the 8-bit cache holds of it; lse may be None."""
     b, hq, d = dims.n_requests, dims.q_heads, cache.head_dim
-    qp, qs = _rows(q, hq, d, "q")
-    if q.shape[0] < b:
-        raise ValueError(f"expected {b} rows in q")
+    qp, qs = _rows_of(b, q, hq, d, "q")
     rc = load().lmoe_decode_attention_fp8(
         ctypes.byref(dims), ctypes.byref(cache), qp, qs, _i32(lens, b, "lens"),
         _i32(block_table, b * dims.max_blocks, "block_table"), _arg(out, b * hq * d, _BF16_ONLY, "out"),
