@@ -147,6 +147,10 @@ __global__ void __launch_bounds__(256)
   __shared__ int s_block[kReadTokens], s_in[kReadTokens];
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < B; b += 256)
+      if (offsets[b] < 0 || offsets[b + 1] < offsets[b] || offsets[b + 1] > n_tokens)
+        set_error(st, LMOE_EDEVICE_CHECK, 231);
   const int t0 = blockIdx.x * per, nt = min(per, n_tokens - t0);
   if ((int)threadIdx.x < nt) {
     const int t = t0 + threadIdx.x;
@@ -154,9 +158,7 @@ __global__ void __launch_bounds__(256)
     if (offsets[0] <= t && t < offsets[B]) {
       const int b = request_of(offsets, 0, B - 1, t);
       const int begin = offsets[b], end = offsets[b + 1];
-      if (begin < 0 || begin > t || end <= t || end > n_tokens) {
-        set_error(st, LMOE_EDEVICE_CHECK, 231);
-      } else {
+      if (begin >= 0 && begin <= t && end > t && end <= n_tokens) {
         const long long p = (long long)(first ? first[b] : 0) + (t - begin);
         const long long page = p >> bs_shift;
         if (p < 0 || page >= max_blocks) {

@@ -206,6 +206,13 @@ def test_read_reports_what_is_out_of_range(lm):
     r.run(lm, want=-5)
     for o, b in zip(r.out, before):
         assert torch.equal(o[60:], b[60:]) and not torch.equal(o[:60], b[:60])
+    # ... also where no row shows it
+    r = Read([20, 40, 20], None, seed=6)
+    r.off[3] = 50
+    before = [o.clone() for o in r.out]
+    r.run(lm, want=-5)
+    for o, b in zip(r.out, before):
+        assert torch.equal(o[60:], b[60:]) and not torch.equal(o[:20], b[:20])
     r = Read([20, 40, 20], None, seed=6)
     r.off[0] = -3
     before = [o.clone() for o in r.out]
