@@ -17,7 +17,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 constexpr int kEnd = 2;          // what a segment's end costs, in tiles
-constexpr float kShift = 14.f;   // P stands in f16 as p * 2^14, see below
+// The base of a row's powers is its largest score when it last moved.  It moves again where a power would pass
+// 2^kSlackM, which fp32 sums do not mind, or one with its value's exponent 2^kSlackE, which keeps f16, where they stand
+// times 2^kShift, below 2^16.  (Where it followed every new maximum, four tiles of ten moved it: MOVED.)
+constexpr float kSlackM = 8.f, kSlackE = 1.9f, kShift = 14.f;
 
 struct DecodeArgs {
   lmoe_kv_cache_fp8 c;
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   extern __shared__ uint8_t s_dynamic[];
   uint8_t* const s_ring = s_dynamic + (-smem_u32(s_dynamic) & 1023u);
   __shared__ uint64_t s_full[W][C::S];
-  __shared__ float4 s_key[W][KT];  // of a tile's keys: the key's scale, 0 or -infinity, the value's exponent
+  __shared__ float2 s_key[W][KT];  // of a tile's keys: the key's scale, the value's exponent
   __shared__ __align__(16) uint8_t s_scale[W][C::S][2 * KT];  // of the ring's tiles: K's, V's
   __shared__ unsigned long long s_scan[W], s_before[C::kThreads];
   __shared__ unsigned s_live[W];
@@ -453,7 +456,9 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   uint2 qf[C::kQueriesInSmem ? 1 : N8][C::kChunks];  // the queries' fragments, as f16 times a power of two of each row's
   uint2* const s_q = reinterpret_cast<uint2*>(s_ring + C::kRing) + warp * N8 * C::kChunks * 32 + lane;  // or here
   float q_scale[N8][2];        // what makes a product with them a score to base 2, for this lane's two columns
-  float o[C::kChunks][N8][4], M[N8][2], Mo[N8][2], L[N8][2];
+  // M, the running maximum of the scores s, and L, the sum of 2^(s - M); with the values' exponents e: E, the running
+  // maximum of s - M + e, and O, the sum of 2^(s - M + e - E + kShift) times the values' codes
+  float o[C::kChunks][N8][4], minus_M[N8][2], E[N8][2], L[N8][2];
   int stage = 0;
   bool fresh = true, whole = false;  // the segment has no tile here yet; its first tile is in this range
   // this lane's row of a 16-key matrix pair, and its half of two pieces
@@ -488,12 +493,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
 #pragma unroll
     for (int i = lane; i < KT; i += 32) {
       const uint32_t kb = s_scale[warp][stage][i], vb = s_scale[warp][stage][KT + i];
-      float4 key = make_float4(e8m0_to_f32(kb), 0.f, vb == 255 ? NAN : (float)vb - 127.f, 0.f);
-      if (last || walk.tile == 0) {
-        const int p = walk.s.p0(walk.tile) + i;
-        if (p < walk.s.lo || (unsigned)p >= (unsigned)walk.s.len) key = make_float4(0.f, -INFINITY, 0.f, 0.f);
-      }
-      s_key[warp][i] = key;
+      s_key[warp][i] = make_float2(e8m0_to_f32(kb), vb == 255 ? NAN : (float)vb - 127.f);
     }
     __syncwarp();
     // (the ring's oldest place is free: its tile was computed before the last __syncwarp)
@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     }
     copies_end();
     stage = stage == C::S - 1 ? 0 : stage + 1;
+    const bool first_tile = fresh;
     if (fresh) {
       fresh = false;
       whole = walk.tile == 0;
@@ -534,8 +535,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
         for (int j = 0; j < 2; ++j) {
           const int ej = __shfl_sync(0xffffffffu, e, (2 * t + j) * 4);
           q_scale[n][j] = ldexpf(a.scale_log2, -ej);
-          M[n][j] = Mo[n][j] = -INFINITY;
-          L[n][j] = 0.f;
+          E[n][j] = -INFINITY;
+          minus_M[n][j] = L[n][j] = 0.f;
         }
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c)
@@ -572,53 +573,97 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
         }
       });
     });
-    // ---- to base 2, with the keys' scales; the same with the values' exponents for the products with them ----
+    // ---- s: to base 2, with the keys' scales, less the base M; so: with the values' exponents too ----
     float so[MT][N8][4];
+    Pair vs[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 key = s_key[warp][mt * 16 + k * 8 + g];
-        const Pair ks = pair(key.x, key.x), see = pair(key.y, key.y), vs = pair(key.z, key.z);
+        const float2 key = s_key[warp][mt * 16 + k * 8 + g];
+        vs[mt][k] = pair(key.y, key.y);
 #pragma unroll
         for (int n = 0; n < N8; ++n) {
-          float *const x = &s[mt][n][k * 2], *const y = &so[mt][n][k * 2];
-          const Pair p = fma2(mul2(pair(x[0], x[1]), pair(q_scale[n][0], q_scale[n][1])), ks, see);
-          const float2 u = apart(p), v = apart(add2(p, vs));
-          x[0] = u.x, x[1] = u.y, y[0] = v.x, y[1] = v.y;
+          float* const x = &s[mt][n][k * 2];
+          const float2 u = apart(fma2(mul2(pair(x[0], x[1]), pair(q_scale[n][0], q_scale[n][1])), pair(key.x, key.x),
+                                      pair(minus_M[n][0], minus_M[n][1])));
+          x[0] = u.x, x[1] = u.y;
         }
       }
-    // ---- running maxima ----
-    bool more = false;
-    float top[N8][2], top_o[N8][2];
+    if (last || walk.tile == 0) {  // rows out of sight
+      const int first = walk.s.p0(walk.tile);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int p = first + mt * 16 + k * 8 + g;
+          const bool see = p >= walk.s.lo && (unsigned)p < (unsigned)walk.s.len;
+          if (!see) vs[mt][k] = pair(0.f, 0.f);
+#pragma unroll
+          for (int n = 0; n < N8; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (!see) s[mt][n][k * 2 + j] = -INFINITY;
+        }
+    }
+    auto add_vs = [&] {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < N8; ++n) {
+            const float2 v = apart(add2(pair(s[mt][n][k * 2], s[mt][n][k * 2 + 1]), vs[mt][k]));
+            so[mt][n][k * 2] = v.x, so[mt][n][k * 2 + 1] = v.y;
+          }
+    };
+    add_vs();
+    // ---- running maxima: M of the scores, E of what stands in so ----
+    auto top_of = [&](const float (&x)[MT][N8][4], int n, int j) {
+      float m = fmaxf(x[0][n][j], x[0][n][2 + j]);
+#pragma unroll
+      for (int mt = 1; mt < MT; ++mt) m = fmaxf(m, fmaxf(x[mt][n][j], x[mt][n][2 + j]));
+      return m;
+    };
+    bool more = first_tile;
+    float top[N8][2];
 #pragma unroll
     for (int n = 0; n < N8; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        top[n][j] = fmaxf(s[0][n][j], s[0][n][2 + j]);
-        top_o[n][j] = fmaxf(so[0][n][j], so[0][n][2 + j]);
-#pragma unroll
-        for (int mt = 1; mt < MT; ++mt) {
-          top[n][j] = fmaxf(top[n][j], fmaxf(s[mt][n][j], s[mt][n][2 + j]));
-          top_o[n][j] = fmaxf(top_o[n][j], fmaxf(so[mt][n][j], so[mt][n][2 + j]));
-        }
-        more |= top[n][j] > M[n][j] || top_o[n][j] > Mo[n][j];
+        top[n][j] = top_of(s, n, j);
+        more |= top[n][j] > kSlackM || top_of(so, n, j) > E[n][j] + kSlackE;
       }
     if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
       for (int n = 0; n < N8; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          float m = top[n][j];
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) {
-            top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(0xffffffffu, top[n][j], x));
-            top_o[n][j] = fmaxf(top_o[n][j], __shfl_xor_sync(0xffffffffu, top_o[n][j], x));
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+          // how far the base moves: to the largest score, the first time also down
+          const float by = first_tile ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
+          L[n][j] = first_tile ? 0.f : L[n][j] * ex2(-by);
+          E[n][j] -= by;
+          minus_M[n][j] -= by;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            s[mt][n][j] -= by;
+            s[mt][n][2 + j] -= by;
           }
-          const float m = fmaxf(M[n][j], top[n][j]), mo = fmaxf(Mo[n][j], top_o[n][j]);
-          L[n][j] *= m == -INFINITY ? 0.f : ex2(M[n][j] - m);
-          const float f = mo == -INFINITY ? 0.f : ex2(Mo[n][j] - mo);
-          M[n][j] = m;
-          Mo[n][j] = mo;
+        }
+      add_vs();
+#pragma unroll
+      for (int n = 0; n < N8; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float m = top_of(so, n, j);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+          m = fmaxf(m, E[n][j]);
+          const float f = m == -INFINITY ? 0.f : ex2(E[n][j] - m);
+          E[n][j] = m;
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c) {
             o[c][n][j] *= f;
@@ -630,21 +675,15 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     uint32_t pf[MT][N8][2];
 #pragma unroll
     for (int n = 0; n < N8; ++n) {
-      float mu[2], mo[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        mu[j] = M[n][j] == -INFINITY ? 0.f : -M[n][j];
-        mo[j] = kShift - (Mo[n][j] == -INFINITY ? 0.f : Mo[n][j]);
-      }
-      const Pair mu2 = pair(mu[0], mu[1]), mo2 = pair(mo[0], mo[1]);
+      const Pair shift = pair(kShift - (E[n][0] == -INFINITY ? 0.f : E[n][0]), kShift - (E[n][1] == -INFINITY ? 0.f : E[n][1]));
       Pair sum = pair(L[n][0], L[n][1]);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float *const x = &s[mt][n][k * 2], *const y = &so[mt][n][k * 2];
-          const float2 u = apart(add2(pair(x[0], x[1]), mu2)), v = apart(add2(pair(y[0], y[1]), mo2));
-          sum = add2(sum, pair(ex2(u.x), ex2(u.y)));
+          const float2 v = apart(add2(pair(y[0], y[1]), shift));
+          sum = add2(sum, pair(ex2(x[0]), ex2(x[1])));
           const __half2 hv = __floats2half2_rn(ex2(v.x), ex2(v.y));
           pf[mt][n][k] = transposed(*reinterpret_cast<const uint32_t*>(&hv));
         }
@@ -685,8 +724,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
           float sum = L[n][j];
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-          // O 2^(Mo - M - kShift) / L; the power in two halves, each in range
-          const float f = M[n][j] == -INFINITY ? 0.f : ex2(0.5f * (Mo[n][j] - M[n][j] - kShift));
+          // O 2^(E - kShift) / L; the power in two halves, each in range
+          const float M = sum == 0.f ? -INFINITY : -minus_M[n][j], f = ex2(0.5f * (E[n][j] - kShift));
           const float f2 = sum == 0.f ? 0.f : f / sum;
           const int r = n * 8 + 2 * t + j;
           if (!done) {
@@ -694,13 +733,13 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
             for (int c = 0; c < C::kChunks; ++c)
               *reinterpret_cast<float2*>(po + r * D + c * 16 + 2 * g) =
                   make_float2(o[c][n][j] * f * f2, o[c][n][2 + j] * f * f2);
-            if (g == 0) ml[r] = make_float2(M[n][j], sum);
+            if (g == 0) ml[r] = make_float2(M, sum);
           } else if (r < rows) {
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
               *reinterpret_cast<uint32_t*>(a.out + (first_row + r) * D + c * 16 + 2 * g) =
                   pack_bf16(o[c][n][j] * f * f2, o[c][n][2 + j] * f * f2);
-            if (a.lse && g == 0) a.lse[first_row + r] = sum == 0.f ? -INFINITY : (M[n][j] + log2f(sum)) * kLn2;
+            if (a.lse && g == 0) a.lse[first_row + r] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
           }
         }
       if (!done && lane == 0) {
@@ -896,7 +935,7 @@ struct DecodeWs {
   size_t rec, ml, o, warp_ml, warp_o, total;
 };
 
-constexpr int kMostWarps = 16;
+constexpr int kMostWarps = 12;
 
 DecodeWs decode_ws(const lmoe_decode_dims* d, const lmoe_kv_cache_fp8* c, int ctas) {
   const size_t rows = 8 * (size_t)eights(d, c), row = c->head_dim * sizeof(float);

@@ -186,6 +186,33 @@ def test_scales_of_any_size(lm, k_exp, v_exp, zero):
         Case([700, 31, 1], d=d, k_exp=k_exp, v_exp=v_exp, zero_rows=zero, seed=6).check(lm)
 
 
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e9, 1e30])
+def test_far_scores(lm, size):
+    """However large the scores are, a row with one position in sight gets that position's value, and one whose first
+    position's score lies far above the others gets the first's."""
+    for d in (64, 128):
+        c = Case([1, 40, 300], hq=8, hk=2, d=d, window=1, v_exp=(-9, 9), seed=7, qscale=size)
+        out, _ = c.run(lm)
+        v = fp8_ref.values(c.codes[1], c.sc[1])
+        c2 = Case([200], hq=8, hk=2, d=d, v_exp=(-9, 9), seed=8)
+        c2.codes[0][np.isin(c2.sc[0], 255, invert=True)] = 0
+        c2.codes[0][c2.table[0][0], :, 0] = 0x38  # ones; the other keys are zero
+        c2.sc[0][c2.table[0][0], :, 0] = 127
+        c2.k.copy_(dev(c2.codes[0]))
+        c2.ks.copy_(dev(c2.sc[0]))
+        c2.q.fill_(size)
+        out2, _ = c2.run(lm)
+        want2 = fp8_ref.values(c2.codes[1], c2.sc[1])[c2.table[0][0], :, 0]
+        pairs = [(out2[0], want2)]
+        for b, n in enumerate((1, 40, 300)):
+            pairs.append((out[b], v[c.table[b][(n - 1) // c.bs], :, (n - 1) % c.bs]))
+        for got, want in pairs:
+            got = got.float().cpu().numpy().astype(np.float64).reshape(2, 4, d)
+            # exact products and a power of two: only the quotient by the sum, 1, is off
+            assert np.abs(got - want[:, None]).max() <= 2.0**-8 * np.abs(want).max()
+            assert (np.abs(got - want[:, None]) <= 2.0**-8 * np.abs(want[:, None])).all()
+
+
 def test_a_key_that_holds_all_with_small_values(lm):
     # the largest score has the smallest values: they must come through at full precision
     c = Case([64], hq=1, hk=1, d=128, seed=9)
