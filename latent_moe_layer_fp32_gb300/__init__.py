@@ -552,6 +552,12 @@ def _rows_of(n, t, heads, width, what):
     return at
 
 
+def _here(t, what):
+    """Launches go to the current device: a tensor of another one is refused, not read from there."""
+    if t.get_device() != _device():
+        raise ValueError(f"{what}: on cuda:{t.get_device()}, but the current device is cuda:{_device()}")
+
+
 def rope_dims_of(n_tokens, q_heads, k_heads, head_dim, rot_dim=None, n_axes=1, interleaved=False, norm=True,
                  eps=1e-6) -> LmoeRopeDims:
     """rot_dim None: the whole head is turned."""
@@ -572,6 +578,7 @@ def lmoe_qk_norm_rope(dims, q, k, q_gain, k_gain, pos, inv_freq, axis, q_out, k_
     if hk:
         kp, ks = _rows_of(t, k, hk, d, "k")
         ko, kos = _rows_of(t, k_out, hk, d, "k_out")
+    _here(q_out if hq else k_out, "q_out" if hq else "k_out")
     rc = load().lmoe_qk_norm_rope(
         ctypes.byref(dims), qp, qs, kp, ks, _arg(q_gain, d, _BF16_ONLY, "q_gain"), _arg(k_gain, d, _BF16_ONLY, "k_gain"),
         _i32(pos, dims.n_axes * t, "pos"), _arg(inv_freq, half, _F32, "inv_freq"), _i32(axis, half, "axis"), qo, qos, ko,
@@ -617,6 +624,7 @@ def lmoe_kv_write_fp8(cache, k_new, v_new, src, slots, ws=None, stream=None):
     kp, ks = _rows(k_new, hk, d, "k_new")
     vp, vs = _rows(v_new, hk, d, "v_new")
     w, nb = _ws_arg(ws)
+    _here(k_new, "k_new")
     rc = load().lmoe_kv_write_fp8(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
                                   _i32(src, n, "src"), _i32(slots, 1, "slots"), n, w, nb, _stream_arg(stream))
     if rc:
@@ -632,6 +640,7 @@ def lmoe_kv_read_fp8(cache, token_offsets, first, block_table, k_out, v_out, ws=
     kp, ks = _rows(k_out, hk, d, "k_out")
     vp, vs = _rows(v_out, hk, d, "v_out")
     w, nb = _ws_arg(ws)
+    _here(k_out, "k_out")
     rc = load().lmoe_kv_read_fp8(ctypes.byref(cache), b, min(k_out.shape[0], v_out.shape[0]), block_table.shape[1],
                                  _i32(token_offsets, 2, "token_offsets"), _i32(first, b, "first"),
                                  _i32(block_table, 1, "block_table"), kp, ks, vp, vs, w, nb, _stream_arg(stream))
@@ -652,6 +661,7 @@ def lmoe_decode_attention_fp8(dims, cache, q, lens, block_table, out, lse, ws, s
     that the 8-bit cache holds of it; lse may be None."""
     b, hq, d = dims.n_requests, dims.q_heads, cache.head_dim
     qp, qs = _rows_of(b, q, hq, d, "q")
+    _here(q, "q")
     rc = load().lmoe_decode_attention_fp8(
         ctypes.byref(dims), ctypes.byref(cache), qp, qs, _i32(lens, b, "lens"),
         _i32(block_table, b * dims.max_blocks, "block_table"), _arg(out, b * hq * d, _BF16_ONLY, "out"),

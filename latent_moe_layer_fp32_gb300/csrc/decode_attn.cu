@@ -1,5 +1,39 @@
 // Attention of one new token a request over the 8-bit paged cache
 // (include/lmoe.h has the contract).
+//
+// A key head's codes are read once for up to 16 query heads: 2 D + 2 bytes a
+// position for 4 D flops a query head, so HBM bounds it up to 8 of them, and the
+// arithmetic from there on.  What follows from that:
+//  - Keys (and the values' columns) are the 16 rows of a tensor-core product and
+//    the query heads its 8 columns, so that 8 heads waste nothing.  Codes become
+//    f16 exactly on their way from shared memory into the fragments; queries
+//    are f16 exactly after a power of two.  A product takes 8 clocks of an SM
+//    quarter and 16% of the tensor pipe's time: tcgen05 would have to read
+//    queries and probabilities as further E4M3 parts from shared memory, for
+//    a pipe that is not what bounds.  (Products of E4M3 codes with queries in
+//    two E4M3 parts, which need no conversion of the keys, were slower: 70.2
+//    instead of 67.8 us for 64 requests of 512 to 8191 positions.)
+//  - The scales are powers of two for a whole row, so K's multiply a score, and
+//    V's are an exponent that is added to the probability's: no element is
+//    multiplied.  The sums O have a running maximum of their own for that, as a
+//    key with small values may hold all of a row's weight.
+//  - The tiles of all requests and heads stand in one line that is cut evenly
+//    over all warps, with no host knowledge of lengths; a segment that is cut
+//    leaves partial sums, joined in the order of the line (by the CTA in shared
+//    memory, across CTAs by a second kernel), so results do not depend on timing.
+//  - A warp has a ring of tiles of its own and meets the others only at the end.
+//    Whole tiles come by bulk tensor copies, evict-first (16-byte copies by
+//    lanes: 75 us instead of 68; without the hint 70 instead of 65); edges come by
+//    lanes, which fill what is out of sight with zeros, so that NaN there has no
+//    effect.  8 warps and 3 tiles with 128 columns, 12 and 2 with 64; a number
+//    that is no multiple of 4 leaves the SM's quarters uneven (10 warps: 75 us).
+//
+// 64 requests of 512 to 8191 positions (365 MB) take 63 to 65 us, 5600 to 5800
+// GB/s; 256 requests of 20 to 8191 (814 MB) 125 us, 6510 GB/s, 96% of the copy
+// rate; one request at 131071 positions 48.3 us.  About 8 us of each are start-up
+// (launch, lengths, page numbers, first copy: 4.5), the join and the second
+// kernel (3.5).  16 heads a key head: 81 us for the 64 requests, bound by the
+// arithmetic's latency (two warps an SM quarter, 1.7 instructions a clock).
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -16,10 +50,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-constexpr int kEnd = 2;          // what a segment's end costs, in tiles
+// What a segment's end weighs in the cut, in tiles: 256 requests take 143 us with 0, 133 with 1, 125 with 2, 126 with 3
+// (and a batch of short ones 19.7, 20.5 and 21.5 us with 1, 2 and 3).
+constexpr int kEnd = 2;
 // The base of a row's powers is its largest score when it last moved.  It moves again where a power would pass
 // 2^kSlackM, which fp32 sums do not mind, or one with its value's exponent 2^kSlackE, which keeps f16, where they stand
-// times 2^kShift, below 2^16.  (Where it followed every new maximum, four tiles of ten moved it: MOVED.)
+// times 2^kShift, below 2^16.  (Where it followed every new maximum, 64 requests of 16
+// heads a key head took 88 us instead of 81.)
 constexpr float kSlackM = 8.f, kSlackE = 1.9f, kShift = 14.f;
 
 struct DecodeArgs {
@@ -30,10 +67,10 @@ struct DecodeArgs {
   uint16_t* out;
   float* lse;
   Status* status;  // the workspace's status word
-  int4* rec;       // [ctas] {request, head group, last CTA of the cut segment or -1, error}
-  float2* ml;      // [2 ctas][NQ] maximum and sum of each piece's rows
-  float* o;        // [2 ctas][NQ][D] their outputs
-  float2* warp_ml; // [ctas kWarps][NQ], pieces that a warp has to put down on its way
+  int4* rec;        // [ctas] {request, key head and query group, last CTA of a cut segment or -1, error}
+  float2* ml;       // [2 ctas][rows] maximum and sum of each piece's rows
+  float* o;         // [2 ctas][rows][D] their outputs
+  float2* warp_ml;  // [ctas][warps][rows] and [D], pieces that a warp has to put down on its way
   float* warp_o;
   int B, G, groups, max_blocks, window, bs_shift, ctas;
   float scale_log2;
@@ -197,7 +234,9 @@ struct Walk {
   }
 };
 
-// N8: groups of eight query rows that a key's codes are used for; W warps; S tiles of KT keys in a warp's ring.
+// N8: groups of eight query rows that a key's codes are used for; W warps; S tiles of KT keys in a warp's ring.  Tiles
+// of 8 KB: with 64 columns, 64 keys instead of 32 make more of a tile's steps independent (window layer 25.6 instead of
+// 27.7 us, 8 heads a key head 39.9 instead of 46.7 us).
 template <int D, int N8>
 struct Cfg {
   static constexpr int W = D == 64 && N8 == 1 ? 12 : 8, KT = 4096 / D, S = D == 128 && N8 == 1 ? 3 : 2;
@@ -211,7 +250,7 @@ struct Cfg {
   // with 16 query rows, their fragments stand in shared memory: registers are what bounds the number of warps
   static constexpr bool kQueriesInSmem = N8 == 2;
   static constexpr int kQueries = kQueriesInSmem ? W * N8 * kChunks * 32 * 8 : 0;
-  static constexpr int kSmem = kRing + kQueries + 1024;  // the ring starts on a 1024-byte boundary (the swizzle's period)
+  static constexpr int kSmem = kRing + kQueries + 1024;  // (the ring starts on 1024 bytes, the swizzle's period)
   static_assert(8192 <= 32 * kThreads, "the most requests: no run has more than a warp's lanes");
   static_assert(kPiece * 4 <= S * kStage, "a warp's last piece takes its ring's place");
   static_assert(KT == 32 || KT == 64, "whole warps of keys");
@@ -235,7 +274,8 @@ __device__ __forceinline__ void unrolled(F&& f) {
 }
 
 template <int D, int N8>
-__global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
+__global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
+    decode_attn_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<D, N8>;
   constexpr int W = C::W, KT = C::KT, MT = KT / 16;
@@ -246,7 +286,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
   __shared__ __align__(16) uint8_t s_scale[W][C::S][2 * KT];  // of the ring's tiles: K's, V's
   __shared__ unsigned long long s_scan[W], s_before[C::kThreads];
   __shared__ unsigned s_live[W];
-  __shared__ int4 s_seg[W][2];  // a warp's pieces, put down on the way and at its range's end: {request, head, group, flags}
+  // a warp's pieces, put down on the way and at its range's end: {request, key head, first query row, flags}
+  __shared__ int4 s_seg[W][2];
   __shared__ float2 s_ml[W][C::kRows];
   __shared__ int s_last, s_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -453,9 +494,10 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     copies_end();
   }
 
-  uint2 qf[C::kQueriesInSmem ? 1 : N8][C::kChunks];  // the queries' fragments, as f16 times a power of two of each row's
-  uint2* const s_q = reinterpret_cast<uint2*>(s_ring + C::kRing) + warp * N8 * C::kChunks * 32 + lane;  // or here
-  float q_scale[N8][2];        // what makes a product with them a score to base 2, for this lane's two columns
+  // the queries' fragments, as f16 times a power of two of each row's, in one place or the other
+  uint2 qf[C::kQueriesInSmem ? 1 : N8][C::kChunks];
+  uint2* const s_q = reinterpret_cast<uint2*>(s_ring + C::kRing) + warp * N8 * C::kChunks * 32 + lane;
+  float q_scale[N8][2];  // what makes a product with them a score to base 2, for this lane's two columns
   // M, the running maximum of the scores s, and L, the sum of 2^(s - M); with the values' exponents e: E, the running
   // maximum of s - M + e, and O, the sum of 2^(s - M + e - E + kShift) times the values' codes
   float o[C::kChunks][N8][4], minus_M[N8][2], E[N8][2], L[N8][2];
@@ -675,7 +717,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
     uint32_t pf[MT][N8][2];
 #pragma unroll
     for (int n = 0; n < N8; ++n) {
-      const Pair shift = pair(kShift - (E[n][0] == -INFINITY ? 0.f : E[n][0]), kShift - (E[n][1] == -INFINITY ? 0.f : E[n][1]));
+      const Pair shift = pair(kShift - (E[n][0] == -INFINITY ? 0.f : E[n][0]),
+                              kShift - (E[n][1] == -INFINITY ? 0.f : E[n][1]));
       Pair sum = pair(L[n][0], L[n][1]);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -807,7 +850,8 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
       if (!outer && ended) {
         if (seg.z + r < a.G) {
           const size_t at = (size_t)seg.x * hq + seg.y * a.G + seg.z + r;
-          *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+          *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
+              make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
           if (a.lse && e % (D / 4) == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
       } else {
@@ -823,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1) decode_attn_kernel(co
 }
 
 // A segment that several CTAs share: its pieces joined in the order of the line, a CTA for the one that its first
-// piece is from.  The first CTA also reports what the others found wrong.
+// piece is from.  Beside that the rows of requests without positions, and by the first CTA what the others found wrong.
 template <int D, int N8>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
   using C = Cfg<D, N8>;
@@ -837,7 +881,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
     for (int i = threadIdx.x; i < a.ctas; i += blockDim.x)
       if (const int e = a.rec[i].w) atomicMax(&s_err, e);
     __syncthreads();
-    if (threadIdx.x == 0) *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
+    if (threadIdx.x == 0)
+      *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
   }
   const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4), hq = a.c.kv_heads * a.G;
   auto fetch = [&](float2 (&ml)[U], float4 (&o)[U], int p0, int end) {

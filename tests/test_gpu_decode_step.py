@@ -166,3 +166,19 @@ def test_a_request_that_finds_no_block_keeps_its_answers(lm):
     want = fp8_ref.values(*fp8_ref.quantise(v[0]))  # one position: the value itself
     assert np.abs(host(loop.out)[0].reshape(2, 2, 64) - want[:, None]).max() <= 2.0**-10 * np.abs(want).max()
     assert not loop.out[1].any() and torch.isneginf(loop.lse[1]).all()
+
+
+def test_another_device_is_refused(lm, monkeypatch):
+    loop = Loop(lm, 2, 4, 2, 64, 16, 2)
+    i32 = dict(device="cuda", dtype=torch.int32)
+    off, rows = torch.zeros(3, **i32), torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    calls = (lambda: lm.lmoe_qk_norm_rope(loop.rope, loop.q, loop.k, None, None, loop.state[0], loop.freq, None, loop.q, loop.k),
+             lambda: lm.lmoe_kv_write_fp8(loop.cache, loop.k, loop.v, None, loop.slots),
+             lambda: lm.lmoe_kv_read_fp8(loop.cache, off, None, loop.table, rows, rows.clone()),
+             lambda: lm.lmoe_decode_attention_fp8(loop.dims, loop.cache, loop.q, loop.state[0], loop.table, loop.out, loop.lse,
+                                                  loop.ws))
+    here = torch.cuda.current_device()
+    monkeypatch.setattr(lm, "_device", lambda: here + 1)  # as if another device were the current one
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
