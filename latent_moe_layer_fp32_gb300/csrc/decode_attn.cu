@@ -28,12 +28,12 @@
 //    effect.  8 warps and 3 tiles with 128 columns, 12 and 2 with 64; a number
 //    that is no multiple of 4 leaves the SM's quarters uneven (10 warps: 75 us).
 //
-// 64 requests of 512 to 8191 positions (365 MB) take 63 to 65 us, 5600 to 5800
-// GB/s; 256 requests of 20 to 8191 (814 MB) 125 us, 6510 GB/s, 96% of the copy
-// rate; one request at 131071 positions 48.3 us.  About 8 us of each are start-up
-// (launch, lengths, page numbers, first copy: 4.5), the join and the second
-// kernel (3.5).  16 heads a key head: 81 us for the 64 requests, bound by the
-// arithmetic's latency (two warps an SM quarter, 1.7 instructions a clock).
+// 64 requests of 512 to 8191 positions (365 MB) take 65 us, 5600 GB/s; 256 requests
+// of 20 to 8191 (814 MB) 137 us, 5950 GB/s, 88% of the copy rate; one request at
+// 131071 positions 48.8 us.  About 8 us of each are start-up (launch, lengths, page
+// numbers, first copy: 4.5), the join and the second kernel (3.5).  16 heads a key
+// head: 81 us for the 64 requests, bound by the arithmetic's latency (two warps an
+// SM quarter, 1.7 instructions a clock).
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -50,8 +50,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-// What a segment's end weighs in the cut, in tiles: 256 requests take 143 us with 0, 133 with 1, 125 with 2, 126 with 3
-// (and a batch of short ones 19.7, 20.5 and 21.5 us with 1, 2 and 3).
+// What a segment's end weighs in the cut, in tiles: 256 requests of 20 to 8191 positions take 168 us with 0, 146 with 1,
+// 137 with 2, 139 with 4; 256 of 3 to 200 positions 21.5, 21.0, 21.4 and 22.6.
 constexpr int kEnd = 2;
 // The base of a row's powers is its largest score when it last moved.  It moves again where a power would pass
 // 2^kSlackM, which fp32 sums do not mind, or one with its value's exponent 2^kSlackE, which keeps f16, where they stand

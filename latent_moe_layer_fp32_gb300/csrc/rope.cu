@@ -9,9 +9,10 @@
 // sines of a token are eight registers (as a table in shared memory, made by each
 // token's CTA: 184 us instead of 113 for the prompt below).
 //
-// 16384 tokens of 72 heads of 128 (604 MB) take 103 us, 5850 GB/s, 86% of the copy
-// rate; one token 2.9 us.  Heads of 80 use 10 of 16 lanes: 5003 tokens of 32 heads
-// (51 MB) take 16 us, bound by instructions and latency.
+// 16384 tokens of 72 heads of 128 (604 MB) take 98.4 us, 6140 GB/s, 91% of the copy
+// rate; one token 2.7 us.  Heads of 80 use 10 of 16 lanes: 5003 tokens of 32 heads
+// (51 MB) take 15.8 us, bound by instructions and latency (three heads on 30 lanes,
+// with sums over ten lanes, took 19.6).
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,8 +23,8 @@ namespace lmoe {
 namespace {
 
 constexpr int kThreads = 256;
-// Units that a warp has under way, twice, and CTAs of an SM: with three CTAs the registers do not suffice (prompt 118
-// instead of 103 us); three or six units a batch take 113 and 103.5 us.
+// Units that a warp has under way, twice, and CTAs of an SM: the prompt takes 98.4 us, with three or five units a batch
+// 110 and 98.2 (and the smaller video 17.1 and 16.3 instead of 15.8), with three CTAs of three units 103.
 constexpr int kBatch = 4, kCtas = 2;
 
 struct RopeArgs {
@@ -89,9 +90,10 @@ __device__ __forceinline__ Pair swapped(Pair p) {
   return pair(f.y, f.x);
 }
 
-// LP lanes a head, so that a unit is 32 / LP heads; PAIRS: neighbours are pairs (else the halves' elements).  The
+// LP lanes a head, so that a unit is 32 / LP heads; PAIRS: neighbours are pairs (else the halves' elements); FULL: a head
+// fills its lanes.  The
 // units of all tokens, a token's queries first, are cut evenly over the warps.
-template <int LP, bool PAIRS>
+template <int LP, bool PAIRS, bool FULL>
 __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int NP = 32 / LP;
   pdl_wait();
@@ -101,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
   const unsigned all = (unsigned)a.T * (unsigned)a.units;
   const unsigned each = all / (unsigned)a.warps, more = all - each * (unsigned)a.warps;
   unsigned u = (unsigned)id * each + min((unsigned)id, more), left = id < a.warps ? each + ((unsigned)id < more) : 0;
-  const bool in = 8 * j < a.d, turned = 8 * j < a.rot;
+  const int d = FULL ? 8 * LP : a.d;
+  const bool in = FULL || 8 * j < d, turned = 8 * j < a.rot;
   const int o1 = !PAIRS && turned ? 4 * j : 8 * j, o2 = !PAIRS && turned ? half + 4 * j : 8 * j + 4;
 
   // this lane's frequencies and gains
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
     gain[side][0] = there ? *reinterpret_cast<const uint2*>(g + o1) : make_uint2(0x3f803f80u, 0x3f803f80u);
     gain[side][1] = there ? *reinterpret_cast<const uint2*>(g + o2) : make_uint2(0x3f803f80u, 0x3f803f80u);
   }
-  const float inv_d = 1.f / (float)a.d;
+  const float inv_d = 1.f / (float)d;
 
   // a batch is up to kBatch units of one token's queries (side 0) or keys; the next one's rows are on their way while
   // one is worked on, and with a token's first its positions
@@ -148,13 +151,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
 #pragma unroll
     for (int e = 0; e < 4; ++e) next.pos[e] = turned ? a.pos[(size_t)ax[e] * a.T + next.t] : 0;
     const int heads = next.side ? a.hk : a.hq;
-    const uint16_t* const src = next.side ? a.k + (size_t)next.t * a.ks : a.q + (size_t)next.t * a.qs;
+    const uint16_t* const src = (next.side ? a.k + (size_t)next.t * a.ks : a.q + (size_t)next.t * a.qs) +
+                                (size_t)(next.first * NP + sub) * d;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = (next.first + i) * NP + sub;
       next.x[i][0] = next.x[i][1] = make_uint2(0, 0);
       if (i < next.n && h < heads && in) {
-        const uint16_t* const row = src + (size_t)h * a.d;
+        const uint16_t* const row = src + i * NP * d;
         if constexpr (PAIRS) {
           const uint4 w = *reinterpret_cast<const uint4*>(row + o1);
           next.x[i][0] = make_uint2(w.x, w.y);
@@ -167,23 +171,38 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
     }
   };
   fetch();
-  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {};
+  // cosines, sines and less the sines of the token, as pairs: of neighbours' angles, or of one angle for a pair
+  // (cos, cos), (-sin, sin)
+  Pair cc[PAIRS ? 4 : 2], ss[PAIRS ? 4 : 2], minus[PAIRS ? 1 : 2];
   unsigned at = ~0u;  // the token of the cosines
   while (next.n > 0) {
     const Batch now = next;
     fetch();
     if (now.t != at) {
       at = now.t;
+      float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {};
       if (turned) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           sincospif((float)(int32_t)((uint64_t)(long long)now.pos[e] * step[e] >> 32) * 0x1p-31f, &s[e], &c[e]);
       }
+      if constexpr (PAIRS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cc[e] = pair(c[e], c[e]), ss[e] = pair(-s[e], s[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          cc[e] = pair(c[2 * e], c[2 * e + 1]);
+          ss[e] = pair(s[2 * e], s[2 * e + 1]);
+          minus[e] = pair(-s[2 * e], -s[2 * e + 1]);
+        }
+      }
     }
     const uint2 g1 = now.side ? gain[1][0] : gain[0][0], g2 = now.side ? gain[1][1] : gain[0][1];
     const Pair g[4] = {unpack(g1.x), unpack(g1.y), unpack(g2.x), unpack(g2.y)};
     const int heads = now.side ? a.hk : a.hq;
-    uint16_t* const dst = now.side ? a.k_out + (size_t)now.t * a.kos : a.q_out + (size_t)now.t * a.qos;
+    uint16_t* const dst = (now.side ? a.k_out + (size_t)now.t * a.kos : a.q_out + (size_t)now.t * a.qos) +
+                          (size_t)(now.first * NP + sub) * d;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (i >= now.n) break;
@@ -202,19 +221,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
       }
       if constexpr (PAIRS) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], pair(c[e], c[e]), mul2(swapped(v[e]), pair(-s[e], s[e])));
+        for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], cc[e], mul2(swapped(v[e]), ss[e]));
       } else if (turned) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const Pair cc = pair(c[2 * e], c[2 * e + 1]), ss = pair(s[2 * e], s[2 * e + 1]);
-          const Pair minus = pair(-s[2 * e], -s[2 * e + 1]), x = v[e], y = v[2 + e];
-          v[e] = fma2(x, cc, mul2(y, minus));
-          v[2 + e] = fma2(y, cc, mul2(x, ss));
+          const Pair x = v[e], y = v[2 + e];
+          v[e] = fma2(x, cc[e], mul2(y, minus[e]));
+          v[2 + e] = fma2(y, cc[e], mul2(x, ss[e]));
         }
       }
       const int h = (now.first + i) * NP + sub;
       if (h < heads && in) {
-        uint16_t* const row = dst + (size_t)h * a.d;
+        uint16_t* const row = dst + i * NP * d;
         if constexpr (PAIRS) {
           *reinterpret_cast<uint4*>(row + o1) = make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3]));
         } else {
@@ -234,8 +252,10 @@ int run_rope(RopeArgs a, bool pairs, int sms, cudaStream_t s) {
   a.uq = (a.hq + NP - 1) / NP;
   a.units = a.uq + (a.hk + NP - 1) / NP;
   a.warps = (int)std::min((long long)a.T * a.units, (long long)sms * kCtas * kWarps);
+  void (*const kern[2][2])(const RopeArgs) = {{qk_norm_rope_kernel<LP, false, false>, qk_norm_rope_kernel<LP, false, true>},
+                                              {qk_norm_rope_kernel<LP, true, false>, qk_norm_rope_kernel<LP, true, true>}};
   return launch_pdl("qk_norm_rope_kernel", dim3((a.warps + kWarps - 1) / kWarps), dim3(kThreads), 0, s,
-                    pairs ? qk_norm_rope_kernel<LP, true> : qk_norm_rope_kernel<LP, false>, a);
+                    kern[pairs][a.d == 8 * LP], a);
 }
 
 }  // namespace
