@@ -396,8 +396,9 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
 
   // ---- a tile's way: its pages are looked up, its rows copied, its products formed ----
   constexpr int kLanes = 32 / MT;  // a group of lanes for each 16 keys
-  int page = 0;                    // block number of the page that holds this lane's 16 keys of the looked-up tile
-  int look_h = 0, look_in = 0, look_lo = 0, look_hi = 0;
+  // block numbers of 512 positions of a request, a lane for 16: those from the tile `pages_tile` on
+  int pages = 0, pages_b = -1, pages_tile = 0;
+  int look_h = 0, look_in = 0, look_lo = 0, look_hi = 0, look_part = 0;  // (its first 16 keys' lane of `pages`)
   bool looked = false;
   int to_stage = 0;
   auto look = [&] {
@@ -414,8 +415,14 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
                                                       (size_t)(ahead.h * a.G + r) * D + lane * 64 % D));
     }
     look_in = p0;
-    const int p = min(max(p0 + lane / kLanes * 16, p0 + look_lo), p0 + look_hi - 1);
-    page = a.table[(size_t)ahead.b * a.max_blocks + (p >> a.bs_shift)];
+    if (ahead.b != pages_b || (unsigned)(ahead.tile - pages_tile) >= 512 / KT) {
+      pages_b = ahead.b;
+      pages_tile = ahead.tile;
+      const long long at = (long long)p0 + lane * 16;
+      const int p = (int)min(max(at, (long long)ahead.s.lo), (long long)ahead.s.len - 1);
+      pages = a.table[(size_t)ahead.b * a.max_blocks + (p >> a.bs_shift)];
+    }
+    look_part = (ahead.tile - pages_tile) * MT;
     ahead.next(a);
   };
   constexpr int kStep = 32 / C::kChunks;  // rows that one copy instruction takes
@@ -431,6 +438,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   uint32_t bulk = 0, parity = 0, by_lanes = 0;
   auto copy = [&] {  // the tile that was looked up
     const uint32_t to = ring32 + to_stage * C::kStage, bit = 1u << to_stage, mask = (1u << a.bs_shift) - 1;
+    const int page = __shfl_sync(0xffffffffu, pages, look_part + lane / kLanes);
     const bool fine = __all_sync(0xffffffffu, (unsigned)page < (unsigned)a.c.n_blocks);
     if (look_lo == 0 && look_hi == KT && fine) {
       // all its rows are in sight: K and V in bulk, a lane a page
