@@ -393,7 +393,7 @@ def lmoe_block_forward(dims, weights: LmoeWeights, norms: LmoeBlockNorms, x, y, 
 _I64 = (torch.int64, torch.uint64)
 _INT32 = torch.int32
 _BF16_ONLY = (torch.bfloat16,)
-_BF16_DTYPE = torch.bfloat16
+_BF16_DTYPE, _FP32 = torch.bfloat16, torch.float32
 
 
 def _arg(t, n, dtypes, what):
@@ -537,25 +537,40 @@ def lmoe_kv_write(cache, k_new, v_new, src, slots, ws=None, stream=None):
         raise LmoeError(rc, "lmoe_kv_write")
 
 
-def _rows_of(n, t, heads, width, what):
-    """_rows of a tensor of at least n rows, with the shortest path for what is right."""
+def _elsewhere(t, dev, what):
+    """Launches go to the current device: a tensor of another one is refused, not read from there."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+
+
+def _rows_of(dev, n, t, heads, width, what):
+    """_rows of a tensor of at least n rows on device dev, with the shortest path for what is right."""
     try:
-        if t.dtype is _BF16_DTYPE and t.is_cuda:
+        if t.dtype is _BF16_DTYPE and t.get_device() == dev:
             (rows, h, w), (step, head, one) = t.shape, t.stride()
             if rows >= n and h == heads and w == width and one == 1 and (head == width or heads == 1):
                 return t.data_ptr(), step if rows > 1 else heads * width
     except (AttributeError, ValueError):
         pass
     at = _rows(t, heads, width, what)  # says what is wrong
+    _elsewhere(t, dev, what)
     if t.shape[0] < n:
         raise ValueError(f"{what}: expected at least {n} rows, got {t.shape[0]}")
     return at
 
 
-def _here(t, what):
-    """Launches go to the current device: a tensor of another one is refused, not read from there."""
-    if t.get_device() != _device():
-        raise ValueError(f"{what}: on cuda:{t.get_device()}, but the current device is cuda:{_device()}")
+def _vec(dev, t, n, dtype, what):
+    """_arg for one type on device dev, likewise."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    at = _arg(t, n, (dtype,), what)
+    _elsewhere(t, dev, what)
+    return at
 
 
 def rope_dims_of(n_tokens, q_heads, k_heads, head_dim, rot_dim=None, n_axes=1, interleaved=False, norm=True,
@@ -569,20 +584,20 @@ def lmoe_qk_norm_rope(dims, q, k, q_gain, k_gain, pos, inv_freq, axis, q_out, k_
     """Norm and rotation of q [T, q_heads, d] and k [T, k_heads, d], bf16 and perhaps slices of one projection;
     gains bf16 [d] or None, pos int32 [n_axes, T], inv_freq fp32 [rot_dim / 2], axis int32 [rot_dim / 2] or None.
     q_out and k_out may be q and k themselves; with no heads a side is None."""
-    t, hq, hk, d, half = dims.n_tokens, dims.q_heads, dims.k_heads, dims.head_dim, dims.rot_dim // 2
+    t, hq, hk, d, half, dev = dims.n_tokens, dims.q_heads, dims.k_heads, dims.head_dim, dims.rot_dim // 2, _device()
     qp = kp = qo = ko = None
     qs = ks = qos = kos = 0
     if hq:
-        qp, qs = _rows_of(t, q, hq, d, "q")
-        qo, qos = _rows_of(t, q_out, hq, d, "q_out")
+        qp, qs = _rows_of(dev, t, q, hq, d, "q")
+        qo, qos = _rows_of(dev, t, q_out, hq, d, "q_out")
     if hk:
-        kp, ks = _rows_of(t, k, hk, d, "k")
-        ko, kos = _rows_of(t, k_out, hk, d, "k_out")
-    _here(q_out if hq else k_out, "q_out" if hq else "k_out")
+        kp, ks = _rows_of(dev, t, k, hk, d, "k")
+        ko, kos = _rows_of(dev, t, k_out, hk, d, "k_out")
     rc = load().lmoe_qk_norm_rope(
-        ctypes.byref(dims), qp, qs, kp, ks, _arg(q_gain, d, _BF16_ONLY, "q_gain"), _arg(k_gain, d, _BF16_ONLY, "k_gain"),
-        _i32(pos, dims.n_axes * t, "pos"), _arg(inv_freq, half, _F32, "inv_freq"), _i32(axis, half, "axis"), qo, qos, ko,
-        kos, _stream_arg(stream))
+        ctypes.byref(dims), qp, qs, kp, ks, _vec(dev, q_gain, d, _BF16_DTYPE, "q_gain"),
+        _vec(dev, k_gain, d, _BF16_DTYPE, "k_gain"), _vec(dev, pos, dims.n_axes * t, _INT32, "pos"),
+        _vec(dev, inv_freq, half, _FP32, "inv_freq"), _vec(dev, axis, half, _INT32, "axis"), qo, qos, ko, kos,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LmoeError(rc, "lmoe_qk_norm_rope")
 
@@ -620,13 +635,13 @@ def kv_cache_fp8_of(k, v, k_scale, v_scale) -> LmoeKvCacheFp8:
 def lmoe_kv_write_fp8(cache, k_new, v_new, src, slots, ws=None, stream=None):
     """lmoe_kv_write into an 8-bit cache: rows src[t] (or t, src None) of bf16 k_new and v_new
     [rows, kv_heads, d] as codes and scales in the cache's slots[t]."""
-    hk, d, n = cache.kv_heads, cache.head_dim, slots.numel()
-    kp, ks = _rows(k_new, hk, d, "k_new")
-    vp, vs = _rows(v_new, hk, d, "v_new")
+    hk, d, n, dev = cache.kv_heads, cache.head_dim, slots.numel(), _device()
+    kp, ks = _rows_of(dev, 1, k_new, hk, d, "k_new")
+    vp, vs = _rows_of(dev, 1, v_new, hk, d, "v_new")
     w, nb = _ws_arg(ws)
-    _here(k_new, "k_new")
     rc = load().lmoe_kv_write_fp8(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
-                                  _i32(src, n, "src"), _i32(slots, 1, "slots"), n, w, nb, _stream_arg(stream))
+                                  _vec(dev, src, n, _INT32, "src"), _vec(dev, slots, 1, _INT32, "slots"), n, w, nb,
+                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LmoeError(rc, "lmoe_kv_write_fp8")
 
@@ -634,16 +649,17 @@ def lmoe_kv_write_fp8(cache, k_new, v_new, src, slots, ws=None, stream=None):
 def lmoe_kv_read_fp8(cache, token_offsets, first, block_table, k_out, v_out, ws=None, stream=None):
     """Positions first[b] (0, first None) and on of every request as rows token_offsets[b] .. token_offsets[b + 1] - 1
     of bf16 k_out and v_out [rows, kv_heads, d]."""
-    hk, d, b = cache.kv_heads, cache.head_dim, token_offsets.numel() - 1
+    hk, d, b, dev = cache.kv_heads, cache.head_dim, token_offsets.numel() - 1, _device()
     if block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError(f"block_table: expected [{b}, max_blocks], got {tuple(block_table.shape)}")
-    kp, ks = _rows(k_out, hk, d, "k_out")
-    vp, vs = _rows(v_out, hk, d, "v_out")
+    kp, ks = _rows_of(dev, 1, k_out, hk, d, "k_out")
+    vp, vs = _rows_of(dev, 1, v_out, hk, d, "v_out")
     w, nb = _ws_arg(ws)
-    _here(k_out, "k_out")
-    rc = load().lmoe_kv_read_fp8(ctypes.byref(cache), b, min(k_out.shape[0], v_out.shape[0]), block_table.shape[1],
-                                 _i32(token_offsets, 2, "token_offsets"), _i32(first, b, "first"),
-                                 _i32(block_table, 1, "block_table"), kp, ks, vp, vs, w, nb, _stream_arg(stream))
+    rc = load().lmoe_kv_read_fp8(
+        ctypes.byref(cache), b, min(k_out.shape[0], v_out.shape[0]), block_table.shape[1],
+        _vec(dev, token_offsets, 2, _INT32, "token_offsets"), _vec(dev, first, b, _INT32, "first"),
+        _vec(dev, block_table, 1, _INT32, "block_table"), kp, ks, vp, vs, w, nb,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LmoeError(rc, "lmoe_kv_read_fp8")
 
@@ -659,13 +675,13 @@ def lmoe_decode_attention_fp8_workspace_bytes(dims: LmoeDecodeDims, cache: LmoeK
 def lmoe_decode_attention_fp8(dims, cache, q, lens, block_table, out, lse, ws, stream=None):
     """One new token a request, q [B, q_heads, d] (perhaps a slice of a projection), over the lens[b] positions
     that the 8-bit cache holds of it; lse may be None."""
-    b, hq, d = dims.n_requests, dims.q_heads, cache.head_dim
-    qp, qs = _rows_of(b, q, hq, d, "q")
-    _here(q, "q")
+    b, hq, d, dev = dims.n_requests, dims.q_heads, cache.head_dim, _device()
+    qp, qs = _rows_of(dev, b, q, hq, d, "q")
     rc = load().lmoe_decode_attention_fp8(
-        ctypes.byref(dims), ctypes.byref(cache), qp, qs, _i32(lens, b, "lens"),
-        _i32(block_table, b * dims.max_blocks, "block_table"), _arg(out, b * hq * d, _BF16_ONLY, "out"),
-        _arg(lse, b * hq, _F32, "lse"), *_ws_arg(ws), _stream_arg(stream))
+        ctypes.byref(dims), ctypes.byref(cache), qp, qs, _vec(dev, lens, b, _INT32, "lens"),
+        _vec(dev, block_table, b * dims.max_blocks, _INT32, "block_table"),
+        _vec(dev, out, b * hq * d, _BF16_DTYPE, "out"), _vec(dev, lse, b * hq, _FP32, "lse"), *_ws_arg(ws),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LmoeError(rc, "lmoe_decode_attention_fp8")
 

@@ -157,9 +157,9 @@ def test_binding_refuses(lib):
     with pytest.raises(ValueError):
         lm.kv_cache_fp8_of(t, t, s, s)  # not on a GPU
     with pytest.raises(TypeError):
-        lm._rows_of(4, t[0].float(), 2, 64, "q")
+        lm._rows_of(0, 4, t[0].float(), 2, 64, "q")
     with pytest.raises(ValueError):
-        lm._rows_of(4, t[0].bfloat16(), 2, 64, "q")
+        lm._rows_of(0, 4, t[0].bfloat16(), 2, 64, "q")
 
 
 def test_the_reference_quantises_as_the_formats_say():
