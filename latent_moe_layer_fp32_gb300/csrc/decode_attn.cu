@@ -76,6 +76,13 @@ struct DecodeArgs {
   float scale_log2;
 };
 
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 to 127
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -174,7 +181,7 @@ struct Sum {
     l = fmaf(l, f, w);
     o = make_float4(fmaf(w, x.x, o.x * f), fmaf(w, x.y, o.y * f), fmaf(w, x.z, o.z * f), fmaf(w, x.w, o.w * f));
   }
-  __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+  __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2; }
 };
 
 // x / y; a 32-bit division where that is enough, as 64-bit ones take hundreds of clocks.
@@ -292,13 +299,14 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   __shared__ int s_last, s_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hq = a.c.kv_heads * a.G;
-  pdl_wait();
-  pdl_trigger();
+  auto piece_at = [&](int w) { return reinterpret_cast<float*>(s_ring + w * C::S * C::kStage); };
+  // (what needs nothing of the launch before, while that one ends)
   if (threadIdx.x == 0) s_err = s_last = 0;
   if (lane < 2) s_seg[warp][lane] = make_int4(0, 0, 0, 0);
-  auto piece_at = [&](int w) { return reinterpret_cast<float*>(s_ring + w * C::S * C::kStage); };
   if (lane < C::S) mbar_init(&s_full[warp][lane], 1);
   fence_barrier_init();
+  pdl_wait();
+  pdl_trigger();
 
   // ---- the line of tiles, and this warp's part of it ----
   unsigned long long total, hi;
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   // block numbers of 512 positions of a request, a lane for 16: those from the tile `pages_tile` on
   int pages = 0, pages_b = -1, pages_tile = 0;
   int look_h = 0, look_in = 0, look_lo = 0, look_hi = 0, look_part = 0;  // (its first 16 keys' lane of `pages`)
-  bool looked = false;
+  bool looked = false;  // a tile has been looked up and not copied
   int to_stage = 0;
   auto look = [&] {
     looked = ahead.left > 0;
@@ -493,15 +501,6 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
     to_stage = to_stage == C::S - 1 ? 0 : to_stage + 1;
   };
 
-  look();
-  for (int i = 0; i < C::S - 1; ++i) {
-    if (looked) {
-      copy();
-      look();
-    }
-    copies_end();
-  }
-
   // the queries' fragments, as f16 times a power of two of each row's, in one place or the other
   uint2 qf[C::kQueriesInSmem ? 1 : N8][C::kChunks];
   uint2* const s_q = reinterpret_cast<uint2*>(s_ring + C::kRing) + warp * N8 * C::kChunks * 32 + lane;
@@ -515,11 +514,16 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   const uint32_t lane_at = (lane & 15) * D + (((lane >> 4) ^ swizzle<D>(lane & 15)) << 4);
 
   bool ok = true;
+  // The first S rounds only look up and copy: one copy of the code for both, as small calls wait for code most of all.
+  int ahead_only = C::S;
   while (walk.left > 0) {
+    const bool compute = ahead_only == 0;
     const int h = walk.h, row0 = walk.group * C::kRows;  // rows of the head's G
     const int rows = min(C::kRows, a.G - row0);
+    const bool last = walk.last(), final = walk.after() <= 0;  // of the segment, of the range
+    const uint32_t st32 = ring32 + stage * C::kStage + lane_at;
     uint2 w[N8][C::kChunks];
-    if (fresh) {  // the segment's queries, on their way while its first tile is waited for
+    if (compute && fresh) {  // the segment's queries, on their way while its first tile is waited for
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
         const int r = n * 8 + g;
@@ -529,29 +533,31 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
           w[n][i] = r < rows ? *reinterpret_cast<const uint2*>(src + i * 16) : make_uint2(0, 0);
       }
     }
-    copies_wait<C::S - 2>();
-    if (bulk >> stage & 1) {
-      // (one answer for the whole warp)
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], parity >> stage & 1, nullptr, 0));
-      if (!ok) break;
-      bulk ^= 1u << stage;
-      parity ^= 1u << stage;
-    }
-    __syncwarp();
-    const uint32_t st32 = ring32 + stage * C::kStage + lane_at;
-    const bool last = walk.last(), final = walk.after() <= 0;  // of the segment, of the range
+    if (compute) {
+      copies_wait<C::S - 2>();
+      if (bulk >> stage & 1) {
+        // (one answer for the whole warp)
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], parity >> stage & 1, nullptr, 0));
+        if (!ok) break;
+        bulk ^= 1u << stage;
+        parity ^= 1u << stage;
+      }
+      __syncwarp();
 #pragma unroll
-    for (int i = lane; i < KT; i += 32) {
-      const uint32_t kb = s_scale[warp][stage][i], vb = s_scale[warp][stage][KT + i];
-      s_key[warp][i] = make_float2(e8m0_to_f32(kb), vb == 255 ? NAN : (float)vb - 127.f);
+      for (int i = lane; i < KT; i += 32) {
+        const uint32_t kb = s_scale[warp][stage][i], vb = s_scale[warp][stage][KT + i];
+        s_key[warp][i] = make_float2(e8m0_to_f32(kb), vb == 255 ? NAN : (float)vb - 127.f);
+      }
+      __syncwarp();
     }
-    __syncwarp();
     // (the ring's oldest place is free: its tile was computed before the last __syncwarp)
-    if (looked) {
-      copy();
-      look();
-    }
+    if (looked) copy();
+    look();
     copies_end();
+    if (!compute) {
+      --ahead_only;
+      continue;
+    }
     stage = stage == C::S - 1 ? 0 : stage + 1;
     const bool first_tile = fresh;
     if (fresh) {
@@ -566,8 +572,9 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = act_exponent(top << 16);
-        const float up = ldexpf(1.f, e);
+        // 2^e brings the largest magnitude to 2^14 to 2^15 (a smaller one of 2^-113 or less stays smaller)
+        const int e = min(126, 141 - (int)(top >> 7));
+        const float up = two_to(e);
 #pragma unroll
         for (int i = 0; i < C::kChunks; ++i) {
           const uint32_t x[2] = {w[n][i].x, w[n][i].y};
@@ -584,7 +591,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int ej = __shfl_sync(0xffffffffu, e, (2 * t + j) * 4);
-          q_scale[n][j] = ldexpf(a.scale_log2, -ej);
+          q_scale[n][j] = a.scale_log2 * two_to(-ej);
           E[n][j] = -INFINITY;
           minus_M[n][j] = L[n][j] = 0.f;
         }
@@ -777,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
           for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
           // O 2^(E - kShift) / L; the power in two halves, each in range
           const float M = sum == 0.f ? -INFINITY : -minus_M[n][j], f = ex2(0.5f * (E[n][j] - kShift));
-          const float f2 = sum == 0.f ? 0.f : f / sum;
+          const float f2 = sum == 0.f ? 0.f : __fdividef(f, sum);
           const int r = n * 8 + 2 * t + j;
           if (!done) {
 #pragma unroll
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
             for (int c = 0; c < C::kChunks; ++c)
               *reinterpret_cast<uint32_t*>(a.out + (first_row + r) * D + c * 16 + 2 * g) =
                   pack_bf16(o[c][n][j] * f * f2, o[c][n][2 + j] * f * f2);
-            if (a.lse && g == 0) a.lse[first_row + r] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+            if (a.lse && g == 0) a.lse[first_row + r] = sum == 0.f ? -INFINITY : (M + lg2(sum)) * kLn2;
           }
         }
       if (!done && lane == 0) {
@@ -853,14 +860,14 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
         l += f;
         acc = make_float4(fmaf(f, x.x, acc.x), fmaf(f, x.y, acc.y), fmaf(f, x.z, acc.z), fmaf(f, x.w, acc.w));
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
       const float4 x = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (!outer && ended) {
         if (seg.z + r < a.G) {
           const size_t at = (size_t)seg.x * hq + seg.y * a.G + seg.z + r;
           *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
               make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-          if (a.lse && e % (D / 4) == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          if (a.lse && e % (D / 4) == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
         }
       } else {
         const size_t at = (size_t)blockIdx.x * 2 + !outer;
@@ -917,7 +924,7 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
       for (int u = 0; u < U; ++u)
         if (p0 + u <= rec.z) sum.add(ml[u], o[u]);
     }
-    const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+    const float inv = sum.l == 0.f ? 0.f : __fdividef(1.f, sum.l);
     const size_t at = (size_t)rec.x * hq + h * a.G + row;
     *reinterpret_cast<uint2*>(a.out + at * D + (e % (D / 4)) * 4) =
         make_uint2(pack_bf16(sum.o.x * inv, sum.o.y * inv), pack_bf16(sum.o.z * inv, sum.o.w * inv));
