@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   if (lane < 2) s_seg[warp][lane] = make_int4(0, 0, 0, 0);
   if (lane < C::S) mbar_init(&s_full[warp][lane], 1);
   fence_barrier_init();
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
 
@@ -314,7 +315,10 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   Walk<KT> walk;
   bool at_end;  // this warp's range ends with the CTA's
   {
-    const int run = (a.B + C::kThreads - 1) / C::kThreads, b0 = threadIdx.x * run, b1 = min(a.B, b0 + run);
+    // runs of requests, a lane each; up to 256 requests every warp looks at all of them, else the CTA's warps share them
+    const bool alone = a.B <= 256;
+    const int run = alone ? (a.B + 31) / 32 : (a.B + C::kThreads - 1) / C::kThreads;
+    const int b0 = (alone ? lane : (int)threadIdx.x) * run, b1 = min(a.B, b0 + run);
     const unsigned segs = (unsigned)(a.c.kv_heads * a.groups);
     unsigned long long tiles = 0;
     unsigned live = 0;
@@ -334,24 +338,27 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
       const unsigned y1 = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) x += x1, y += y1;
     }
-    if (lane == 31) {
-      s_scan[warp] = x;
-      s_live[warp] = y;
-    }
-    __syncthreads();
-    unsigned long long tiles_before = x - tiles, all = 0;
-    unsigned live_before = y - live, all_live = 0;
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) tiles_before += s_scan[w], live_before += s_live[w];
-      all += s_scan[w];
-      all_live += s_live[w];
+    unsigned long long tiles_before = x - tiles, all = __shfl_sync(0xffffffffu, x, 31);
+    unsigned live_before = y - live, all_live = __shfl_sync(0xffffffffu, y, 31);
+    if (!alone) {
+      if (lane == 31) {
+        s_scan[warp] = x;
+        s_live[warp] = y;
+      }
+      __syncthreads();
+      all = all_live = 0;
+      for (int w = 0; w < W; ++w) {
+        if (w < warp) tiles_before += s_scan[w], live_before += s_live[w];
+        all += s_scan[w];
+        all_live += s_live[w];
+      }
     }
     if (bad) atomicCAS(&s_err, 0, 241);
     all *= segs;
     // what a segment's end weighs: no more than a warp has tiles
     walk.end = (int)min((unsigned long long)kEnd, quot(all, (unsigned)(a.ctas * W)));
     total = all + (unsigned long long)all_live * segs * walk.end;
-    s_before[threadIdx.x] = (tiles_before + (unsigned long long)live_before * walk.end) * segs;
+    const unsigned long long before = (tiles_before + (unsigned long long)live_before * walk.end) * segs;
     // as many CTAs as have a tile for each warp
     n_ctas = (unsigned)min((unsigned long long)a.ctas, (all + W - 1) / W);
     const unsigned c = blockIdx.x;
@@ -366,13 +373,22 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
     const unsigned long long at = lo + warps.first(warp);
     walk.left = (long long)(warps.each + ((unsigned)warp < warps.more));
     at_end = lo + warps.first(warp + 1) == hi;
-    __syncthreads();
+    if (!alone) {
+      s_before[threadIdx.x] = before;
+      __syncthreads();
+    }
     if (walk.left > 0) {
       // the last run of requests that begins at or before this warp's range, and in it the request: a lane each
       int owner = -1;
+      unsigned long long skip;
+      if (alone) {
+        owner += __popc(__ballot_sync(0xffffffffu, before <= at));
+        skip = at - __shfl_sync(0xffffffffu, before, owner);
+      } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) owner += __popc(__ballot_sync(0xffffffffu, s_before[i * 32 + lane] <= at));
-      unsigned long long skip = at - s_before[owner];
+        for (int i = 0; i < W; ++i) owner += __popc(__ballot_sync(0xffffffffu, s_before[i * 32 + lane] <= at));
+        skip = at - s_before[owner];
+      }
       walk.b = owner * run;
       if (run > 1) {
         const int b = walk.b + lane;
