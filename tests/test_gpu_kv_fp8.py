@@ -41,7 +41,7 @@ def caches(blocks, hk, bs, d, order="head", fill=3):
 
 @pytest.mark.parametrize("order", ["head", "slot"])
 @pytest.mark.parametrize("n,hk,bs,d,gather,pad", [(1, 8, 16, 128, False, 0), (3, 1, 16, 64, True, 8),
-                                                  (211, 3, 32, 64, True, 64), (100, 8, 64, 128, False, 1024),
+                                                  (211, 3, 32, 64, True, 64), (100, 8, 64, 128, False, 1040),
                                                   (77, 5, 256, 128, True, 0), (259, 2, 128, 64, False, 24),
                                                   (1025, 1, 16, 64, True, 0)])
 def test_write(lm, n, hk, bs, d, gather, pad, order):

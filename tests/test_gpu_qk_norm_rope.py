@@ -86,7 +86,7 @@ def test_widths(lm, d, rot, interleaved):
 
 
 @pytest.mark.parametrize("T,hq,hk,d", [(1, 64, 8, 128), (1, 1, 0, 64), (1, 0, 1, 64), (7, 5, 1, 128), (700, 1, 1, 64),
-                                       (2500, 2, 0, 64), (3000, 0, 3, 80), (1300, 40, 8, 128), (900, 12, 2, 256),
+                                       (2500, 2, 0, 64), (3000, 0, 3, 80), (1300, 40, 8, 128), (900, 11, 2, 256),
                                        (2, 1024, 1024, 8), (1, 1024, 3, 128)])
 def test_shapes(lm, T, hq, hk, d):
     for il in (False, True):
