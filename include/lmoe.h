@@ -556,7 +556,7 @@ LMOE_API int lmoe_kv_write_fp8(const lmoe_kv_cache_fp8* cache, const uint16_t* k
  *   first    int32 [B], or NULL for 0: positions before it are skipped
  *   block_table    int32 [B][max_blocks]
  *   k_out, v_out   out bf16 [n_tokens][kv_heads][head_dim], strides k_stride
- *            and v_stride (multiples of 8)
+ *            and v_stride (multiples of 8); their rows do not overlap
  *   ws       optional, as for lmoe_tree_masks: rows whose request's offsets
  *            descend or pass n_tokens, whose position is below 0 or past the
  *            table, or whose block is outside the cache are reported there
@@ -594,7 +594,7 @@ LMOE_API size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims
  *   block_table  int32 [B][max_blocks]
  *   out      out bf16 [B][q_heads][head_dim], contiguous
  *   lse      out fp32 [B][q_heads], or NULL
- * q and out are 16-byte aligned, lens, block_table and lse 4-byte.
+ * out and lse overlap no input and not one another; q and out are 16-byte aligned, lens, block_table and lse 4-byte.
  * Scores, their maximum and sum, and the accumulators are fp32.  For the
  * product with the values a probability times its value's scale is rounded to
  * 11 bits (below 2^-28 of the row's largest such product, to multiples of

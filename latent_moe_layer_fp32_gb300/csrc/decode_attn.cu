@@ -863,16 +863,20 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
         acc = reinterpret_cast<const float4*>(a.warp_o + at * C::kPiece)[e];
       }
       float m = way_ml.x;
-#pragma unroll 4
-      for (int w = w0; w <= w1; ++w) m = fmaxf(m, s_ml[w][r].x);
+      float2 ml[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        ml[w] = w >= w0 && w <= w1 ? s_ml[w][r] : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, ml[w].x);
+      }
       const float mu = m == -INFINITY ? 0.f : m;
       float l = ex2(way_ml.x - mu) * way_ml.y;
       acc = make_float4(acc.x * l, acc.y * l, acc.z * l, acc.w * l);
-#pragma unroll 4
-      for (int w = w0; w <= w1; ++w) {
-        const float2 ml = s_ml[w][r];
-        const float4 x = reinterpret_cast<const float4*>(piece_at(w))[e];
-        const float f = ex2(ml.x - mu) * ml.y;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w >= w0 && w <= w1) x = reinterpret_cast<const float4*>(piece_at(w))[e];
+        const float f = ex2(ml[w].x - mu) * ml[w].y;
         l += f;
         acc = make_float4(fmaf(f, x.x, acc.x), fmaf(f, x.y, acc.y), fmaf(f, x.z, acc.z), fmaf(f, x.w, acc.w));
       }
