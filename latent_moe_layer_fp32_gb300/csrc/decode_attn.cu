@@ -28,12 +28,12 @@
 //    effect.  8 warps and 3 tiles with 128 columns, 12 and 2 with 64; a number
 //    that is no multiple of 4 leaves the SM's quarters uneven (10 warps: 75 us).
 //
-// 64 requests of 512 to 8191 positions (365 MB) take 65 us, 5600 GB/s; 256 requests
-// of 20 to 8191 (814 MB) 137 us, 5950 GB/s, 88% of the copy rate; one request at
-// 131071 positions 48.8 us.  About 8 us of each are start-up (launch, lengths, page
-// numbers, first copy: 4.5), the join and the second kernel (3.5).  16 heads a key
-// head: 81 us for the 64 requests, bound by the arithmetic's latency (two warps an
-// SM quarter, 1.7 instructions a clock).
+// 64 requests of 512 to 8191 positions (365 MB) take 64 us, 5710 GB/s; 256 requests
+// of 20 to 8191 (814 MB) 135 us, 6030 GB/s, 89% of the copy rate; one request at
+// 131071 positions 48.8 us, at 1021 8.8 us.  About 8 us of each are start-up (launch,
+// lengths, page numbers, first copy: 4.5), the join and the second kernel (3.5).  16
+// heads a key head: 79.6 us for the 64 requests, bound by the arithmetic's latency
+// (two warps an SM quarter, 1.7 instructions a clock).
 #include <algorithm>
 #include <atomic>
 #include <cstring>
