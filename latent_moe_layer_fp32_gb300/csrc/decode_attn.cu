@@ -174,12 +174,9 @@ struct Sum {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  __device__ __forceinline__ void add(float2 ml, float4 x) {
-    const float top = fmaxf(m, ml.x), mu = top == -INFINITY ? 0.f : top;
-    const float f = ex2(m - mu), w = ex2(ml.x - mu) * ml.y;
-    m = top;
-    l = fmaf(l, f, w);
-    o = make_float4(fmaf(w, x.x, o.x * f), fmaf(w, x.y, o.y * f), fmaf(w, x.z, o.z * f), fmaf(w, x.w, o.w * f));
+  __device__ __forceinline__ void add(float w, float4 x) {
+    l += w;
+    o = make_float4(fmaf(w, x.x, o.x), fmaf(w, x.y, o.y), fmaf(w, x.z, o.z), fmaf(w, x.w, o.w));
   }
   __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2; }
 };
@@ -906,7 +903,6 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
 template <int D, int N8>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
   using C = Cfg<D, N8>;
-  constexpr int U = 4;  // pieces under way
   __shared__ int s_err;
   pdl_wait();
   pdl_trigger();
@@ -920,29 +916,45 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecodeArgs a) {
       *a.status = Status{s_err > 250 ? LMOE_ETIMEOUT : s_err ? LMOE_EDEVICE_CHECK : LMOE_OK, s_err};
   }
   const int e = blockIdx.y * blockDim.x + threadIdx.x, r = e / (D / 4), hq = a.c.kv_heads * a.G;
-  auto fetch = [&](float2 (&ml)[U], float4 (&o)[U], int p0, int end) {
+  Sum sum;
+  // n pieces from p0 on (those up to `end` are there) into the sum: fetched at once, then joined
+  auto fetch = [&](auto n, auto& ml, auto& o, int p0, int end) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < n; ++u) {
       const int p = min(p0 + u, end);
       const size_t at = (size_t)p * 2 + (p == (int)blockIdx.x);
       ml[u] = a.ml[at * C::kRows + r];
       o[u] = reinterpret_cast<const float4*>(a.o + at * C::kPiece)[e];
     }
   };
+  auto join = [&](auto n, const auto& ml, const auto& o, int p0, int end) {
+    float m = sum.m;
+#pragma unroll
+    for (int u = 0; u < n; ++u) m = p0 + u <= end ? fmaxf(m, ml[u].x) : m;
+    const float mu = m == -INFINITY ? 0.f : m, f = ex2(sum.m - mu);
+    sum.m = m;
+    sum.l *= f;
+    sum.o = make_float4(sum.o.x * f, sum.o.y * f, sum.o.z * f, sum.o.w * f);
+#pragma unroll
+    for (int u = 0; u < n; ++u)
+      if (p0 + u <= end) sum.add(ex2(ml[u].x - mu) * ml[u].y, o[u]);
+  };
   // the first pieces before it is known whether there are any
-  float2 ml[U];
-  float4 o[U];
-  fetch(ml, o, blockIdx.x, a.ctas - 1);
+  constexpr std::integral_constant<int, 4> kFirst{};
+  constexpr std::integral_constant<int, 8> kMore{};
+  float2 ml[kFirst.value];
+  float4 o[kFirst.value];
+  fetch(kFirst, ml, o, blockIdx.x, a.ctas - 1);
   const int4 rec = a.rec[blockIdx.x];
   int len = (int)blockIdx.x < a.B && blockIdx.y == 0 ? a.lens[blockIdx.x] : 1;
   const int h = rec.y >> 8, row = (rec.y & 255) * 8 + r;
   if (rec.z >= 0 && row < a.G) {
-    Sum sum;
-    for (int p0 = blockIdx.x; p0 <= rec.z; p0 += U) {
-      if (p0 > (int)blockIdx.x) fetch(ml, o, p0, rec.z);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (p0 + u <= rec.z) sum.add(ml[u], o[u]);
+    join(kFirst, ml, o, blockIdx.x, rec.z);
+    for (int p0 = blockIdx.x + kFirst; p0 <= rec.z; p0 += kMore) {
+      float2 ml8[kMore.value];
+      float4 o8[kMore.value];
+      fetch(kMore, ml8, o8, p0, rec.z);
+      join(kMore, ml8, o8, p0, rec.z);
     }
     const float inv = sum.l == 0.f ? 0.f : __fdividef(1.f, sum.l);
     const size_t at = (size_t)rec.x * hq + h * a.G + row;
