@@ -493,7 +493,7 @@ typedef struct {
  *   inv_freq fp32 [rot_dim / 2], of magnitude below 1024 (a larger or
  *            non-finite one gives angles without meaning)
  *   axis     int32 [rot_dim / 2], the axis of each frequency, or NULL for axis
- *            0; a pair whose axis is outside [0, n_axes) is not turned
+ *            0; a pair whose axis is outside [0, n_axes) is turned by 0
  *   q_out, k_out  out bf16, shaped and strided as the inputs are, with
  *            strides of their own; may be q and k themselves (with their
  *            strides), else they overlap no input

@@ -11,8 +11,8 @@
 //
 // 16384 tokens of 72 heads of 128 (604 MB) take 98.4 us, 6140 GB/s, 91% of the copy
 // rate; one token 2.7 us.  Heads of 80 use 10 of 16 lanes: 5003 tokens of 32 heads
-// (51 MB) take 15.8 us, bound by instructions and latency (three heads on 30 lanes,
-// with sums over ten lanes, took 19.6).
+// (51 MB) take 16.5 us, bound by instructions and latency (three heads on 30 lanes,
+// with sums over ten lanes, took 4 us more).
 #include <algorithm>
 
 #include "common.cuh"
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 // Units that a warp has under way, twice, and CTAs of an SM: the prompt takes 98.4 us, with three or five units a batch
-// 110 and 98.2 (and the smaller video 17.1 and 16.3 instead of 15.8), with three CTAs of three units 103.
+// 110 and 98.2 (and the smaller video 1.3 and 0.5 us more), with three CTAs of three units 103.
 constexpr int kBatch = 4, kCtas = 2;
 
 struct RopeArgs {
@@ -91,8 +91,7 @@ __device__ __forceinline__ Pair swapped(Pair p) {
 }
 
 // LP lanes a head, so that a unit is 32 / LP heads; PAIRS: neighbours are pairs (else the halves' elements); FULL: a head
-// fills its lanes.  The
-// units of all tokens, a token's queries first, are cut evenly over the warps.
+// fills its lanes.  The units of all tokens, a token's queries first, are cut evenly over the warps.
 template <int LP, bool PAIRS, bool FULL>
 __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int NP = 32 / LP;
@@ -219,9 +218,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], pair(r, r)), g[e]);
       }
+      // (not by an angle of 0 what is not turned: an infinity would make its neighbour NaN)
       if constexpr (PAIRS) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], cc[e], mul2(swapped(v[e]), ss[e]));
+        for (int e = 0; e < 4; ++e) {
+          const Pair x = fma2(v[e], cc[e], mul2(swapped(v[e]), ss[e]));
+          v[e] = turned ? x : v[e];
+        }
       } else if (turned) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

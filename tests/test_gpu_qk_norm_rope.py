@@ -138,6 +138,18 @@ def test_nan_and_infinity_stay_in_their_head(lm):
     assert torch.equal(q, ref[0]) and torch.equal(k, ref[1])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_what_is_not_turned_stays_as_it_is(lm, interleaved):
+    """Without a norm, elements from rot_dim on are copied: infinities, NaN and zeros of both signs too."""
+    c = Case(5, 2, 1, 64, rot=24, norm=False, interleaved=interleaved, seed=12)
+    c.q[:, :, 24:].copy_(torch.tensor([float("inf"), 1.0, -0.0, float("-inf"), 0.0, float("nan"), 2.0, -0.0] * 5))
+    q, k = c.run(lm)
+    got, want = q[:, :, 24:].contiguous(), c.q[:, :, 24:].contiguous()
+    nan = torch.isnan(want)  # (any NaN for a NaN, all else to the bit)
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan])
+    assert torch.equal(k[:, :, 24:], c.k[:, :, 24:]) and torch.isfinite(q[:, :, :24]).all()
+
+
 def test_in_place_and_into_wider_rows(lm):
     for il in (False, True):
         c = Case(70, 6, 2, 128, pad=40, interleaved=il, seed=8)
