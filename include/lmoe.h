@@ -596,15 +596,14 @@ LMOE_API size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims
  *   lse      out fp32 [B][q_heads], or NULL
  * out and lse overlap no input and not one another; q and out are 16-byte aligned, lens, block_table and lse 4-byte.
  * Scores, their maximum and sum, and the accumulators are fp32.  For the
- * product with the values a probability times its value's scale is rounded to
- * 11 bits (below 2^-28 of the row's largest such product, to multiples of
- * 2^-38 of it); the sums keep it unrounded; one below 2^-126 of its row's
- * largest may count as none.  So out is off by up to 2^-11 of
- * sum_j p_j |v_j|, besides its own rounding to bf16 (by 0.0017 of its norm on
- * random rows, which is that rounding).  The tensor cores' accumulators may
- * round towards zero: up to 0.4% are lost where one of about 1200 warps adds up
- * a million positions, in proportion beyond.  The results do not depend on
- * timing.
+ * product with the values a probability times its value's scale stands as two
+ * f16 parts, off by at most 2^-22 of itself or 2^-39 of the row's largest such
+ * product, whichever is more; the sums keep it unrounded; one below 2^-126 of its
+ * row's largest may count as none.  So what out is off by is its own rounding to
+ * bf16 (0.0017 of its norm on random rows), also where values cancel.  The
+ * tensor cores' accumulators may round towards zero: up to 0.8% are lost where
+ * one of about 1200 warps adds up a million positions, in proportion beyond.
+ * The results do not depend on timing.
  * Reported on the device (LMOE_EDEVICE_CHECK through lmoe_status_check): a
  * length below 0 or past its table (the request's rows are not written), a
  * block number outside the cache (they hold no meaning).  Nothing is read out

@@ -741,8 +741,10 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
           }
         }
     }
-    // ---- probabilities: their sums in fp32, and as f16 fragments ----
-    uint32_t pf[MT][N8][2];
+    // ---- probabilities: their sums in fp32, and as fragments of two f16 parts (with one, of 11 bits, values that cancel
+    // showed it: 2^-11 of sum p |v|; the second costs 64 requests 65.9 instead of 63.3 us, 256 requests 137 instead of
+    // 136, the window layer 23.8 instead of 22.7, 16 heads a key head 89.4 instead of 78.8) ----
+    uint32_t pf[MT][N8][2], rest[MT][N8][2];
 #pragma unroll
     for (int n = 0; n < N8; ++n) {
       const Pair shift = pair(kShift - (E[n][0] == -INFINITY ? 0.f : E[n][0]),
@@ -755,8 +757,12 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
           const float *const x = &s[mt][n][k * 2], *const y = &so[mt][n][k * 2];
           const float2 v = apart(add2(pair(y[0], y[1]), shift));
           sum = add2(sum, pair(ex2(x[0]), ex2(x[1])));
-          const __half2 hv = __floats2half2_rn(ex2(v.x), ex2(v.y));
+          const float2 p = make_float2(ex2(v.x), ex2(v.y));
+          const __half2 hv = __floats2half2_rn(p.x, p.y);
+          const float2 up = __half22float2(hv);
+          const __half2 lv = __floats2half2_rn(p.x - up.x, p.y - up.y);
           pf[mt][n][k] = transposed(*reinterpret_cast<const uint32_t*>(&hv));
+          rest[mt][n][k] = transposed(*reinterpret_cast<const uint32_t*>(&lv));
         }
       const float2 l = apart(sum);
       L[n][0] = l.x;
@@ -775,7 +781,10 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
           e4m3x4_to_f16x4(__byte_perm(r[2 * x], 0, 0x3120), a0, a1);
           e4m3x4_to_f16x4(__byte_perm(r[2 * x + 1], 0, 0x3120), a2, a3);
 #pragma unroll
-          for (int n = 0; n < N8; ++n) mma_f16(o[c + x][n], a0, a1, a2, a3, pf[mt][n][0], pf[mt][n][1]);
+          for (int n = 0; n < N8; ++n) {
+            mma_f16(o[c + x][n], a0, a1, a2, a3, pf[mt][n][0], pf[mt][n][1]);
+            mma_f16(o[c + x][n], a0, a1, a2, a3, rest[mt][n][0], rest[mt][n][1]);
+          }
         }
       });
     });
