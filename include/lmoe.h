@@ -587,8 +587,9 @@ LMOE_API size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims
  * `window` of them.  Query head h reads kv head h / (q_heads / kv_heads):
  *   out[b][h] = sum_j p_j v_j,  p = softmax of scale * (q . k_j);
  *   lse[b][h] = ln sum_j exp(scale * (q . k_j)).
- * A request with no positions gets out = 0 and lse = -infinity.  Slots that
- * are not in sight have no effect, whatever they hold.
+ * A request with no positions gets out = 0 and lse = -infinity, and so does a
+ * row all of whose scores are -infinity.  Slots that are not in sight have no
+ * effect, whatever they hold.
  *   q        bf16 [B][q_heads][head_dim], q_stride elements from token to token
  *   lens     int32 [B], at most max_blocks * block_size
  *   block_table  int32 [B][max_blocks]

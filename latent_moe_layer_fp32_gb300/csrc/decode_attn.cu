@@ -523,6 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
   float o[C::kChunks][N8][4], minus_M[N8][2], E[N8][2], L[N8][2];
   int stage = 0;
   bool fresh = true, whole = false;  // the segment has no tile here yet; its first tile is in this range
+  unsigned based = 0;  // a bit for each of this lane's rows that has a base: a score above -infinity
   // this lane's row of a 16-key matrix pair, and its half of two pieces
   const uint32_t lane_at = (lane & 15) * D + (((lane >> 4) ^ swizzle<D>(lane & 15)) << 4);
 
@@ -572,9 +573,9 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
       continue;
     }
     stage = stage == C::S - 1 ? 0 : stage + 1;
-    const bool first_tile = fresh;
     if (fresh) {
       fresh = false;
+      based = 0;
       whole = walk.tile == 0;
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
       for (int mt = 1; mt < MT; ++mt) m = fmaxf(m, fmaxf(x[mt][n][j], x[mt][n][2 + j]));
       return m;
     };
-    bool more = first_tile;
+    bool more = based != (1u << 2 * N8) - 1;
     float top[N8][2];
 #pragma unroll
     for (int n = 0; n < N8; ++n)
@@ -712,9 +713,11 @@ __global__ void __launch_bounds__(Cfg<D, N8>::kThreads, 1)
           float m = top[n][j];
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-          // how far the base moves: to the largest score, the first time also down
-          const float by = first_tile ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
-          L[n][j] = first_tile ? 0.f : L[n][j] * ex2(-by);
+          // how far the base moves: to the largest score, the first time also down (until then L is 0, or NaN)
+          const bool had = based >> (2 * n + j) & 1;
+          const float by = had ? fmaxf(m, 0.f) : m == -INFINITY ? 0.f : m;
+          if (had) L[n][j] *= ex2(-by);
+          if (m != -INFINITY) based |= 1u << (2 * n + j);
           E[n][j] -= by;
           minus_M[n][j] -= by;
 #pragma unroll
