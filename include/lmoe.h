@@ -487,8 +487,8 @@ typedef struct {
 /*   q, k     bf16 [T][heads][head_dim], q_stride and k_stride elements from
  *            token to token (multiples of 8: slices of a fused projection
  *            fit), 16-byte aligned; not read, and may be NULL, with no heads
- *   q_gain, k_gain  bf16 [head_dim], 8-byte aligned, or NULL for ones; only
- *            a norm reads them
+ *   q_gain, k_gain  bf16 [head_dim], 8-byte aligned, or NULL for ones; read
+ *            by a norm only, and by a side that has heads
  *   pos      int32 [n_axes][T]; any value, also below 0
  *   inv_freq fp32 [rot_dim / 2], of magnitude below 1024 (a larger or
  *            non-finite one gives angles without meaning)

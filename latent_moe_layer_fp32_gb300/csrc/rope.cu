@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     const uint16_t* const g = side ? a.k_gain : a.q_gain;
-    const bool there = a.norm && g && in;
+    const bool there = g && in;
     gain[side][0] = there ? *reinterpret_cast<const uint2*>(g + o1) : make_uint2(0x3f803f80u, 0x3f803f80u);
     gain[side][1] = there ? *reinterpret_cast<const uint2*>(g + o2) : make_uint2(0x3f803f80u, 0x3f803f80u);
   }
@@ -301,8 +301,9 @@ extern "C" int lmoe_qk_norm_rope(const lmoe_rope_dims* d, const uint16_t* q, int
   a.k = k;
   a.q_out = q_out;
   a.k_out = k_out;
-  a.q_gain = q_gain;
-  a.k_gain = k_gain;
+  // (only the gains that a norm reads: that of a side without heads may be any pointer)
+  a.q_gain = d->norm && d->q_heads ? q_gain : nullptr;
+  a.k_gain = d->norm && d->k_heads ? k_gain : nullptr;
   a.pos = pos;
   a.axis = axis;
   a.freq = inv_freq;
