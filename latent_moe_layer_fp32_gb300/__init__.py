@@ -99,6 +99,7 @@ class LmoeKvCacheFp8(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("n_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("maps", ctypes.c_void_p)]
+    _on = None  # the device of the tensors that kv_cache_fp8_of made it of
 
     def __setattr__(self, name, value):
         super().__setattr__(name, value)
@@ -543,6 +544,20 @@ def _elsewhere(t, dev, what):
         raise ValueError(f"{what}: on cuda:{t.get_device()}, but the current device is cuda:{dev}")
 
 
+def _cache_on(dev, cache):
+    """Likewise for a cache's tensors (a descriptor made by hand does not say where they are)."""
+    if cache._on is not None and cache._on != dev:
+        raise ValueError(f"cache: on cuda:{cache._on}, but the current device is cuda:{dev}")
+    return ctypes.byref(cache)
+
+
+def _ws_on(dev, ws):
+    at = _ws_arg(ws)
+    if ws is not None:
+        _elsewhere(ws, dev, "ws")
+    return at
+
+
 def _rows_of(dev, n, t, heads, width, what):
     """_rows of a tensor of at least n rows on device dev, with the shortest path for what is right."""
     try:
@@ -626,6 +641,10 @@ def kv_cache_fp8_of(k, v, k_scale, v_scale) -> LmoeKvCacheFp8:
     cache = LmoeKvCacheFp8(k.data_ptr(), v.data_ptr(), _arg(k_scale, n * h * b, _SCALES, "k_scale"),
                            _arg(v_scale, n * h * b, _SCALES, "v_scale"), n, b, h, d, k.stride(0), k.stride(1),
                            k.stride(2), None)
+    cache._on = k.get_device()
+    for t, what in ((v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None and t.get_device() != cache._on:
+            raise ValueError(f"{what}: on cuda:{t.get_device()}, but k is on cuda:{cache._on}")
     maps = LmoeKvMapsFp8()
     _check(load().lmoe_kv_maps_fp8_init(ctypes.byref(cache), ctypes.byref(maps)), "lmoe_kv_maps_fp8_init")
     cache.maps = ctypes.addressof(maps)  # they live as long as a descriptor that has their address
@@ -638,8 +657,8 @@ def lmoe_kv_write_fp8(cache, k_new, v_new, src, slots, ws=None, stream=None):
     hk, d, n, dev = cache.kv_heads, cache.head_dim, slots.numel(), _device()
     kp, ks = _rows_of(dev, 1, k_new, hk, d, "k_new")
     vp, vs = _rows_of(dev, 1, v_new, hk, d, "v_new")
-    w, nb = _ws_arg(ws)
-    rc = load().lmoe_kv_write_fp8(ctypes.byref(cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
+    w, nb = _ws_on(dev, ws)
+    rc = load().lmoe_kv_write_fp8(_cache_on(dev, cache), kp, ks, vp, vs, min(k_new.shape[0], v_new.shape[0]),
                                   _vec(dev, src, n, _INT32, "src"), _vec(dev, slots, 1, _INT32, "slots"), n, w, nb,
                                   _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
@@ -654,9 +673,9 @@ def lmoe_kv_read_fp8(cache, token_offsets, first, block_table, k_out, v_out, ws=
         raise ValueError(f"block_table: expected [{b}, max_blocks], got {tuple(block_table.shape)}")
     kp, ks = _rows_of(dev, 1, k_out, hk, d, "k_out")
     vp, vs = _rows_of(dev, 1, v_out, hk, d, "v_out")
-    w, nb = _ws_arg(ws)
+    w, nb = _ws_on(dev, ws)
     rc = load().lmoe_kv_read_fp8(
-        ctypes.byref(cache), b, min(k_out.shape[0], v_out.shape[0]), block_table.shape[1],
+        _cache_on(dev, cache), b, min(k_out.shape[0], v_out.shape[0]), block_table.shape[1],
         _vec(dev, token_offsets, 2, _INT32, "token_offsets"), _vec(dev, first, b, _INT32, "first"),
         _vec(dev, block_table, 1, _INT32, "block_table"), kp, ks, vp, vs, w, nb,
         _raw_stream(dev) if stream is None else stream.cuda_stream)
@@ -678,9 +697,9 @@ def lmoe_decode_attention_fp8(dims, cache, q, lens, block_table, out, lse, ws, s
     b, hq, d, dev = dims.n_requests, dims.q_heads, cache.head_dim, _device()
     qp, qs = _rows_of(dev, b, q, hq, d, "q")
     rc = load().lmoe_decode_attention_fp8(
-        ctypes.byref(dims), ctypes.byref(cache), qp, qs, _vec(dev, lens, b, _INT32, "lens"),
+        ctypes.byref(dims), _cache_on(dev, cache), qp, qs, _vec(dev, lens, b, _INT32, "lens"),
         _vec(dev, block_table, b * dims.max_blocks, _INT32, "block_table"),
-        _vec(dev, out, b * hq * d, _BF16_DTYPE, "out"), _vec(dev, lse, b * hq, _FP32, "lse"), *_ws_arg(ws),
+        _vec(dev, out, b * hq * d, _BF16_DTYPE, "out"), _vec(dev, lse, b * hq, _FP32, "lse"), *_ws_on(dev, ws),
         _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LmoeError(rc, "lmoe_decode_attention_fp8")
