@@ -588,6 +588,19 @@ def _vec(dev, t, n, dtype, what):
     return at
 
 
+def _lines(dev, t, n, width, dtype, what):
+    """_vec of n rows of `width` elements: a tensor whose rows are of another length would be read as other rows.
+    What has no rows, or pieces of them (all flat, or heads in one dimension), is taken as it lies."""
+    at = _vec(dev, t, n * width, dtype, what)
+    if at and n > 1 and t.stride(0) != width:
+        piece, left = 1, list(t.shape)
+        while left and piece * left[-1] < width:
+            piece *= left.pop()
+        if len(left) > 1 and piece * left[-1] != width or width % piece:
+            raise ValueError(f"{what}: expected rows of {width} elements, got {tuple(t.shape)}")
+    return at
+
+
 def rope_dims_of(n_tokens, q_heads, k_heads, head_dim, rot_dim=None, n_axes=1, interleaved=False, norm=True,
                  eps=1e-6) -> LmoeRopeDims:
     """rot_dim None: the whole head is turned."""
@@ -610,7 +623,7 @@ def lmoe_qk_norm_rope(dims, q, k, q_gain, k_gain, pos, inv_freq, axis, q_out, k_
         ko, kos = _rows_of(dev, t, k_out, hk, d, "k_out")
     rc = load().lmoe_qk_norm_rope(
         ctypes.byref(dims), qp, qs, kp, ks, _vec(dev, q_gain, d, _BF16_DTYPE, "q_gain"),
-        _vec(dev, k_gain, d, _BF16_DTYPE, "k_gain"), _vec(dev, pos, dims.n_axes * t, _INT32, "pos"),
+        _vec(dev, k_gain, d, _BF16_DTYPE, "k_gain"), _lines(dev, pos, dims.n_axes, t, _INT32, "pos"),
         _vec(dev, inv_freq, half, _FP32, "inv_freq"), _vec(dev, axis, half, _INT32, "axis"), qo, qos, ko, kos,
         _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
@@ -698,8 +711,8 @@ def lmoe_decode_attention_fp8(dims, cache, q, lens, block_table, out, lse, ws, s
     qp, qs = _rows_of(dev, b, q, hq, d, "q")
     rc = load().lmoe_decode_attention_fp8(
         ctypes.byref(dims), _cache_on(dev, cache), qp, qs, _vec(dev, lens, b, _INT32, "lens"),
-        _vec(dev, block_table, b * dims.max_blocks, _INT32, "block_table"),
-        _vec(dev, out, b * hq * d, _BF16_DTYPE, "out"), _vec(dev, lse, b * hq, _FP32, "lse"), *_ws_on(dev, ws),
+        _lines(dev, block_table, b, dims.max_blocks, _INT32, "block_table"),
+        _lines(dev, out, b, hq * d, _BF16_DTYPE, "out"), _lines(dev, lse, b, hq, _FP32, "lse"), *_ws_on(dev, ws),
         _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LmoeError(rc, "lmoe_decode_attention_fp8")
