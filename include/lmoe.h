@@ -596,7 +596,11 @@ LMOE_API size_t lmoe_decode_attention_fp8_workspace_bytes(const lmoe_decode_dims
  *   out      out bf16 [B][q_heads][head_dim], contiguous
  *   lse      out fp32 [B][q_heads], or NULL
  * out and lse overlap no input and not one another; q and out are 16-byte aligned, lens, block_table and lse 4-byte.
- * Scores, their maximum and sum, and the accumulators are fp32.  For the
+ * A query's elements enter as f16 times a power of two of their row: exact where
+ * they are at least 2^-31 of its largest magnitude, else off by at most 2^-39 of
+ * it.  Scores, formed as ((q . codes) scale) 2^e with the keys' codes and scales
+ * 2^e (what leaves fp32's range before the last product stays out of it), their
+ * maximum and sum, and the accumulators are fp32.  For the
  * product with the values a probability times its value's scale stands as two
  * f16 parts, off by at most 2^-22 of itself or 2^-39 of the row's largest such
  * product, whichever is more; the sums keep it unrounded; one below 2^-126 of its

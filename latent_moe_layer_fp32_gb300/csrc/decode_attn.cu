@@ -7,7 +7,8 @@
 //  - Keys (and the values' columns) are the 16 rows of a tensor-core product and
 //    the query heads its 8 columns, so that 8 heads waste nothing.  Codes become
 //    f16 exactly on their way from shared memory into the fragments; queries
-//    are f16 exactly after a power of two.  A product takes 8 clocks of an SM
+//    are f16 after a power of two of their row, exactly down to 2^-31 of its
+//    largest element.  A product takes 8 clocks of an SM
 //    quarter and 16% of the tensor pipe's time: tcgen05 would have to read
 //    queries and probabilities as further E4M3 parts from shared memory, for
 //    a pipe that is not what bounds.  (Products of E4M3 codes with queries in
