@@ -557,10 +557,13 @@ LMOE_API int lmoe_kv_write_fp8(const lmoe_kv_cache_fp8* cache, const uint16_t* k
  *   block_table    int32 [B][max_blocks]
  *   k_out, v_out   out bf16 [n_tokens][kv_heads][head_dim], strides k_stride
  *            and v_stride (multiples of 8); their rows do not overlap
- *   ws       optional, as for lmoe_tree_masks: rows whose request's offsets
- *            descend or pass n_tokens, whose position is below 0 or past the
- *            table, or whose block is outside the cache are reported there
- *            and left as they were in any case
+ *   ws       optional, as for lmoe_tree_masks: offsets below 0, that descend or
+ *            that pass n_tokens, positions below 0 or past the table and blocks
+ *            outside the cache are reported there; rows of such requests,
+ *            positions and blocks are left as they were in any case
+ * Rows before token_offsets[0] and from token_offsets[B] on are outside all
+ * requests, also where offsets between them pass these; where descending offsets
+ * give a row to several requests, it gets the position of one of them.
  * Values are exact (an E4M3 code times a power of two is a bf16 value), but for
  * those outside bf16's range, which round as any fp32 value does. */
 LMOE_API int lmoe_kv_read_fp8(const lmoe_kv_cache_fp8* cache, int32_t n_requests, int32_t n_tokens,
