@@ -497,10 +497,11 @@ typedef struct {
  *   q_out, k_out  out bf16, shaped and strided as the inputs are, with
  *            strides of their own; may be q and k themselves (with their
  *            strides), else they overlap no input
- * pos and inv_freq may be NULL with rot_dim 0.  The angle is the exact product
- * of position and frequency, taken modulo a turn in 64-bit fixed point, so far
- * positions lose nothing; sums and products are fp32 (squares of magnitudes
- * above 1e18 overflow there), and y is rounded to bf16 once. */
+ * pos and inv_freq may be NULL with rot_dim 0.  The angle is the product of
+ * position and frequency in 64-bit fixed point modulo a turn, off by at most
+ * |pos| 2^-64 turns, and then rounded to fp32; so far positions and angles near 0
+ * lose nothing; sums and products are fp32 (squares of magnitudes above 1e18
+ * overflow there), and y is rounded to bf16 once. */
 LMOE_API int lmoe_qk_norm_rope(const lmoe_rope_dims* dims, const uint16_t* q, int64_t q_stride, const uint16_t* k,
                                int64_t k_stride, const uint16_t* q_gain, const uint16_t* k_gain, const int32_t* pos,
                                const float* inv_freq, const int32_t* axis, uint16_t* q_out, int64_t q_out_stride,

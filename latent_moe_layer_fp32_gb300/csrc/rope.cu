@@ -11,7 +11,7 @@
 //
 // 16384 tokens of 72 heads of 128 (604 MB) take 98.4 us, 6140 GB/s, 91% of the copy
 // rate; one token 2.7 us.  Heads of 80 use 10 of 16 lanes: 5003 tokens of 32 heads
-// (51 MB) take 16.5 us, bound by instructions and latency (three heads on 30 lanes,
+// (51 MB) take 16.6 us, bound by instructions and latency (three heads on 30 lanes,
 // with sums over ten lanes, took 4 us more).
 #include <algorithm>
 
@@ -53,6 +53,14 @@ __device__ __forceinline__ uint64_t turn_step(float f) {
   const uint64_t w2 = __umul64hi(m, kHi) + (low < w1);
   const uint64_t r = e <= 0 ? low : e < 64 ? low >> e | w2 << (64 - e) : e < 128 ? w2 >> (e - 64) : 0;
   return bits >> 31 ? 0 - r : r;
+}
+
+// 2^-64 turns modulo a turn as half turns, -1 to 1; the lower half goes along as a signed number, so that angles near 0
+// of both signs keep their bits (without it the sine of 1e-7 is off by 1%; as one 64-bit conversion one token takes 2.9
+// instead of 2.7 us, the video below 16.8 instead of 16.6).
+__device__ __forceinline__ float half_turns(uint64_t x) {
+  const int lo = (int)(uint32_t)x, hi = (int)((uint32_t)(x >> 32) + ((uint32_t)x >> 31));
+  return fmaf((float)lo, 0x1p-63f, (float)hi * 0x1p-31f);
 }
 
 // Two fp32 values in one register pair.
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
       if (turned) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          sincospif((float)(int32_t)((uint64_t)(long long)now.pos[e] * step[e] >> 32) * 0x1p-31f, &s[e], &c[e]);
+          sincospif(half_turns((uint64_t)(long long)now.pos[e] * step[e]), &s[e], &c[e]);
       }
       if constexpr (PAIRS) {
 #pragma unroll
@@ -218,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_rope_kernel(const Rop
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], pair(r, r)), g[e]);
       }
-      // (not by an angle of 0 what is not turned: an infinity would make its neighbour NaN)
+      // (not by an angle of 0 what is not turned: an infinity would make its neighbour NaN; a branch around the pairs, as
+      // around the halves, takes the video 17.0 instead of 16.6 us)
       if constexpr (PAIRS) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
