@@ -501,7 +501,8 @@ typedef struct {
  * position and frequency in 64-bit fixed point modulo a turn, off by at most
  * |pos| 2^-64 turns, and then rounded to fp32; so far positions and angles near 0
  * lose nothing; sums and products are fp32 (squares of magnitudes above 1e18
- * overflow there), and y is rounded to bf16 once. */
+ * overflow there, below 1e-19 they lose bits or vanish, which eps covers where it is
+ * not 0), and y is rounded to bf16 once. */
 LMOE_API int lmoe_qk_norm_rope(const lmoe_rope_dims* dims, const uint16_t* q, int64_t q_stride, const uint16_t* k,
                                int64_t k_stride, const uint16_t* q_gain, const uint16_t* k_gain, const int32_t* pos,
                                const float* inv_freq, const int32_t* axis, uint16_t* q_out, int64_t q_out_stride,

@@ -9,7 +9,7 @@
 //    f16 exactly on their way from shared memory into the fragments; queries
 //    are f16 after a power of two of their row, exactly down to 2^-31 of its
 //    largest element.  A product takes 8 clocks of an SM
-//    quarter and 16% of the tensor pipe's time: tcgen05 would have to read
+//    quarter and 23% of the tensor pipe's time: tcgen05 would have to read
 //    queries and probabilities as further E4M3 parts from shared memory, for
 //    a pipe that is not what bounds.  (Products of E4M3 codes with queries in
 //    two E4M3 parts, which need no conversion of the keys, were slower: 70.2
@@ -29,12 +29,13 @@
 //    effect.  8 warps and 3 tiles with 128 columns, 12 and 2 with 64; a number
 //    that is no multiple of 4 leaves the SM's quarters uneven (10 warps: 75 us).
 //
-// 64 requests of 512 to 8191 positions (365 MB) take 64 us, 5710 GB/s; 256 requests
-// of 20 to 8191 (814 MB) 135 us, 6030 GB/s, 89% of the copy rate; one request at
-// 131071 positions 48.8 us, at 1021 8.8 us.  About 8 us of each are start-up (launch,
+// 64 requests of 512 to 8191 positions (365 MB) take 66.2 us, 5510 GB/s; 256 requests
+// of 20 to 8191 (814 MB) 138 us, 5900 GB/s, 87% of the copy rate; one request at
+// 131071 positions 50.8 us, at 1021 8.8 us.  About 8 us of each are start-up (launch,
 // lengths, page numbers, first copy: 4.5), the join and the second kernel (3.5).  16
-// heads a key head: 79.6 us for the 64 requests, bound by the arithmetic's latency
-// (two warps an SM quarter, 1.7 instructions a clock).
+// heads a key head: 90 us for the 64 requests, bound by the arithmetic's latency (two
+// warps an SM quarter, 1.7 instructions a clock, more than half of the stalls waits
+// of fixed length).
 #include <algorithm>
 #include <atomic>
 #include <cstring>
