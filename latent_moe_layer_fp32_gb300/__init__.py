@@ -592,7 +592,7 @@ def _lines(dev, t, n, width, dtype, what):
     """_vec of n rows of `width` elements: a tensor whose rows are of another length would be read as other rows.
     What has no rows, or pieces of them (all flat, or heads in one dimension), is taken as it lies."""
     at = _vec(dev, t, n * width, dtype, what)
-    if at and n > 1 and t.stride(0) != width:
+    if at and n > 1 and t.stride(0) != width > 0:  # (no width at all is the library's to refuse)
         piece, left = 1, list(t.shape)
         while left and piece * left[-1] < width:
             piece *= left.pop()

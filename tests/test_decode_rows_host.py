@@ -46,3 +46,12 @@ def test_positions(lib):  # noqa: F811
             call(**(args | two | dict(pos=good)))
     with pytest.raises(Called):  # one axis: the first three of a longer buffer
         call(**(args | dict(pos=ints(1, 8))))
+
+
+def test_widths_that_there_are_not(lib):  # noqa: F811
+    call, args = calls()["decode"]
+    for bad in (dict(max_blocks=0), dict(max_blocks=-1), dict(q_heads=0)):
+        a = dict(n_requests=3, q_heads=4, max_blocks=4, scale=0.125) | bad
+        more = dict(q=on(torch.zeros(3, 0, 64, dtype=torch.bfloat16))) if "q_heads" in bad else {}
+        with pytest.raises(Called):  # the library's answer is its own error
+            call(**(args | dict(dims=lm.decode_dims_of(**a)) | more))
