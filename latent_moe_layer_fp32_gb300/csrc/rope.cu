@@ -11,7 +11,7 @@
 //
 // 16384 tokens of 72 heads of 128 (604 MB) take 98.7 us, 6120 GB/s, 90% of the copy
 // rate; one token 2.7 us.  Heads of 80 use 10 of 16 lanes: 5003 tokens of 32 heads
-// (51 MB) take 16.7 us, bound by instructions (2.5 a clock) (three heads on 30 lanes,
+// (51 MB) take 16.7 us, bound by instructions, 2.5 a clock (three heads on 30 lanes,
 // with sums over ten lanes, took 4 us more).
 #include <algorithm>
 
